@@ -361,6 +361,126 @@ int pc_em_step(pc_handle h, float* params, const float* param_flows, float step_
 int pc_em_step_corrected(pc_handle h, float* params, const float* param_flows, const float* z_flows,
                          float step_size, float pseudocount, void* stream);
 
+/* ---- operators of the network in front of a conditional circuit -------------
+ *
+ * A circuit with LowRank groups takes per-sample factors A_b, B_b, which a
+ * network computes from what the samples are conditioned on, and pc_backward
+ * returns dLL/dA and dLL/dB, from which that network learns.  The calls below
+ * are the parts of such a network that plain matrix products do not cover:
+ * normalisation, mixing along a sequence with a decaying state (whole
+ * sequences, their gradients, and one token at a time), and the orthogonalised
+ * update of its matrices -- or of the factors themselves -- from their
+ * gradients.  They need no handle:
+ *  - `device` is the HIP device that every pointer of the call belongs to.
+ *  - `dtype` is the type of the tensors given as void*: PC_DTYPE_*; sums,
+ *    statistics and states are float32 or wider.  Parameters (weight, bias,
+ *    log_decay), statistics and states are float32.
+ *  - Strides are in elements; the last dimension of every tensor has stride 1.
+ *    No alignment beyond the element's own is needed.
+ *  - Streams, workspaces, return values and errors are those of every other
+ *    call (no allocation, no synchronisation: they can be captured into a HIP
+ *    graph).  Two calls that may run at the same time need two workspaces.
+ *    The workspace is aligned to 16 bytes; nothing in it is kept between calls.
+ *  - Outputs must not overlap inputs, except where a call says so. */
+#define PC_DTYPE_F32  0
+#define PC_DTYPE_BF16 1
+#define PC_DTYPE_F16  2
+
+/* Layer norm over the last dimension of [rows, cols] (1 <= cols <= 16384):
+ *   y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(var + eps),
+ * var the mean of the squared centred values.  weight, bias: float32 [cols],
+ * null for 1 and 0.  mean, rstd: float32 [rows], nullable (the backward pass
+ * needs them).  y may be x (same stride).
+ * Errors: PC_ERR_INVALID_ARG (null pointers, sizes, strides below cols, eps
+ * negative or not finite), PC_ERR_UNSUPPORTED (cols > 16384, unknown dtype). */
+int pc_layer_norm_forward(int device, int dtype, int64_t rows, int32_t cols, const void* x, int64_t x_stride,
+                          const float* weight, const float* bias, float eps, void* y, int64_t y_stride,
+                          float* mean, float* rstd, void* stream);
+
+/* Its gradients, from the mean and rstd of the forward pass, with
+ * n = (x - mean) rstd and g = dy weight:
+ *   dx = rstd (g - mean(g) - n mean(g n)),  dweight = sum dy n,  dbias = sum dy
+ * (sums over the rows, overwritten; either may be null).  dx may be dy or x
+ * (same stride).  The workspace is needed for dweight or dbias only.  Results
+ * are the same bits at every run. */
+int pc_layer_norm_workspace_bytes(int64_t rows, int32_t cols, size_t* bytes);
+int pc_layer_norm_backward(int device, int dtype, int64_t rows, int32_t cols, const void* dy, int64_t dy_stride,
+                           const void* x, int64_t x_stride, const float* weight, const float* mean, const float* rstd,
+                           void* dx, int64_t dx_stride, float* dweight, float* dbias,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* A [tokens, heads, dim] tensor: its first element and two strides. */
+typedef struct pc_heads {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} pc_heads;
+
+/* Linear attention with a fixed decay for each head: along every sequence
+ *   S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,   o_t = scale q_t^T S_t
+ * with S [dim_k, dim_v] for each sequence and head.  Fields not used by a call
+ * are ignored.
+ *  heads, kv_heads: heads of q and o, and of k and v; kv_heads divides heads,
+ *    and head h reads key / value head h / (heads / kv_heads).
+ *  dim_k, dim_v: 1 .. 128.
+ *  num_tokens, num_seqs (<= 65535), cu_seqlens: device int32 [num_seqs + 1],
+ *    sequence i holds tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (any length,
+ *    0 included; tokens outside every sequence are neither read nor written).
+ *    Null: one sequence of all tokens (num_seqs 1).  Entries out of range are
+ *    clamped to [0, num_tokens].
+ *  max_seqlen: a bound of the longest sequence, for the choice of the split
+ *    (results do not depend on it beyond rounding; a bound that is too small
+ *    only costs speed).
+ *  log_decay: device float32 [heads], <= 0 (-inf: no memory).
+ *  scale: finite, not 0.
+ *  state_in, state_out: device float32 [num_seqs, heads, dim_k, dim_v], the
+ *    states before and after the sequences, nullable (0 / not wanted); they
+ *    may be the same buffer.  An empty sequence hands its state through.
+ * A value that is not finite reaches the outputs of its own and later tokens
+ * of its sequence only. */
+typedef struct pc_linear_attention {
+  int32_t dtype;
+  int32_t heads, kv_heads, dim_k, dim_v;
+  int32_t num_seqs;
+  int64_t num_tokens;
+  int64_t max_seqlen;
+  const int32_t* cu_seqlens;
+  const float* log_decay;
+  float scale;
+  pc_heads q, k, v, o;
+  const float* state_in;
+  float* state_out;
+  /* backward: the gradient of o, and those of q, k, v (overwritten) */
+  pc_heads d_o, d_q, d_k, d_v;
+  const float* dstate_out;   /* gradient of state_out, nullable: 0 */
+  float* dstate_in;          /* gradient of state_in, nullable: not wanted; may be dstate_out */
+  /* single tokens: a pool of states, updated in place */
+  float* state;              /* [num_slots, heads, dim_k, dim_v] */
+  int64_t num_slots;
+  const int32_t* slots;      /* device int32 [num_tokens], nullable: row b uses slot b */
+} pc_linear_attention;
+
+/* Workspace of the forward (backward 0) or backward (1) pass; the sizes,
+ * num_seqs, max_seqlen and num_tokens of `d` are used. */
+int pc_linear_attention_workspace_bytes(const pc_linear_attention* d, int backward, size_t* bytes);
+
+/* Whole sequences: o (and state_out) from q, k, v (and state_in).
+ * Errors: PC_ERR_INVALID_ARG, PC_ERR_UNSUPPORTED (dims above 128, more than
+ * 65535 sequences, unknown dtype), PC_ERR_WORKSPACE, PC_ERR_HIP. */
+int pc_linear_attention_forward(int device, const pc_linear_attention* d, void* ws, size_t ws_bytes, void* stream);
+
+/* The gradients d_q, d_k, d_v (and dstate_in) from d_o (and dstate_out), q, k,
+ * v and state_in; the gradients of a shared key / value head are the sums over
+ * the heads that share it, in float32 before they are rounded.  log_decay is a
+ * constant and has no gradient. */
+int pc_linear_attention_backward(int device, const pc_linear_attention* d, void* ws, size_t ws_bytes, void* stream);
+
+/* One token for each row: num_tokens rows of q, k, v, o; row b updates the
+ * state of slot slots[b] (or b) in place and reads it.  Rows whose slot is not
+ * in [0, num_slots) are padding: nothing of them is read or written.  Rows that
+ * name the same slot are successive tokens of that state, in the rows' order. */
+int pc_linear_attention_step(int device, const pc_linear_attention* d, void* stream);
+
 /* Message of the calling thread's last failed call ("" if none). */
 const char* pc_last_error(void);
 

@@ -30,6 +30,8 @@ KERNEL_KINDS = ["sum_fwd_gemm", "elem_flow_gemm", "param_flow_gemm", "weight_spl
 MODES = {"auto": PC_PREC_AUTO, "fp32": PC_PREC_FP32, "tf32": PC_PREC_TF32}
 GEMM_KINDS = {"fwd": 0, "elem": 1, "param": 2}
 
+PC_DTYPE_F32, PC_DTYPE_BF16, PC_DTYPE_F16 = range(3)
+
 _i32p = C.POINTER(C.c_int32)
 
 
@@ -63,6 +65,21 @@ class pc_layout_summary(C.Structure):
                 ("device", C.c_int32)]
 
 
+class pc_heads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class pc_linear_attention(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("heads", C.c_int32), ("kv_heads", C.c_int32), ("dim_k", C.c_int32),
+                ("dim_v", C.c_int32), ("num_seqs", C.c_int32), ("num_tokens", C.c_int64), ("max_seqlen", C.c_int64),
+                ("cu_seqlens", C.c_void_p), ("log_decay", C.c_void_p), ("scale", C.c_float),
+                ("q", pc_heads), ("k", pc_heads), ("v", pc_heads), ("o", pc_heads),
+                ("state_in", C.c_void_p), ("state_out", C.c_void_p),
+                ("d_o", pc_heads), ("d_q", pc_heads), ("d_k", pc_heads), ("d_v", pc_heads),
+                ("dstate_out", C.c_void_p), ("dstate_in", C.c_void_p),
+                ("state", C.c_void_p), ("num_slots", C.c_int64), ("slots", C.c_void_p)]
+
+
 EXPORTS = {
     "pc_compile_layout": (C.c_int, [C.POINTER(pc_circuit_desc), C.c_int, C.POINTER(C.c_void_p)]),
     "pc_destroy": (C.c_int, [C.c_void_p]),
@@ -81,6 +98,19 @@ EXPORTS = {
     "pc_em_step": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_float, C.c_float, C.c_void_p]),
     "pc_em_step_corrected": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_float, C.c_float,
                                        C.c_void_p]),
+    "pc_layer_norm_forward": (C.c_int, [C.c_int, C.c_int, C.c_int64, C.c_int32, C.c_void_p, C.c_int64, C.c_void_p,
+                                        C.c_void_p, C.c_float, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p,
+                                        C.c_void_p]),
+    "pc_layer_norm_workspace_bytes": (C.c_int, [C.c_int64, C.c_int32, C.POINTER(C.c_size_t)]),
+    "pc_layer_norm_backward": (C.c_int, [C.c_int, C.c_int, C.c_int64, C.c_int32, C.c_void_p, C.c_int64, C.c_void_p,
+                                         C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
+                                         C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "pc_linear_attention_workspace_bytes": (C.c_int, [C.POINTER(pc_linear_attention), C.c_int, C.POINTER(C.c_size_t)]),
+    "pc_linear_attention_forward": (C.c_int, [C.c_int, C.POINTER(pc_linear_attention), C.c_void_p, C.c_size_t,
+                                              C.c_void_p]),
+    "pc_linear_attention_backward": (C.c_int, [C.c_int, C.POINTER(pc_linear_attention), C.c_void_p, C.c_size_t,
+                                               C.c_void_p]),
+    "pc_linear_attention_step": (C.c_int, [C.c_int, C.POINTER(pc_linear_attention), C.c_void_p]),
     "pc_last_error": (C.c_char_p, []),
     "pc_layout_info": (C.c_int, [C.c_void_p, C.POINTER(pc_layout_summary)]),
     "pc_layer_class": (C.c_int, [C.c_void_p, C.c_int, C.POINTER(C.c_int)]),
@@ -411,6 +441,195 @@ def workspace(h: Handle, batch: int, device="cuda", all_modes=False):
             n = max(n, pc_workspace_bytes(h, batch))
         pc_set_precision(h, mode)
     return _torch().empty(max(n, 1), dtype=_torch().uint8, device=device)
+
+
+# ---------------------------------------------------------------------------
+# operators of the network in front of a conditional circuit (no handle)
+# ---------------------------------------------------------------------------
+
+def _dtype(t, what):
+    torch = _torch()
+    code = {torch.float32: PC_DTYPE_F32, torch.bfloat16: PC_DTYPE_BF16, torch.float16: PC_DTYPE_F16}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what} must be float32, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _operand(t, like, dtype, shape, what):
+    """The data pointer of a GPU tensor of this dtype and shape on like's
+    device whose last dimension has stride 1 (any other strides)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must live on the GPU")
+    if t.device != like.device:
+        raise ValueError(f"{what} is on {t.device}, not on {like.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {what} must have stride 1")
+    return t.data_ptr()
+
+
+def _dense(t, like, dtype, shape, what):
+    """_operand of a contiguous tensor; None stays None."""
+    if t is None:
+        return None
+    p = _operand(t, like, dtype, shape, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return p
+
+
+def _ws_ptr(ws, like):
+    """(pointer, bytes) of a workspace (the library checks its size)."""
+    if ws is None:
+        return None, 0
+    torch = _torch()
+    return _dense(ws, like, torch.uint8, (ws.numel(),), "ws"), ws.numel()
+
+
+def _stream_of(t, stream):
+    """The given stream, else the current one of the tensor's device."""
+    if stream is not None:
+        return int(stream)
+    return _torch().cuda.current_stream(t.device).cuda_stream
+
+
+def _bytes(f, *args):
+    n = C.c_size_t()
+    _check(f(*args, C.byref(n)))
+    return n.value
+
+
+def _matrix(t, what):
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions")
+    return t
+
+
+def pc_layer_norm_forward(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, stream=None):
+    """y = layer norm of the rows of x [rows, cols] (rows may be strided); weight, bias: float32 [cols] or None;
+    mean, rstd: float32 [rows], kept for the backward pass, or None."""
+    f32 = _torch().float32
+    rows, cols = _matrix(x, "x").shape
+    px, py = _operand(x, x, x.dtype, x.shape, "x"), _operand(y, x, x.dtype, x.shape, "y")
+    _check(lib().pc_layer_norm_forward(
+        x.device.index, _dtype(x, "x"), rows, cols, px, x.stride(0), _dense(weight, x, f32, (cols,), "weight"),
+        _dense(bias, x, f32, (cols,), "bias"), eps, py, y.stride(0), _dense(mean, x, f32, (rows,), "mean"),
+        _dense(rstd, x, f32, (rows,), "rstd"), _stream_of(x, stream)))
+
+
+def layer_norm_workspace(rows: int, cols: int, device="cuda"):
+    """A workspace tensor for pc_layer_norm_backward."""
+    n = _bytes(lib().pc_layer_norm_workspace_bytes, int(rows), int(cols))
+    return _torch().empty(n, dtype=_torch().uint8, device=device)
+
+
+def pc_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, ws=None, stream=None):
+    """dx, dweight and dbias (float32 [cols], or None; all overwritten) from dy, x and the forward's mean and rstd;
+    ws: layer_norm_workspace(rows, cols), needed for dweight and dbias."""
+    f32 = _torch().float32
+    rows, cols = _matrix(x, "x").shape
+    px = _operand(x, x, x.dtype, x.shape, "x")
+    pdy, pdx = _operand(dy, x, x.dtype, x.shape, "dy"), _operand(dx, x, x.dtype, x.shape, "dx")
+    pws, nws = _ws_ptr(ws, x)
+    _check(lib().pc_layer_norm_backward(
+        x.device.index, _dtype(x, "x"), rows, cols, pdy, dy.stride(0), px, x.stride(0),
+        _dense(weight, x, f32, (cols,), "weight"), _dense(mean, x, f32, (rows,), "mean"),
+        _dense(rstd, x, f32, (rows,), "rstd"), pdx, dx.stride(0), _dense(dweight, x, f32, (cols,), "dweight"),
+        _dense(dbias, x, f32, (cols,), "dbias"), pws, nws, _stream_of(x, stream)))
+
+
+def _heads(t, like, shape, what):
+    return pc_heads(_operand(t, like, like.dtype, shape, what), t.stride(0), t.stride(1))
+
+
+def _attention(q, k, v, log_decay, scale):
+    """The descriptor of q [tokens, heads, dim_k], k [tokens, kv_heads, dim_k], v [tokens, kv_heads, dim_v]."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must have three dimensions (tokens, heads, dim)")
+    T, H, dk = q.shape
+    K, dv = k.shape[1], v.shape[2]
+    d = pc_linear_attention(dtype=_dtype(q, "q"), heads=H, kv_heads=K, dim_k=dk, dim_v=dv, num_tokens=T,
+                            scale=float(dk ** -0.5 if scale is None else scale))
+    d.q, d.k, d.v = _heads(q, q, (T, H, dk), "q"), _heads(k, q, (T, K, dk), "k"), _heads(v, q, (T, K, dv), "v")
+    if log_decay is not None:
+        d.log_decay = _dense(log_decay, q, _torch().float32, (H,), "log_decay")
+    return d, (T, H, K, dk, dv)
+
+
+def _sequences(d, q, cu_seqlens, max_seqlen):
+    if cu_seqlens is None:
+        d.num_seqs = 1
+    else:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must have one dimension and at least one entry")
+        d.num_seqs = cu_seqlens.numel() - 1
+        d.cu_seqlens = _dense(cu_seqlens, q, _torch().int32, cu_seqlens.shape, "cu_seqlens")
+    d.max_seqlen = q.shape[0] if max_seqlen is None else int(max_seqlen)
+    return d.num_seqs
+
+
+def linear_attention_workspace(q, k, v, cu_seqlens=None, max_seqlen=None, backward=False):
+    """A workspace tensor for pc_linear_attention_forward, or with backward for pc_linear_attention_backward, on
+    tensors of these shapes."""
+    d, _ = _attention(q, k, v, None, None)
+    _sequences(d, q, cu_seqlens, max_seqlen)
+    n = _bytes(lib().pc_linear_attention_workspace_bytes, C.byref(d), 1 if backward else 0)
+    return _torch().empty(n, dtype=_torch().uint8, device=q.device)
+
+
+def pc_linear_attention_forward(q, k, v, log_decay, o, cu_seqlens=None, max_seqlen=None, state_in=None, state_out=None,
+                                scale=None, ws=None, stream=None):
+    """o [tokens, heads, dim_v] from q, k, v along every sequence, S_t = exp(log_decay) S_{t-1} + k_t v_t^T,
+    o_t = scale q_t^T S_t.  cu_seqlens: int32 [sequences + 1] on the GPU (None: one sequence); max_seqlen: a bound of
+    the longest (None: the number of tokens); states: float32 [sequences, heads, dim_k, dim_v]; scale: None for
+    dim_k ** -0.5; ws: linear_attention_workspace(...)."""
+    f32 = _torch().float32
+    d, (T, H, K, dk, dv) = _attention(q, k, v, log_decay, scale)
+    n = _sequences(d, q, cu_seqlens, max_seqlen)
+    d.o = _heads(o, q, (T, H, dv), "o")
+    d.state_in = _dense(state_in, q, f32, (n, H, dk, dv), "state_in")
+    d.state_out = _dense(state_out, q, f32, (n, H, dk, dv), "state_out")
+    pws, nws = _ws_ptr(ws, q)
+    _check(lib().pc_linear_attention_forward(q.device.index, C.byref(d), pws, nws, _stream_of(q, stream)))
+
+
+def pc_linear_attention_backward(do, q, k, v, log_decay, dq, dk, dv, cu_seqlens=None, max_seqlen=None, state_in=None,
+                                 dstate_out=None, dstate_in=None, scale=None, ws=None, stream=None):
+    """dq, dk, dv (and dstate_in) from do (and dstate_out), with the forward call's other arguments;
+    ws: linear_attention_workspace(..., backward=True)."""
+    f32 = _torch().float32
+    d, (T, H, K, nk, nv) = _attention(q, k, v, log_decay, scale)
+    n = _sequences(d, q, cu_seqlens, max_seqlen)
+    d.d_o = _heads(do, q, (T, H, nv), "do")
+    d.d_q = _heads(dq, q, (T, H, nk), "dq")
+    d.d_k = _heads(dk, q, (T, K, nk), "dk")
+    d.d_v = _heads(dv, q, (T, K, nv), "dv")
+    d.state_in = _dense(state_in, q, f32, (n, H, nk, nv), "state_in")
+    d.dstate_out = _dense(dstate_out, q, f32, (n, H, nk, nv), "dstate_out")
+    d.dstate_in = _dense(dstate_in, q, f32, (n, H, nk, nv), "dstate_in")
+    pws, nws = _ws_ptr(ws, q)
+    _check(lib().pc_linear_attention_backward(q.device.index, C.byref(d), pws, nws, _stream_of(q, stream)))
+
+
+def pc_linear_attention_step(q, k, v, log_decay, state, o, slots=None, scale=None, stream=None):
+    """One token for each row of q [rows, heads, dim_k], k, v, o: row b updates state[slots[b]] (slots: int32 [rows] on
+    the GPU, None: state[b]) of state [slots, heads, dim_k, dim_v] (float32) in place and reads it.  A slot out of
+    range marks a padding row; rows of the same slot are successive tokens, in the rows' order."""
+    torch = _torch()
+    d, (T, H, K, dk, dv) = _attention(q, k, v, log_decay, scale)
+    d.o = _heads(o, q, (T, H, dv), "o")
+    if state.dim() != 4:
+        raise ValueError("state must have four dimensions (slots, heads, dim_k, dim_v)")
+    d.state = _dense(state, q, torch.float32, (state.shape[0], H, dk, dv), "state")
+    d.num_slots = state.shape[0]
+    d.slots = _dense(slots, q, torch.int32, (T,), "slots")
+    _check(lib().pc_linear_attention_step(q.device.index, C.byref(d), _stream_of(q, stream)))
 
 
 class StepGraph:

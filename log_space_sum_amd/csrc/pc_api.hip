@@ -17,6 +17,7 @@
 #include "pc_elem.h"
 #include "pc_host.h"
 #include "pc_kernels.h"
+#include "pc_runtime.h"
 
 using namespace pc;
 
@@ -24,16 +25,14 @@ namespace {
 
 thread_local std::string g_err;
 
-int set_error(int code, const std::string& msg) {
+}  // namespace
+
+int pc::set_error(int code, const std::string& msg) {
   g_err = msg;
   return code;
 }
 
-#define HIPCHECK(x)                                                                       \
-  do {                                                                                    \
-    hipError_t e_ = (x);                                                                  \
-    if (e_ != hipSuccess) fail(PC_ERR_HIP, std::string(#x) + ": " + hipGetErrorString(e_)); \
-  } while (0)
+namespace {
 
 template <typename T>
 T* upload(const std::vector<T>& v) {
@@ -49,18 +48,6 @@ void release(T*& p) {
   if (p) (void)hipFree(p);
   p = nullptr;
 }
-
-struct DeviceGuard {
-  int prev = -1;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) prev = -1;
-    if (prev != dev) HIPCHECK(hipSetDevice(dev));
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-  }
-};
 
 enum KernelKind {
   KK_FWD = 0, KK_ELEM, KK_PARAM, KK_SPLIT, KK_COLMAX, KK_EXP, KK_GPACK, KK_INFWD, KK_INBWD,
@@ -105,11 +92,6 @@ struct Timed : EventSink {
     *stop = (hipEvent_t)ev.stop;
   }
 };
-
-void check_launch() {
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) fail(PC_ERR_HIP, std::string("kernel launch: ") + hipGetErrorString(e));
-}
 
 bool planes_ok(int pa, int pb) {
   return (pa == 1 && pb == 1) || (pa == 2 && pb == 1) || (pa == 1 && pb == 2) || (pa == 2 && pb == 2) ||

@@ -1,0 +1,118 @@
+// pc_ops.h -- argument blocks and launchers of the sequence-network operators
+// (layer norm, linear attention with decay, orthogonalised update).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/pc.h"
+#include "pc_launch.h"
+
+namespace pc {
+
+// ---- element types ---------------------------------------------------------
+// bfloat16 as its 16 bits; conversions round to nearest even and keep NaN.
+struct bf16 {
+  uint16_t u;
+};
+typedef _Float16 f16;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(f16 x) { return (float)x; }
+__device__ __forceinline__ float to_f32(bf16 x) { return __uint_as_float((uint32_t)x.u << 16); }
+__device__ __forceinline__ uint16_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float f);
+template <>
+__device__ __forceinline__ float from_f32<float>(float f) { return f; }
+template <>
+__device__ __forceinline__ f16 from_f32<f16>(float f) { return (f16)f; }
+template <>
+__device__ __forceinline__ bf16 from_f32<bf16>(float f) { return bf16{bf16_bits(f)}; }
+
+// ---- layer norm ------------------------------------------------------------
+struct NormArgs {
+  int64_t rows;
+  int32_t cols;
+  const void* x;
+  int64_t x_stride;
+  const void* dy;       // backward
+  int64_t dy_stride;
+  const float* weight;  // nullable: 1
+  const float* bias;    // nullable: 0
+  float eps;
+  void* y;              // forward: y; backward: dx
+  int64_t y_stride;
+  float* mean;
+  float* rstd;
+  float* part;          // backward: [parts][2][cols] partial sums of dweight, dbias
+  int32_t parts;
+  float* dweight;
+  float* dbias;
+};
+constexpr int NORM_MAX_COLS = 16384;
+int norm_parts(int64_t rows, int cols);
+void launch_norm_fwd(const NormArgs& a, int dtype, hipStream_t s);
+void launch_norm_bwd(const NormArgs& a, int dtype, hipStream_t s);
+
+// ---- linear attention with a decay for each head ---------------------------
+// One walk along the sequences (see k_linattn.hip): tensors a (contracted with
+// the state), b and c (which make the state), the output, and the states.
+struct MixTensor {
+  const void* p;
+  int64_t ts, hs;       // token and head strides (elements)
+  int32_t div;          // heads that share one of the tensor's: head h reads h / div
+};
+struct MixArgs {
+  int32_t seqs, heads, da, dc;
+  int64_t tokens;
+  const int32_t* cu;    // [seqs + 1], null: one sequence of all tokens
+  const float* log_decay;
+  MixTensor a, b, c;
+  void* out;
+  int64_t o_ts, o_hs;
+  int32_t out_f32;      // the output is a float32 partial, whatever the tensors' type
+  int32_t rev;          // tokens from the sequence's end to its start
+  int32_t off;          // 1: the carried state is decayed before a token joins it, 0: after
+  float pscale, wscale, oscale;   // factors of the inside products, of a token's part in the state, of the state's output
+  const float* init;    // [seqs, heads, da x dc], nullable: 0
+  float* fin;           // the states after the last token, nullable
+  int32_t st_r, st_c;   // strides of a state's row (da) and column (dc)
+  float* seg;           // [seqs, nsegs, heads, da x dc] states at the segments' starts, when nsegs > 1
+  int32_t nsegs;
+  int64_t seglen;
+};
+struct MixScanArgs {
+  int32_t seqs, heads, nsegs, elems;
+  int64_t tokens, seglen;
+  const int32_t* cu;
+  const float* log_decay;
+  const float* init;
+  float* seg;
+};
+struct MixSumArgs {     // out[t, h] = sum of the group's heads of part[t, h * group ..], of the sequences' tokens
+  int64_t tokens;
+  int32_t seqs, kv_heads, group, dim;
+  const int32_t* cu;
+  const float* part;    // [tokens, kv_heads * group, dim]
+  void* out;
+  int64_t o_ts, o_hs;
+};
+struct MixStepArgs {
+  int32_t batch, heads, group, dk, dv, slots;
+  const void *q, *k, *v;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;
+  const float* log_decay;
+  float scale;
+  float* state;         // [slots, heads, dk, dv]
+  const int32_t* slot;  // [batch], null: row b uses slot b
+  void* o;
+  int64_t o_ts, o_hs;
+};
+constexpr int MIX_MAX_DIM = 128;
+void launch_mix_walk(const MixArgs& a, int dtype, hipStream_t s);    // outputs (and final states)
+void launch_mix_states(const MixArgs& a, int dtype, hipStream_t s);  // each segment's own state into seg
+void launch_mix_scan(const MixScanArgs& a, hipStream_t s);           // seg: own states -> states at the starts
+void launch_mix_sum(const MixSumArgs& a, int dtype, hipStream_t s);
+void launch_mix_step(const MixStepArgs& a, int dtype, hipStream_t s);
+
+}  // namespace pc

@@ -1,0 +1,459 @@
+// pc_ops_api.hip -- the C ABI of the sequence-network operators: argument
+// checks, the linear attention's split into segments, and the launch lists.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <exception>
+#include <string>
+
+#include "pc_ops.h"
+#include "pc_runtime.h"
+
+using namespace pc;
+
+namespace {
+
+template <typename F>
+int guarded(F&& f) {
+  try {
+    f();
+    return PC_OK;
+  } catch (const Error& e) {
+    return set_error(e.code, e.msg);
+  } catch (const std::exception& e) {
+    return set_error(PC_ERR_INVALID_ARG, e.what());
+  }
+}
+
+void need(bool ok, const std::string& what) {
+  if (!ok) fail(PC_ERR_INVALID_ARG, what);
+}
+
+void check_device(int device) {
+  if (device < 0) fail(PC_ERR_NO_DEVICE, "device " + std::to_string(device));
+}
+
+void check_dtype(int dtype) {
+  if (dtype != PC_DTYPE_F32 && dtype != PC_DTYPE_BF16 && dtype != PC_DTYPE_F16)
+    fail(PC_ERR_UNSUPPORTED, "unknown dtype " + std::to_string(dtype));
+}
+
+void check_ws(const void* ws, size_t have, size_t want) {
+  if (want == 0) return;
+  if (!ws || have < want)
+    fail(PC_ERR_WORKSPACE, "workspace of " + std::to_string(ws ? have : 0) + " bytes, needs " + std::to_string(want));
+  need((uintptr_t)ws % 16 == 0, "workspace not aligned to 16 bytes");
+}
+
+// ---- layer norm --------------------------------------------------------------
+
+void check_norm(int64_t rows, int32_t cols) {
+  need(rows >= 0 && rows <= INT_MAX, "rows must be in [0, 2^31)");
+  need(cols >= 1, "cols must be at least 1");
+  if (cols > NORM_MAX_COLS)
+    fail(PC_ERR_UNSUPPORTED, std::to_string(cols) + " columns (at most " + std::to_string(NORM_MAX_COLS) + ")");
+}
+
+size_t norm_ws(int64_t rows, int32_t cols) { return (size_t)norm_parts(rows, cols) * 2 * cols * sizeof(float); }
+
+// ---- linear attention ----------------------------------------------------------
+
+void check_mix(const pc_linear_attention* d) {
+  need(d, "null descriptor");
+  check_dtype(d->dtype);
+  need(d->heads >= 1 && d->kv_heads >= 1 && d->heads % d->kv_heads == 0, "kv_heads must divide heads");
+  need(d->heads <= 65535, "more than 65535 heads");
+  need(d->dim_k >= 1 && d->dim_v >= 1, "dim_k and dim_v must be at least 1");
+  if (d->dim_k > MIX_MAX_DIM || d->dim_v > MIX_MAX_DIM)
+    fail(PC_ERR_UNSUPPORTED, "dim_k " + std::to_string(d->dim_k) + ", dim_v " + std::to_string(d->dim_v) + " (at most " +
+                                 std::to_string(MIX_MAX_DIM) + ")");
+  need(d->num_tokens >= 0 && d->num_tokens <= INT_MAX, "num_tokens must be in [0, 2^31)");
+}
+
+void check_seqs(const pc_linear_attention* d) {
+  check_mix(d);
+  need(d->num_seqs >= 0, "num_seqs must be at least 0");
+  if (d->num_seqs > 65535) fail(PC_ERR_UNSUPPORTED, std::to_string(d->num_seqs) + " sequences (at most 65535)");
+  need(d->max_seqlen >= 0, "max_seqlen must be at least 0");
+}
+
+void check_call(const pc_linear_attention* d) {
+  check_seqs(d);
+  need(d->cu_seqlens || d->num_seqs == 1, "without cu_seqlens num_seqs is 1");
+  need(d->log_decay, "null log_decay");
+  need(std::isfinite(d->scale) && d->scale != 0.0f, "scale must be finite and not 0");
+}
+
+void check_heads(const pc_linear_attention* d, const pc_heads& t, const char* what) {
+  need(t.data || d->num_tokens == 0, std::string("null ") + what);
+  need(t.token_stride >= 0 && t.head_stride >= 0, std::string("negative stride of ") + what);
+}
+// an output's elements must be distinct
+void check_out(const pc_linear_attention* d, const pc_heads& t, int heads, int dim, const char* what) {
+  check_heads(d, t, what);
+  const int64_t ts = t.token_stride, hs = t.head_stride;
+  const bool tokens_outside = (heads == 1 || hs >= dim) && (d->num_tokens <= 1 || ts >= (heads - 1) * hs + dim);
+  const bool heads_outside = (d->num_tokens <= 1 || ts >= dim) && (heads == 1 || hs >= (d->num_tokens - 1) * ts + dim);
+  need(tokens_outside || heads_outside, std::string("elements of ") + what + " overlap");
+}
+
+// Segments of the longest sequence.  One walk of a (sequence, head) is a chain
+// of chunks, so where sequences and heads are too few to fill the card the
+// sequences are cut; a cut costs a second reading of b and c and a state for
+// each segment and head, so a segment has at least 256 tokens.
+struct Split {
+  int nsegs;
+  int64_t len;
+};
+Split mix_segments(const pc_linear_attention* d) {
+  const int64_t walks = std::max<int64_t>(1, (int64_t)d->num_seqs * d->heads);
+  const int64_t longest = std::max<int64_t>(1, std::min(d->max_seqlen, d->num_tokens));
+  int64_t n = std::min((512 + walks - 1) / walks, (longest + 255) / 256);
+  n = std::max<int64_t>(1, n);
+  const int64_t len = ((longest + n - 1) / n + 63) / 64 * 64;
+  return {(int)((longest + len - 1) / len), len};
+}
+
+struct MixWs {
+  size_t seg_f = 0, seg_r = 0, dk = 0, dv = 0, total = 0;
+};
+MixWs mix_ws(const pc_linear_attention* d, bool backward) {
+  MixWs w;
+  const Split sp = mix_segments(d);
+  const size_t states = sp.nsegs > 1 ? (size_t)d->num_seqs * sp.nsegs * d->heads * d->dim_k * d->dim_v * sizeof(float) : 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = w.total;
+    w.total += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  w.seg_f = take(states);
+  if (backward) {
+    w.seg_r = take(states);
+    if (d->heads != d->kv_heads) {
+      w.dk = take((size_t)d->num_tokens * d->heads * d->dim_k * sizeof(float));
+      w.dv = take((size_t)d->num_tokens * d->heads * d->dim_v * sizeof(float));
+    }
+  }
+  return w;
+}
+
+MixTensor tensor(const pc_heads& t, int div) { return {t.data, t.token_stride, t.head_stride, div}; }
+
+MixArgs mix_base(const pc_linear_attention* d, const Split& sp) {
+  MixArgs a{};
+  a.seqs = d->num_seqs;
+  a.heads = d->heads;
+  a.tokens = d->num_tokens;
+  a.cu = d->cu_seqlens;
+  a.log_decay = d->log_decay;
+  a.pscale = d->scale;
+  a.nsegs = sp.nsegs;
+  a.seglen = sp.len;
+  return a;
+}
+
+// The states at the segments' starts (nothing to do for one segment).
+void mix_starts(const pc_linear_attention* d, const MixArgs& a, const float* init, hipStream_t s) {
+  if (a.nsegs <= 1) return;
+  launch_mix_states(a, d->dtype, s);
+  check_launch();
+  MixScanArgs c{};
+  c.seqs = a.seqs;
+  c.heads = a.heads;
+  c.nsegs = a.nsegs;
+  c.elems = d->dim_k * d->dim_v;
+  c.tokens = a.tokens;
+  c.seglen = a.seglen;
+  c.cu = a.cu;
+  c.log_decay = a.log_decay;
+  c.init = init;
+  c.seg = a.seg;
+  launch_mix_scan(c, s);
+  check_launch();
+}
+
+}  // namespace
+
+extern "C" {
+
+int pc_layer_norm_forward(int device, int dtype, int64_t rows, int32_t cols, const void* x, int64_t x_stride,
+                          const float* weight, const float* bias, float eps, void* y, int64_t y_stride,
+                          float* mean, float* rstd, void* stream) {
+  return guarded([&] {
+    check_device(device);
+    check_dtype(dtype);
+    check_norm(rows, cols);
+    need(std::isfinite(eps) && eps >= 0.0f, "eps must be finite and at least 0");
+    if (rows == 0) return;
+    need(x && y, "null x or y");
+    need(x_stride >= cols || (x_stride >= 0 && rows == 1), "x_stride below cols");
+    need(y_stride >= cols || (y_stride >= 0 && rows == 1), "y_stride below cols");
+    DeviceGuard dg(device);
+    NormArgs a{};
+    a.rows = rows;
+    a.cols = cols;
+    a.x = x;
+    a.x_stride = x_stride;
+    a.weight = weight;
+    a.bias = bias;
+    a.eps = eps;
+    a.y = y;
+    a.y_stride = y_stride;
+    a.mean = mean;
+    a.rstd = rstd;
+    launch_norm_fwd(a, dtype, (hipStream_t)stream);
+    check_launch();
+  });
+}
+
+int pc_layer_norm_workspace_bytes(int64_t rows, int32_t cols, size_t* bytes) {
+  return guarded([&] {
+    need(bytes, "null bytes");
+    check_norm(rows, cols);
+    *bytes = norm_ws(rows, cols);
+  });
+}
+
+int pc_layer_norm_backward(int device, int dtype, int64_t rows, int32_t cols, const void* dy, int64_t dy_stride,
+                           const void* x, int64_t x_stride, const float* weight, const float* mean, const float* rstd,
+                           void* dx, int64_t dx_stride, float* dweight, float* dbias,
+                           void* ws, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    check_device(device);
+    check_dtype(dtype);
+    check_norm(rows, cols);
+    need(rows == 0 || (dy && x && mean && rstd && dx), "null dy, x, mean, rstd or dx");
+    for (int64_t st : {dy_stride, x_stride, dx_stride}) need(st >= cols || (st >= 0 && rows <= 1), "a row stride is below cols");
+    const bool params = dweight || dbias;
+    if (rows == 0 && !params) return;
+    if (params) check_ws(ws, ws_bytes, norm_ws(rows, cols));
+    DeviceGuard dg(device);
+    NormArgs a{};
+    a.rows = rows;
+    a.cols = cols;
+    a.x = x;
+    a.x_stride = x_stride;
+    a.dy = dy;
+    a.dy_stride = dy_stride;
+    a.weight = weight;
+    a.y = dx;
+    a.y_stride = dx_stride;
+    a.mean = const_cast<float*>(mean);
+    a.rstd = const_cast<float*>(rstd);
+    a.part = params ? (float*)ws : nullptr;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    launch_norm_bwd(a, dtype, (hipStream_t)stream);
+    check_launch();
+  });
+}
+
+int pc_linear_attention_workspace_bytes(const pc_linear_attention* d, int backward, size_t* bytes) {
+  return guarded([&] {
+    need(bytes, "null bytes");
+    check_seqs(d);
+    *bytes = mix_ws(d, backward != 0).total;
+  });
+}
+
+int pc_linear_attention_forward(int device, const pc_linear_attention* d, void* ws, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    check_device(device);
+    check_call(d);
+    check_heads(d, d->q, "q");
+    check_heads(d, d->k, "k");
+    check_heads(d, d->v, "v");
+    check_out(d, d->o, d->heads, d->dim_v, "o");
+    const MixWs w = mix_ws(d, false);
+    check_ws(ws, ws_bytes, w.total);
+    if (d->num_seqs == 0) return;
+    DeviceGuard dg(device);
+    const hipStream_t s = (hipStream_t)stream;
+    const int group = d->heads / d->kv_heads;
+    MixArgs a = mix_base(d, mix_segments(d));
+    a.da = d->dim_k;
+    a.dc = d->dim_v;
+    a.st_r = d->dim_v;
+    a.st_c = 1;
+    a.a = tensor(d->q, 1);
+    a.b = tensor(d->k, group);
+    a.c = tensor(d->v, group);
+    a.out = d->o.data;
+    a.o_ts = d->o.token_stride;
+    a.o_hs = d->o.head_stride;
+    a.off = 1;
+    a.wscale = 1.0f;
+    a.oscale = d->scale;
+    a.init = d->state_in;
+    a.fin = d->state_out;
+    a.seg = (float*)((char*)ws + w.seg_f);
+    mix_starts(d, a, d->state_in, s);
+    launch_mix_walk(a, d->dtype, s);
+    check_launch();
+  });
+}
+
+int pc_linear_attention_backward(int device, const pc_linear_attention* d, void* ws, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    check_device(device);
+    check_call(d);
+    check_heads(d, d->q, "q");
+    check_heads(d, d->k, "k");
+    check_heads(d, d->v, "v");
+    check_heads(d, d->d_o, "d_o");
+    check_out(d, d->d_q, d->heads, d->dim_k, "d_q");
+    check_out(d, d->d_k, d->kv_heads, d->dim_k, "d_k");
+    check_out(d, d->d_v, d->kv_heads, d->dim_v, "d_v");
+    const MixWs w = mix_ws(d, true);
+    check_ws(ws, ws_bytes, w.total);
+    if (d->num_seqs == 0) return;
+    DeviceGuard dg(device);
+    const hipStream_t s = (hipStream_t)stream;
+    const int group = d->heads / d->kv_heads, dk = d->dim_k, dv = d->dim_v;
+    char* base = (char*)ws;
+    const MixTensor q = tensor(d->q, 1), k = tensor(d->k, group), v = tensor(d->v, group), go = tensor(d->d_o, 1);
+    // the states of the forward pass at the segments' starts, for dq
+    MixArgs f = mix_base(d, mix_segments(d));
+    f.off = 1;
+    f.wscale = 1.0f;
+    f.seg = (float*)(base + w.seg_f);
+    MixArgs fs = f;
+    fs.da = dk;
+    fs.dc = dv;
+    fs.st_r = dv;
+    fs.st_c = 1;
+    fs.b = k;
+    fs.c = v;
+    mix_starts(d, fs, d->state_in, s);
+    // dq: contracted with the state's columns
+    f.da = dv;
+    f.dc = dk;
+    f.st_r = 1;
+    f.st_c = dv;
+    f.a = go;
+    f.b = v;
+    f.c = k;
+    f.oscale = d->scale;
+    f.init = d->state_in;
+    f.out = d->d_q.data;
+    f.o_ts = d->d_q.token_stride;
+    f.o_hs = d->d_q.head_stride;
+    launch_mix_walk(f, d->dtype, s);
+    check_launch();
+    // the adjoint states from the sequences' ends.  The carried state is the
+    // one already decayed onto the token before (off 0), so it starts as the
+    // given gradient and ends as the gradient of state_in; scale belongs to a
+    // token's part in it.
+    MixArgs r = mix_base(d, mix_segments(d));
+    r.rev = 1;
+    r.off = 0;
+    r.wscale = d->scale;
+    r.oscale = 1.0f;
+    r.init = d->dstate_out;
+    r.seg = (float*)(base + w.seg_r);
+    MixArgs rk = r;
+    r.da = dk;
+    r.dc = dv;
+    r.st_r = dv;
+    r.st_c = 1;
+    r.a = k;
+    r.b = q;
+    r.c = go;
+    mix_starts(d, r, d->dstate_out, s);
+    rk.da = dv;
+    rk.dc = dk;
+    rk.st_r = 1;
+    rk.st_c = dv;
+    rk.a = v;
+    rk.b = go;
+    rk.c = q;
+    auto target = [&](MixArgs& a, const pc_heads& to, size_t part, int dim) {
+      if (group == 1) {
+        a.out = to.data;
+        a.o_ts = to.token_stride;
+        a.o_hs = to.head_stride;
+      } else {
+        a.out = base + part;
+        a.o_ts = (int64_t)d->heads * dim;
+        a.o_hs = dim;
+        a.out_f32 = 1;
+      }
+    };
+    target(rk, d->d_k, w.dk, dk);
+    target(r, d->d_v, w.dv, dv);
+    launch_mix_walk(rk, d->dtype, s);
+    check_launch();
+    // last, since dstate_in may be dstate_out
+    r.fin = d->dstate_in;
+    launch_mix_walk(r, d->dtype, s);
+    check_launch();
+    if (group > 1 && d->num_tokens > 0) {
+      auto sum = [&](const pc_heads& to, size_t part, int dim) {
+        MixSumArgs m{};
+        m.tokens = d->num_tokens;
+        m.seqs = d->num_seqs;
+        m.kv_heads = d->kv_heads;
+        m.group = group;
+        m.dim = dim;
+        m.cu = d->cu_seqlens;
+        m.part = (const float*)(base + part);
+        m.out = to.data;
+        m.o_ts = to.token_stride;
+        m.o_hs = to.head_stride;
+        launch_mix_sum(m, d->dtype, s);
+        check_launch();
+      };
+      sum(d->d_k, w.dk, dk);
+      sum(d->d_v, w.dv, dv);
+    }
+  });
+}
+
+int pc_linear_attention_step(int device, const pc_linear_attention* d, void* stream) {
+  return guarded([&] {
+    check_device(device);
+    check_mix(d);
+    need(d->log_decay, "null log_decay");
+    need(std::isfinite(d->scale) && d->scale != 0.0f, "scale must be finite and not 0");
+    check_heads(d, d->q, "q");
+    check_heads(d, d->k, "k");
+    check_heads(d, d->v, "v");
+    check_out(d, d->o, d->heads, d->dim_v, "o");
+    need(d->num_slots >= 0 && d->num_slots <= INT_MAX, "num_slots must be in [0, 2^31)");
+    need(d->slots || d->num_slots >= d->num_tokens, "fewer slots than rows");
+    need((int64_t)d->heads * d->num_tokens <= INT_MAX, "more than 2^31 rows times heads");
+    if (d->num_tokens == 0 || d->num_slots == 0) return;
+    need(d->state, "null state");
+    DeviceGuard dg(device);
+    MixStepArgs a{};
+    a.batch = (int)d->num_tokens;
+    a.heads = d->heads;
+    a.group = d->heads / d->kv_heads;
+    a.dk = d->dim_k;
+    a.dv = d->dim_v;
+    a.slots = (int)d->num_slots;
+    a.q = d->q.data;
+    a.k = d->k.data;
+    a.v = d->v.data;
+    a.q_ts = d->q.token_stride;
+    a.q_hs = d->q.head_stride;
+    a.k_ts = d->k.token_stride;
+    a.k_hs = d->k.head_stride;
+    a.v_ts = d->v.token_stride;
+    a.v_hs = d->v.head_stride;
+    a.log_decay = d->log_decay;
+    a.scale = d->scale;
+    a.state = d->state;
+    a.slot = d->slots;
+    a.o = d->o.data;
+    a.o_ts = d->o.token_stride;
+    a.o_hs = d->o.head_stride;
+    launch_mix_step(a, d->dtype, (hipStream_t)stream);
+    check_launch();
+  });
+}
+
+}  // extern "C"
