@@ -481,6 +481,27 @@ int pc_linear_attention_backward(int device, const pc_linear_attention* d, void*
  * name the same slot are successive tokens of that state, in the rows' order. */
 int pc_linear_attention_step(int device, const pc_linear_attention* d, void* stream);
 
+/* Orthogonalised update: each of `batch` matrices [rows, cols] is replaced by
+ * an approximation of its nearest orthogonal one (U V^T of its singular value
+ * decomposition), by Newton-Schulz steps.  With X = G / (|G| + eps), |G| the
+ * Frobenius norm, taken on the side of the smaller dimension, every step is
+ *   X <- a X + (b A + c A^2) X,   A = X X^T
+ * with step i's (a, b, c) = coefficients[3 i .. 3 i + 2] (host array; 1 .. 32
+ * steps).  A product must keep the singular values, which start in [0, 1],
+ * bounded: coefficients with which one could pass 1024 are refused.
+ * G and out: dtype, rows and matrices at their strides (g_batch etc., elements;
+ * out may be G with the same strides).  Products run at float32 level for
+ * float32 and float16 matrices; for bfloat16 ones A's operands are rounded to
+ * 11 bits.  A matrix of zeros gives zeros (eps > 0); one with a value that is
+ * not finite gives values that are not.
+ * Errors: PC_ERR_INVALID_ARG (sizes, strides, eps, steps, coefficients),
+ * PC_ERR_UNSUPPORTED (a dimension above 32768, batch above 65535, unknown
+ * dtype), PC_ERR_WORKSPACE, PC_ERR_HIP. */
+int pc_orthogonalize_workspace_bytes(int dtype, int64_t batch, int32_t rows, int32_t cols, size_t* bytes);
+int pc_orthogonalize(int device, int dtype, int64_t batch, int32_t rows, int32_t cols, const void* g, int64_t g_batch,
+                     int64_t g_row, void* out, int64_t out_batch, int64_t out_row, int32_t steps,
+                     const float* coefficients, float eps, void* ws, size_t ws_bytes, void* stream);
+
 /* Message of the calling thread's last failed call ("" if none). */
 const char* pc_last_error(void);
 

@@ -111,6 +111,10 @@ EXPORTS = {
     "pc_linear_attention_backward": (C.c_int, [C.c_int, C.POINTER(pc_linear_attention), C.c_void_p, C.c_size_t,
                                                C.c_void_p]),
     "pc_linear_attention_step": (C.c_int, [C.c_int, C.POINTER(pc_linear_attention), C.c_void_p]),
+    "pc_orthogonalize_workspace_bytes": (C.c_int, [C.c_int, C.c_int64, C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
+    "pc_orthogonalize": (C.c_int, [C.c_int, C.c_int, C.c_int64, C.c_int32, C.c_int32, C.c_void_p, C.c_int64, C.c_int64,
+                                   C.c_void_p, C.c_int64, C.c_int64, C.c_int32, C.POINTER(C.c_float), C.c_float,
+                                   C.c_void_p, C.c_size_t, C.c_void_p]),
     "pc_last_error": (C.c_char_p, []),
     "pc_layout_info": (C.c_int, [C.c_void_p, C.POINTER(pc_layout_summary)]),
     "pc_layer_class": (C.c_int, [C.c_void_p, C.c_int, C.POINTER(C.c_int)]),
@@ -630,6 +634,41 @@ def pc_linear_attention_step(q, k, v, log_decay, state, o, slots=None, scale=Non
     d.num_slots = state.shape[0]
     d.slots = _dense(slots, q, torch.int32, (T,), "slots")
     _check(lib().pc_linear_attention_step(q.device.index, C.byref(d), _stream_of(q, stream)))
+
+
+def _matrices(t, what):
+    """(batch, rows, cols, batch stride, row stride) of a matrix or a batch of them."""
+    if t.dim() == 2:
+        return 1, t.shape[0], t.shape[1], 0, t.stride(0)
+    if t.dim() == 3:
+        return t.shape[0], t.shape[1], t.shape[2], t.stride(0), t.stride(1)
+    raise ValueError(f"{what} must have two or three dimensions")
+
+
+def orthogonalize_workspace(g):
+    """A workspace tensor for pc_orthogonalize on matrices like g."""
+    b, r, c, _, _ = _matrices(g, "g")
+    n = _bytes(lib().pc_orthogonalize_workspace_bytes, _dtype(g, "g"), b, r, c)
+    return _torch().empty(n, dtype=_torch().uint8, device=g.device)
+
+
+def pc_orthogonalize(g, out, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, ws=None, stream=None):
+    """out = the matrices of g [rows, cols] or [batch, rows, cols] after `steps` Newton-Schulz steps from
+    g / (|g| + eps), X <- a X + (b A + c A^2) X with A = X X^T; coefficients: (a, b, c), or one such triple for each
+    step; out may be g.  ws: orthogonalize_workspace(g)."""
+    b, r, c, gb, gr = _matrices(g, "g")
+    pg, po = _operand(g, g, g.dtype, g.shape, "g"), _operand(out, g, g.dtype, g.shape, "out")
+    _, _, _, ob, orow = _matrices(out, "out")
+    steps = int(steps)
+    each = list(coefficients)
+    if each and not isinstance(each[0], (tuple, list)):
+        each = [each] * steps
+    if len(each) != steps or any(len(x) != 3 for x in each):
+        raise ValueError("coefficients must be (a, b, c) or one such triple for each step")
+    flat = (C.c_float * max(1, 3 * steps))(*[float(v) for x in each for v in x])
+    pws, nws = _ws_ptr(ws, g)
+    _check(lib().pc_orthogonalize(g.device.index, _dtype(g, "g"), b, r, c, pg, gb, gr, po, ob, orow, steps, flat,
+                                  float(eps), pws, nws, _stream_of(g, stream)))
 
 
 class StepGraph:

@@ -1,0 +1,455 @@
+// k_orth.hip -- the orthogonalised update: Newton-Schulz steps
+//   X <- a X + (b A + c A^2) X,  A = X X^T,  from X = G / (|G| + eps),  X [m, n], m <= n.
+//
+// Two ways, by the smaller dimension m:
+//
+// m <= 64 (LowRank factors and their like, many and thin): X after all steps
+// is Q X_0 with Q a polynomial in A_0, so the steps run on m x m matrices,
+//   M = a I + b A + c A^2,   Q <- Q M,   A <- A M^2,
+// and the matrix itself is read twice and written once.  Squaring the matrix
+// costs half of the digits, so A, M and Q are held in 64 bits (one workgroup
+// a matrix, on the float64 matrix instruction); the result is then at least as
+// exact as float32 steps on X.
+//
+// Larger m: three products a step on the float16 matrix instruction.  An
+// operand is split into two float16 planes of a value scaled by a power of two
+// (hi + lo: 22 bits; the spectra are bounded, so the scales are known before
+// the call), and hi hi + hi lo + lo hi are summed in float32: the accuracy of
+// float32 steps at three times the cost of a 16-bit product.  The symmetric
+// products (A, A^2) compute the tiles on and above the diagonal only.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "pc_ops.h"
+#include "pc_ring.h"
+
+namespace pc {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// X[i][p] of a matrix: i along m, p along n
+template <typename IO>
+__device__ __forceinline__ int64_t at_x(const OrthIo& io, int64_t row_stride, int64_t i, int64_t p) {
+  return io.tall ? p * row_stride + i : i * row_stride + p;
+}
+
+// ---------------------------------------------------------------------------
+// m <= 64: one workgroup a matrix
+// ---------------------------------------------------------------------------
+
+// C = A B of symmetric commuting [16 MB]^2 matrices in LDS (row stride LD):
+// the part on and above the diagonal, mirrored by store().
+template <int MB, int LD, int W, typename F>
+__device__ __forceinline__ void small_product(const double* A, const double* B, F&& store) {
+  constexpr int T = MB * (MB + 1) / 2, MINE = (T + W - 1) / W;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  f64x4 acc[MINE];
+#pragma unroll
+  for (int k = 0; k < MINE; ++k) {
+    int jb = 0, ib = wave + W * k;
+    if (ib >= T) continue;
+    while (ib > jb) ib -= ++jb;
+    acc[k] = f64x4{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+    for (int q = 0; q < 4 * MB; ++q)
+      acc[k] = __builtin_amdgcn_mfma_f64_16x16x4f64(A[(16 * ib + l16) * LD + 4 * q + g], B[(16 * jb + l16) * LD + 4 * q + g],
+                                                    acc[k], 0, 0, 0);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < MINE; ++k) {
+    int jb = 0, ib = wave + W * k;
+    if (ib >= T) continue;
+    while (ib > jb) ib -= ++jb;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (16 * ib + g + 4 * r <= 16 * jb + l16) store(16 * ib + g + 4 * r, 16 * jb + l16, acc[k][r]);
+  }
+  __syncthreads();
+}
+
+template <typename IO, int MB, int NT>
+__global__ __launch_bounds__(NT) void orth_small(OrthIo io, OrthPoly poly) {
+  constexpr int D = 16 * MB, LD = D + 2, W = NT / 64, T = MB * (MB + 1) / 2;
+  __shared__ double sA[D * LD], sM[D * LD], sQ[D * LD], sT[D * LD];
+  __shared__ double s_inv;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const IO* x = (const IO*)io.g + (int64_t)blockIdx.x * io.g_batch;
+  const int m = io.m, n = io.n;
+
+  // A = G G^T in 64 bits: every wave its share of p, four consecutive p a lane
+  f64x4 acc[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) acc[t] = f64x4{0.0, 0.0, 0.0, 0.0};
+  for (int p0 = wave * 16; p0 < n; p0 += W * 16) {
+    float v[MB][4];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      const int i = 16 * b + l16;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int p = p0 + 4 * g + e;
+        v[b][e] = i < m && p < n ? to_f32(x[at_x<IO>(io, io.g_row, i, p)]) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      int t = 0;
+#pragma unroll
+      for (int jb = 0; jb < MB; ++jb)
+#pragma unroll
+        for (int ib = 0; ib <= jb; ++ib, ++t)
+          acc[t] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)v[ib][e], (double)v[jb][e], acc[t], 0, 0, 0);
+    }
+  }
+  for (int e = tid; e < D * LD; e += NT) sA[e] = 0.0;
+  for (int w = 0; w < W; ++w) {   // the waves' parts in their order
+    __syncthreads();
+    if (w != wave) continue;
+    int t = 0;
+#pragma unroll
+    for (int jb = 0; jb < MB; ++jb)
+#pragma unroll
+      for (int ib = 0; ib <= jb; ++ib, ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sA[(16 * ib + g + 4 * r) * LD + 16 * jb + l16] += acc[t][r];
+  }
+  __syncthreads();
+  if (tid == 0) {
+    double tr = 0.0;
+    for (int i = 0; i < m; ++i) tr += sA[i * LD + i];
+    s_inv = 1.0 / (sqrt(tr) + (double)io.eps);
+  }
+  __syncthreads();
+  const double inv = s_inv;
+  for (int e = tid; e < D * D; e += NT) {
+    const int i = e / D, j = e % D;
+    const double v = (i <= j ? sA[i * LD + j] : sA[j * LD + i]) * inv * inv;
+    sT[i * LD + j] = v;
+    sQ[i * LD + j] = i == j ? 1.0 : 0.0;
+  }
+  __syncthreads();
+  for (int e = tid; e < D * D; e += NT) sA[e / D * LD + e % D] = sT[e / D * LD + e % D];
+  __syncthreads();
+
+  for (int s = 0; s < poly.steps; ++s) {
+    const double a = poly.c[s][0], b = poly.c[s][1], c = poly.c[s][2];
+    small_product<MB, LD, W>(sA, sA, [&](int i, int j, double v) {
+      sM[i * LD + j] = sM[j * LD + i] = (i == j ? a : 0.0) + b * sA[i * LD + j] + c * v;
+    });
+    if (s == 0) {
+      for (int e = tid; e < D * D; e += NT) sQ[e / D * LD + e % D] = sM[e / D * LD + e % D];
+      __syncthreads();
+    } else {
+      small_product<MB, LD, W>(sQ, sM, [&](int i, int j, double v) { sQ[i * LD + j] = sQ[j * LD + i] = v; });
+    }
+    if (s + 1 < poly.steps) {
+      small_product<MB, LD, W>(sA, sM, [&](int i, int j, double v) { sT[i * LD + j] = sT[j * LD + i] = v; });
+      small_product<MB, LD, W>(sT, sM, [&](int i, int j, double v) { sA[i * LD + j] = sA[j * LD + i] = v; });
+    }
+  }
+
+  // out = (Q / |G|) G
+  float q[MB][MB][4];   // [block of i][block of k][e]: Q[16 ib + l16][16 kb + 4 g + e]
+#pragma unroll
+  for (int ib = 0; ib < MB; ++ib)
+#pragma unroll
+    for (int kb = 0; kb < MB; ++kb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[ib][kb][e] = (float)(sQ[(16 * ib + l16) * LD + 16 * kb + 4 * g + e] * inv);
+  IO* y = (IO*)io.out + (int64_t)blockIdx.x * io.o_batch;
+  for (int p0 = wave * 16; p0 < n; p0 += W * 16) {
+    const int p = p0 + l16;
+    float v[MB][4];
+#pragma unroll
+    for (int kb = 0; kb < MB; ++kb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = 16 * kb + 4 * g + e;
+        v[kb][e] = k < m && p < n ? to_f32(x[at_x<IO>(io, io.g_row, k, p)]) : 0.0f;
+      }
+#pragma unroll
+    for (int ib = 0; ib < MB; ++ib) {
+      f32x4 o = {};
+#pragma unroll
+      for (int kb = 0; kb < MB; ++kb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o = io.tall ? __builtin_amdgcn_mfma_f32_16x16x4f32(v[kb][e], q[ib][kb][e], o, 0, 0, 0)
+                      : __builtin_amdgcn_mfma_f32_16x16x4f32(q[ib][kb][e], v[kb][e], o, 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = io.tall ? 16 * ib + l16 : 16 * ib + 4 * g + r;
+        const int pp = io.tall ? p0 + 4 * g + r : p;
+        if (i < m && pp < n) y[at_x<IO>(io, io.o_row, i, pp)] = from_f32<IO>(o[r]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// larger m: norm, planes, products
+// ---------------------------------------------------------------------------
+
+// Partial sums of the squares, in 64 bits; grid (ORTH_NORM_BLOCKS, batch).
+template <typename IO>
+__global__ __launch_bounds__(256) void orth_norm(OrthIo io, double* part) {
+  __shared__ double red[4];
+  const int rows = io.tall ? io.n : io.m, cols = io.tall ? io.m : io.n;
+  const IO* x = (const IO*)io.g + (int64_t)blockIdx.y * io.g_batch;
+  double s = 0.0;
+  const int across = (cols + 255) / 256;   // spans of 256 columns
+  for (int64_t u = blockIdx.x; u < (int64_t)rows * across; u += ORTH_NORM_BLOCKS) {
+    const int64_t r = u / across;
+    const int c = (int)(u % across) * 256 + threadIdx.x;
+    if (c < cols) {
+      const double v = to_f32(x[r * io.g_row + c]);
+      s += v * v;
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) part[(int64_t)blockIdx.y * ORTH_NORM_BLOCKS + blockIdx.x] = red[0] + red[1] + red[2] + red[3];
+}
+
+// A value's planes.
+__device__ __forceinline__ void planes_of(float v, uint16_t& hi, uint16_t& lo) {
+  const f16 h = (f16)v;
+  hi = __builtin_bit_cast(uint16_t, h);
+  lo = __builtin_bit_cast(uint16_t, (f16)(v - (float)h));
+}
+__device__ __forceinline__ float f16_value(uint16_t u) { return (float)__builtin_bit_cast(f16, u); }
+
+// The planes of X = scale G / (|G| + eps) and of its transpose, pads 0; one
+// 32 x 32 tile a block, grid (np / 32, mp / 32, batch).
+template <typename IO>
+__global__ __launch_bounds__(256) void orth_split(OrthIo io, const double* part, float scale, int mp, int np, OrthMat x,
+                                                  OrthMat xt) {
+  __shared__ float tile[32][33];
+  __shared__ float s_mul;
+  const int p0 = blockIdx.x * 32, i0 = blockIdx.y * 32;
+  const int64_t b = blockIdx.z;
+  if (threadIdx.x < 64) {
+    double s = part[b * ORTH_NORM_BLOCKS + threadIdx.x];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+    if (threadIdx.x == 0) s_mul = (float)((double)scale / (sqrt(s) + (double)io.eps));
+  }
+  const IO* g = (const IO*)io.g + b * io.g_batch;
+  const int c = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {   // rows of the tensor: along i or, tall, along p
+    const int r = (threadIdx.x >> 5) + 8 * k;
+    const int i = i0 + (io.tall ? c : r), p = p0 + (io.tall ? r : c);
+    const float v = i < io.m && p < io.n ? to_f32(g[at_x<IO>(io, io.g_row, i, p)]) : 0.0f;
+    tile[i - i0][p - p0] = v;
+  }
+  __syncthreads();
+  const float mul = s_mul;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = (threadIdx.x >> 5) + 8 * k;
+    uint16_t hi, lo;
+    planes_of(tile[r][c] * mul, hi, lo);
+    const int64_t e = b * x.batch + panel(i0 + r, p0 + c, mp);
+    x.p[e] = hi;
+    x.p[e + x.plane] = lo;
+    planes_of(tile[c][r] * mul, hi, lo);
+    const int64_t t = b * xt.batch + panel(p0 + r, i0 + c, np);
+    xt.p[t] = hi;
+    xt.p[t + xt.plane] = lo;
+  }
+}
+
+// C = A B^T on 128 x 128 tiles, four waves of 64 x 64, K in slices of 32
+// through a two-stage LDS ring.  PL planes of each operand: 1 one product, 2
+// three.  Slot s of a row's four 16-byte chunks holds chunk s ^ ((row >> 2) & 3),
+// so the 16 rows a wave reads at a time lie in different banks.
+template <int EPI, int PL, typename IO>
+__global__ __launch_bounds__(256, 2) void orth_gemm(OrthGemmArgs a) {
+  constexpr int TILE = ORTH_TILE, SLICE = TILE * 64;   // bytes of an operand plane's slice
+  constexpr int STAGE = 2 * PL * SLICE;
+  constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
+  __shared__ __align__(16) char lds[2 * STAGE];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int64_t z = blockIdx.z;
+  int ti, tj;
+  if constexpr (SYM) {   // tiles on and above the diagonal, column after column
+    tj = (int)((sqrtf(8.0f * (float)blockIdx.x + 1.0f) - 1.0f) * 0.5f);
+    while ((tj + 1) * (tj + 2) / 2 <= (int)blockIdx.x) ++tj;
+    while (tj * (tj + 1) / 2 > (int)blockIdx.x) --tj;
+    ti = (int)blockIdx.x - tj * (tj + 1) / 2;
+  } else {
+    const int nt = a.N / TILE;
+    ti = blockIdx.x / nt;
+    tj = blockIdx.x % nt;
+  }
+  const int row0 = ti * TILE, col0 = tj * TILE;
+  const uint16_t* pa = a.a.p + z * a.a.batch;
+  const uint16_t* pb = a.b.p + z * a.b.batch;
+
+  // 1 KB (16 rows of 64 bytes) an instruction: wave w loads rows 32 w .. 32 w + 31
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+  const uint32_t src = (uint32_t)((lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16));
+  auto issue = [&](int stage, int kb) {
+#pragma unroll
+    for (int op = 0; op < 2; ++op) {
+      const uint16_t* base = op ? pb : pa;
+      const int R = op ? a.N : a.M, r0 = op ? col0 : row0;
+      const int64_t plane = op ? a.b.plane : a.a.plane;
+#pragma unroll
+      for (int p = 0; p < PL; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint16_t* from = base + p * plane + ((int64_t)kb * R + r0 + 32 * wave + 16 * h) * 32;
+          lds_load16(from, src, lds0 + stage * STAGE + (op * PL + p) * SLICE + (32 * wave + 16 * h) * 64);
+        }
+    }
+  };
+  f32x16 acc[2][2] = {};
+  const int wr = (wave >> 1) * 64, wc = (wave & 1) * 64, l32 = lane & 31, hf = lane >> 5;
+  const int nk = a.K / 32;
+  issue(0, 0);
+  for (int kb = 0; kb < nk; ++kb) {
+    __builtin_amdgcn_s_waitcnt(WaitVmLgkm<0>::imm);
+    ring_barrier();   // the slice is there, and every wave is done with the other stage
+    if (kb + 1 < nk) issue((kb + 1) & 1, kb + 1);
+    const char* st = lds + (kb & 1) * STAGE;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      f16x8 fa[PL][2], fb[PL][2];
+#pragma unroll
+      for (int p = 0; p < PL; ++p)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int ra = wr + 32 * t + l32, rb = wc + 32 * t + l32, ch = 2 * ks + hf;
+          fa[p][t] = *(const f16x8*)(st + p * SLICE + ra * 64 + ((ch ^ ((ra >> 2) & 3)) * 16));
+          fb[p][t] = *(const f16x8*)(st + (PL + p) * SLICE + rb * 64 + ((ch ^ ((rb >> 2) & 3)) * 16));
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if constexpr (PL == 2) {
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[1][i], fb[0][j], acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[1][j], acc[i][j], 0, 0, 0);
+          }
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[0][j], acc[i][j], 0, 0, 0);
+        }
+    }
+  }
+
+  // a lane holds rows 8 (r / 4) + 4 hf + r % 4 of column l32 of every 32 x 32 tile
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int col = col0 + wc + 32 * j + l32;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = row0 + wr + 32 * i + 8 * q + 4 * hf;
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          v[r] = a.sacc * acc[i][j][4 * q + r];
+          if constexpr (EPI != ORTH_GRAM) {
+            const int64_t e = z * a.old.batch + panel(row + r, col, a.M);
+            v[r] += a.sold * (f16_value(a.old.p[e]) + f16_value(a.old.p[e + a.old.plane]));
+          }
+        }
+        if constexpr (EPI == ORTH_OUT) {
+          const OrthIo& io = a.io;
+          IO* y = (IO*)io.out + z * io.o_batch;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (row + r < io.m && col < io.n) y[at_x<IO>(io, io.o_row, row + r, col)] = from_f32<IO>(v[r]);
+        } else {
+          uint16_t hi[4], lo[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) planes_of(v[r], hi[r], lo[r]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int64_t e = z * a.c.batch + panel(row + r, col, a.M);
+            a.c.p[e] = hi[r];
+            a.c.p[e + a.c.plane] = lo[r];
+          }
+          if (!SYM || ti != tj) {
+            const OrthMat& t = SYM ? a.c : a.ct;
+            const int64_t e = z * t.batch + panel(col, row, a.N);
+            __builtin_memcpy(__builtin_assume_aligned(t.p + e, 8), hi, 8);
+            __builtin_memcpy(__builtin_assume_aligned(t.p + e + t.plane, 8), lo, 8);
+          }
+        }
+      }
+    }
+}
+
+template <typename IO>
+void small(const OrthIo& io, const OrthPoly& p, hipStream_t s) {
+  const dim3 grid((unsigned)io.batch);
+  if (io.m <= 16) launch_kernel(orth_small<IO, 1, 1024>, grid, dim3(1024), 0, s, io, p);
+  else if (io.m <= 32) launch_kernel(orth_small<IO, 2, 512>, grid, dim3(512), 0, s, io, p);
+  else launch_kernel(orth_small<IO, 4, 512>, grid, dim3(512), 0, s, io, p);
+}
+
+template <int EPI, typename IO>
+void gemm(const OrthGemmArgs& a, int planes, hipStream_t s) {
+  const unsigned mt = (unsigned)(a.M / ORTH_TILE), nt = (unsigned)(a.N / ORTH_TILE);
+  const bool sym = EPI == ORTH_GRAM || EPI == ORTH_POLY;
+  const dim3 grid(sym ? mt * (mt + 1) / 2 : mt * nt, 1, (unsigned)a.io.batch);
+  if (planes == 1) launch_kernel(orth_gemm<EPI, 1, IO>, grid, dim3(256), 0, s, a);
+  else launch_kernel(orth_gemm<EPI, 2, IO>, grid, dim3(256), 0, s, a);
+}
+
+}  // namespace
+
+#define PC_ORTH_TYPES(f)                    \
+  if (dtype == PC_DTYPE_F32) {              \
+    f(float)                                \
+  } else if (dtype == PC_DTYPE_F16) {       \
+    f(f16)                                  \
+  } else {                                  \
+    f(bf16)                                 \
+  }
+
+void launch_orth_small(const OrthIo& io, const OrthPoly& p, int dtype, hipStream_t s) {
+#define F(T) small<T>(io, p, s);
+  PC_ORTH_TYPES(F)
+#undef F
+}
+
+void launch_orth_norm(const OrthIo& io, int dtype, double* part, hipStream_t s) {
+  const dim3 grid(ORTH_NORM_BLOCKS, (unsigned)io.batch);
+#define F(T) launch_kernel(orth_norm<T>, grid, dim3(256), 0, s, io, part);
+  PC_ORTH_TYPES(F)
+#undef F
+}
+
+void launch_orth_split(const OrthIo& io, int dtype, const double* part, float scale, int mp, int np, const OrthMat& x,
+                       const OrthMat& xt, hipStream_t s) {
+  const dim3 grid((unsigned)(np / 32), (unsigned)(mp / 32), (unsigned)io.batch);
+#define F(T) launch_kernel(orth_split<T>, grid, dim3(256), 0, s, io, part, scale, mp, np, x, xt);
+  PC_ORTH_TYPES(F)
+#undef F
+}
+
+void launch_orth_gemm(const OrthGemmArgs& a, int epi, int planes, int dtype, hipStream_t s) {
+  if (epi == ORTH_GRAM) gemm<ORTH_GRAM, float>(a, planes, s);
+  else if (epi == ORTH_POLY) gemm<ORTH_POLY, float>(a, planes, s);
+  else if (epi == ORTH_APPLY) gemm<ORTH_APPLY, float>(a, planes, s);
+  else {
+#define F(T) gemm<ORTH_OUT, T>(a, planes, s);
+    PC_ORTH_TYPES(F)
+#undef F
+  }
+}
+
+}  // namespace pc

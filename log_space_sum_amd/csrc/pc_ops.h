@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/pc.h"
+#include "pc_device.h"
 #include "pc_launch.h"
 
 namespace pc {
@@ -114,5 +115,47 @@ void launch_mix_states(const MixArgs& a, int dtype, hipStream_t s);  // each seg
 void launch_mix_scan(const MixScanArgs& a, hipStream_t s);           // seg: own states -> states at the starts
 void launch_mix_sum(const MixSumArgs& a, int dtype, hipStream_t s);
 void launch_mix_step(const MixStepArgs& a, int dtype, hipStream_t s);
+
+// ---- orthogonalised update ---------------------------------------------------
+// m <= n: the smaller and the larger dimension of the matrices; tall: the rows
+// are the larger one.  X [m, n] is the matrix or its transpose.
+struct OrthIo {
+  int64_t batch;
+  int32_t m, n, tall;
+  const void* g;
+  int64_t g_batch, g_row;
+  void* out;
+  int64_t o_batch, o_row;
+  float eps;
+};
+constexpr int ORTH_SMALL = 64;       // all steps on the Gram matrix, in 64 bits, up to this m
+constexpr int ORTH_MAX_STEPS = 32;
+struct OrthPoly {
+  int32_t steps;
+  float c[ORTH_MAX_STEPS][3];
+};
+constexpr int ORTH_TILE = 128;       // rows and columns of the operands are padded to it
+constexpr int ORTH_NORM_BLOCKS = 64; // partial sums of a matrix's norm
+// Operands of the products: float16 planes (hi, lo) of scaled values in
+// K-blocked panels, one after the other for the matrices of the batch.
+struct OrthMat {
+  uint16_t* p;
+  int64_t plane;        // elements from the hi to the lo plane
+  int64_t batch;        // elements from one matrix to the next
+};
+enum OrthEpi { ORTH_GRAM, ORTH_POLY, ORTH_APPLY, ORTH_OUT };
+struct OrthGemmArgs {
+  int32_t M, N, K;      // padded; C [M, N] = A [M, K] B [N, K]^T
+  OrthMat a, b;
+  OrthMat old;          // POLY: A, APPLY / OUT: X (panels of [M, N])
+  OrthMat c, ct;        // the result's panels and its transpose's (GRAM / POLY: c alone, both halves)
+  float sacc, sold;     // result = sacc acc + sold old
+  OrthIo io;            // OUT
+};
+void launch_orth_small(const OrthIo& io, const OrthPoly& p, int dtype, hipStream_t s);
+void launch_orth_norm(const OrthIo& io, int dtype, double* part, hipStream_t s);
+void launch_orth_split(const OrthIo& io, int dtype, const double* part, float scale, int mp, int np, const OrthMat& x,
+                       const OrthMat& xt, hipStream_t s);
+void launch_orth_gemm(const OrthGemmArgs& a, int epi, int planes, int dtype, hipStream_t s);
 
 }  // namespace pc

@@ -175,6 +175,77 @@ void mix_starts(const pc_linear_attention* d, const MixArgs& a, const float* ini
   check_launch();
 }
 
+// ---- orthogonalised update -----------------------------------------------------
+
+struct OrthPlan {
+  int m, n, mp, np;
+  bool small;
+  OrthMat x[2], xt[2], a, b;
+  size_t part, total;
+};
+OrthPlan orth_plan(int64_t batch, int32_t rows, int32_t cols, void* ws) {
+  OrthPlan p{};
+  p.m = std::min(rows, cols);
+  p.n = std::max(rows, cols);
+  p.small = p.m <= ORTH_SMALL;
+  if (p.small || batch == 0) return p;
+  p.mp = (int)round_up(p.m, ORTH_TILE);
+  p.np = (int)round_up(p.n, ORTH_TILE);
+  auto mat = [&](int64_t rows_, int64_t cols_) {
+    OrthMat o{};
+    o.plane = batch * rows_ * cols_;
+    o.batch = rows_ * cols_;
+    o.p = (uint16_t*)((char*)ws + p.total);
+    p.total += (size_t)round_up(2 * o.plane * (int64_t)sizeof(uint16_t), 256);
+    return o;
+  };
+  for (int k = 0; k < 2; ++k) {
+    p.x[k] = mat(p.mp, p.np);
+    p.xt[k] = mat(p.np, p.mp);
+  }
+  p.a = mat(p.mp, p.mp);
+  p.b = mat(p.mp, p.mp);
+  p.part = p.total;
+  p.total += (size_t)batch * ORTH_NORM_BLOCKS * sizeof(double);
+  return p;
+}
+
+void check_orth(int dtype, int64_t batch, int32_t rows, int32_t cols) {
+  check_dtype(dtype);
+  need(batch >= 0, "batch must be at least 0");
+  need(rows >= 1 && cols >= 1, "rows and cols must be at least 1");
+  if (batch > 65535) fail(PC_ERR_UNSUPPORTED, std::to_string(batch) + " matrices (at most 65535)");
+  if (rows > 32768 || cols > 32768)
+    fail(PC_ERR_UNSUPPORTED, std::to_string(rows) + " x " + std::to_string(cols) + " matrices (at most 32768)");
+}
+
+// Bounds of the singular values at every step and of the step's polynomial
+// b t + c t^2 (t the squared singular value): where they start in [0, 1], over
+// a fine grid with a margin.
+struct OrthBounds {
+  double x[ORTH_MAX_STEPS + 1], p[ORTH_MAX_STEPS];
+};
+OrthBounds orth_bounds(int steps, const float* c) {
+  OrthBounds o;
+  double top = 1.0;
+  for (int s = 0; s < steps; ++s) {
+    o.x[s] = top;
+    double next = 0.0, poly = 0.0;
+    for (int k = 0; k <= 4096; ++k) {
+      const double x = top * k / 4096, t = x * x, q = (double)c[3 * s + 1] * t + (double)c[3 * s + 2] * t * t;
+      poly = std::max(poly, std::fabs(q));
+      next = std::max(next, std::fabs((double)c[3 * s] * x + q * x));
+    }
+    o.p[s] = poly;
+    top = 1.02 * next;
+    if (!(top <= 1024.0)) fail(PC_ERR_INVALID_ARG, "coefficients of step " + std::to_string(s) + " let the matrix grow past 1024");
+  }
+  o.x[steps] = top;
+  return o;
+}
+// The power of two that scales values up to `top` into float16's upper range.
+float orth_scale(double top) { return (float)std::ldexp(1.0, std::min(30, 14 - (int)std::ceil(std::log2(std::max(top, 1e-6))))); }
+
 }  // namespace
 
 extern "C" {
@@ -453,6 +524,106 @@ int pc_linear_attention_step(int device, const pc_linear_attention* d, void* str
     a.o_hs = d->o.head_stride;
     launch_mix_step(a, d->dtype, (hipStream_t)stream);
     check_launch();
+  });
+}
+
+int pc_orthogonalize_workspace_bytes(int dtype, int64_t batch, int32_t rows, int32_t cols, size_t* bytes) {
+  return guarded([&] {
+    need(bytes, "null bytes");
+    check_orth(dtype, batch, rows, cols);
+    *bytes = orth_plan(batch, rows, cols, nullptr).total;
+  });
+}
+
+int pc_orthogonalize(int device, int dtype, int64_t batch, int32_t rows, int32_t cols, const void* g, int64_t g_batch,
+                     int64_t g_row, void* out, int64_t out_batch, int64_t out_row, int32_t steps,
+                     const float* coefficients, float eps, void* ws, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    check_device(device);
+    check_orth(dtype, batch, rows, cols);
+    need(steps >= 1 && steps <= ORTH_MAX_STEPS, "steps must be in [1, " + std::to_string(ORTH_MAX_STEPS) + "]");
+    need(coefficients, "null coefficients");
+    need(std::isfinite(eps) && eps >= 0.0f, "eps must be finite and at least 0");
+    OrthPoly poly{};
+    poly.steps = steps;
+    for (int k = 0; k < 3 * steps; ++k) {
+      need(std::isfinite(coefficients[k]), "a coefficient is not finite");
+      poly.c[k / 3][k % 3] = coefficients[k];
+    }
+    const OrthBounds bound = orth_bounds(steps, coefficients);
+    need(batch == 0 || (g && out), "null matrices");
+    need(g_row >= cols || (g_row >= 0 && rows == 1), "g_row below cols");
+    need(out_row >= cols || (out_row >= 0 && rows == 1), "out_row below cols");
+    const int64_t span = (rows - 1) * out_row + cols;
+    need(g_batch >= 0, "g_batch is negative");
+    need(batch <= 1 || out_batch >= span || (out_batch >= cols && out_row >= (batch - 1) * out_batch + cols),
+         "the matrices of out overlap");
+    OrthPlan p = orth_plan(batch, rows, cols, ws);
+    check_ws(ws, ws_bytes, p.total);
+    if (batch == 0) return;
+    DeviceGuard dg(device);
+    const hipStream_t s = (hipStream_t)stream;
+    OrthIo io{};
+    io.batch = batch;
+    io.m = p.m;
+    io.n = p.n;
+    io.tall = rows > cols;
+    io.g = g;
+    io.g_batch = g_batch;
+    io.g_row = g_row;
+    io.out = out;
+    io.o_batch = out_batch;
+    io.o_row = out_row;
+    io.eps = eps;
+    if (p.small) {
+      launch_orth_small(io, poly, dtype, s);
+      check_launch();
+      return;
+    }
+    double* part = (double*)((char*)ws + p.part);
+    launch_orth_norm(io, dtype, part, s);
+    check_launch();
+    float sx = orth_scale(bound.x[0]);
+    launch_orth_split(io, dtype, part, sx, p.mp, p.np, p.x[0], p.xt[0], s);
+    check_launch();
+    for (int k = 0; k < steps; ++k) {
+      const float *c = coefficients + 3 * k;
+      const OrthMat &x = p.x[k & 1], &xt = p.xt[k & 1];
+      const float sa = orth_scale(bound.x[k] * bound.x[k]), sb = orth_scale(bound.p[k]);
+      const float sn = k + 1 < steps ? orth_scale(bound.x[k + 1]) : 1.0f;
+      // A = X X^T.  bfloat16 results: its operands in one plane (11 bits), an
+      // error of 2^-12 of A that reaches the result as about a quarter of
+      // bfloat16's own rounding, for a sixth of the matrix instructions
+      OrthGemmArgs a{};
+      a.io = io;
+      a.M = a.N = p.mp;
+      a.K = p.np;
+      a.a = a.b = x;
+      a.c = p.a;
+      a.sacc = sa / (sx * sx);
+      launch_orth_gemm(a, ORTH_GRAM, dtype == PC_DTYPE_BF16 ? 1 : 2, dtype, s);
+      check_launch();
+      // B = b A + c A^2
+      a.K = p.mp;
+      a.a = a.b = a.old = p.a;
+      a.c = p.b;
+      a.sacc = sb * c[2] / (sa * sa);
+      a.sold = sb * c[1] / sa;
+      launch_orth_gemm(a, ORTH_POLY, 2, dtype, s);
+      check_launch();
+      // X <- a X + B X
+      a.N = p.np;
+      a.a = p.b;
+      a.b = xt;
+      a.old = x;
+      a.c = p.x[(k + 1) & 1];
+      a.ct = p.xt[(k + 1) & 1];
+      a.sacc = sn / (sb * sx);
+      a.sold = sn * c[0] / sx;
+      launch_orth_gemm(a, k + 1 < steps ? ORTH_APPLY : ORTH_OUT, 2, dtype, s);
+      check_launch();
+      sx = sn;
+    }
   });
 }
 
