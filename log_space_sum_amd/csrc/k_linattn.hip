@@ -29,10 +29,10 @@
 //
 // Precision: bfloat16 tensors are multiplied in bfloat16 with float32 sums.
 // The decay weights are not exact in bfloat16: l^{n-off-j} c_j is split into
-// three bfloat16 planes and the carried state into two for the output's
-// product, so the state keeps float32 accuracy however long the walk; the
-// inside products (a_i . b_j) l^{i-j} are rounded once to bfloat16, half a
-// step of the output's own type.  float32 and float16 tensors run on the
+// three bfloat16 planes, so the state keeps float32 accuracy however long the
+// walk; in the output's products the carried state and the inside products
+// (a_i . b_j) l^{i-j} are split into two (2^-17 of a value is left out, far
+// below the output's own rounding; one plane would add 2^-9 of every term).  float32 and float16 tensors run on the
 // float32 matrix instruction throughout (float16's range cannot hold the
 // state or its planes).
 #include <hip/hip_runtime.h>
@@ -68,6 +68,7 @@ struct Ops<bf16> {
   static constexpr int PAD = 8;
   static constexpr int CPLANES = 3;  // planes of the weighted c, and of the state in the output's product
   static constexpr int SPLANES = 2;
+  static constexpr int PPLANES = 2;  // of the inside products
   typedef uint2 quad;
   static __device__ __forceinline__ f32x4 mma(quad a0, quad a1, quad b0, quad b1, f32x4 acc) {
     const uint4 a = {a0.x, a0.y, a1.x, a1.y}, b = {b0.x, b0.y, b1.x, b1.y};
@@ -98,6 +99,7 @@ struct Ops<float> {
   static constexpr int PAD = 4;
   static constexpr int CPLANES = 1;
   static constexpr int SPLANES = 1;
+  static constexpr int PPLANES = 1;
   typedef f32x4 quad;
   static __device__ __forceinline__ f32x4 mma(quad a0, quad a1, quad b0, quad b1, f32x4 acc) {
 #pragma unroll
@@ -171,11 +173,11 @@ __global__ __launch_bounds__(256, 2) void mix_walk(MixArgs m) {
   constexpr int DA = 16 * DKB, DC = 64 * NB;
   constexpr int LA = DA + O::PAD, LC = DC + O::PAD, LP = C + O::PAD;
   constexpr int UA = C * DA / EV / 256, UC = C * DC / EV / 256;   // staged units of a thread
-  constexpr int CP = O::CPLANES, SP = O::SPLANES;
+  constexpr int CP = O::CPLANES, SP = O::SPLANES, PP = O::PPLANES;
   __shared__ __align__(16) CT sa[WALK ? C * LA : 8];
   __shared__ __align__(16) CT sb[C * LA];
   __shared__ __align__(16) CT sc[C * LC];
-  __shared__ __align__(16) CT sp[WALK ? C * LP : 8];
+  __shared__ __align__(16) CT sp[WALK ? PP * C * LP : 8];
 
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int head = blockIdx.x, seq = blockIdx.z;
@@ -233,8 +235,8 @@ __global__ __launch_bounds__(256, 2) void mix_walk(MixArgs m) {
 #pragma unroll
     for (int ib = 0; ib < CB; ++ib) iw[ib] = m.oscale * decay_pow(gam, (float)(16 * ib + l16 + m.off));
     // the products' tiles right of the diagonal that a 32-wide step reads: always 0
-    for (int e = tid; e < C * 16; e += 256) {
-      const int i = e >> 4, ib = i >> 4;
+    for (int e = tid; e < PP * C * 16; e += 256) {
+      const int i = e >> 4, ib = (i % C) >> 4;
       if ((ib & 1) == 0) sp[i * LP + 16 * (ib + 1) + (e & 15)] = CT{};
     }
   }
@@ -321,7 +323,10 @@ __global__ __launch_bounds__(256, 2) void mix_walk(MixArgs m) {
           f32x4 w;
 #pragma unroll
           for (int r = 0; r < 4; ++r) w[r] = md[k][r] == 0.0f && (ib == jb && 4 * g + r > l16) ? 0.0f : acc[r] * md[k][r];
-          *(quad*)(sp + (16 * ib + l16) * LP + 16 * jb + 4 * g) = O::round(w);
+          quad pl[PP];
+          split<CT, PP>(w, pl);
+#pragma unroll
+          for (int p = 0; p < PP; ++p) *(quad*)(sp + (p * C + 16 * ib + l16) * LP + 16 * jb + 4 * g) = pl[p];
         }
       }
       // the state's part of the output
@@ -373,10 +378,13 @@ __global__ __launch_bounds__(256, 2) void mix_walk(MixArgs m) {
         if constexpr (WALK) {
 #pragma unroll
           for (int ib = b; ib < CB; ++ib) {
-            const CT* ri = sp + (16 * ib + l16) * LP + 16 * b + 4 * g;
-            const quad p0 = O::row(ri), p1 = O::row(ri + 16);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) o[ib][nb] = O::mma(c0[nb], c1[nb], p0, p1, o[ib][nb]);
+            for (int p = PP - 1; p >= 0; --p) {
+              const CT* ri = sp + (p * C + 16 * ib + l16) * LP + 16 * b + 4 * g;
+              const quad p0 = O::row(ri), p1 = O::row(ri + 16);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) o[ib][nb] = O::mma(c0[nb], c1[nb], p0, p1, o[ib][nb]);
+            }
           }
         }
 #pragma unroll

@@ -81,7 +81,7 @@ __global__ __launch_bounds__(block_of<TPR>()) void norm_fwd(NormArgs a) {
   __shared__ float red[2 * (BLK / 64)];
   int slot = 0;
   const int lane = threadIdx.x % TPR;
-  const float inv = 1.0f / (float)a.cols;
+  const float count = (float)a.cols;
   // every group of a block runs the same number of rounds: the sums of wide rows hold barriers
   for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < a.rows; r0 += (int64_t)gridDim.x * G) {
     const int64_t row = r0 + threadIdx.x / TPR;
@@ -97,7 +97,7 @@ __global__ __launch_bounds__(block_of<TPR>()) void norm_fwd(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < V; ++e) s += v[i][e] = to_f32(u.v[e]);
     }
-    const float mean = row_sum<TPR>(s, red, slot) * inv;
+    const float mean = row_sum<TPR>(s, red, slot) / count;
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(block_of<TPR>()) void norm_fwd(NormArgs a) {
         v[i][e] = c < a.cols ? v[i][e] - mean : 0.0f;
         q += v[i][e] * v[i][e];
       }
-    const float rstd = 1.0f / sqrtf(row_sum<TPR>(q, red, slot) * inv + a.eps);
+    const float rstd = 1.0f / sqrtf(row_sum<TPR>(q, red, slot) / count + a.eps);
     if (!on) continue;
     if (lane == 0) {
       if (a.mean) a.mean[row] = mean;

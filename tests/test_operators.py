@@ -1,0 +1,213 @@
+"""The operators in front of a conditional circuit on the CPU: the float64 definitions against differences and
+against each other, and every refusal of the C ABI (refused before any device work)."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+import log_space_sum_amd as L
+from oracle import ops_oracle as R
+
+
+def _difference(f, x, d, h=1e-6):
+    return (f(x + h * d) - f(x - h * d)) / (2 * h)
+
+
+def test_layer_norm_gradient_is_the_difference():
+    rng = np.random.default_rng(0)
+    x, dy, w, b = rng.normal(size=(5, 7)), rng.normal(size=(5, 7)), rng.normal(size=7), rng.normal(size=7)
+    _, mean, rstd = R.layer_norm(x, w, b)
+    dx, dw, db = R.layer_norm_grad(dy, x, mean, rstd, w)
+    for value, grad, f in ((x, dx, lambda z: (R.layer_norm(z, w, b)[0] * dy).sum()),
+                           (w, dw, lambda z: (R.layer_norm(x, z, b)[0] * dy).sum()),
+                           (b, db, lambda z: (R.layer_norm(x, w, z)[0] * dy).sum())):
+        d = rng.normal(size=value.shape)
+        # central differences: truncation h^2, rounding eps / h
+        np.testing.assert_allclose((grad * d).sum(), _difference(f, value, d), rtol=1e-7, atol=1e-7)
+
+
+def test_linear_attention_gradient_is_the_difference():
+    rng = np.random.default_rng(1)
+    cu = [0, 3, 3, 4, 9]
+    q, k, v = rng.normal(size=(9, 4, 3)), rng.normal(size=(9, 2, 3)), rng.normal(size=(9, 2, 5))
+    g, s = -np.array([0.0, 0.1, 1.0, np.inf]), rng.normal(size=(4, 4, 3, 5))
+    do, ds = rng.normal(size=(9, 4, 5)), rng.normal(size=(4, 4, 3, 5))
+
+    def loss(q, k, v, s):
+        o, e = R.linear_attention(q, k, v, g, cu, 0.7, s)
+        return (o * do).sum() + (e * ds).sum()
+
+    grads = R.linear_attention_grad(do, q, k, v, g, cu, 0.7, s, ds)
+    args = [q, k, v, s]
+    for i, grad in enumerate(grads):
+        d = rng.normal(size=args[i].shape)
+        f = lambda z: loss(*[z if j == i else a for j, a in enumerate(args)])  # noqa: E731
+        np.testing.assert_allclose((grad * d).sum(), _difference(f, args[i], d), rtol=1e-6, atol=1e-6)
+
+
+def test_orthogonalize_moves_the_singular_values():
+    rng = np.random.default_rng(2)
+    g = rng.normal(size=(6, 4))
+    co = [(3.4445, -4.7750, 2.0315)] * 5
+    x = R.orthogonalize(g, co, 0.0)
+    u, s, vt = np.linalg.svd(g, full_matrices=False)
+    t = s / np.sqrt((s * s).sum())
+    for a, b, c in co:
+        t = a * t + b * t ** 3 + c * t ** 5
+    np.testing.assert_allclose(x, (u * t) @ vt, rtol=1e-10, atol=1e-12)
+
+
+# ---- refusals: host-side checks, nothing reaches a device -------------------
+
+P = 4096   # an address that is never read
+FLOATS = (C.c_float * 96)(*([3.4445, -4.7750, 2.0315] * 32))
+
+
+def _refuses(code, rc):
+    assert rc == code, (rc, L.pc_last_error())
+    assert L.pc_last_error()
+
+
+NORM = dict(device=0, dtype=0, rows=4, cols=8, x=P, xs=8, w=None, b=None, eps=1e-5, y=P, ys=8, mean=None, rstd=None)
+
+
+@pytest.mark.parametrize("code,change", [
+    (L.PC_ERR_NO_DEVICE, dict(device=-1)), (L.PC_ERR_UNSUPPORTED, dict(dtype=3)),
+    (L.PC_ERR_INVALID_ARG, dict(rows=-1)), (L.PC_ERR_INVALID_ARG, dict(rows=2 ** 31)),
+    (L.PC_ERR_INVALID_ARG, dict(cols=0)), (L.PC_ERR_UNSUPPORTED, dict(cols=16385, xs=16385, ys=16385)),
+    (L.PC_ERR_INVALID_ARG, dict(x=None)), (L.PC_ERR_INVALID_ARG, dict(y=None)),
+    (L.PC_ERR_INVALID_ARG, dict(xs=7)), (L.PC_ERR_INVALID_ARG, dict(ys=7)),
+    (L.PC_ERR_INVALID_ARG, dict(eps=-1.0)), (L.PC_ERR_INVALID_ARG, dict(eps=float("nan"))),
+])
+def test_layer_norm_forward_refuses(code, change):
+    a = {**NORM, **change}
+    _refuses(code, L.lib().pc_layer_norm_forward(a["device"], a["dtype"], a["rows"], a["cols"], a["x"], a["xs"], a["w"],
+                                                 a["b"], a["eps"], a["y"], a["ys"], a["mean"], a["rstd"], None))
+
+
+def _norm_ws(rows, cols):
+    n = C.c_size_t()
+    assert L.lib().pc_layer_norm_workspace_bytes(rows, cols, C.byref(n)) == L.PC_OK
+    return n.value
+
+
+NBWD = dict(device=0, dtype=1, rows=4, cols=8, dy=P, dys=8, x=P, xs=8, w=None, mean=P, rstd=P, dx=P, dxs=8, dw=P, db=P,
+            ws=P, nws=1 << 30)
+
+
+@pytest.mark.parametrize("code,change", [
+    (L.PC_ERR_INVALID_ARG, dict(dy=None)), (L.PC_ERR_INVALID_ARG, dict(mean=None)), (L.PC_ERR_INVALID_ARG, dict(rstd=None)),
+    (L.PC_ERR_INVALID_ARG, dict(dx=None)), (L.PC_ERR_INVALID_ARG, dict(dys=3)), (L.PC_ERR_INVALID_ARG, dict(dxs=3)),
+    (L.PC_ERR_WORKSPACE, dict(ws=None)), (L.PC_ERR_WORKSPACE, dict(nws=8)), (L.PC_ERR_INVALID_ARG, dict(ws=P + 4)),
+    (L.PC_ERR_UNSUPPORTED, dict(cols=20000)),
+])
+def test_layer_norm_backward_refuses(code, change):
+    a = {**NBWD, **change}
+    _refuses(code, L.lib().pc_layer_norm_backward(*[a[k] for k in ("device", "dtype", "rows", "cols", "dy", "dys", "x", "xs",
+                                                                   "w", "mean", "rstd", "dx", "dxs", "dw", "db", "ws",
+                                                                   "nws")], None))
+
+
+def test_layer_norm_workspace():
+    assert _norm_ws(0, 8) == 0
+    assert 0 < _norm_ws(4, 8) <= _norm_ws(4096, 8)
+    # the partial sums stay a small part of what the pass moves
+    assert _norm_ws(1 << 20, 4096) < (1 << 20) * 4096 * 4 // 64
+
+
+def _attention(**change):
+    d = L.pc_linear_attention(dtype=1, heads=4, kv_heads=2, dim_k=16, dim_v=24, num_seqs=2, num_tokens=10, max_seqlen=10,
+                              cu_seqlens=P, log_decay=P, scale=0.25, state=P, num_slots=16)
+    for n, h, w in (("q", 4, 16), ("k", 2, 16), ("v", 2, 24), ("o", 4, 24), ("d_o", 4, 24), ("d_q", 4, 16), ("d_k", 2, 16),
+                    ("d_v", 2, 24)):
+        setattr(d, n, L.pc_heads(P, h * w, w))
+    for k, v in change.items():
+        setattr(d, k, v)
+    return d
+
+
+BOTH = [
+    (L.PC_ERR_UNSUPPORTED, dict(dtype=7)), (L.PC_ERR_INVALID_ARG, dict(heads=0)), (L.PC_ERR_INVALID_ARG, dict(kv_heads=3)),
+    (L.PC_ERR_INVALID_ARG, dict(dim_k=0)), (L.PC_ERR_UNSUPPORTED, dict(dim_k=129)), (L.PC_ERR_UNSUPPORTED, dict(dim_v=256)),
+    (L.PC_ERR_INVALID_ARG, dict(num_tokens=-1)), (L.PC_ERR_INVALID_ARG, dict(log_decay=None)),
+    (L.PC_ERR_INVALID_ARG, dict(scale=0.0)), (L.PC_ERR_INVALID_ARG, dict(scale=float("inf"))),
+    (L.PC_ERR_INVALID_ARG, dict(q=L.pc_heads(None, 64, 16))), (L.PC_ERR_INVALID_ARG, dict(k=L.pc_heads(P, -1, 16))),
+]
+SEQS = [
+    (L.PC_ERR_INVALID_ARG, dict(num_seqs=-1)), (L.PC_ERR_UNSUPPORTED, dict(num_seqs=65536)),
+    (L.PC_ERR_INVALID_ARG, dict(max_seqlen=-1)), (L.PC_ERR_INVALID_ARG, dict(cu_seqlens=None)),
+]
+
+
+@pytest.mark.parametrize("code,change", BOTH + SEQS + [(L.PC_ERR_INVALID_ARG, dict(o=L.pc_heads(P, 95, 24))),
+                                                       (L.PC_ERR_INVALID_ARG, dict(o=L.pc_heads(P, 96, 23)))])
+def test_linear_attention_forward_refuses(code, change):
+    _refuses(code, L.lib().pc_linear_attention_forward(0, C.byref(_attention(**change)), P, 1 << 40, None))
+
+
+@pytest.mark.parametrize("code,change", BOTH + SEQS + [(L.PC_ERR_INVALID_ARG, dict(d_o=L.pc_heads(None, 96, 24))),
+                                                       (L.PC_ERR_INVALID_ARG, dict(d_q=L.pc_heads(P, 0, 0))),
+                                                       (L.PC_ERR_INVALID_ARG, dict(d_k=L.pc_heads(P, 32, 15))),
+                                                       (L.PC_ERR_INVALID_ARG, dict(d_v=L.pc_heads(P, 0, 24)))])
+def test_linear_attention_backward_refuses(code, change):
+    _refuses(code, L.lib().pc_linear_attention_backward(0, C.byref(_attention(**change)), P, 1 << 40, None))
+
+
+@pytest.mark.parametrize("code,change", BOTH + [(L.PC_ERR_INVALID_ARG, dict(state=None)),
+                                                (L.PC_ERR_INVALID_ARG, dict(num_slots=-1)),
+                                                (L.PC_ERR_INVALID_ARG, dict(num_slots=9)),   # fewer than rows, no slots
+                                                (L.PC_ERR_INVALID_ARG, dict(o=L.pc_heads(P, 20, 24)))])
+def test_linear_attention_step_refuses(code, change):
+    _refuses(code, L.lib().pc_linear_attention_step(0, C.byref(_attention(**change)), None))
+
+
+def test_linear_attention_workspace():
+    n = C.c_size_t()
+    f = L.lib().pc_linear_attention_workspace_bytes
+    # many heads and short sequences: no split, no workspace; gradients of shared heads are summed from it
+    d = _attention(num_seqs=256, num_tokens=256 * 10)
+    assert f(C.byref(d), 0, C.byref(n)) == L.PC_OK and n.value == 0
+    assert f(C.byref(d), 1, C.byref(n)) == L.PC_OK and n.value >= 2560 * 4 * (16 + 24) * 4
+    long = _attention(num_seqs=1, num_tokens=1 << 15, max_seqlen=1 << 15)
+    assert f(C.byref(long), 0, C.byref(n)) == L.PC_OK and n.value > 0
+    _refuses(L.PC_ERR_WORKSPACE, L.lib().pc_linear_attention_forward(0, C.byref(long), P, n.value - 1, None))
+    _refuses(L.PC_ERR_WORKSPACE, L.lib().pc_linear_attention_backward(0, C.byref(long), P, n.value, None))
+    _refuses(L.PC_ERR_INVALID_ARG, f(None, 0, C.byref(n)))
+    _refuses(L.PC_ERR_INVALID_ARG, f(C.byref(d), 0, None))
+
+
+ORTH = dict(device=0, dtype=0, batch=2, rows=96, cols=80, g=P, gb=7680, gr=80, out=P, ob=7680, orow=80, steps=5, co=FLOATS,
+            eps=1e-7, ws=P, nws=1 << 40)
+DIVERGES = (C.c_float * 96)(*([8.0, 0.0, 0.0] * 32))
+NOT_FINITE = (C.c_float * 96)(*([3.0, float("nan"), 0.0] * 32))
+
+
+@pytest.mark.parametrize("code,change", [
+    (L.PC_ERR_NO_DEVICE, dict(device=-1)), (L.PC_ERR_UNSUPPORTED, dict(dtype=-1)), (L.PC_ERR_INVALID_ARG, dict(batch=-1)),
+    (L.PC_ERR_UNSUPPORTED, dict(batch=65536)), (L.PC_ERR_INVALID_ARG, dict(rows=0)),
+    (L.PC_ERR_UNSUPPORTED, dict(rows=32769)), (L.PC_ERR_INVALID_ARG, dict(g=None)), (L.PC_ERR_INVALID_ARG, dict(gr=79)),
+    (L.PC_ERR_INVALID_ARG, dict(orow=79)), (L.PC_ERR_INVALID_ARG, dict(ob=7679)), (L.PC_ERR_INVALID_ARG, dict(gb=-1)),
+    (L.PC_ERR_INVALID_ARG, dict(steps=0)), (L.PC_ERR_INVALID_ARG, dict(steps=33)), (L.PC_ERR_INVALID_ARG, dict(co=None)),
+    (L.PC_ERR_INVALID_ARG, dict(co=DIVERGES)), (L.PC_ERR_INVALID_ARG, dict(co=NOT_FINITE)),
+    (L.PC_ERR_INVALID_ARG, dict(eps=-1e-9)), (L.PC_ERR_WORKSPACE, dict(nws=100)), (L.PC_ERR_WORKSPACE, dict(ws=None)),
+])
+def test_orthogonalize_refuses(code, change):
+    a = {**ORTH, **change}
+    _refuses(code, L.lib().pc_orthogonalize(*[a[k] for k in ("device", "dtype", "batch", "rows", "cols", "g", "gb", "gr", "out",
+                                                             "ob", "orow", "steps", "co", "eps", "ws", "nws")], None))
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(3, 4)
+    with pytest.raises(ValueError, match="GPU"):
+        L.pc_layer_norm_forward(x, None, None, torch.empty_like(x))
+    with pytest.raises(ValueError, match="two dimensions"):
+        L.pc_layer_norm_forward(x[0], None, None, x[0])
+    q = torch.zeros(5, 2, 4)
+    with pytest.raises(ValueError, match="GPU"):
+        L.pc_linear_attention_forward(q, q, q, None, q)
+    with pytest.raises(ValueError, match="three dimensions"):
+        L.pc_linear_attention_step(q[0], q, q, None, q, q)
+    with pytest.raises(ValueError, match="dimensions"):
+        L.pc_orthogonalize(x[0], x[0])
