@@ -436,6 +436,7 @@ typedef struct pc_heads {
  *  state_in, state_out: device float32 [num_seqs, heads, dim_k, dim_v], the
  *    states before and after the sequences, nullable (0 / not wanted); they
  *    may be the same buffer.  An empty sequence hands its state through.
+ *  Token strides are at most 2^23.
  * A value that is not finite reaches the outputs of its own and later tokens
  * of its sequence only. */
 typedef struct pc_linear_attention {
@@ -466,7 +467,7 @@ int pc_linear_attention_workspace_bytes(const pc_linear_attention* d, int backwa
 
 /* Whole sequences: o (and state_out) from q, k, v (and state_in).
  * Errors: PC_ERR_INVALID_ARG, PC_ERR_UNSUPPORTED (dims above 128, more than
- * 65535 sequences, unknown dtype), PC_ERR_WORKSPACE, PC_ERR_HIP. */
+ * 65535 sequences, a token stride above 2^23, unknown dtype), PC_ERR_WORKSPACE, PC_ERR_HIP. */
 int pc_linear_attention_forward(int device, const pc_linear_attention* d, void* ws, size_t ws_bytes, void* stream);
 
 /* The gradients d_q, d_k, d_v (and dstate_in) from d_o (and dstate_out), q, k,

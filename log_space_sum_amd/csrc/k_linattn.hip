@@ -16,9 +16,9 @@
 //   o_i = l^{i+off} a_i^T S + sum_{j <= i} l^{i-j} (a_i . b_j) c_j,
 //   S  <- l^n S + sum_j l^{n-off-j} b_j c_j^T
 //
-// are matrix products.  A workgroup of four waves walks one (sequence, head);
-// each wave carries dc / 4 columns of the state in its registers for the whole
-// walk, in the accumulator layout, in which four consecutive rows lie in one
+// are matrix products.  A workgroup of four or eight waves walks one (sequence,
+// head); each wave carries 16 columns of the state in its registers for the
+// whole walk, in the accumulator layout, in which four consecutive rows lie in one
 // lane: with the contraction's order permuted alike on both sides, the same
 // registers are the operand of the next product, so the state never passes
 // through LDS.  Only the [C, C] products a_i . b_j do (one tile a wave).
@@ -47,6 +47,8 @@ namespace pc {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
@@ -65,7 +67,8 @@ template <>
 struct Ops<bf16> {
   static constexpr int C = 64;       // tokens of a chunk
   static constexpr int EV = 8;       // elements of a staged unit
-  static constexpr int PAD = 8;
+  // row padding of the tiles read by rows, and by columns (16 lanes' 4 rows of 32 bytes lie in different banks then)
+  static constexpr int PAD = 8, CPAD = 16;
   static constexpr int CPLANES = 3;  // planes of the weighted c, and of the state in the output's product
   static constexpr int SPLANES = 2;
   static constexpr int PPLANES = 2;  // of the inside products
@@ -75,6 +78,14 @@ struct Ops<bf16> {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
   }
   static __device__ __forceinline__ quad row(const bf16* p) { return *(const quad*)p; }
+  // Tiles read by rows alone are stored so that a lane's two quads of a 32-wide
+  // block lie side by side: one 16-byte read.  at(): the place of element j.
+  static __device__ __forceinline__ int at(int j) { return (j & ~31) + 8 * ((j >> 2) & 3) + 4 * ((j >> 4) & 1) + (j & 3); }
+  static __device__ __forceinline__ void row2(const bf16* r, int block, int g, quad& x, quad& y) {
+    const uint4 v = *(const uint4*)(r + 32 * block + 8 * g);
+    x = quad{v.x, v.y};
+    y = quad{v.z, v.w};
+  }
   // Four rows of one column: the 16 lanes of a group hand in 4 x 16 elements,
   // each four consecutive ones, and get back a column each.
   static __device__ __forceinline__ quad col(const bf16* tile, int stride) {
@@ -83,7 +94,7 @@ struct Ops<bf16> {
     return __builtin_bit_cast(quad, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p)));
   }
   static __device__ __forceinline__ uint32_t pack(float x, float y) {
-    return (uint32_t)bf16_bits(x) | ((uint32_t)bf16_bits(y) << 16);
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));   // one instruction
   }
   static __device__ __forceinline__ quad round(f32x4 v) { return quad{pack(v[0], v[1]), pack(v[2], v[3])}; }
   static __device__ __forceinline__ f32x4 wide(quad q) {
@@ -96,7 +107,7 @@ template <>
 struct Ops<float> {
   static constexpr int C = 32;
   static constexpr int EV = 4;
-  static constexpr int PAD = 4;
+  static constexpr int PAD = 4, CPAD = 4;
   static constexpr int CPLANES = 1;
   static constexpr int SPLANES = 1;
   static constexpr int PPLANES = 1;
@@ -109,6 +120,11 @@ struct Ops<float> {
     return acc;
   }
   static __device__ __forceinline__ quad row(const float* p) { return *(const quad*)p; }
+  static __device__ __forceinline__ int at(int j) { return j; }
+  static __device__ __forceinline__ void row2(const float* r, int block, int g, quad& x, quad& y) {
+    x = row(r + 32 * block + 4 * g);
+    y = row(r + 32 * block + 16 + 4 * g);
+  }
   static __device__ __forceinline__ quad col(const float* tile, int stride) {
     const int l = threadIdx.x & 63;
     const float* p = tile + 4 * (l >> 4) * stride + (l & 15);
@@ -129,25 +145,64 @@ __device__ __forceinline__ void split(f32x4 v, typename Ops<CT>::quad (&planes)[
   }
 }
 
-// EV elements of a row, of which `have` exist (the others are 0), as loaded.
+// How the dims meet the tiles and units: FULL both are tile sizes, UNITS both
+// are whole units, ANY neither.
+enum Fit { FULL, UNITS, ANY };
+
+// EV elements of a row as loaded, from an address that exists also where the
+// row has fewer than `have` (the others are cleared when they are staged).
 template <typename IO, int EV>
 struct Unit {
   IO v[EV];
 };
-template <typename IO, int EV>
-__device__ __forceinline__ Unit<IO, EV> load_unit(const IO* p, int have) {
+template <Fit F, typename IO, int EV>
+__device__ __forceinline__ Unit<IO, EV> load_unit(const char* base, uint32_t offset, int d, int dim) {
   Unit<IO, EV> u;
-  if (have >= EV) {
-    __builtin_memcpy(&u, p, sizeof(u));
+  const IO* p = (const IO*)(base + offset);
+  if constexpr (F == FULL) {
+    __builtin_memcpy(&u, p + d, sizeof(u));
+  } else if constexpr (F == UNITS) {
+    __builtin_memcpy(&u, p + (d < dim ? d : 0), sizeof(u));
   } else {
 #pragma unroll
-    for (int e = 0; e < EV; ++e) u.v[e] = e < have ? p[e] : IO{};
+    for (int e = 0; e < EV; ++e) u.v[e] = p[min(d + e, dim - 1)];
   }
   return u;
 }
-__device__ __forceinline__ bool not_finite(bf16 x) { return (x.u & 0x7f80) == 0x7f80; }
-__device__ __forceinline__ bool not_finite(f16 x) { return (__builtin_bit_cast(uint16_t, x) & 0x7c00) == 0x7c00; }
-__device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+template <Fit F, typename IO, int EV>
+__device__ __forceinline__ void clear(Unit<IO, EV>& u, bool row, int d, int dim) {
+  if (!row || (F == UNITS && d >= dim)) u = Unit<IO, EV>{};
+  if constexpr (F == ANY) {
+#pragma unroll
+    for (int e = 0; e < EV; ++e)
+      if (d + e >= dim) u.v[e] = IO{};
+  }
+}
+
+// Whether a unit holds a value that is not finite (an exponent of ones).
+template <int EV>
+__device__ __forceinline__ bool not_finite(const Unit<bf16, EV>& u) {
+  uint32_t w[EV / 2], r = 0;
+  __builtin_memcpy(w, &u, sizeof(w));
+#pragma unroll
+  for (int e = 0; e < EV / 2; ++e) r |= (w[e] & 0x7f807f80u) + 0x00800080u;   // carries into a half's top bit
+  return (r & 0x80008000u) != 0;
+}
+template <int EV>
+__device__ __forceinline__ bool not_finite(const Unit<f16, EV>& u) {
+  uint32_t w[EV / 2], r = 0;
+  __builtin_memcpy(w, &u, sizeof(w));
+#pragma unroll
+  for (int e = 0; e < EV / 2; ++e) r |= (w[e] & 0x7c007c00u) + 0x04000400u;
+  return (r & 0x80008000u) != 0;
+}
+template <int EV>
+__device__ __forceinline__ bool not_finite(const Unit<float, EV>& u) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int e = 0; e < EV; ++e) r |= (__float_as_uint(u.v[e]) & 0x7f800000u) + 0x00800000u;
+  return (r & 0x80000000u) != 0;
+}
 
 template <typename CT, typename IO, int EV>
 __device__ __forceinline__ void stage(CT* dst, const Unit<IO, EV>& u) {
@@ -161,25 +216,44 @@ __device__ __forceinline__ void stage(CT* dst, const Unit<IO, EV>& u) {
   }
 }
 
+// The same into a tile read by rows (elements at Ops::at).
+template <typename CT, typename IO, int EV>
+__device__ __forceinline__ void stage_rows(CT* row, int d, const Unit<IO, EV>& u) {
+  if constexpr (std::is_same_v<CT, bf16>) {
+    static_assert(EV == 8, "two quads");
+    CT* p = row + Ops<CT>::at(d);
+    __builtin_memcpy(__builtin_assume_aligned(p, 8), &u, 8);
+    __builtin_memcpy(__builtin_assume_aligned(p + 8, 8), (const char*)&u + 8, 8);   // the next quad's place
+  } else {
+    stage<CT, IO, EV>(row + d, u);
+  }
+}
+
 // ---- the walk ---------------------------------------------------------------
-// DKB: 16-blocks of the contracted dimension (even), NB: 16-blocks of output
-// columns a wave carries.  WALK false: only the state, from zero, of every
-// segment but a sequence's last, into `seg`.
-template <typename IO, typename CT, int DKB, int NB, bool WALK>
-__global__ __launch_bounds__(256, 2) void mix_walk(MixArgs m) {
+// DKB: 16-blocks of the contracted dimension (even); NW: waves, each with 16
+// output columns.  WALK false: only the state, from zero, of every segment but
+// a sequence's last, into `seg`.
+template <typename IO, typename CT, int DKB, int NW, Fit F, bool WALK>
+__global__ __launch_bounds__(64 * NW, F == FULL ? 4 : 2) void mix_walk(MixArgs m) {
   using O = Ops<CT>;
   using quad = typename O::quad;
-  constexpr int C = O::C, CB = C / 16, EV = O::EV;
-  constexpr int DA = 16 * DKB, DC = 64 * NB;
-  constexpr int LA = DA + O::PAD, LC = DC + O::PAD, LP = C + O::PAD;
-  constexpr int UA = C * DA / EV / 256, UC = C * DC / EV / 256;   // staged units of a thread
+  constexpr int C = O::C, CB = C / 16, EV = O::EV, NT = 64 * NW;
+  constexpr int DA = 16 * DKB, DC = 16 * NW;
+  constexpr int LA = DA + O::PAD, LB = DA + O::CPAD, LC = DC + O::CPAD, LP = C + O::PAD;
+  constexpr int UA = C * DA / EV / NT, UC = C * DC / EV / NT;   // staged units of a thread
+  static_assert(UA * NT * EV == C * DA && UC * NT * EV == C * DC, "whole units");
   constexpr int CP = O::CPLANES, SP = O::SPLANES, PP = O::PPLANES;
+  constexpr int PAIRS = CB * (CB + 1) / 2, MINE = (PAIRS + NW - 1) / NW;
   __shared__ __align__(16) CT sa[WALK ? C * LA : 8];
-  __shared__ __align__(16) CT sb[C * LA];
+  __shared__ __align__(16) CT sb[C * LB];
   __shared__ __align__(16) CT sc[C * LC];
   __shared__ __align__(16) CT sp[WALK ? PP * C * LP : 8];
+  // weights: of a token's part in the state (for the chunk's size), of the
+  // inside products at distance d = i - j (at C - 1 - d; 0 behind C - 1), and
+  // of the state in token i's output
+  __shared__ __align__(16) float swt[C], sdec[2 * C], siw[C];
 
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int head = blockIdx.x, seq = blockIdx.z;
   int sgm = blockIdx.y;
   int64_t t0 = 0, t1 = m.tokens;
@@ -196,12 +270,13 @@ __global__ __launch_bounds__(256, 2) void mix_walk(MixArgs m) {
   const IO* pa = (const IO*)m.a.p + (int64_t)(head / m.a.div) * m.a.hs;
   const IO* pb = (const IO*)m.b.p + (int64_t)(head / m.b.div) * m.b.hs;
   const IO* pc = (const IO*)m.c.p + (int64_t)(head / m.c.div) * m.c.hs;
-  const int64_t elems = (int64_t)m.da * m.dc;
-  const int col0 = wave * 16 * NB + l16;   // this lane's column of block 0
-  const bool wave_on = wave * 16 * NB < m.dc;
+  const int da = F == FULL ? DA : m.da, dc = F == FULL ? DC : m.dc;
+  const int64_t elems = (int64_t)da * dc;
+  const int col = wave * 16 + l16;         // this lane's column of the state
+  const bool wave_on = F == FULL || wave * 16 < dc;
 
-  // the carried state: lane l16 of group g holds rows 16 kb + 4 g + r of column col0 + 16 nb
-  f32x4 st[DKB][NB];
+  // the carried state: lane l16 of group g holds rows 16 kb + 4 g + r of its column
+  f32x4 st[DKB];
   {
     const float* from = nullptr;
     if (WALK) from = m.nsegs > 1 ? m.seg + (((int64_t)seq * m.nsegs + sgm) * m.heads + head) * elems
@@ -209,222 +284,222 @@ __global__ __launch_bounds__(256, 2) void mix_walk(MixArgs m) {
 #pragma unroll
     for (int kb = 0; kb < DKB; ++kb)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * kb + 4 * g + r, col = col0 + 16 * nb;
-          st[kb][nb][r] = from && row < m.da && col < m.dc ? from[(int64_t)row * m.st_r + (int64_t)col * m.st_c] : 0.0f;
-        }
-  }
-
-  // constants of the chunk: the masked decays of this wave's tiles of the
-  // inside products, and the output's weight of the state for its tokens
-  constexpr int PAIRS = CB * (CB + 1) / 2, MINE = (PAIRS + 3) / 4;
-  float md[WALK ? MINE : 1][4], iw[WALK ? CB : 1];
-  if constexpr (WALK) {
-#pragma unroll
-    for (int k = 0; k < MINE; ++k) {
-      int ib = 0, jb = wave + 4 * k;
-      while (jb > ib) jb -= ++ib;   // pair number -> (ib, jb), jb <= ib
-#pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int d = 16 * (ib - jb) + l16 - 4 * g - r;
-        md[k][r] = d >= 0 ? m.pscale * decay_pow(gam, (float)d) : 0.0f;
+        const int row = 16 * kb + 4 * g + r;
+        st[kb][r] = from && (F == FULL || (row < da && col < dc)) ? from[row * m.st_r + col * m.st_c] : 0.0f;
       }
-    }
-#pragma unroll
-    for (int ib = 0; ib < CB; ++ib) iw[ib] = m.oscale * decay_pow(gam, (float)(16 * ib + l16 + m.off));
+  }
+  if constexpr (WALK) {
+    for (int e = tid; e < 2 * C; e += NT) sdec[e] = e < C ? m.pscale * decay_pow(gam, (float)(C - 1 - e)) : 0.0f;
+    for (int e = tid; e < C; e += NT) siw[e] = m.oscale * decay_pow(gam, (float)(e + m.off));
     // the products' tiles right of the diagonal that a 32-wide step reads: always 0
-    for (int e = tid; e < PP * C * 16; e += 256) {
+    for (int e = tid; e < PP * C * 16; e += NT) {
       const int i = e >> 4, ib = (i % C) >> 4;
-      if ((ib & 1) == 0) sp[i * LP + 16 * (ib + 1) + (e & 15)] = CT{};
+      if ((ib & 1) == 0) sp[i * LP + O::at(16 * (ib + 1) + (e & 15))] = CT{};
     }
   }
 
+  // Rows pos .. pos + n - 1 (n >= 1); a row behind them loads one of them.
+  // The base is uniform, a lane's offset 32 bits wide.
   Unit<IO, EV> ra[WALK ? UA : 1], rb[UA], rc[UC];
+  const uint32_t a_row = (uint32_t)(m.a.ts * sizeof(IO)), b_row = (uint32_t)(m.b.ts * sizeof(IO)),
+                 c_row = (uint32_t)(m.c.ts * sizeof(IO));
   auto fetch = [&](int64_t pos, int n) {
+    const int64_t first = m.rev ? t1 - pos - n : t0 + pos;
+    const char *qa = (const char*)(pa + first * m.a.ts), *qb = (const char*)(pb + first * m.b.ts),
+               *qc = (const char*)(pc + first * m.c.ts);
 #pragma unroll
     for (int u = 0; u < UA; ++u) {
-      const int id = u * 256 + tid, i = id / (DA / EV), d = id % (DA / EV) * EV;
-      const int64_t t = m.rev ? t1 - 1 - pos - i : t0 + pos + i;
-      const int have = i < n ? m.da - d : 0;
-      if constexpr (WALK) ra[u] = load_unit<IO, EV>(pa + t * m.a.ts + d, have);
-      rb[u] = load_unit<IO, EV>(pb + t * m.b.ts + d, have);
+      const int id = u * NT + tid, i = min(id / (DA / EV), n - 1), d = id % (DA / EV) * EV;
+      const uint32_t r = (uint32_t)(m.rev ? n - 1 - i : i);
+      if constexpr (WALK) ra[u] = load_unit<F, IO, EV>(qa, r * a_row, d, da);
+      rb[u] = load_unit<F, IO, EV>(qb, r * b_row, d, da);
     }
 #pragma unroll
     for (int u = 0; u < UC; ++u) {
-      const int id = u * 256 + tid, i = id / (DC / EV), d = id % (DC / EV) * EV;
-      const int64_t t = m.rev ? t1 - 1 - pos - i : t0 + pos + i;
-      rc[u] = load_unit<IO, EV>(pc + t * m.c.ts + d, i < n ? m.dc - d : 0);
+      const int id = u * NT + tid, i = min(id / (DC / EV), n - 1), d = id % (DC / EV) * EV;
+      const uint32_t r = (uint32_t)(m.rev ? n - 1 - i : i);
+      rc[u] = load_unit<F, IO, EV>(qc, r * c_row, d, dc);
     }
   };
 
-  float wc[CB][4];      // weights of a token's part in the state
   float ln = 1.0f;
-  int wn = -1;          // the chunk size they are of
+  int wn = -1;             // the chunk size that ln and swt are of
   int64_t single = pos0;   // tokens before this position go one by one
   int64_t pos = pos0;
   if (pos < pos1) fetch(pos, (int)min((int64_t)C, pos1 - pos));
   while (pos < pos1) {
     int n = pos < single ? 1 : (int)min((int64_t)C, pos1 - pos);
+    auto clear_tail = [&] {
+      if (F == FULL && n == C) return;
+#pragma unroll
+      for (int u = 0; u < UA; ++u) {
+        const int id = u * NT + tid, i = id / (DA / EV), d = id % (DA / EV) * EV;
+        if constexpr (WALK) clear<F>(ra[u], i < n, d, da);
+        clear<F>(rb[u], i < n, d, da);
+      }
+#pragma unroll
+      for (int u = 0; u < UC; ++u) {
+        const int id = u * NT + tid, i = id / (DC / EV), d = id % (DC / EV) * EV;
+        clear<F>(rc[u], i < n, d, dc);
+      }
+    };
+    clear_tail();
     // A value that is not finite would reach the tokens before it in the chunk
     // through a zero product: such a chunk is walked token by token.
     bool bad = false;
     if (n > 1) {
 #pragma unroll
-      for (int u = 0; u < UC; ++u)
-#pragma unroll
-        for (int e = 0; e < EV; ++e) bad |= not_finite(rc[u].v[e]);
+      for (int u = 0; u < UC; ++u) bad |= not_finite(rc[u]);
     }
     if (__syncthreads_or(bad)) {   // (also: every wave is done with the last chunk's tiles)
       single = pos + n;
       n = 1;
       fetch(pos, n);
+      clear_tail();
     }
 #pragma unroll
     for (int u = 0; u < UA; ++u) {
-      const int id = u * 256 + tid, at = id / (DA / EV) * LA + id % (DA / EV) * EV;
-      if constexpr (WALK) stage<CT, IO, EV>(sa + at, ra[u]);
-      stage<CT, IO, EV>(sb + at, rb[u]);
+      const int id = u * NT + tid, i = id / (DA / EV), d = id % (DA / EV) * EV;
+      if constexpr (WALK) stage_rows<CT, IO, EV>(sa + i * LA, d, ra[u]);
+      stage<CT, IO, EV>(sb + i * LB + d, rb[u]);
     }
 #pragma unroll
     for (int u = 0; u < UC; ++u) {
-      const int id = u * 256 + tid;
+      const int id = u * NT + tid;
       stage<CT, IO, EV>(sc + id / (DC / EV) * LC + id % (DC / EV) * EV, rc[u]);
     }
-    __syncthreads();
-    const int64_t next = pos + n;
-    if (next < pos1) fetch(next, next < single ? 1 : (int)min((int64_t)C, pos1 - next));
     if (n != wn) {
       wn = n;
       ln = decay_pow(gam, (float)n);
-#pragma unroll
-      for (int b = 0; b < CB; ++b)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 16 * b + 4 * g + e;
-          wc[b][e] = j < n ? m.wscale * decay_pow(gam, (float)(n - m.off - j)) : 0.0f;
-        }
+      if (tid < C) swt[tid] = tid < n ? m.wscale * decay_pow(gam, (float)(n - m.off - tid)) : 0.0f;
     }
-    f32x4 o[WALK ? CB : 1][NB];
+    __syncthreads();
+    const int64_t next = pos + n;
+    f32x4 o[WALK ? CB : 1];
     if constexpr (WALK) {
       // inside products b_j . a_i, transposed: a lane holds four j of one i
 #pragma unroll
       for (int k = 0; k < MINE; ++k) {
-        int ib = 0, jb = wave + 4 * k;
-        while (jb > ib) jb -= ++ib;
-        if (wave + 4 * k < PAIRS) {
+        int ib = 0, jb = wave + NW * k;
+        while (jb > ib) jb -= ++ib;   // pair number -> (ib, jb), jb <= ib
+        if (wave + NW * k < PAIRS) {
           f32x4 acc = {};
-          const CT* rj = sb + (16 * jb + l16) * LA + 4 * g;
-          const CT* ri = sa + (16 * ib + l16) * LA + 4 * g;
+          const CT* rj = sb + (16 * jb + l16) * LB + 4 * g;
+          const CT* ri = sa + (16 * ib + l16) * LA;
 #pragma unroll
-          for (int kb = 0; kb < DKB; kb += 2)
-            acc = O::mma(O::row(rj + 16 * kb), O::row(rj + 16 * kb + 16), O::row(ri + 16 * kb), O::row(ri + 16 * kb + 16), acc);
-          f32x4 w;
+          for (int kb = 0; kb < DKB; kb += 2) {
+            quad a0, a1;
+            O::row2(ri, kb / 2, g, a0, a1);
+            acc = O::mma(O::row(rj + 16 * kb), O::row(rj + 16 * kb + 16), a0, a1, acc);
+          }
+          const float* dec = sdec + C - 1 - 16 * (ib - jb) - l16 + 4 * g;
+          const int ahead = ib == jb ? l16 - 4 * g : C;   // elements behind it are later tokens
+          f32x4 w = {dec[0], dec[1], dec[2], dec[3]};
+          w *= acc;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) w[r] = md[k][r] == 0.0f && (ib == jb && 4 * g + r > l16) ? 0.0f : acc[r] * md[k][r];
+          for (int r = 0; r < 4; ++r) w[r] = r > ahead ? 0.0f : w[r];
           quad pl[PP];
           split<CT, PP>(w, pl);
 #pragma unroll
-          for (int p = 0; p < PP; ++p) *(quad*)(sp + (p * C + 16 * ib + l16) * LP + 16 * jb + 4 * g) = pl[p];
+          for (int p = 0; p < PP; ++p) *(quad*)(sp + (p * C + 16 * ib + l16) * LP + O::at(16 * jb + 4 * g)) = pl[p];
         }
       }
       // the state's part of the output
 #pragma unroll
-      for (int ib = 0; ib < CB; ++ib)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) o[ib][nb] = f32x4{};
+      for (int ib = 0; ib < CB; ++ib) o[ib] = f32x4{};
       if (wave_on) {
 #pragma unroll
         for (int kb = 0; kb < DKB; kb += 2) {
-          quad s0[NB][SP], s1[NB][SP];
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            split<CT, SP>(st[kb][nb], s0[nb]);
-            split<CT, SP>(st[kb + 1][nb], s1[nb]);
-          }
+          quad s0[SP], s1[SP];
+          split<CT, SP>(st[kb], s0);
+          split<CT, SP>(st[kb + 1], s1);
+          quad a0[CB], a1[CB];
 #pragma unroll
           for (int ib = 0; ib < CB; ++ib) {
-            const CT* ri = sa + (16 * ib + l16) * LA + 16 * kb + 4 * g;
-            const quad a0 = O::row(ri), a1 = O::row(ri + 16);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int p = SP - 1; p >= 0; --p) o[ib][nb] = O::mma(s0[nb][p], s1[nb][p], a0, a1, o[ib][nb]);
+            O::row2(sa + (16 * ib + l16) * LA, kb / 2, g, a0[ib], a1[ib]);
           }
+#pragma unroll
+          for (int p = SP - 1; p >= 0; --p)
+#pragma unroll
+            for (int ib = 0; ib < CB; ++ib) o[ib] = O::mma(s0[p], s1[p], a0[ib], a1[ib], o[ib]);
         }
 #pragma unroll
-        for (int ib = 0; ib < CB; ++ib)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) o[ib][nb] *= iw[ib];
+        for (int ib = 0; ib < CB; ++ib) o[ib] *= siw[16 * ib + l16];
       }
       __syncthreads();
     }
+    // The next chunk's rows, in flight over this chunk's second half (earlier,
+    // their registers would not fit beside the first half's).  Behind the last
+    // chunk: its last row again, since under a condition the loads would wait
+    // for each other.
+    fetch(min(next, pos1 - 1), next < single ? 1 : (int)min((int64_t)C, max(pos1 - next, (int64_t)1)));
     if (wave_on) {
 #pragma unroll
-      for (int kb = 0; kb < DKB; ++kb)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) st[kb][nb] *= ln;
+      for (int kb = 0; kb < DKB; ++kb) st[kb] *= ln;
 #pragma unroll
       for (int b = 0; b < CB; b += 2) {
-        quad c0[NB], c1[NB], w0[NB][CP], w1[NB][CP];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          c0[nb] = O::col(sc + 16 * b * LC + wave * 16 * NB + 16 * nb, LC);
-          c1[nb] = O::col(sc + (16 * b + 16) * LC + wave * 16 * NB + 16 * nb, LC);
-          split<CT, CP>(O::wide(c0[nb]) * f32x4{wc[b][0], wc[b][1], wc[b][2], wc[b][3]}, w0[nb]);
-          split<CT, CP>(O::wide(c1[nb]) * f32x4{wc[b + 1][0], wc[b + 1][1], wc[b + 1][2], wc[b + 1][3]}, w1[nb]);
-        }
+        quad w0[CP], w1[CP];
+        const quad c0 = O::col(sc + 16 * b * LC + wave * 16, LC);
+        const quad c1 = O::col(sc + (16 * b + 16) * LC + wave * 16, LC);
+        split<CT, CP>(O::wide(c0) * *(const f32x4*)(swt + 16 * b + 4 * g), w0);
+        split<CT, CP>(O::wide(c1) * *(const f32x4*)(swt + 16 * b + 16 + 4 * g), w1);
         if constexpr (WALK) {
 #pragma unroll
-          for (int ib = b; ib < CB; ++ib) {
+          for (int p = PP - 1; p >= 0; --p)
 #pragma unroll
-            for (int p = PP - 1; p >= 0; --p) {
-              const CT* ri = sp + (p * C + 16 * ib + l16) * LP + 16 * b + 4 * g;
-              const quad p0 = O::row(ri), p1 = O::row(ri + 16);
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) o[ib][nb] = O::mma(c0[nb], c1[nb], p0, p1, o[ib][nb]);
+            for (int ib = b; ib < CB; ++ib) {
+              quad p0, p1;
+              O::row2(sp + (p * C + 16 * ib + l16) * LP, b / 2, g, p0, p1);
+              o[ib] = O::mma(c0, c1, p0, p1, o[ib]);
             }
-          }
         }
+        // (four blocks of rows side by side: no product waits for the one before it)
+        constexpr int KG = 2;
 #pragma unroll
-        for (int kb = 0; kb < DKB; ++kb) {
-          const quad b0 = O::col(sb + 16 * b * LA + 16 * kb, LA), b1 = O::col(sb + (16 * b + 16) * LA + 16 * kb, LA);
+        for (int k0 = 0; k0 < DKB; k0 += KG) {
+          quad b0[KG], b1[KG];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+          for (int k = 0; k < KG; ++k) {
+            b0[k] = O::col(sb + 16 * b * LB + 16 * (k0 + k), LB);
+            b1[k] = O::col(sb + (16 * b + 16) * LB + 16 * (k0 + k), LB);
+          }
 #pragma unroll
-            for (int p = CP - 1; p >= 0; --p) st[kb][nb] = O::mma(b0, b1, w0[nb][p], w1[nb][p], st[kb][nb]);
+          for (int p = CP - 1; p >= 0; --p)
+#pragma unroll
+            for (int k = 0; k < KG; ++k) st[k0 + k] = O::mma(b0[k], b1[k], w0[p], w1[p], st[k0 + k]);
         }
       }
       if constexpr (WALK) {
         // transposed outputs: a lane holds four columns of one token
+        const int oc = wave * 16 + 4 * g, have = dc - oc;
+        const int64_t base = (m.rev ? t1 - pos - n : t0 + pos) * m.o_ts + (int64_t)head * m.o_hs;
 #pragma unroll
         for (int ib = 0; ib < CB; ++ib) {
           const int i = 16 * ib + l16;
-          if (i >= n) continue;
-          const int64_t t = m.rev ? t1 - 1 - pos - i : t0 + pos + i;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const int col = wave * 16 * NB + 16 * nb + 4 * g, have = m.dc - col;
-            if (have <= 0) continue;
-            const int64_t at = t * m.o_ts + (int64_t)head * m.o_hs + col;
-            if (m.out_f32) {
-              float* q = (float*)m.out + at;
-              if (have >= 4) {
-                __builtin_memcpy(q, &o[ib][nb], 16);
-              } else {
-                for (int r = 0; r < have; ++r) q[r] = o[ib][nb][r];
-              }
+          if (i >= n || (F != FULL && have <= 0)) continue;
+          const uint32_t at = (uint32_t)(m.rev ? n - 1 - i : i) * (uint32_t)m.o_ts + oc;
+          if (m.out_f32) {
+            float* q = (float*)m.out + base + at;
+            if (F == FULL || have >= 4) {
+              __builtin_memcpy(q, &o[ib], 16);
             } else {
-              IO* q = (IO*)m.out + at;
-              IO w[4];
+              for (int r = 0; r < have; ++r) q[r] = o[ib][r];
+            }
+          } else {
+            IO* q = (IO*)m.out + base + at;
+            IO w[4];
+            if constexpr (std::is_same_v<IO, bf16>) {
+              const uint2 two = O::round(o[ib]);
+              __builtin_memcpy(w, &two, 8);
+            } else {
 #pragma unroll
-              for (int r = 0; r < 4; ++r) w[r] = from_f32<IO>(o[ib][nb][r]);
-              if (have >= 4) {
-                __builtin_memcpy(q, w, sizeof(w));
-              } else {
-                for (int r = 0; r < have; ++r) q[r] = w[r];
-              }
+              for (int r = 0; r < 4; ++r) w[r] = from_f32<IO>(o[ib][r]);
+            }
+            if (F == FULL || have >= 4) {
+              __builtin_memcpy(q, w, sizeof(w));
+            } else {
+              for (int r = 0; r < have; ++r) q[r] = w[r];
             }
           }
         }
@@ -440,12 +515,10 @@ __global__ __launch_bounds__(256, 2) void mix_walk(MixArgs m) {
 #pragma unroll
   for (int kb = 0; kb < DKB; ++kb)
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * kb + 4 * g + r, col = col0 + 16 * nb;
-        if (row < m.da && col < m.dc) to[(int64_t)row * m.st_r + (int64_t)col * m.st_c] = st[kb][nb][r];
-      }
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * kb + 4 * g + r;
+      if (F == FULL || (row < da && col < dc)) to[row * m.st_r + col * m.st_c] = st[kb][r];
+    }
 }
 
 // The states at the segments' starts from the segments' own states, in place:
@@ -573,17 +646,24 @@ __global__ __launch_bounds__(256) void mix_step(MixStepArgs m) {
   }
 }
 
+template <typename IO, typename CT, bool WALK, int DKB, int NW>
+void walk_fit(const MixArgs& a, dim3 grid, hipStream_t s) {
+  constexpr int EV = Ops<CT>::EV;
+  if (a.da == 16 * DKB && a.dc == 16 * NW) launch_kernel(mix_walk<IO, CT, DKB, NW, FULL, WALK>, grid, dim3(64 * NW), 0, s, a);
+  else if (a.da % EV == 0 && a.dc % EV == 0) launch_kernel(mix_walk<IO, CT, DKB, NW, UNITS, WALK>, grid, dim3(64 * NW), 0, s, a);
+  else launch_kernel(mix_walk<IO, CT, DKB, NW, ANY, WALK>, grid, dim3(64 * NW), 0, s, a);
+}
 template <typename IO, typename CT, bool WALK, int DKB>
-void walk_nb(const MixArgs& a, dim3 grid, hipStream_t s) {
-  if (a.dc <= 64) launch_kernel(mix_walk<IO, CT, DKB, 1, WALK>, grid, dim3(256), 0, s, a);
-  else launch_kernel(mix_walk<IO, CT, DKB, 2, WALK>, grid, dim3(256), 0, s, a);
+void walk_waves(const MixArgs& a, dim3 grid, hipStream_t s) {
+  if (a.dc <= 64) walk_fit<IO, CT, WALK, DKB, 4>(a, grid, s);
+  else walk_fit<IO, CT, WALK, DKB, 8>(a, grid, s);
 }
 template <typename IO, typename CT, bool WALK>
 void walk(const MixArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.heads, (unsigned)(WALK ? a.nsegs : a.nsegs - 1), (unsigned)a.seqs);
-  if (a.da <= 32) walk_nb<IO, CT, WALK, 2>(a, grid, s);
-  else if (a.da <= 64) walk_nb<IO, CT, WALK, 4>(a, grid, s);
-  else walk_nb<IO, CT, WALK, 8>(a, grid, s);
+  if (a.da <= 32 && a.dc <= 64) walk_fit<IO, CT, WALK, 2, 4>(a, grid, s);
+  else if (a.da <= 64) walk_waves<IO, CT, WALK, 4>(a, grid, s);
+  else walk_waves<IO, CT, WALK, 8>(a, grid, s);
 }
 template <bool WALK>
 void walk_type(const MixArgs& a, int dtype, hipStream_t s) {

@@ -204,14 +204,15 @@ __global__ __launch_bounds__(256) void orth_norm(OrthIo io, double* part) {
   const int rows = io.tall ? io.n : io.m, cols = io.tall ? io.m : io.n;
   const IO* x = (const IO*)io.g + (int64_t)blockIdx.y * io.g_batch;
   double s = 0.0;
-  const int across = (cols + 255) / 256;   // spans of 256 columns
+  const int across = (cols + 1023) / 1024;   // spans of 1024 columns, four loads in flight
   for (int64_t u = blockIdx.x; u < (int64_t)rows * across; u += ORTH_NORM_BLOCKS) {
     const int64_t r = u / across;
-    const int c = (int)(u % across) * 256 + threadIdx.x;
-    if (c < cols) {
-      const double v = to_f32(x[r * io.g_row + c]);
-      s += v * v;
-    }
+    const int c0 = (int)(u % across) * 1024 + threadIdx.x;
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = c0 + 256 * k < cols ? to_f32(x[r * io.g_row + c0 + 256 * k]) : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s += (double)v[k] * (double)v[k];
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
@@ -238,7 +239,9 @@ __global__ __launch_bounds__(256) void orth_split(OrthIo io, const double* part,
   const int p0 = blockIdx.x * 32, i0 = blockIdx.y * 32;
   const int64_t b = blockIdx.z;
   if (threadIdx.x < 64) {
-    double s = part[b * ORTH_NORM_BLOCKS + threadIdx.x];
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < ORTH_NORM_BLOCKS / 64; ++k) s += part[b * ORTH_NORM_BLOCKS + 64 * k + threadIdx.x];
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
     if (threadIdx.x == 0) s_mul = (float)((double)scale / (sqrt(s) + (double)io.eps));

@@ -110,6 +110,7 @@ struct MixStepArgs {
   int64_t o_ts, o_hs;
 };
 constexpr int MIX_MAX_DIM = 128;
+constexpr int64_t MIX_MAX_STRIDE = 1 << 23;   // elements from a token to the next: 64 rows within 2^31 bytes
 void launch_mix_walk(const MixArgs& a, int dtype, hipStream_t s);    // outputs (and final states)
 void launch_mix_states(const MixArgs& a, int dtype, hipStream_t s);  // each segment's own state into seg
 void launch_mix_scan(const MixScanArgs& a, hipStream_t s);           // seg: own states -> states at the starts
@@ -135,7 +136,7 @@ struct OrthPoly {
   float c[ORTH_MAX_STEPS][3];
 };
 constexpr int ORTH_TILE = 128;       // rows and columns of the operands are padded to it
-constexpr int ORTH_NORM_BLOCKS = 64; // partial sums of a matrix's norm
+constexpr int ORTH_NORM_BLOCKS = 512; // partial sums of a matrix's norm
 // Operands of the products: float16 planes (hi, lo) of scaled values in
 // K-blocked panels, one after the other for the matrices of the batch.
 struct OrthMat {

@@ -90,6 +90,9 @@ void check_call(const pc_linear_attention* d) {
 void check_heads(const pc_linear_attention* d, const pc_heads& t, const char* what) {
   need(t.data || d->num_tokens == 0, std::string("null ") + what);
   need(t.token_stride >= 0 && t.head_stride >= 0, std::string("negative stride of ") + what);
+  // a chunk's rows are addressed with 32-bit byte offsets
+  if (t.token_stride > MIX_MAX_STRIDE)
+    fail(PC_ERR_UNSUPPORTED, std::string("token stride of ") + what + " above " + std::to_string(MIX_MAX_STRIDE));
 }
 // an output's elements must be distinct
 void check_out(const pc_linear_attention* d, const pc_heads& t, int heads, int dim, const char* what) {
