@@ -30,25 +30,34 @@ struct Vec {
 };
 
 // 16 bytes from an address that only T's own alignment is known of (one
-// instruction: gfx950 loads and stores unaligned vectors).
+// instruction: gfx950 loads and stores unaligned vectors; through a 128-bit
+// value, since an array would be taken apart into elements).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <typename T>
 __device__ __forceinline__ Vec<T> load_vec(const T* p) {
-  Vec<T> r;
+  u32x4 r;
   __builtin_memcpy(&r, p, 16);
-  return r;
+  return __builtin_bit_cast(Vec<T>, r);
 }
 template <typename T>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T>& v) {
-  __builtin_memcpy(p, &v, 16);
+  const u32x4 r = __builtin_bit_cast(u32x4, v);
+  __builtin_memcpy(p, &r, 16);
 }
 
 template <typename T>
 __device__ __forceinline__ Vec<T> load_part(const T* p, int have) {   // elements behind `have` are 0
-  Vec<T> r;
-  if (have >= Vec<T>::N) return load_vec(p);
+  u32x4 r;
+  if (have >= Vec<T>::N) {
+    __builtin_memcpy(&r, p, 16);
+  } else {
+    Vec<T> t = {};
 #pragma unroll
-  for (int e = 0; e < Vec<T>::N; ++e) r.v[e] = e < have ? p[e] : T{};
-  return r;
+    for (int e = 0; e < Vec<T>::N; ++e)
+      if (e < have) t.v[e] = p[e];
+    r = __builtin_bit_cast(u32x4, t);
+  }
+  return __builtin_bit_cast(Vec<T>, r);
 }
 
 // Sum over the TPR threads of a row's group, the same value in every thread.
@@ -73,7 +82,7 @@ __device__ __forceinline__ float row_sum(float x, float* red, int& slot) {
 
 // Threads of a block: groups of TPR, one row each.
 template <int TPR>
-constexpr int block_of() { return TPR > 256 ? TPR : 256; }
+constexpr int block_of() { return TPR > 64 ? TPR : 256; }
 
 template <typename T, int TPR, int R>
 __global__ __launch_bounds__(block_of<TPR>()) void norm_fwd(NormArgs a) {
@@ -144,6 +153,32 @@ __global__ __launch_bounds__(block_of<TPR>()) void norm_fwd(NormArgs a) {
   }
 }
 
+// Two sums at once.
+template <int TPR>
+__device__ __forceinline__ void row_sums(float& x, float& y, float* red, int& slot) {
+#pragma unroll
+  for (int d = 1; d < (TPR < 64 ? TPR : 64); d <<= 1) {
+    x += __shfl_xor(x, d, 64);
+    y += __shfl_xor(y, d, 64);
+  }
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    float* r = red + slot * 2 * W;
+    if ((threadIdx.x & 63) == 0) {
+      r[threadIdx.x >> 6] = x;
+      r[W + (threadIdx.x >> 6)] = y;
+    }
+    __syncthreads();
+    x = y = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      x += r[w];
+      y += r[W + w];
+    }
+    slot ^= 1;
+  }
+}
+
 template <typename T, int TPR, int R>
 __global__ __launch_bounds__(block_of<TPR>()) void norm_bwd(NormArgs a) {
   constexpr int V = Vec<T>::N, BLK = block_of<TPR>(), G = BLK / TPR;
@@ -160,38 +195,48 @@ __global__ __launch_bounds__(block_of<TPR>()) void norm_bwd(NormArgs a) {
       w[i][e] = c < a.cols ? (a.weight ? a.weight[c] : 1.0f) : 0.0f;
       dw[i][e] = db[i][e] = 0.0f;
     }
-  for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < a.rows; r0 += (int64_t)gridDim.x * G) {
-    const int64_t row = r0 + group;
-    const bool on = row < a.rows;
-    const T* x = (const T*)a.x + (on ? row : 0) * a.x_stride;
-    const T* dy = (const T*)a.dy + (on ? row : 0) * a.dy_stride;
-    Vec<T> ux[R], ud[R];
+  Vec<T> ux[R], ud[R];
+  float mean, rstd;
+  // a row behind the last loads the last one's values: the loads need no condition
+  auto fetch = [&](int64_t r0) {
+    const int64_t row = min(r0 + group, a.rows - 1);
+    const T* x = (const T*)a.x + row * a.x_stride;
+    const T* dy = (const T*)a.dy + row * a.dy_stride;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int c = (i * TPR + lane) * V;
       ux[i] = ud[i] = Vec<T>{};
-      if (on && c < a.cols) {
+      if (c < a.cols) {
         ux[i] = load_part(x + c, a.cols - c);
         ud[i] = load_part(dy + c, a.cols - c);
       }
     }
-    const float mean = on ? a.mean[row] : 0.0f, rstd = on ? a.rstd[row] : 0.0f;
+    mean = a.mean[row];
+    rstd = a.rstd[row];
+  };
+  const int64_t step = (int64_t)gridDim.x * G;
+  fetch((int64_t)blockIdx.x * G);
+  for (int64_t r0 = (int64_t)blockIdx.x * G; r0 < a.rows; r0 += step) {
+    const int64_t row = r0 + group;
+    const bool on = row < a.rows;
+    const float rs = rstd;
     float n[R][V], g[R][V], s = 0.0f, t = 0.0f;
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const bool in = on && (i * TPR + lane) * V + e < a.cols;
-        const float d = to_f32(ud[i].v[e]);
-        n[i][e] = in ? (to_f32(ux[i].v[e]) - mean) * rstd : 0.0f;
+        const float d = on ? to_f32(ud[i].v[e]) : 0.0f;
+        n[i][e] = in ? (to_f32(ux[i].v[e]) - mean) * rs : 0.0f;
         g[i][e] = d * w[i][e];
         dw[i][e] += d * n[i][e];
         db[i][e] += d;
         s += g[i][e];
         t += g[i][e] * n[i][e];
       }
-    const float mg = row_sum<TPR>(s, red, slot) * inv;
-    const float mgn = row_sum<TPR>(t, red, slot) * inv;
+    fetch(r0 + step);   // the next row, in flight over the sums and the store
+    row_sums<TPR>(s, t, red, slot);
+    const float mg = s * inv, mgn = t * inv;
     if (!on) continue;
     T* dx = (T*)a.y + row * a.y_stride;
 #pragma unroll
@@ -200,7 +245,7 @@ __global__ __launch_bounds__(block_of<TPR>()) void norm_bwd(NormArgs a) {
       if (c >= a.cols) continue;
       Vec<T> o;
 #pragma unroll
-      for (int e = 0; e < V; ++e) o.v[e] = from_f32<T>(rstd * (g[i][e] - mg - n[i][e] * mgn));
+      for (int e = 0; e < V; ++e) o.v[e] = from_f32<T>(rs * (g[i][e] - mg - n[i][e] * mgn));
       if (a.cols - c >= V) {
         store_vec(dx + c, o);
       } else {
@@ -224,21 +269,23 @@ __global__ __launch_bounds__(block_of<TPR>()) void norm_bwd(NormArgs a) {
     }
 }
 
-// Sums the partial sums of the 2 cols columns: 16 columns a block, 16 threads
-// each (16 partial rows in flight), joined in a fixed order.
+// Sums the partial sums of the 2 cols columns: 32 columns a block, every eighth
+// partial row a thread (eight loads in flight), joined in a fixed order.
 __global__ __launch_bounds__(256) void norm_bwd_sum(NormArgs a) {
-  __shared__ float red[16][17];
-  const int col = threadIdx.x & 15, part = threadIdx.x >> 4;
-  const int c = blockIdx.x * 16 + col, n = 2 * a.cols;
+  __shared__ float red[8][33];
+  const int col = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + col, n = 2 * a.cols;
   float s = 0.0f;
-  if (c < n)
-    for (int p = part; p < a.parts; p += 16) s += a.part[(int64_t)p * n + c];
+  if (c < n) {
+#pragma unroll 8
+    for (int p = part; p < a.parts; p += 8) s += a.part[(int64_t)p * n + c];
+  }
   red[part][col] = s;
   __syncthreads();
   if (part == 0 && c < n) {
     s = 0.0f;
 #pragma unroll
-    for (int p = 0; p < 16; ++p) s += red[p][col];
+    for (int p = 0; p < 8; ++p) s += red[p][col];
     float* out = c < a.cols ? a.dweight : a.dbias;
     if (out) out[c < a.cols ? c : c - a.cols] = s;
   }
@@ -247,23 +294,25 @@ __global__ __launch_bounds__(256) void norm_bwd_sum(NormArgs a) {
 struct Shape {
   int tpr, r;
 };
-// Threads of a row and vectors of a thread: whole waves hold short rows'
-// several, at most 4 vectors a thread.
-Shape shape_of(int cols, int vec) {
+// Threads of a row and vectors of a thread.  Forward: a wave as far as four
+// vectors a thread go, since its sums need no barrier.  Backward: one vector a
+// thread, since it holds five values for each element.
+Shape shape_of(int cols, int vec, bool backward) {
   const int nv = (cols + vec - 1) / vec;
   for (int tpr : {8, 16, 32, 64})
     if (nv <= tpr) return {tpr, 1};
-  if (nv <= 128) return {64, 2};
-  if (nv <= 256) return {64, 4};
-  if (nv <= 512) return {256, 2};
-  if (nv <= 1024) return {256, 4};
-  if (nv <= 2048) return {1024, 2};
-  return {1024, 4};
+  if (!backward) {
+    if (nv <= 128) return {64, 2};
+    if (nv <= 256) return {64, 4};
+  }
+  for (int tpr : {128, 256, 512, 1024})
+    if (nv <= tpr) return {tpr, 1};
+  return nv <= 2048 ? Shape{1024, 2} : Shape{1024, 4};
 }
 
 template <typename T, typename F>
-void dispatch(int cols, F&& f) {
-  const Shape s = shape_of(cols, Vec<T>::N);
+void dispatch(int cols, bool backward, F&& f) {
+  const Shape s = shape_of(cols, Vec<T>::N, backward);
 #define PC_NORM_CASE(TPR, R)                                                \
   if (s.tpr == TPR && s.r == R) {                                           \
     f(std::integral_constant<int, TPR>{}, std::integral_constant<int, R>{}); \
@@ -275,8 +324,10 @@ void dispatch(int cols, F&& f) {
   PC_NORM_CASE(64, 1)
   PC_NORM_CASE(64, 2)
   PC_NORM_CASE(64, 4)
-  PC_NORM_CASE(256, 2)
-  PC_NORM_CASE(256, 4)
+  PC_NORM_CASE(128, 1)
+  PC_NORM_CASE(256, 1)
+  PC_NORM_CASE(512, 1)
+  PC_NORM_CASE(1024, 1)
   PC_NORM_CASE(1024, 2)
   PC_NORM_CASE(1024, 4)
 #undef PC_NORM_CASE
@@ -284,7 +335,7 @@ void dispatch(int cols, F&& f) {
 
 template <typename T>
 void fwd(const NormArgs& a, hipStream_t s) {
-  dispatch<T>(a.cols, [&](auto tpr, auto r) {
+  dispatch<T>(a.cols, false, [&](auto tpr, auto r) {
     constexpr int TPR = decltype(tpr)::value, BLK = block_of<TPR>(), G = BLK / TPR;
     const int64_t need = (a.rows + G - 1) / G;
     launch_kernel(norm_fwd<T, TPR, decltype(r)::value>, dim3((unsigned)std::min<int64_t>(need, 1 << 20)), dim3(BLK), 0, s, a);
@@ -293,7 +344,7 @@ void fwd(const NormArgs& a, hipStream_t s) {
 
 template <typename T>
 void bwd(const NormArgs& a, hipStream_t s) {
-  dispatch<T>(a.cols, [&](auto tpr, auto r) {
+  dispatch<T>(a.cols, true, [&](auto tpr, auto r) {
     constexpr int TPR = decltype(tpr)::value, BLK = block_of<TPR>(), G = BLK / TPR;
     NormArgs b = a;
     const int64_t need = (a.rows + G - 1) / G;
@@ -304,7 +355,7 @@ void bwd(const NormArgs& a, hipStream_t s) {
     }
     b.parts = (int)(grid * G);
     if (grid > 0) launch_kernel(norm_bwd<T, TPR, decltype(r)::value>, dim3((unsigned)grid), dim3(BLK), 0, s, b);
-    if (a.dweight || a.dbias) launch_kernel(norm_bwd_sum, dim3((unsigned)((2 * a.cols + 15) / 16)), dim3(256), 0, s, b);
+    if (a.dweight || a.dbias) launch_kernel(norm_bwd_sum, dim3((unsigned)((2 * a.cols + 31) / 32)), dim3(256), 0, s, b);
   });
 }
 
