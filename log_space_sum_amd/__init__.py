@@ -329,9 +329,15 @@ def pc_kernel_times(h: Handle) -> dict:
 # passes (torch tensors: device memory and streams only)
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t, dtype, numel=None, what="tensor"):
@@ -451,56 +457,86 @@ def workspace(h: Handle, batch: int, device="cuda", all_modes=False):
 # operators of the network in front of a conditional circuit (no handle)
 # ---------------------------------------------------------------------------
 
+# (These calls can be a few microseconds of device work, so their checks are
+# kept to a few attribute reads; what is wrong is found out when something is.)
+
+_DTYPES = None
+
+
 def _dtype(t, what):
-    torch = _torch()
-    code = {torch.float32: PC_DTYPE_F32, torch.bfloat16: PC_DTYPE_BF16, torch.float16: PC_DTYPE_F16}.get(t.dtype)
+    global _DTYPES
+    if _DTYPES is None:
+        torch = _torch()
+        _DTYPES = {torch.float32: PC_DTYPE_F32, torch.bfloat16: PC_DTYPE_BF16, torch.float16: PC_DTYPE_F16}
+    code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{what} must be float32, bfloat16 or float16, got {t.dtype}")
     return code
 
 
-def _operand(t, like, dtype, shape, what):
-    """The data pointer of a GPU tensor of this dtype and shape on like's
-    device whose last dimension has stride 1 (any other strides)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+def _device(t, what):
+    """The index of the GPU that the tensor lives on."""
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{what} must be a torch tensor")
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{what} must live on the GPU")
-    if t.device != like.device:
-        raise ValueError(f"{what} is on {t.device}, not on {like.device}")
+    return dev
+
+
+def _wrong(t, dev, dtype, shape, what):
+    if _device(t, what) != dev:
+        raise ValueError(f"{what} is on {t.device}, not on cuda:{dev}")
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _operand(t, dev, dtype, shape, what):
+    """The data pointer of a tensor of this device, dtype and shape whose last
+    dimension has stride 1 (any other strides)."""
+    try:
+        ok = t.get_device() == dev and t.dtype == dtype and t.shape == shape
+    except AttributeError:
+        ok = False
+    if not ok:
+        _wrong(t, dev, dtype, shape, what)
+    if t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError(f"the last dimension of {what} must have stride 1")
     return t.data_ptr()
 
 
-def _dense(t, like, dtype, shape, what):
+def _dense(t, dev, dtype, shape, what):
     """_operand of a contiguous tensor; None stays None."""
     if t is None:
         return None
-    p = _operand(t, like, dtype, shape, what)
+    p = _operand(t, dev, dtype, shape, what)
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return p
 
 
-def _ws_ptr(ws, like):
+def _ws_ptr(ws, dev):
     """(pointer, bytes) of a workspace (the library checks its size)."""
     if ws is None:
         return None, 0
-    torch = _torch()
-    return _dense(ws, like, torch.uint8, (ws.numel(),), "ws"), ws.numel()
+    n = ws.numel()
+    return _dense(ws, dev, _torch().uint8, (n,), "ws"), n
 
 
-def _stream_of(t, stream):
-    """The given stream, else the current one of the tensor's device."""
+def _stream_of(dev, stream):
+    """The given stream, else the current one of the device."""
     if stream is not None:
         return int(stream)
-    return _torch().cuda.current_stream(t.device).cuda_stream
+    return _raw_stream(dev)
+
+
+def _raw_stream(dev):
+    global _raw_stream
+    torch = _torch()     # the handle itself where torch hands it out, without an object around it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(dev)
 
 
 def _bytes(f, *args):
@@ -518,13 +554,14 @@ def _matrix(t, what):
 def pc_layer_norm_forward(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, stream=None):
     """y = layer norm of the rows of x [rows, cols] (rows may be strided); weight, bias: float32 [cols] or None;
     mean, rstd: float32 [rows], kept for the backward pass, or None."""
-    f32 = _torch().float32
-    rows, cols = _matrix(x, "x").shape
-    px, py = _operand(x, x, x.dtype, x.shape, "x"), _operand(y, x, x.dtype, x.shape, "y")
+    dev, f32 = _device(_matrix(x, "x"), "x"), _torch().float32
+    shape, dt = x.shape, x.dtype
+    rows, cols = shape
+    px, py = _operand(x, dev, dt, shape, "x"), _operand(y, dev, dt, shape, "y")
     _check(lib().pc_layer_norm_forward(
-        x.device.index, _dtype(x, "x"), rows, cols, px, x.stride(0), _dense(weight, x, f32, (cols,), "weight"),
-        _dense(bias, x, f32, (cols,), "bias"), eps, py, y.stride(0), _dense(mean, x, f32, (rows,), "mean"),
-        _dense(rstd, x, f32, (rows,), "rstd"), _stream_of(x, stream)))
+        dev, _dtype(x, "x"), rows, cols, px, x.stride(0), _dense(weight, dev, f32, (cols,), "weight"),
+        _dense(bias, dev, f32, (cols,), "bias"), eps, py, y.stride(0), _dense(mean, dev, f32, (rows,), "mean"),
+        _dense(rstd, dev, f32, (rows,), "rstd"), _stream_of(dev, stream)))
 
 
 def layer_norm_workspace(rows: int, cols: int, device="cuda"):
@@ -536,53 +573,58 @@ def layer_norm_workspace(rows: int, cols: int, device="cuda"):
 def pc_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, ws=None, stream=None):
     """dx, dweight and dbias (float32 [cols], or None; all overwritten) from dy, x and the forward's mean and rstd;
     ws: layer_norm_workspace(rows, cols), needed for dweight and dbias."""
-    f32 = _torch().float32
-    rows, cols = _matrix(x, "x").shape
-    px = _operand(x, x, x.dtype, x.shape, "x")
-    pdy, pdx = _operand(dy, x, x.dtype, x.shape, "dy"), _operand(dx, x, x.dtype, x.shape, "dx")
-    pws, nws = _ws_ptr(ws, x)
+    dev, f32 = _device(_matrix(x, "x"), "x"), _torch().float32
+    shape, dt = x.shape, x.dtype
+    rows, cols = shape
+    px = _operand(x, dev, dt, shape, "x")
+    pdy, pdx = _operand(dy, dev, dt, shape, "dy"), _operand(dx, dev, dt, shape, "dx")
+    pws, nws = _ws_ptr(ws, dev)
     _check(lib().pc_layer_norm_backward(
-        x.device.index, _dtype(x, "x"), rows, cols, pdy, dy.stride(0), px, x.stride(0),
-        _dense(weight, x, f32, (cols,), "weight"), _dense(mean, x, f32, (rows,), "mean"),
-        _dense(rstd, x, f32, (rows,), "rstd"), pdx, dx.stride(0), _dense(dweight, x, f32, (cols,), "dweight"),
-        _dense(dbias, x, f32, (cols,), "dbias"), pws, nws, _stream_of(x, stream)))
+        dev, _dtype(x, "x"), rows, cols, pdy, dy.stride(0), px, x.stride(0), _dense(weight, dev, f32, (cols,), "weight"),
+        _dense(mean, dev, f32, (rows,), "mean"), _dense(rstd, dev, f32, (rows,), "rstd"), pdx, dx.stride(0),
+        _dense(dweight, dev, f32, (cols,), "dweight"), _dense(dbias, dev, f32, (cols,), "dbias"), pws, nws,
+        _stream_of(dev, stream)))
 
 
-def _heads(t, like, shape, what):
-    return pc_heads(_operand(t, like, like.dtype, shape, what), t.stride(0), t.stride(1))
+def _heads(to, t, dev, dtype, shape, what):
+    to.data = _operand(t, dev, dtype, shape, what)
+    to.token_stride, to.head_stride, _ = t.stride()
 
 
 def _attention(q, k, v, log_decay, scale):
     """The descriptor of q [tokens, heads, dim_k], k [tokens, kv_heads, dim_k], v [tokens, kv_heads, dim_v]."""
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must have three dimensions (tokens, heads, dim)")
+    dev, dt = _device(q, "q"), q.dtype
     T, H, dk = q.shape
     K, dv = k.shape[1], v.shape[2]
-    d = pc_linear_attention(dtype=_dtype(q, "q"), heads=H, kv_heads=K, dim_k=dk, dim_v=dv, num_tokens=T,
-                            scale=float(dk ** -0.5 if scale is None else scale))
-    d.q, d.k, d.v = _heads(q, q, (T, H, dk), "q"), _heads(k, q, (T, K, dk), "k"), _heads(v, q, (T, K, dv), "v")
-    if log_decay is not None:
-        d.log_decay = _dense(log_decay, q, _torch().float32, (H,), "log_decay")
-    return d, (T, H, K, dk, dv)
+    d = pc_linear_attention(_dtype(q, "q"), H, K, dk, dv)
+    d.num_tokens = T
+    d.scale = dk ** -0.5 if scale is None else scale
+    _heads(d.q, q, dev, dt, (T, H, dk), "q")
+    _heads(d.k, k, dev, dt, (T, K, dk), "k")
+    _heads(d.v, v, dev, dt, (T, K, dv), "v")
+    d.log_decay = _dense(log_decay, dev, _torch().float32, (H,), "log_decay")
+    return d, dev, dt, (T, H, K, dk, dv)
 
 
-def _sequences(d, q, cu_seqlens, max_seqlen):
+def _sequences(d, dev, cu_seqlens, max_seqlen):
     if cu_seqlens is None:
         d.num_seqs = 1
     else:
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must have one dimension and at least one entry")
         d.num_seqs = cu_seqlens.numel() - 1
-        d.cu_seqlens = _dense(cu_seqlens, q, _torch().int32, cu_seqlens.shape, "cu_seqlens")
-    d.max_seqlen = q.shape[0] if max_seqlen is None else int(max_seqlen)
+        d.cu_seqlens = _dense(cu_seqlens, dev, _torch().int32, cu_seqlens.shape, "cu_seqlens")
+    d.max_seqlen = d.num_tokens if max_seqlen is None else int(max_seqlen)
     return d.num_seqs
 
 
 def linear_attention_workspace(q, k, v, cu_seqlens=None, max_seqlen=None, backward=False):
     """A workspace tensor for pc_linear_attention_forward, or with backward for pc_linear_attention_backward, on
     tensors of these shapes."""
-    d, _ = _attention(q, k, v, None, None)
-    _sequences(d, q, cu_seqlens, max_seqlen)
+    d, dev, _, _ = _attention(q, k, v, None, None)
+    _sequences(d, dev, cu_seqlens, max_seqlen)
     n = _bytes(lib().pc_linear_attention_workspace_bytes, C.byref(d), 1 if backward else 0)
     return _torch().empty(n, dtype=_torch().uint8, device=q.device)
 
@@ -594,13 +636,13 @@ def pc_linear_attention_forward(q, k, v, log_decay, o, cu_seqlens=None, max_seql
     the longest (None: the number of tokens); states: float32 [sequences, heads, dim_k, dim_v]; scale: None for
     dim_k ** -0.5; ws: linear_attention_workspace(...)."""
     f32 = _torch().float32
-    d, (T, H, K, dk, dv) = _attention(q, k, v, log_decay, scale)
-    n = _sequences(d, q, cu_seqlens, max_seqlen)
-    d.o = _heads(o, q, (T, H, dv), "o")
-    d.state_in = _dense(state_in, q, f32, (n, H, dk, dv), "state_in")
-    d.state_out = _dense(state_out, q, f32, (n, H, dk, dv), "state_out")
-    pws, nws = _ws_ptr(ws, q)
-    _check(lib().pc_linear_attention_forward(q.device.index, C.byref(d), pws, nws, _stream_of(q, stream)))
+    d, dev, dt, (T, H, K, dk, dv) = _attention(q, k, v, log_decay, scale)
+    n = _sequences(d, dev, cu_seqlens, max_seqlen)
+    _heads(d.o, o, dev, dt, (T, H, dv), "o")
+    d.state_in = _dense(state_in, dev, f32, (n, H, dk, dv), "state_in")
+    d.state_out = _dense(state_out, dev, f32, (n, H, dk, dv), "state_out")
+    pws, nws = _ws_ptr(ws, dev)
+    _check(lib().pc_linear_attention_forward(dev, d, pws, nws, _stream_of(dev, stream)))
 
 
 def pc_linear_attention_backward(do, q, k, v, log_decay, dq, dk, dv, cu_seqlens=None, max_seqlen=None, state_in=None,
@@ -608,17 +650,17 @@ def pc_linear_attention_backward(do, q, k, v, log_decay, dq, dk, dv, cu_seqlens=
     """dq, dk, dv (and dstate_in) from do (and dstate_out), with the forward call's other arguments;
     ws: linear_attention_workspace(..., backward=True)."""
     f32 = _torch().float32
-    d, (T, H, K, nk, nv) = _attention(q, k, v, log_decay, scale)
-    n = _sequences(d, q, cu_seqlens, max_seqlen)
-    d.d_o = _heads(do, q, (T, H, nv), "do")
-    d.d_q = _heads(dq, q, (T, H, nk), "dq")
-    d.d_k = _heads(dk, q, (T, K, nk), "dk")
-    d.d_v = _heads(dv, q, (T, K, nv), "dv")
-    d.state_in = _dense(state_in, q, f32, (n, H, nk, nv), "state_in")
-    d.dstate_out = _dense(dstate_out, q, f32, (n, H, nk, nv), "dstate_out")
-    d.dstate_in = _dense(dstate_in, q, f32, (n, H, nk, nv), "dstate_in")
-    pws, nws = _ws_ptr(ws, q)
-    _check(lib().pc_linear_attention_backward(q.device.index, C.byref(d), pws, nws, _stream_of(q, stream)))
+    d, dev, dt, (T, H, K, nk, nv) = _attention(q, k, v, log_decay, scale)
+    n = _sequences(d, dev, cu_seqlens, max_seqlen)
+    _heads(d.d_o, do, dev, dt, (T, H, nv), "do")
+    _heads(d.d_q, dq, dev, dt, (T, H, nk), "dq")
+    _heads(d.d_k, dk, dev, dt, (T, K, nk), "dk")
+    _heads(d.d_v, dv, dev, dt, (T, K, nv), "dv")
+    d.state_in = _dense(state_in, dev, f32, (n, H, nk, nv), "state_in")
+    d.dstate_out = _dense(dstate_out, dev, f32, (n, H, nk, nv), "dstate_out")
+    d.dstate_in = _dense(dstate_in, dev, f32, (n, H, nk, nv), "dstate_in")
+    pws, nws = _ws_ptr(ws, dev)
+    _check(lib().pc_linear_attention_backward(dev, d, pws, nws, _stream_of(dev, stream)))
 
 
 def pc_linear_attention_step(q, k, v, log_decay, state, o, slots=None, scale=None, stream=None):
@@ -626,14 +668,14 @@ def pc_linear_attention_step(q, k, v, log_decay, state, o, slots=None, scale=Non
     the GPU, None: state[b]) of state [slots, heads, dim_k, dim_v] (float32) in place and reads it.  A slot out of
     range marks a padding row; rows of the same slot are successive tokens, in the rows' order."""
     torch = _torch()
-    d, (T, H, K, dk, dv) = _attention(q, k, v, log_decay, scale)
-    d.o = _heads(o, q, (T, H, dv), "o")
+    d, dev, dt, (T, H, K, dk, dv) = _attention(q, k, v, log_decay, scale)
+    _heads(d.o, o, dev, dt, (T, H, dv), "o")
     if state.dim() != 4:
         raise ValueError("state must have four dimensions (slots, heads, dim_k, dim_v)")
-    d.state = _dense(state, q, torch.float32, (state.shape[0], H, dk, dv), "state")
     d.num_slots = state.shape[0]
-    d.slots = _dense(slots, q, torch.int32, (T,), "slots")
-    _check(lib().pc_linear_attention_step(q.device.index, C.byref(d), _stream_of(q, stream)))
+    d.state = _dense(state, dev, torch.float32, (d.num_slots, H, dk, dv), "state")
+    d.slots = _dense(slots, dev, torch.int32, (T,), "slots")
+    _check(lib().pc_linear_attention_step(dev, d, _stream_of(dev, stream)))
 
 
 def _matrices(t, what):
@@ -657,7 +699,8 @@ def pc_orthogonalize(g, out, steps=5, coefficients=(3.4445, -4.7750, 2.0315), ep
     g / (|g| + eps), X <- a X + (b A + c A^2) X with A = X X^T; coefficients: (a, b, c), or one such triple for each
     step; out may be g.  ws: orthogonalize_workspace(g)."""
     b, r, c, gb, gr = _matrices(g, "g")
-    pg, po = _operand(g, g, g.dtype, g.shape, "g"), _operand(out, g, g.dtype, g.shape, "out")
+    dev = _device(g, "g")
+    pg, po = _operand(g, dev, g.dtype, g.shape, "g"), _operand(out, dev, g.dtype, g.shape, "out")
     _, _, _, ob, orow = _matrices(out, "out")
     steps = int(steps)
     each = list(coefficients)
@@ -666,9 +709,9 @@ def pc_orthogonalize(g, out, steps=5, coefficients=(3.4445, -4.7750, 2.0315), ep
     if len(each) != steps or any(len(x) != 3 for x in each):
         raise ValueError("coefficients must be (a, b, c) or one such triple for each step")
     flat = (C.c_float * max(1, 3 * steps))(*[float(v) for x in each for v in x])
-    pws, nws = _ws_ptr(ws, g)
-    _check(lib().pc_orthogonalize(g.device.index, _dtype(g, "g"), b, r, c, pg, gb, gr, po, ob, orow, steps, flat,
-                                  float(eps), pws, nws, _stream_of(g, stream)))
+    pws, nws = _ws_ptr(ws, dev)
+    _check(lib().pc_orthogonalize(dev, _dtype(g, "g"), b, r, c, pg, gb, gr, po, ob, orow, steps, flat, eps, pws, nws,
+                                  _stream_of(dev, stream)))
 
 
 class StepGraph:

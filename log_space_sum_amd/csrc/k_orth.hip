@@ -48,7 +48,7 @@ __device__ __forceinline__ int64_t at_x(const OrthIo& io, int64_t row_stride, in
 template <int MB, int LD, int W, typename F>
 __device__ __forceinline__ void small_product(const double* A, const double* B, F&& store) {
   constexpr int T = MB * (MB + 1) / 2, MINE = (T + W - 1) / W;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   f64x4 acc[MINE];
 #pragma unroll
   for (int k = 0; k < MINE; ++k) {
@@ -74,12 +74,70 @@ __device__ __forceinline__ void small_product(const double* A, const double* B, 
   __syncthreads();
 }
 
+// The same of one block of 16: a lane's four results, rows g + 4 r of column
+// l16, are by the symmetry also its operand's four values, columns 4 q + g of
+// row l16.  No matrix leaves its registers.  (Two sums: a float64 matrix
+// instruction waits long for the one before it.)
+__device__ __forceinline__ f64x4 product16(f64x4 a, f64x4 b) {
+  f64x4 c = {0.0, 0.0, 0.0, 0.0}, d = c;
+  c = __builtin_amdgcn_mfma_f64_16x16x4f64(a[0], b[0], c, 0, 0, 0);
+  d = __builtin_amdgcn_mfma_f64_16x16x4f64(a[1], b[1], d, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f64_16x16x4f64(a[2], b[2], c, 0, 0, 0);
+  d = __builtin_amdgcn_mfma_f64_16x16x4f64(a[3], b[3], d, 0, 0, 0);
+  return c + d;
+}
+
+// Four consecutive p of row i (zeros behind m and n; the loads need no
+// condition), p0 + 4 g ... for lane group g.
+template <typename IO>
+__device__ __forceinline__ f32x4 load_p(const IO* x, const OrthIo& io, int i, int p) {
+  const bool row = i < io.m;
+  const int64_t ii = row ? i : 0;
+  f32x4 v;
+  if (!io.tall && p + 4 <= io.n) {
+    IO u[4];
+    __builtin_memcpy(u, x + ii * io.g_row + p, sizeof(u));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = row ? to_f32(u[e]) : 0.0f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float t = to_f32(x[at_x<IO>(io, io.g_row, ii, min(p + e, io.n - 1))]);
+      v[e] = row && p + e < io.n ? t : 0.0f;
+    }
+  }
+  return v;
+}
+// Four consecutive i of column p.
+template <typename IO>
+__device__ __forceinline__ f32x4 load_i(const IO* x, const OrthIo& io, int i, int p) {
+  const int64_t pp = min(p, io.n - 1);
+  f32x4 v;
+  if (io.tall && i + 4 <= io.m) {
+    IO u[4];
+    __builtin_memcpy(u, x + pp * io.g_row + i, sizeof(u));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = p < io.n ? to_f32(u[e]) : 0.0f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float t = to_f32(x[at_x<IO>(io, io.g_row, min(i + e, io.m - 1), pp)]);
+      v[e] = i + e < io.m && p < io.n ? t : 0.0f;
+    }
+  }
+  return v;
+}
+
 template <typename IO, int MB, int NT>
 __global__ __launch_bounds__(NT) void orth_small(OrthIo io, OrthPoly poly) {
   constexpr int D = 16 * MB, LD = D + 2, W = NT / 64, T = MB * (MB + 1) / 2;
-  __shared__ double sA[D * LD], sM[D * LD], sQ[D * LD], sT[D * LD];
+  // the waves' parts of the Gram matrix, then the matrices of the steps
+  constexpr int PARTS = W < 4 ? W : (T * W * 256 > 4 * D * LD ? 4 : W);
+  constexpr int POOL = PARTS * T * 256 > 4 * D * LD ? PARTS * T * 256 : 4 * D * LD;
+  __shared__ double pool[POOL];
   __shared__ double s_inv;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  double *sA = pool, *sM = pool + D * LD, *sQ = pool + 2 * D * LD, *sT = pool + 3 * D * LD;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const IO* x = (const IO*)io.g + (int64_t)blockIdx.x * io.g_batch;
   const int m = io.m, n = io.n;
 
@@ -88,16 +146,9 @@ __global__ __launch_bounds__(NT) void orth_small(OrthIo io, OrthPoly poly) {
 #pragma unroll
   for (int t = 0; t < T; ++t) acc[t] = f64x4{0.0, 0.0, 0.0, 0.0};
   for (int p0 = wave * 16; p0 < n; p0 += W * 16) {
-    float v[MB][4];
+    f32x4 v[MB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      const int i = 16 * b + l16;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int p = p0 + 4 * g + e;
-        v[b][e] = i < m && p < n ? to_f32(x[at_x<IO>(io, io.g_row, i, p)]) : 0.0f;
-      }
-    }
+    for (int b = 0; b < MB; ++b) v[b] = load_p<IO>(x, io, 16 * b + l16, p0 + 4 * g);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       int t = 0;
@@ -108,86 +159,137 @@ __global__ __launch_bounds__(NT) void orth_small(OrthIo io, OrthPoly poly) {
           acc[t] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)v[ib][e], (double)v[jb][e], acc[t], 0, 0, 0);
     }
   }
-  for (int e = tid; e < D * LD; e += NT) sA[e] = 0.0;
-  for (int w = 0; w < W; ++w) {   // the waves' parts in their order
+  // the waves' parts, added in a fixed order
+  for (int round = 0; round < W; round += PARTS) {
+    if (wave >= round && wave < round + PARTS) {
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          double* s = pool + ((wave - round) * T + t) * 256 + r * 64 + lane;
+          *s = round ? *s + acc[t][r] : acc[t][r];
+        }
+    }
     __syncthreads();
-    if (w != wave) continue;
-    int t = 0;
-#pragma unroll
-    for (int jb = 0; jb < MB; ++jb)
-#pragma unroll
-      for (int ib = 0; ib <= jb; ++ib, ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sA[(16 * ib + g + 4 * r) * LD + 16 * jb + l16] += acc[t][r];
   }
-  __syncthreads();
-  if (tid == 0) {
-    double tr = 0.0;
-    for (int i = 0; i < m; ++i) tr += sA[i * LD + i];
-    s_inv = 1.0 / (sqrt(tr) + (double)io.eps);
+  double own[(T * 256 + NT - 1) / NT];
+#pragma unroll
+  for (int k = 0; k < (T * 256 + NT - 1) / NT; ++k) {
+    const int e = k * NT + tid;
+    own[k] = 0.0;
+    if (e < T * 256)
+#pragma unroll
+      for (int w = 0; w < PARTS; ++w) own[k] += pool[w * T * 256 + e];
   }
-  __syncthreads();
-  const double inv = s_inv;
-  for (int e = tid; e < D * D; e += NT) {
-    const int i = e / D, j = e % D;
-    const double v = (i <= j ? sA[i * LD + j] : sA[j * LD + i]) * inv * inv;
-    sT[i * LD + j] = v;
-    sQ[i * LD + j] = i == j ? 1.0 : 0.0;
-  }
-  __syncthreads();
-  for (int e = tid; e < D * D; e += NT) sA[e / D * LD + e % D] = sT[e / D * LD + e % D];
   __syncthreads();
 
-  for (int s = 0; s < poly.steps; ++s) {
-    const double a = poly.c[s][0], b = poly.c[s][1], c = poly.c[s][2];
-    small_product<MB, LD, W>(sA, sA, [&](int i, int j, double v) {
-      sM[i * LD + j] = sM[j * LD + i] = (i == j ? a : 0.0) + b * sA[i * LD + j] + c * v;
-    });
-    if (s == 0) {
-      for (int e = tid; e < D * D; e += NT) sQ[e / D * LD + e % D] = sM[e / D * LD + e % D];
-      __syncthreads();
-    } else {
-      small_product<MB, LD, W>(sQ, sM, [&](int i, int j, double v) { sQ[i * LD + j] = sQ[j * LD + i] = v; });
+  float q[MB][MB][4];   // [block of i][block of k][e]: Q[16 ib + l16][16 kb + 4 g + e] / |G|
+  if constexpr (MB == 1) {
+    // one wave takes all steps in its registers
+#pragma unroll
+    for (int k = 0; k < (256 + NT - 1) / NT; ++k)
+      if (k * NT + tid < 256) pool[k * NT + tid] = own[k];
+    __syncthreads();
+    if (wave == 0) {
+      f64x4 A, Q = {0.0, 0.0, 0.0, 0.0};
+      double tr = 0.0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        A[r] = pool[r * 64 + lane];
+        if (g + 4 * r == l16) tr += A[r];
+      }
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) tr += __shfl_xor(tr, d, 64);
+      const double inv = 1.0 / (sqrt(tr) + (double)io.eps);
+      A *= inv * inv;
+      for (int s = 0; s < poly.steps; ++s) {
+        const double a = poly.c[s][0], b = poly.c[s][1], c = poly.c[s][2];
+        f64x4 M = b * A + c * product16(A, A);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) M[r] += g + 4 * r == l16 ? a : 0.0;
+        Q = s ? product16(Q, M) : M;
+        if (s + 1 < poly.steps) A = product16(product16(A, M), M);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) pool[256 + l16 * LD + g + 4 * r] = Q[r] * inv;
     }
-    if (s + 1 < poly.steps) {
-      small_product<MB, LD, W>(sA, sM, [&](int i, int j, double v) { sT[i * LD + j] = sT[j * LD + i] = v; });
-      small_product<MB, LD, W>(sT, sM, [&](int i, int j, double v) { sA[i * LD + j] = sA[j * LD + i] = v; });
+    // columns g + 4 r of row l16 -> columns 4 g + e
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[0][0][e] = (float)pool[256 + l16 * LD + 4 * g + e];
+  } else {
+    for (int e = tid; e < D * LD; e += NT) sA[e] = 0.0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < (T * 256 + NT - 1) / NT; ++k) {
+      const int e = k * NT + tid;
+      if (e >= T * 256) continue;
+      int jb = 0, ib = e >> 8;
+      while (ib > jb) ib -= ++jb;
+      const int i = 16 * ib + ((e & 63) >> 4) + 4 * ((e >> 6) & 3), j = 16 * jb + (e & 15);
+      if (i <= j) sA[i * LD + j] = sA[j * LD + i] = own[k];
     }
+    __syncthreads();
+    if (wave == 0) {
+      double tr = 0.0;
+      for (int i = lane; i < m; i += 64) tr += sA[i * LD + i];
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) tr += __shfl_xor(tr, d, 64);
+      if (lane == 0) s_inv = 1.0 / (sqrt(tr) + (double)io.eps);
+    }
+    __syncthreads();
+    const double inv = s_inv;
+    for (int e = tid; e < D * D; e += NT) sA[e / D * LD + e % D] *= inv * inv;
+    __syncthreads();
+    for (int s = 0; s < poly.steps; ++s) {
+      const double a = poly.c[s][0], b = poly.c[s][1], c = poly.c[s][2];
+      small_product<MB, LD, W>(sA, sA, [&](int i, int j, double v) {
+        const double u = (i == j ? a : 0.0) + b * sA[i * LD + j] + c * v;
+        sM[i * LD + j] = sM[j * LD + i] = u;
+        if (s == 0) sQ[i * LD + j] = sQ[j * LD + i] = u;
+      });
+      if (s > 0) small_product<MB, LD, W>(sQ, sM, [&](int i, int j, double v) { sQ[i * LD + j] = sQ[j * LD + i] = v; });
+      if (s + 1 < poly.steps) {
+        small_product<MB, LD, W>(sA, sM, [&](int i, int j, double v) { sT[i * LD + j] = sT[j * LD + i] = v; });
+        small_product<MB, LD, W>(sT, sM, [&](int i, int j, double v) { sA[i * LD + j] = sA[j * LD + i] = v; });
+      }
+    }
+#pragma unroll
+    for (int ib = 0; ib < MB; ++ib)
+#pragma unroll
+      for (int kb = 0; kb < MB; ++kb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[ib][kb][e] = (float)(sQ[(16 * ib + l16) * LD + 16 * kb + 4 * g + e] * inv);
   }
 
   // out = (Q / |G|) G
-  float q[MB][MB][4];   // [block of i][block of k][e]: Q[16 ib + l16][16 kb + 4 g + e]
-#pragma unroll
-  for (int ib = 0; ib < MB; ++ib)
-#pragma unroll
-    for (int kb = 0; kb < MB; ++kb)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) q[ib][kb][e] = (float)(sQ[(16 * ib + l16) * LD + 16 * kb + 4 * g + e] * inv);
   IO* y = (IO*)io.out + (int64_t)blockIdx.x * io.o_batch;
+#pragma unroll 2
   for (int p0 = wave * 16; p0 < n; p0 += W * 16) {
     const int p = p0 + l16;
-    float v[MB][4];
+    f32x4 v[MB];
 #pragma unroll
-    for (int kb = 0; kb < MB; ++kb)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int k = 16 * kb + 4 * g + e;
-        v[kb][e] = k < m && p < n ? to_f32(x[at_x<IO>(io, io.g_row, k, p)]) : 0.0f;
-      }
+    for (int kb = 0; kb < MB; ++kb) v[kb] = load_i<IO>(x, io, 16 * kb + 4 * g, p);
 #pragma unroll
     for (int ib = 0; ib < MB; ++ib) {
       f32x4 o = {};
 #pragma unroll
       for (int kb = 0; kb < MB; ++kb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o = io.tall ? __builtin_amdgcn_mfma_f32_16x16x4f32(v[kb][e], q[ib][kb][e], o, 0, 0, 0)
-                      : __builtin_amdgcn_mfma_f32_16x16x4f32(q[ib][kb][e], v[kb][e], o, 0, 0, 0);
+        for (int e = 0; e < 4; ++e) o = __builtin_amdgcn_mfma_f32_16x16x4f32(q[ib][kb][e], v[kb][e], o, 0, 0, 0);
+      // a lane holds rows i = 4 g + r of column p
+      const int i = 16 * ib + 4 * g;
+      if (p < n) {
+        if (io.tall && i + 4 <= m) {
+          IO u[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = io.tall ? 16 * ib + l16 : 16 * ib + 4 * g + r;
-        const int pp = io.tall ? p0 + 4 * g + r : p;
-        if (i < m && pp < n) y[at_x<IO>(io, io.o_row, i, pp)] = from_f32<IO>(o[r]);
+          for (int r = 0; r < 4; ++r) u[r] = from_f32<IO>(o[r]);
+          __builtin_memcpy(y + (int64_t)p * io.o_row + i, u, sizeof(u));
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (i + r < m) y[at_x<IO>(io, io.o_row, i + r, p)] = from_f32<IO>(o[r]);
+        }
       }
     }
   }
@@ -204,15 +306,22 @@ __global__ __launch_bounds__(256) void orth_norm(OrthIo io, double* part) {
   const int rows = io.tall ? io.n : io.m, cols = io.tall ? io.m : io.n;
   const IO* x = (const IO*)io.g + (int64_t)blockIdx.y * io.g_batch;
   double s = 0.0;
-  const int across = (cols + 1023) / 1024;   // spans of 1024 columns, four loads in flight
+  const int across = (cols + 2047) / 2048;   // spans of 2048 columns, eight of them a thread
   for (int64_t u = blockIdx.x; u < (int64_t)rows * across; u += ORTH_NORM_BLOCKS) {
-    const int64_t r = u / across;
-    const int c0 = (int)(u % across) * 1024 + threadIdx.x;
-    float v[4];
+    const IO* p = x + u / across * io.g_row;
+    const int c = (int)(u % across) * 2048 + threadIdx.x * 8;
+    float v[8];
+    if (c + 8 <= cols) {
+      IO w[8];
+      __builtin_memcpy(w, p + c, sizeof(w));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = c0 + 256 * k < cols ? to_f32(x[r * io.g_row + c0 + 256 * k]) : 0.0f;
+      for (int k = 0; k < 8; ++k) v[k] = to_f32(w[k]);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) s += (double)v[k] * (double)v[k];
+      for (int k = 0; k < 8; ++k) v[k] = c + k < cols ? to_f32(p[c + k]) : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += (double)v[k] * (double)v[k];
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
@@ -272,16 +381,19 @@ __global__ __launch_bounds__(256) void orth_split(OrthIo io, const double* part,
   }
 }
 
-// C = A B^T on 128 x 128 tiles, four waves of 64 x 64, K in slices of 32
-// through a two-stage LDS ring.  PL planes of each operand: 1 one product, 2
+// C = A B^T on TILE x TILE tiles, four waves of half of that, K in slices of 32
+// through an LDS ring of ST stages: two where two workgroups a compute unit
+// cover each other's waits, more where there are too few workgroups for that.
+// TILE 128, or 64 where tiles of 128 would leave compute units without one.  PL planes of each operand: 1 one product, 2
 // three.  Slot s of a row's four 16-byte chunks holds chunk s ^ ((row >> 2) & 3),
 // so the 16 rows a wave reads at a time lie in different banks.
-template <int EPI, int PL, typename IO>
+template <int EPI, int PL, int TILE, int ST, typename IO>
 __global__ __launch_bounds__(256, 2) void orth_gemm(OrthGemmArgs a) {
-  constexpr int TILE = ORTH_TILE, SLICE = TILE * 64;   // bytes of an operand plane's slice
+  constexpr int SLICE = TILE * 64;   // bytes of an operand plane's slice
+  constexpr int WT = TILE / 2, NF = WT / 32, LR = TILE / 4;   // a wave's rows, its 32-row blocks, the rows it loads
   constexpr int STAGE = 2 * PL * SLICE;
   constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
-  __shared__ __align__(16) char lds[2 * STAGE];
+  __shared__ __align__(16) char lds[ST * STAGE];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int64_t z = blockIdx.z;
   int ti, tj;
@@ -299,7 +411,7 @@ __global__ __launch_bounds__(256, 2) void orth_gemm(OrthGemmArgs a) {
   const uint16_t* pa = a.a.p + z * a.a.batch;
   const uint16_t* pb = a.b.p + z * a.b.batch;
 
-  // 1 KB (16 rows of 64 bytes) an instruction: wave w loads rows 32 w .. 32 w + 31
+  // 1 KB (16 rows of 64 bytes) an instruction: wave w loads rows LR w .. LR w + LR - 1
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const uint32_t src = (uint32_t)((lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16));
   auto issue = [&](int stage, int kb) {
@@ -311,36 +423,42 @@ __global__ __launch_bounds__(256, 2) void orth_gemm(OrthGemmArgs a) {
 #pragma unroll
       for (int p = 0; p < PL; ++p)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint16_t* from = base + p * plane + ((int64_t)kb * R + r0 + 32 * wave + 16 * h) * 32;
-          lds_load16(from, src, lds0 + stage * STAGE + (op * PL + p) * SLICE + (32 * wave + 16 * h) * 64);
+        for (int h = 0; h < LR / 16; ++h) {
+          const uint16_t* from = base + p * plane + ((int64_t)kb * R + r0 + LR * wave + 16 * h) * 32;
+          lds_load16(from, src, lds0 + stage * STAGE + (op * PL + p) * SLICE + (LR * wave + 16 * h) * 64);
         }
     }
   };
-  f32x16 acc[2][2] = {};
-  const int wr = (wave >> 1) * 64, wc = (wave & 1) * 64, l32 = lane & 31, hf = lane >> 5;
+  f32x16 acc[NF][NF] = {};
+  const int wr = (wave >> 1) * WT, wc = (wave & 1) * WT, l32 = lane & 31, hf = lane >> 5;
   const int nk = a.K / 32;
-  issue(0, 0);
+  // A slice's loads of a wave; slices behind the last are loaded again from the
+  // last, so that the count of loads in flight is the same in every round.
+  constexpr int LOADS = 2 * PL * (LR / 16);
+  for (int s = 0; s < ST - 1; ++s) issue(s, min(s, nk - 1));
+  int cur = 0, fill = ST - 1;
   for (int kb = 0; kb < nk; ++kb) {
-    __builtin_amdgcn_s_waitcnt(WaitVmLgkm<0>::imm);
-    ring_barrier();   // the slice is there, and every wave is done with the other stage
-    if (kb + 1 < nk) issue((kb + 1) & 1, kb + 1);
-    const char* st = lds + (kb & 1) * STAGE;
+    __builtin_amdgcn_s_waitcnt(WaitVmLgkm<LOADS * (ST - 2)>::imm);
+    ring_barrier();   // slice kb is there, and every wave is done with the stage that is filled next
+    issue(fill, min(kb + ST - 1, nk - 1));
+    const char* st = lds + cur * STAGE;
+    cur = cur + 1 == ST ? 0 : cur + 1;
+    fill = fill + 1 == ST ? 0 : fill + 1;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      f16x8 fa[PL][2], fb[PL][2];
+      f16x8 fa[PL][NF], fb[PL][NF];
 #pragma unroll
       for (int p = 0; p < PL; ++p)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < NF; ++t) {
           const int ra = wr + 32 * t + l32, rb = wc + 32 * t + l32, ch = 2 * ks + hf;
           fa[p][t] = *(const f16x8*)(st + p * SLICE + ra * 64 + ((ch ^ ((ra >> 2) & 3)) * 16));
           fb[p][t] = *(const f16x8*)(st + (PL + p) * SLICE + rb * 64 + ((ch ^ ((rb >> 2) & 3)) * 16));
         }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < NF; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < NF; ++j) {
           if constexpr (PL == 2) {
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[1][i], fb[0][j], acc[i][j], 0, 0, 0);
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[1][j], acc[i][j], 0, 0, 0);
@@ -350,11 +468,13 @@ __global__ __launch_bounds__(256, 2) void orth_gemm(OrthGemmArgs a) {
     }
   }
 
+  __builtin_amdgcn_s_waitcnt(WaitVmLgkm<0>::imm);   // no load may reach LDS after the workgroup's end
+
   // a lane holds rows 8 (r / 4) + 4 hf + r % 4 of column l32 of every 32 x 32 tile
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < NF; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < NF; ++j) {
       const int col = col0 + wc + 32 * j + l32;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -403,13 +523,21 @@ void small(const OrthIo& io, const OrthPoly& p, hipStream_t s) {
   else launch_kernel(orth_small<IO, 4, 512>, grid, dim3(512), 0, s, io, p);
 }
 
+template <int EPI, int PL, typename IO>
+void gemm_tiles(const OrthGemmArgs& a, hipStream_t s) {
+  const bool sym = EPI == ORTH_GRAM || EPI == ORTH_POLY;
+  auto grid = [&](int tile) {
+    const unsigned mt = (unsigned)(a.M / tile), nt = (unsigned)(a.N / tile);
+    return dim3(sym ? mt * (mt + 1) / 2 : mt * nt, 1, (unsigned)a.io.batch);
+  };
+  const dim3 g = grid(128);
+  if ((int64_t)g.x * g.z >= 256) launch_kernel(orth_gemm<EPI, PL, 128, 2, IO>, g, dim3(256), 0, s, a);
+  else launch_kernel(orth_gemm<EPI, PL, 64, 4, IO>, grid(64), dim3(256), 0, s, a);
+}
 template <int EPI, typename IO>
 void gemm(const OrthGemmArgs& a, int planes, hipStream_t s) {
-  const unsigned mt = (unsigned)(a.M / ORTH_TILE), nt = (unsigned)(a.N / ORTH_TILE);
-  const bool sym = EPI == ORTH_GRAM || EPI == ORTH_POLY;
-  const dim3 grid(sym ? mt * (mt + 1) / 2 : mt * nt, 1, (unsigned)a.io.batch);
-  if (planes == 1) launch_kernel(orth_gemm<EPI, 1, IO>, grid, dim3(256), 0, s, a);
-  else launch_kernel(orth_gemm<EPI, 2, IO>, grid, dim3(256), 0, s, a);
+  if (planes == 1) gemm_tiles<EPI, 1, IO>(a, s);
+  else gemm_tiles<EPI, 2, IO>(a, s);
 }
 
 }  // namespace

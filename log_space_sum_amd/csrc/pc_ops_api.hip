@@ -223,23 +223,36 @@ void check_orth(int dtype, int64_t batch, int32_t rows, int32_t cols) {
 }
 
 // Bounds of the singular values at every step and of the step's polynomial
-// b t + c t^2 (t the squared singular value): where they start in [0, 1], over
-// a fine grid with a margin.
+// b t + c t^2 (t the squared singular value), where they start in [0, 1]: the
+// largest magnitudes at the interval's ends and the extrema inside it, with a
+// margin for rounding.
 struct OrthBounds {
   double x[ORTH_MAX_STEPS + 1], p[ORTH_MAX_STEPS];
 };
-OrthBounds orth_bounds(int steps, const float* c) {
+OrthBounds orth_bounds(int steps, const float* coef) {
   OrthBounds o;
   double top = 1.0;
   for (int s = 0; s < steps; ++s) {
+    const double a = coef[3 * s], b = coef[3 * s + 1], c = coef[3 * s + 2], tmax = top * top;
     o.x[s] = top;
     double next = 0.0, poly = 0.0;
-    for (int k = 0; k <= 4096; ++k) {
-      const double x = top * k / 4096, t = x * x, q = (double)c[3 * s + 1] * t + (double)c[3 * s + 2] * t * t;
-      poly = std::max(poly, std::fabs(q));
-      next = std::max(next, std::fabs((double)c[3 * s] * x + q * x));
+    auto at = [&](double t) {
+      if (!(t >= 0.0 && t <= tmax)) return;
+      poly = std::max(poly, std::fabs(t * (b + c * t)));
+      next = std::max(next, std::fabs(std::sqrt(t) * (a + t * (b + c * t))));
+    };
+    at(tmax);
+    if (c != 0.0) {
+      at(-b / (2.0 * c));                                 // of the polynomial
+      const double d = 9.0 * b * b - 20.0 * a * c;        // of a x + b x^3 + c x^5: a + 3 b t + 5 c t^2 = 0
+      if (d >= 0.0) {
+        at((-3.0 * b + std::sqrt(d)) / (10.0 * c));
+        at((-3.0 * b - std::sqrt(d)) / (10.0 * c));
+      }
+    } else if (b != 0.0) {
+      at(-a / (3.0 * b));
     }
-    o.p[s] = poly;
+    o.p[s] = 1.02 * poly;
     top = 1.02 * next;
     if (!(top <= 1024.0)) fail(PC_ERR_INVALID_ARG, "coefficients of step " + std::to_string(s) + " let the matrix grow past 1024");
   }
