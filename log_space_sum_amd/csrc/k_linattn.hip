@@ -234,7 +234,7 @@ __device__ __forceinline__ void stage_rows(CT* row, int d, const Unit<IO, EV>& u
 // output columns.  WALK false: only the state, from zero, of every segment but
 // a sequence's last, into `seg`.
 template <typename IO, typename CT, int DKB, int NW, Fit F, bool WALK>
-__global__ __launch_bounds__(64 * NW, F == FULL ? 4 : 2) void mix_walk(MixArgs m) {
+__global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_walk(MixArgs m) {
   using O = Ops<CT>;
   using quad = typename O::quad;
   constexpr int C = O::C, CB = C / 16, EV = O::EV, NT = 64 * NW;
@@ -252,6 +252,7 @@ __global__ __launch_bounds__(64 * NW, F == FULL ? 4 : 2) void mix_walk(MixArgs m
   // inside products at distance d = i - j (at C - 1 - d; 0 behind C - 1), and
   // of the state in token i's output
   __shared__ __align__(16) float swt[C], sdec[2 * C], siw[C];
+  __shared__ int sbad[2];
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int head = blockIdx.x, seq = blockIdx.z;
@@ -282,12 +283,18 @@ __global__ __launch_bounds__(64 * NW, F == FULL ? 4 : 2) void mix_walk(MixArgs m
     if (WALK) from = m.nsegs > 1 ? m.seg + (((int64_t)seq * m.nsegs + sgm) * m.heads + head) * elems
                                  : (m.init ? m.init + ((int64_t)seq * m.heads + head) * elems : nullptr);
 #pragma unroll
-    for (int kb = 0; kb < DKB; ++kb)
+    for (int kb = 0; kb < DKB; ++kb) {
+      const int row = 16 * kb + 4 * g;
+      st[kb] = f32x4{};
+      if (!from) continue;
+      if (m.st_r == 1 && (F == FULL || (row + 4 <= da && col < dc))) {
+        __builtin_memcpy(&st[kb], from + row + (int64_t)col * m.st_c, 16);   // transposed: a lane's rows lie side by side
+      } else {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * kb + 4 * g + r;
-        st[kb][r] = from && (F == FULL || (row < da && col < dc)) ? from[row * m.st_r + col * m.st_c] : 0.0f;
+        for (int r = 0; r < 4; ++r)
+          if (F == FULL || (row + r < da && col < dc)) st[kb][r] = from[(row + r) * m.st_r + col * m.st_c];
       }
+    }
   }
   if constexpr (WALK) {
     for (int e = tid; e < 2 * C; e += NT) sdec[e] = e < C ? m.pscale * decay_pow(gam, (float)(C - 1 - e)) : 0.0f;
@@ -323,6 +330,9 @@ __global__ __launch_bounds__(64 * NW, F == FULL ? 4 : 2) void mix_walk(MixArgs m
     }
   };
 
+  if (tid < 2) sbad[tid] = 0;
+  __syncthreads();
+  int turn = 0;
   float ln = 1.0f;
   int wn = -1;             // the chunk size that ln and swt are of
   int64_t single = pos0;   // tokens before this position go one by one
@@ -352,7 +362,12 @@ __global__ __launch_bounds__(64 * NW, F == FULL ? 4 : 2) void mix_walk(MixArgs m
 #pragma unroll
       for (int u = 0; u < UC; ++u) bad |= not_finite(rc[u]);
     }
-    if (__syncthreads_or(bad)) {   // (also: every wave is done with the last chunk's tiles)
+    if (bad) sbad[turn] = 1;
+    __syncthreads();               // (also: every wave is done with the last chunk's tiles)
+    const bool any = sbad[turn] != 0;
+    turn ^= 1;
+    if (tid == 0) sbad[turn] = 0;  // the next chunk's, written behind the next barrier
+    if (any) {
       single = pos + n;
       n = 1;
       fetch(pos, n);
@@ -376,6 +391,15 @@ __global__ __launch_bounds__(64 * NW, F == FULL ? 4 : 2) void mix_walk(MixArgs m
     }
     __syncthreads();
     const int64_t next = pos + n;
+    // The next chunk's rows, in flight over this chunk (with eight waves, whose
+    // registers are fewer, over its second half).  Behind the last chunk: its
+    // last row again, since under a condition the loads would wait for each
+    // other.
+    constexpr bool EARLY = NW == 4 || !WALK;
+    auto fetch_next = [&] {
+      fetch(min(next, pos1 - 1), next < single ? 1 : (int)min((int64_t)C, max(pos1 - next, (int64_t)1)));
+    };
+    if (EARLY) fetch_next();
     f32x4 o[WALK ? CB : 1];
     if constexpr (WALK) {
       // inside products b_j . a_i, transposed: a lane holds four j of one i
@@ -429,11 +453,7 @@ __global__ __launch_bounds__(64 * NW, F == FULL ? 4 : 2) void mix_walk(MixArgs m
       }
       __syncthreads();
     }
-    // The next chunk's rows, in flight over this chunk's second half (earlier,
-    // their registers would not fit beside the first half's).  Behind the last
-    // chunk: its last row again, since under a condition the loads would wait
-    // for each other.
-    fetch(min(next, pos1 - 1), next < single ? 1 : (int)min((int64_t)C, max(pos1 - next, (int64_t)1)));
+    if (!EARLY) fetch_next();
     if (wave_on) {
 #pragma unroll
       for (int kb = 0; kb < DKB; ++kb) st[kb] *= ln;
@@ -663,6 +683,7 @@ void walk(const MixArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.heads, (unsigned)(WALK ? a.nsegs : a.nsegs - 1), (unsigned)a.seqs);
   if (a.da <= 32 && a.dc <= 64) walk_fit<IO, CT, WALK, 2, 4>(a, grid, s);
   else if (a.da <= 64) walk_waves<IO, CT, WALK, 4>(a, grid, s);
+  else if (a.da <= 96 && a.dc <= 64) walk_fit<IO, CT, WALK, 6, 4>(a, grid, s);
   else walk_waves<IO, CT, WALK, 8>(a, grid, s);
 }
 template <bool WALK>

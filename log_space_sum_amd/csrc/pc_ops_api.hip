@@ -106,16 +106,19 @@ void check_out(const pc_linear_attention* d, const pc_heads& t, int heads, int d
 // Segments of the longest sequence.  One walk of a (sequence, head) is a chain
 // of chunks, so where sequences and heads are too few to fill the card the
 // sequences are cut; a cut costs a second reading of b and c and a state for
-// each segment and head, so a segment has at least 256 tokens.
+// each segment and head, so a segment has at least four chunks.  Ragged batches
+// are counted as full sequences of the same number of tokens.
 struct Split {
   int nsegs;
   int64_t len;
 };
 Split mix_segments(const pc_linear_attention* d) {
-  const int64_t walks = std::max<int64_t>(1, (int64_t)d->num_seqs * d->heads);
   const int64_t longest = std::max<int64_t>(1, std::min(d->max_seqlen, d->num_tokens));
-  int64_t n = std::min((512 + walks - 1) / walks, (longest + 255) / 256);
-  n = std::max<int64_t>(1, n);
+  const int64_t full = std::min<int64_t>(d->num_seqs, (d->num_tokens + longest - 1) / longest);
+  const int64_t walks = std::max<int64_t>(1, full * d->heads);
+  const int64_t room = std::max(d->dim_k, d->dim_v) > 64 ? 512 : 1024;   // walks that the card holds at a time
+  const int64_t least = d->dtype == PC_DTYPE_BF16 ? 256 : 128;
+  const int64_t n = std::max<int64_t>(1, std::min((room + walks - 1) / walks, (longest + least - 1) / least));
   const int64_t len = ((longest + n - 1) / n + 63) / 64 * 64;
   return {(int)((longest + len - 1) / len), len};
 }

@@ -227,7 +227,7 @@ def test_linear_attention_strides(typ):
     q, k, v = packed[..., :dk], packed[..., dk:2 * dk], packed[..., 2 * dk:2 * dk + dv]
     g = put(DECAYS[:H])
     o = torch.empty((H, n, dv), device=DEV, dtype=types[typ]).transpose(0, 1)
-    L.pc_linear_attention_forward(q, k, v, g, o, scale=0.2)
+    L.pc_linear_attention_forward(q, k, v, g, o, scale=0.2, ws=L.linear_attention_workspace(q, k, v))
     A = [get(t) for t in (q, k, v, g)]
     ro, _ = R.linear_attention(*A, [0, n], 0.2)
     mo, _ = R.linear_attention(*[np.abs(a) for a in A[:3]], A[3], [0, n], 0.2)
@@ -253,13 +253,14 @@ def test_linear_attention_values_that_are_not_finite(typ):
     q, k, v, do, cu, dcu = _att(rng, lens, 2, 2, 32, 48, typ)
     g = put(np.array([-0.1, -0.01]))
     clean = torch.empty((230, 2, 48), device=DEV, dtype=types[typ])
-    L.pc_linear_attention_forward(q, k, v, g, clean, dcu)
+    ws = L.linear_attention_workspace(q, k, v, dcu)
+    L.pc_linear_attention_forward(q, k, v, g, clean, dcu, ws=ws)
     k2, v2, q2 = k.clone(), v.clone(), q.clone()
     v2[130, 0, 5] = float("nan")     # sequence 1, head 0, one column
     k2[150, 1, 3] = float("inf")     # sequence 1, head 1
     q2[10, 0] = float("nan")         # its own output
     o = torch.empty_like(clean)
-    L.pc_linear_attention_forward(q2, k2, v2, g, o, dcu)
+    L.pc_linear_attention_forward(q2, k2, v2, g, o, dcu, ws=ws)
     bad = torch.zeros_like(o, dtype=torch.bool)
     bad[130:190, 0, 5] = True
     bad[150:190, 1] = True
@@ -281,7 +282,7 @@ def test_linear_attention_clamps_bad_offsets():
     cu = torch.tensor([-4, 30, 20, 50, 1000], dtype=torch.int32, device=DEV)   # -> 0..30, (none), 20..50, 50..70
     g = put(np.array([-0.1, -0.2]))
     o, s1 = torch.full((70, 2, 16), 3.0, device=DEV), torch.empty((4, 2, 16, 16), device=DEV)
-    L.pc_linear_attention_forward(q, k, v, g, o, cu, state_out=s1)
+    L.pc_linear_attention_forward(q, k, v, g, o, cu, state_out=s1, ws=L.linear_attention_workspace(q, k, v, cu))
     _, rs = R.linear_attention(*[get(t) for t in (q, k, v, g)], [50, 70], 0.25)
     near(s1[3:], rs, 200 * E32 * 70, "the last sequence's state")
     assert not s1[1].any()
