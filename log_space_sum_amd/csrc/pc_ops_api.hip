@@ -610,17 +610,23 @@ int pc_orthogonalize(int device, int dtype, int64_t batch, int32_t rows, int32_t
       const OrthMat &x = p.x[k & 1], &xt = p.xt[k & 1];
       const float sa = orth_scale(bound.x[k] * bound.x[k]), sb = orth_scale(bound.p[k]);
       const float sn = k + 1 < steps ? orth_scale(bound.x[k + 1]) : 1.0f;
-      // A = X X^T.  bfloat16 results: its operands in one plane (11 bits), an
-      // error of 2^-12 of A that reaches the result as about a quarter of
-      // bfloat16's own rounding, for a sixth of the matrix instructions
+      // Planes of the products' operands.  float32 and float16 results: two
+      // everywhere (22 bits).  bfloat16 results: A's operands in one (11 bits)
+      // in every step, and all of the first two of five or more steps, whose
+      // error the later steps do not raise: together within 8e-4 of the result
+      // (normwise; square, wide, orthogonal, rank-1 and power-law spectra),
+      // against 1.7e-3 of bfloat16's own rounding, for 19/30 of the matrix
+      // instructions.  (One plane in any later step costs 1e-3 or more.)
+      const bool bf = dtype == PC_DTYPE_BF16, early = bf && k < 2 && k + 3 < steps;
       OrthGemmArgs a{};
       a.io = io;
+      // A = X X^T
       a.M = a.N = p.mp;
       a.K = p.np;
       a.a = a.b = x;
       a.c = p.a;
       a.sacc = sa / (sx * sx);
-      launch_orth_gemm(a, ORTH_GRAM, dtype == PC_DTYPE_BF16 ? 1 : 2, dtype, s);
+      launch_orth_gemm(a, ORTH_GRAM, bf ? 1 : 2, dtype, s);
       check_launch();
       // B = b A + c A^2
       a.K = p.mp;
@@ -628,7 +634,7 @@ int pc_orthogonalize(int device, int dtype, int64_t batch, int32_t rows, int32_t
       a.c = p.b;
       a.sacc = sb * c[2] / (sa * sa);
       a.sold = sb * c[1] / sa;
-      launch_orth_gemm(a, ORTH_POLY, 2, dtype, s);
+      launch_orth_gemm(a, ORTH_POLY, early ? 1 : 2, dtype, s);
       check_launch();
       // X <- a X + B X
       a.N = p.np;
@@ -639,7 +645,7 @@ int pc_orthogonalize(int device, int dtype, int64_t batch, int32_t rows, int32_t
       a.ct = p.xt[(k + 1) & 1];
       a.sacc = sn / (sb * sx);
       a.sold = sn * c[0] / sx;
-      launch_orth_gemm(a, k + 1 < steps ? ORTH_APPLY : ORTH_OUT, 2, dtype, s);
+      launch_orth_gemm(a, k + 1 < steps ? ORTH_APPLY : ORTH_OUT, early ? 1 : 2, dtype, s);
       check_launch();
       sx = sn;
     }

@@ -62,13 +62,13 @@ def linear_attention_grad(do, q, k, v, log_decay, cu, scale, state=None, dstate=
     return dq, dkk.reshape(T, K, grp, dk).sum(2), dvv.reshape(T, K, grp, dv).sum(2), out
 
 
-def orthogonalize(g, coefficients, eps, gram_operand=lambda x: x):
-    """Newton-Schulz steps on one matrix; gram_operand: the rounding of X in A = X X^T."""
+def orthogonalize(g, coefficients, eps, operands=lambda step: (lambda x: x,) * 3):
+    """Newton-Schulz steps on one matrix; operands(step): the rounding of the operands of A = X X^T, A A and B X."""
     tall = g.shape[0] > g.shape[1]
     x = g.T if tall else g
     x = x / (np.sqrt((x * x).sum()) + eps)
-    for a, b, c in coefficients:
-        r = gram_operand(x)
-        A = r @ r.T
-        x = a * x + (b * A + c * (A @ A)) @ x
+    for step, (a, b, c) in enumerate(coefficients):
+        gram, square, apply = operands(step)
+        A = gram(x) @ gram(x).T
+        x = a * x + apply(b * A + c * (square(A) @ square(A))) @ apply(x)
     return x.T if tall else x
