@@ -381,14 +381,133 @@ __global__ __launch_bounds__(256) void orth_split(OrthIo io, const double* part,
   }
 }
 
+// Row and column of a tile: on and above the diagonal, column after column, or
+// row after row.
+template <bool SYM>
+__device__ __forceinline__ void place(int tile, int nt, int& ti, int& tj) {
+  if constexpr (SYM) {
+    tj = (int)((sqrtf(8.0f * (float)tile + 1.0f) - 1.0f) * 0.5f);
+    while ((tj + 1) * (tj + 2) / 2 <= tile) ++tj;
+    while (tj * (tj + 1) / 2 > tile) --tj;
+    ti = tile - tj * (tj + 1) / 2;
+  } else {
+    ti = tile / nt;
+    tj = tile % nt;
+  }
+}
+
+// What is done with a wave's WT x WT piece of a product, at row row_w and column
+// col_w: scaled, the other terms added, rounded and written.  A lane holds rows
+// 8 (r / 4) + 4 hf + r % 4 of column l32 of every 32 x 32 block.  Panels go
+// through `mine`, a piece of LDS of the wave's own, one plane at a time:
+// 32-column blocks of WT rows of 64 bytes, which are whole kilobytes of the
+// panel in memory.
+template <int EPI, int NF, typename IO>
+__device__ __forceinline__ void finish(const OrthGemmArgs& a, f32x16 (&acc)[NF][NF], int row_w, int col_w, bool off_diagonal,
+                                       int64_t z, char* mine) {
+  constexpr int WT = 32 * NF;
+  constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, hf = lane >> 5;
+  constexpr int LINES = WT * WT * 2 / 1024, PER = WT / 16;   // kilobytes, and those of a block
+  auto line = [&](const OrthMat& t, int rows, int r0, int k0, int n) {   // a lane's 16 bytes of kilobyte n
+    return t.p + z * t.batch + panel(r0 + n % PER * 16 + (lane >> 2), k0 + n / PER * 32 + (lane & 3) * 8, rows);
+  };
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j) acc[i][j] *= a.sacc;
+  if (a.old.p) {
+    for (int p = 0; p < 2; ++p) {
+      uint4 in[LINES];
+#pragma unroll
+      for (int n = 0; n < LINES; ++n) in[n] = *(const uint4*)(line(a.old, a.M, row_w, col_w, n) + p * a.old.plane);
+#pragma unroll
+      for (int n = 0; n < LINES; ++n) *(uint4*)(mine + n * 1024 + lane * 16) = in[n];
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            acc[i][j][r] += a.sold * f16_value(*(const uint16_t*)(mine + ((j * WT + 32 * i + 8 * (r >> 2) + 4 * hf + (r & 3)) * 32 + l32) * 2));
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  if constexpr (EPI == ORTH_POLY) {   // a I
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (row_w + 32 * i + 8 * (r >> 2) + 4 * hf + (r & 3) == col_w + 32 * j + l32) acc[i][j][r] += a.diag;
+  }
+  if constexpr (EPI == ORTH_OUT) {
+    const OrthIo& io = a.io;
+    IO* y = (IO*)io.out + z * io.o_batch;
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int row = row_w + 32 * i + 8 * (r >> 2) + 4 * hf + (r & 3), col = col_w + 32 * j + l32;
+          if (row < io.m && col < io.n) y[at_x<IO>(io, io.o_row, row, col)] = from_f32<IO>(acc[i][j][r]);
+        }
+    return;
+  }
+  const bool mirror = !SYM || off_diagonal;
+  const OrthMat& turned = SYM ? a.c : a.ct;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    if (p < a.cplanes) {
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            *(f16*)(mine + ((j * WT + 32 * i + 8 * (r >> 2) + 4 * hf + (r & 3)) * 32 + l32) * 2) = (f16)acc[i][j][r];
+#pragma unroll
+      for (int n = 0; n < LINES; ++n)
+        *(uint4*)(line(a.c, a.M, row_w, col_w, n) + p * a.c.plane) = *(const uint4*)(mine + n * 1024 + lane * 16);
+      __builtin_amdgcn_wave_barrier();
+      if (mirror) {
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+          for (int j = 0; j < NF; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              f16 h[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) h[r] = (f16)acc[i][j][4 * q + r];
+              __builtin_memcpy(__builtin_assume_aligned(mine + ((i * WT + 32 * j + l32) * 32 + 8 * q + 4 * hf) * 2, 8), h, 8);
+            }
+#pragma unroll
+        for (int n = 0; n < LINES; ++n)
+          *(uint4*)(line(turned, a.N, col_w, row_w, n) + p * turned.plane) = *(const uint4*)(mine + n * 1024 + lane * 16);
+        __builtin_amdgcn_wave_barrier();
+      }
+      // what the plane leaves
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] -= (float)(f16)acc[i][j][r];
+    }
+  }
+}
+
 // C = A B^T on TILE x TILE tiles, four waves of half of that, K in slices of 32
 // through an LDS ring of ST stages: two where two workgroups a compute unit
 // cover each other's waits, more where there are too few workgroups for that.
 // TILE 128, or 64 where tiles of 128 would leave compute units without one.  PL planes of each operand: 1 one product, 2
 // three.  Slot s of a row's four 16-byte chunks holds chunk s ^ ((row >> 2) & 3),
 // so the 16 rows a wave reads at a time lie in different banks.
-template <int EPI, int PL, int TILE, int ST, typename IO>
-__global__ __launch_bounds__(256, 2) void orth_gemm(OrthGemmArgs a) {
+template <int EPI, int PL, int TILE, int ST, bool PART, typename IO>
+__global__ __launch_bounds__(256, PL == 1 && EPI == ORTH_GRAM ? 3 : 2) void orth_gemm(OrthGemmArgs a) {
   constexpr int SLICE = TILE * 64;   // bytes of an operand plane's slice
   constexpr int WT = TILE / 2, NF = WT / 32, LR = TILE / 4;   // a wave's rows, its 32-row blocks, the rows it loads
   constexpr int STAGE = 2 * PL * SLICE;
@@ -397,16 +516,10 @@ __global__ __launch_bounds__(256, 2) void orth_gemm(OrthGemmArgs a) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int64_t z = blockIdx.z;
   int ti, tj;
-  if constexpr (SYM) {   // tiles on and above the diagonal, column after column
-    tj = (int)((sqrtf(8.0f * (float)blockIdx.x + 1.0f) - 1.0f) * 0.5f);
-    while ((tj + 1) * (tj + 2) / 2 <= (int)blockIdx.x) ++tj;
-    while (tj * (tj + 1) / 2 > (int)blockIdx.x) --tj;
-    ti = (int)blockIdx.x - tj * (tj + 1) / 2;
-  } else {
-    const int nt = a.N / TILE;
-    ti = blockIdx.x / nt;
-    tj = blockIdx.x % nt;
-  }
+  // PART: the tiles from a.full on, each in a.split parts along K, whose sums go
+  // to a.parts and are joined by orth_join.
+  const int tile = PART ? a.full + (int)blockIdx.x / a.split : (int)blockIdx.x;
+  place<SYM>(tile, a.N / TILE, ti, tj);
   const int row0 = ti * TILE, col0 = tj * TILE;
   const uint16_t* pa = a.a.p + z * a.a.batch;
   const uint16_t* pb = a.b.p + z * a.b.batch;
@@ -431,16 +544,21 @@ __global__ __launch_bounds__(256, 2) void orth_gemm(OrthGemmArgs a) {
   };
   f32x16 acc[NF][NF] = {};
   const int wr = (wave >> 1) * WT, wc = (wave & 1) * WT, l32 = lane & 31, hf = lane >> 5;
-  const int nk = a.K / 32;
+  int k0 = 0, nk = a.K / 32;   // the slices of this workgroup
+  if constexpr (PART) {
+    const int all = nk, part = (int)blockIdx.x % a.split;
+    k0 = (int)((int64_t)all * part / a.split);
+    nk = (int)((int64_t)all * (part + 1) / a.split) - k0;
+  }
   // A slice's loads of a wave; slices behind the last are loaded again from the
   // last, so that the count of loads in flight is the same in every round.
   constexpr int LOADS = 2 * PL * (LR / 16);
-  for (int s = 0; s < ST - 1; ++s) issue(s, min(s, nk - 1));
+  for (int s = 0; s < ST - 1; ++s) issue(s, k0 + min(s, nk - 1));
   int cur = 0, fill = ST - 1;
   for (int kb = 0; kb < nk; ++kb) {
     __builtin_amdgcn_s_waitcnt(WaitVmLgkm<LOADS * (ST - 2)>::imm);
     ring_barrier();   // slice kb is there, and every wave is done with the stage that is filled next
-    issue(fill, min(kb + ST - 1, nk - 1));
+    issue(fill, k0 + min(kb + ST - 1, nk - 1));
     const char* st = lds + cur * STAGE;
     cur = cur + 1 == ST ? 0 : cur + 1;
     fill = fill + 1 == ST ? 0 : fill + 1;
@@ -469,50 +587,47 @@ __global__ __launch_bounds__(256, 2) void orth_gemm(OrthGemmArgs a) {
   }
 
   __builtin_amdgcn_s_waitcnt(WaitVmLgkm<0>::imm);   // no load may reach LDS after the workgroup's end
+  if constexpr (PART) {   // [tile, part][wave][16 registers of four][lane]
+    float* to = a.parts + ((int64_t)blockIdx.x * 4 + wave) * (NF * NF * 1024) + lane * 4;
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *(f32x4*)(to + ((i * NF + j) * 4 + q) * 256) =
+              f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+  } else {
+    ring_barrier();   // every wave is done with the ring
+    finish<EPI, NF, IO>(a, acc, row0 + wr, col0 + wc, ti != tj, z, lds + wave * (WT * WT * 2));
+  }
+}
 
-  // a lane holds rows 8 (r / 4) + 4 hf + r % 4 of column l32 of every 32 x 32 tile
+// The tiles that were split along K: one wave a quarter, its parts added in
+// their order.
+template <int EPI, typename IO>
+__global__ __launch_bounds__(64) void orth_join(OrthGemmArgs a) {
+  constexpr int NF = 2;
+  constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
+  __shared__ __align__(16) char lds[64 * 64 * 2];
+  const int wave = blockIdx.x & 3, tile = blockIdx.x >> 2;
+  int ti, tj;
+  place<SYM>(a.full + tile, a.N / 128, ti, tj);
+  f32x16 acc[NF][NF] = {};
+  for (int p = 0; p < a.split; ++p) {
+    const float* from = a.parts + (((int64_t)tile * a.split + p) * 4 + wave) * (NF * NF * 1024) + threadIdx.x * 4;
 #pragma unroll
-  for (int i = 0; i < NF; ++i)
+    for (int i = 0; i < NF; ++i)
 #pragma unroll
-    for (int j = 0; j < NF; ++j) {
-      const int col = col0 + wc + 32 * j + l32;
+      for (int j = 0; j < NF; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = row0 + wr + 32 * i + 8 * q + 4 * hf;
-        float v[4];
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 v = *(const f32x4*)(from + ((i * NF + j) * 4 + q) * 256);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          v[r] = a.sacc * acc[i][j][4 * q + r];
-          if constexpr (EPI != ORTH_GRAM) {
-            const int64_t e = z * a.old.batch + panel(row + r, col, a.M);
-            v[r] += a.sold * (f16_value(a.old.p[e]) + f16_value(a.old.p[e + a.old.plane]));
-          }
+          for (int r = 0; r < 4; ++r) acc[i][j][4 * q + r] += v[r];
         }
-        if constexpr (EPI == ORTH_OUT) {
-          const OrthIo& io = a.io;
-          IO* y = (IO*)io.out + z * io.o_batch;
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (row + r < io.m && col < io.n) y[at_x<IO>(io, io.o_row, row + r, col)] = from_f32<IO>(v[r]);
-        } else {
-          uint16_t hi[4], lo[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) planes_of(v[r], hi[r], lo[r]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int64_t e = z * a.c.batch + panel(row + r, col, a.M);
-            a.c.p[e] = hi[r];
-            a.c.p[e + a.c.plane] = lo[r];
-          }
-          if (!SYM || ti != tj) {
-            const OrthMat& t = SYM ? a.c : a.ct;
-            const int64_t e = z * t.batch + panel(col, row, a.N);
-            __builtin_memcpy(__builtin_assume_aligned(t.p + e, 8), hi, 8);
-            __builtin_memcpy(__builtin_assume_aligned(t.p + e + t.plane, 8), lo, 8);
-          }
-        }
-      }
-    }
+  }
+  finish<EPI, NF, IO>(a, acc, ti * 128 + (wave >> 1) * 64, tj * 128 + (wave & 1) * 64, ti != tj, 0, lds);
 }
 
 template <typename IO>
@@ -530,9 +645,24 @@ void gemm_tiles(const OrthGemmArgs& a, hipStream_t s) {
     const unsigned mt = (unsigned)(a.M / tile), nt = (unsigned)(a.N / tile);
     return dim3(sym ? mt * (mt + 1) / 2 : mt * nt, 1, (unsigned)a.io.batch);
   };
-  const dim3 g = grid(128);
-  if ((int64_t)g.x * g.z >= 256) launch_kernel(orth_gemm<EPI, PL, 128, 2, IO>, g, dim3(256), 0, s, a);
-  else launch_kernel(orth_gemm<EPI, PL, 64, 4, IO>, grid(64), dim3(256), 0, s, a);
+  dim3 g = grid(128);
+  if ((int64_t)g.x * g.z < 256) {
+    launch_kernel(orth_gemm<EPI, PL, 64, 4, false, IO>, grid(64), dim3(256), 0, s, a);
+    return;
+  }
+  // Whole rounds of one workgroup a compute unit take whole tiles; the tiles
+  // left over, which would take another round for a few of them (528 tiles of a
+  // symmetric 4096: 16), are split along K into up to 8 parts each.
+  OrthGemmArgs b = a;
+  b.full = (int)(g.x / 256 * 256);
+  const int rest = (int)g.x - b.full;
+  b.split = a.parts && rest ? std::min(ORTH_PARTS / rest, 8) : 1;
+  if (b.split > 1) g.x = (unsigned)b.full;
+  launch_kernel(orth_gemm<EPI, PL, 128, 2, false, IO>, g, dim3(256), 0, s, b);
+  if (b.split > 1) {
+    launch_kernel(orth_gemm<EPI, PL, 128, 2, true, IO>, dim3((unsigned)(rest * b.split)), dim3(256), 0, s, b);
+    launch_kernel(orth_join<EPI, IO>, dim3((unsigned)rest * 4), dim3(64), 0, s, b);
+  }
 }
 template <int EPI, typename IO>
 void gemm(const OrthGemmArgs& a, int planes, hipStream_t s) {

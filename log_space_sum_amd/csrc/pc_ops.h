@@ -144,13 +144,18 @@ struct OrthMat {
   int64_t plane;        // elements from the hi to the lo plane
   int64_t batch;        // elements from one matrix to the next
 };
+constexpr int ORTH_PARTS = 512;       // partial tiles of a product's last round
 enum OrthEpi { ORTH_GRAM, ORTH_POLY, ORTH_APPLY, ORTH_OUT };
 struct OrthGemmArgs {
   int32_t M, N, K;      // padded; C [M, N] = A [M, K] B [N, K]^T
   OrthMat a, b;
-  OrthMat old;          // POLY: A, APPLY / OUT: X (panels of [M, N])
+  OrthMat old;          // added to the product, nullable (panels of [M, N])
   OrthMat c, ct;        // the result's panels and its transpose's (GRAM / POLY: c alone, both halves)
   float sacc, sold;     // result = sacc acc + sold old
+  float diag;           // POLY: + diag I
+  int32_t cplanes;      // planes of the result that are written
+  float* parts;         // room for ORTH_PARTS tiles' partial sums, nullable (one matrix only)
+  int32_t full, split;  // set at the launch: tiles taken whole, parts of each tile behind them
   OrthIo io;            // OUT
 };
 void launch_orth_small(const OrthIo& io, const OrthPoly& p, int dtype, hipStream_t s);

@@ -187,7 +187,8 @@ struct OrthPlan {
   int m, n, mp, np;
   bool small;
   OrthMat x[2], xt[2], a, b;
-  size_t part, total;
+  size_t part, parts, total;
+  bool split;
 };
 OrthPlan orth_plan(int64_t batch, int32_t rows, int32_t cols, void* ws) {
   OrthPlan p{};
@@ -213,6 +214,9 @@ OrthPlan orth_plan(int64_t batch, int32_t rows, int32_t cols, void* ws) {
   p.b = mat(p.mp, p.mp);
   p.part = p.total;
   p.total += (size_t)batch * ORTH_NORM_BLOCKS * sizeof(double);
+  p.split = batch == 1 && (int64_t)(p.mp / ORTH_TILE) * (p.np / ORTH_TILE) >= 256;
+  p.parts = (size_t)round_up((int64_t)p.total, 256);
+  if (p.split) p.total = p.parts + (size_t)ORTH_PARTS * ORTH_TILE * ORTH_TILE * sizeof(float);
   return p;
 }
 
@@ -225,8 +229,8 @@ void check_orth(int dtype, int64_t batch, int32_t rows, int32_t cols) {
     fail(PC_ERR_UNSUPPORTED, std::to_string(rows) + " x " + std::to_string(cols) + " matrices (at most 32768)");
 }
 
-// Bounds of the singular values at every step and of the step's polynomial
-// b t + c t^2 (t the squared singular value), where they start in [0, 1]: the
+// Bounds of the singular values at every step and of the step's polynomials
+// b t + c t^2 and a + b t + c t^2 (t the squared singular value), where they start in [0, 1]: the
 // largest magnitudes at the interval's ends and the extrema inside it, with a
 // margin for rounding.
 struct OrthBounds {
@@ -241,9 +245,10 @@ OrthBounds orth_bounds(int steps, const float* coef) {
     double next = 0.0, poly = 0.0;
     auto at = [&](double t) {
       if (!(t >= 0.0 && t <= tmax)) return;
-      poly = std::max(poly, std::fabs(t * (b + c * t)));
+      poly = std::max({poly, std::fabs(t * (b + c * t)), std::fabs(a + t * (b + c * t))});
       next = std::max(next, std::fabs(std::sqrt(t) * (a + t * (b + c * t))));
     };
+    at(0.0);
     at(tmax);
     if (c != 0.0) {
       at(-b / (2.0 * c));                                 // of the polynomial
@@ -620,27 +625,33 @@ int pc_orthogonalize(int device, int dtype, int64_t batch, int32_t rows, int32_t
       const bool bf = dtype == PC_DTYPE_BF16, early = bf && k < 2 && k + 3 < steps;
       OrthGemmArgs a{};
       a.io = io;
+      a.parts = p.split ? (float*)((char*)ws + p.parts) : nullptr;
       // A = X X^T
       a.M = a.N = p.mp;
       a.K = p.np;
       a.a = a.b = x;
       a.c = p.a;
       a.sacc = sa / (sx * sx);
+      a.cplanes = 2;
       launch_orth_gemm(a, ORTH_GRAM, bf ? 1 : 2, dtype, s);
       check_launch();
-      // B = b A + c A^2
+      // B = a I + b A + c A^2, then X <- B X.  One plane: without a I, whose
+      // part of X is added in float32 instead (it is most of the result, and
+      // would be rounded with X)
       a.K = p.mp;
       a.a = a.b = a.old = p.a;
       a.c = p.b;
       a.sacc = sb * c[2] / (sa * sa);
       a.sold = sb * c[1] / sa;
+      a.diag = early ? 0.0f : sb * c[0];
+      a.cplanes = early ? 1 : 2;
       launch_orth_gemm(a, ORTH_POLY, early ? 1 : 2, dtype, s);
       check_launch();
-      // X <- a X + B X
+      a.cplanes = 2;
       a.N = p.np;
       a.a = p.b;
       a.b = xt;
-      a.old = x;
+      a.old = early ? x : OrthMat{};
       a.c = p.x[(k + 1) & 1];
       a.ct = p.xt[(k + 1) & 1];
       a.sacc = sn / (sb * sx);
