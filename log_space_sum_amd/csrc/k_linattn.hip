@@ -234,7 +234,8 @@ __device__ __forceinline__ void stage_rows(CT* row, int d, const Unit<IO, EV>& u
 // output columns.  WALK false: only the state, from zero, of every segment but
 // a sequence's last, into `seg`.
 template <typename IO, typename CT, int DKB, int NW, Fit F, bool WALK>
-__global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_walk(MixArgs m) {
+__global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_walk(MixMany many) {
+  const MixArgs& m = many.w[blockIdx.z / many.seqs];
   using O = Ops<CT>;
   using quad = typename O::quad;
   constexpr int C = O::C, CB = C / 16, EV = O::EV, NT = 64 * NW;
@@ -255,7 +256,7 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
   __shared__ int sbad[2];
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, l16 = lane & 15;
-  const int head = blockIdx.x, seq = blockIdx.z;
+  const int head = blockIdx.x, seq = blockIdx.z % many.seqs;
   int sgm = blockIdx.y;
   int64_t t0 = 0, t1 = m.tokens;
   if (m.cu) {
@@ -543,9 +544,10 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
 
 // The states at the segments' starts from the segments' own states, in place:
 // start_0 = init, start_{s+1} = l^seglen start_s + own_s.
-__global__ __launch_bounds__(256) void mix_scan(MixScanArgs m) {
+__global__ __launch_bounds__(256) void mix_scan(MixScanArgs m0, MixScanArgs m1) {
+  const MixScanArgs& m = (int)blockIdx.z < m0.seqs ? m0 : m1;
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int head = blockIdx.y, seq = blockIdx.z;
+  const int head = blockIdx.y, seq = blockIdx.z % m0.seqs;
   if (e >= m.elems) return;
   int64_t t0 = 0, t1 = m.tokens;
   if (m.cu) {
@@ -567,7 +569,8 @@ __global__ __launch_bounds__(256) void mix_scan(MixScanArgs m) {
 // Gradients of shared key / value heads: the sum over the heads that share one,
 // in their order.  Only tokens of the sequences are written.
 template <typename IO>
-__global__ __launch_bounds__(256) void mix_sum(MixSumArgs m) {
+__global__ __launch_bounds__(256) void mix_sum(MixSumArgs m0, MixSumArgs m1) {
+  const MixSumArgs& m = blockIdx.y ? m1 : m0;
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = m.kv_heads * m.dim;
   const int64_t t = e / per;
@@ -667,47 +670,59 @@ __global__ __launch_bounds__(256) void mix_step(MixStepArgs m) {
 }
 
 template <typename IO, typename CT, bool WALK, int DKB, int NW>
-void walk_fit(const MixArgs& a, dim3 grid, hipStream_t s) {
+void walk_fit(const MixMany& a, dim3 grid, hipStream_t s) {
   constexpr int EV = Ops<CT>::EV;
-  if (a.da == 16 * DKB && a.dc == 16 * NW) launch_kernel(mix_walk<IO, CT, DKB, NW, FULL, WALK>, grid, dim3(64 * NW), 0, s, a);
-  else if (a.da % EV == 0 && a.dc % EV == 0) launch_kernel(mix_walk<IO, CT, DKB, NW, UNITS, WALK>, grid, dim3(64 * NW), 0, s, a);
+  const int da = a.w[0].da, dc = a.w[0].dc;
+  if (da == 16 * DKB && dc == 16 * NW) launch_kernel(mix_walk<IO, CT, DKB, NW, FULL, WALK>, grid, dim3(64 * NW), 0, s, a);
+  else if (da % EV == 0 && dc % EV == 0) launch_kernel(mix_walk<IO, CT, DKB, NW, UNITS, WALK>, grid, dim3(64 * NW), 0, s, a);
   else launch_kernel(mix_walk<IO, CT, DKB, NW, ANY, WALK>, grid, dim3(64 * NW), 0, s, a);
 }
 template <typename IO, typename CT, bool WALK, int DKB>
-void walk_waves(const MixArgs& a, dim3 grid, hipStream_t s) {
-  if (a.dc <= 64) walk_fit<IO, CT, WALK, DKB, 4>(a, grid, s);
+void walk_waves(const MixMany& a, dim3 grid, hipStream_t s) {
+  if (a.w[0].dc <= 64) walk_fit<IO, CT, WALK, DKB, 4>(a, grid, s);
   else walk_fit<IO, CT, WALK, DKB, 8>(a, grid, s);
 }
 template <typename IO, typename CT, bool WALK>
-void walk(const MixArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.heads, (unsigned)(WALK ? a.nsegs : a.nsegs - 1), (unsigned)a.seqs);
-  if (a.da <= 32 && a.dc <= 64) walk_fit<IO, CT, WALK, 2, 4>(a, grid, s);
-  else if (a.da <= 64) walk_waves<IO, CT, WALK, 4>(a, grid, s);
-  else if (a.da <= 96 && a.dc <= 64) walk_fit<IO, CT, WALK, 6, 4>(a, grid, s);
+void walk(const MixMany& a, hipStream_t s) {
+  const MixArgs& w = a.w[0];
+  const dim3 grid((unsigned)w.heads, (unsigned)(WALK ? w.nsegs : w.nsegs - 1), (unsigned)(a.seqs * a.n));
+  if (w.da <= 32 && w.dc <= 64) walk_fit<IO, CT, WALK, 2, 4>(a, grid, s);
+  else if (w.da <= 64) walk_waves<IO, CT, WALK, 4>(a, grid, s);
+  else if (w.da <= 96 && w.dc <= 64) walk_fit<IO, CT, WALK, 6, 4>(a, grid, s);
   else walk_waves<IO, CT, WALK, 8>(a, grid, s);
 }
 template <bool WALK>
-void walk_type(const MixArgs& a, int dtype, hipStream_t s) {
-  if (dtype == PC_DTYPE_BF16) walk<bf16, bf16, WALK>(a, s);
-  else if (dtype == PC_DTYPE_F16) walk<f16, float, WALK>(a, s);
-  else walk<float, float, WALK>(a, s);
+void walk_type(const MixArgs* a, int n, int dtype, hipStream_t s) {
+  MixMany many{};
+  for (int k = 0; k < n; ++k) {   // as many in one launch as have one shape and fit the grid
+    many.w[many.n++] = a[k];
+    many.seqs = a[k].seqs;
+    if (k + 1 < n && a[k + 1].da == a[k].da && a[k + 1].dc == a[k].dc && (int64_t)(many.n + 1) * a[k].seqs <= 65535) continue;
+    if (dtype == PC_DTYPE_BF16) walk<bf16, bf16, WALK>(many, s);
+    else if (dtype == PC_DTYPE_F16) walk<f16, float, WALK>(many, s);
+    else walk<float, float, WALK>(many, s);
+    many = MixMany{};
+  }
 }
 
 }  // namespace
 
-void launch_mix_walk(const MixArgs& a, int dtype, hipStream_t s) { walk_type<true>(a, dtype, s); }
-void launch_mix_states(const MixArgs& a, int dtype, hipStream_t s) { walk_type<false>(a, dtype, s); }
+void launch_mix_walk(const MixArgs* a, int n, int dtype, hipStream_t s) { walk_type<true>(a, n, dtype, s); }
+void launch_mix_states(const MixArgs* a, int n, int dtype, hipStream_t s) { walk_type<false>(a, n, dtype, s); }
 
-void launch_mix_scan(const MixScanArgs& a, hipStream_t s) {
-  launch_kernel(mix_scan, dim3((unsigned)((a.elems + 255) / 256), (unsigned)a.heads, (unsigned)a.seqs), dim3(256), 0, s, a);
+void launch_mix_scan(const MixScanArgs* a, int n, hipStream_t s) {
+  const bool both = n == 2 && 2 * (int64_t)a[0].seqs <= 65535;
+  for (int k = 0; k < n; k += both ? 2 : 1)
+    launch_kernel(mix_scan, dim3((unsigned)((a[k].elems + 255) / 256), (unsigned)a[k].heads, (unsigned)(a[k].seqs * (both ? 2 : 1))),
+                  dim3(256), 0, s, a[k], a[both ? 1 : k]);
 }
 
-void launch_mix_sum(const MixSumArgs& a, int dtype, hipStream_t s) {
-  const int64_t n = a.tokens * a.kv_heads * a.dim;
-  const dim3 grid((unsigned)((n + 255) / 256));
-  if (dtype == PC_DTYPE_F32) launch_kernel(mix_sum<float>, grid, dim3(256), 0, s, a);
-  else if (dtype == PC_DTYPE_F16) launch_kernel(mix_sum<f16>, grid, dim3(256), 0, s, a);
-  else launch_kernel(mix_sum<bf16>, grid, dim3(256), 0, s, a);
+void launch_mix_sum(const MixSumArgs& a, const MixSumArgs& b, int dtype, hipStream_t s) {
+  const int64_t n = a.tokens * a.kv_heads * std::max(a.dim, b.dim);
+  const dim3 grid((unsigned)((n + 255) / 256), 2);
+  if (dtype == PC_DTYPE_F32) launch_kernel(mix_sum<float>, grid, dim3(256), 0, s, a, b);
+  else if (dtype == PC_DTYPE_F16) launch_kernel(mix_sum<f16>, grid, dim3(256), 0, s, a, b);
+  else launch_kernel(mix_sum<bf16>, grid, dim3(256), 0, s, a, b);
 }
 
 void launch_mix_step(const MixStepArgs& a, int dtype, hipStream_t s) {

@@ -501,8 +501,7 @@ __device__ __forceinline__ void finish(const OrthGemmArgs& a, f32x16 (&acc)[NF][
 }
 
 // C = A B^T on TILE x TILE tiles, four waves of half of that, K in slices of 32
-// through an LDS ring of ST stages: two where two workgroups a compute unit
-// cover each other's waits, more where there are too few workgroups for that.
+// through an LDS ring of ST stages, KS slices a stage.
 // TILE 128, or 64 where tiles of 128 would leave compute units without one.  PL planes of each operand: 1 one product, 2
 // three.  Slot s of a row's four 16-byte chunks holds chunk s ^ ((row >> 2) & 3),
 // so the 16 rows a wave reads at a time lie in different banks.
@@ -511,8 +510,9 @@ __global__ __launch_bounds__(256, PL == 1 && EPI == ORTH_GRAM ? 3 : 2) void orth
   constexpr int SLICE = TILE * 64;   // bytes of an operand plane's slice
   constexpr int WT = TILE / 2, NF = WT / 32, LR = TILE / 4;   // a wave's rows, its 32-row blocks, the rows it loads
   constexpr int STAGE = 2 * PL * SLICE;
+  constexpr int KS = TILE == 64 ? 2 : 1;   // slices of a round (K is padded to four)
   constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
-  __shared__ __align__(16) char lds[ST * STAGE];
+  __shared__ __align__(16) char lds[ST * KS * STAGE];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int64_t z = blockIdx.z;
   int ti, tj;
@@ -527,7 +527,7 @@ __global__ __launch_bounds__(256, PL == 1 && EPI == ORTH_GRAM ? 3 : 2) void orth
   // 1 KB (16 rows of 64 bytes) an instruction: wave w loads rows LR w .. LR w + LR - 1
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const uint32_t src = (uint32_t)((lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16));
-  auto issue = [&](int stage, int kb) {
+  auto issue_slice = [&](int stage, int kb) {
 #pragma unroll
     for (int op = 0; op < 2; ++op) {
       const uint16_t* base = op ? pb : pa;
@@ -547,29 +547,37 @@ __global__ __launch_bounds__(256, PL == 1 && EPI == ORTH_GRAM ? 3 : 2) void orth
   int k0 = 0, nk = a.K / 32;   // the slices of this workgroup
   if constexpr (PART) {
     const int all = nk, part = (int)blockIdx.x % a.split;
-    k0 = (int)((int64_t)all * part / a.split);
-    nk = (int)((int64_t)all * (part + 1) / a.split) - k0;
+    k0 = (int)((int64_t)(all / 4) * part / a.split) * 4;   // fours of slices: whole rounds
+    nk = (int)((int64_t)(all / 4) * (part + 1) / a.split) * 4 - k0;
   }
-  // A slice's loads of a wave; slices behind the last are loaded again from the
-  // last, so that the count of loads in flight is the same in every round.
-  constexpr int LOADS = 2 * PL * (LR / 16);
-  for (int s = 0; s < ST - 1; ++s) issue(s, k0 + min(s, nk - 1));
+  // Loads of a wave in a round; rounds behind the last load its slices again, so
+  // that the count of loads in flight is the same in every round.
+  constexpr int LOADS = 2 * PL * (LR / 16) * KS;
+  const int rounds = nk / KS;
+  auto issue = [&](int stage, int round) {
+#pragma unroll
+    for (int k = 0; k < KS; ++k) issue_slice(stage * KS + k, k0 + min(round, rounds - 1) * KS + k);
+  };
+  for (int s = 0; s < ST - 1; ++s) issue(s, s);
   int cur = 0, fill = ST - 1;
-  for (int kb = 0; kb < nk; ++kb) {
+  f32x16 cross[NF == 1 ? 1 : NF][NF == 1 ? 1 : NF] = {};   // of the small planes, where one block a wave would wait for itself
+  for (int rd = 0; rd < rounds; ++rd) {
     __builtin_amdgcn_s_waitcnt(WaitVmLgkm<LOADS * (ST - 2)>::imm);
-    ring_barrier();   // slice kb is there, and every wave is done with the stage that is filled next
-    issue(fill, k0 + min(kb + ST - 1, nk - 1));
-    const char* st = lds + cur * STAGE;
+    ring_barrier();   // the round's slices are there, and every wave is done with the stage that is filled next
+    issue(fill, rd + ST - 1);
+    const char* st0 = lds + cur * (KS * STAGE);
     cur = cur + 1 == ST ? 0 : cur + 1;
     fill = fill + 1 == ST ? 0 : fill + 1;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
+    for (int k = 0; k < 2 * KS; ++k) {
+      const char* st = st0 + (k >> 1) * STAGE;
+      const int ch = 2 * (k & 1) + hf;
       f16x8 fa[PL][NF], fb[PL][NF];
 #pragma unroll
       for (int p = 0; p < PL; ++p)
 #pragma unroll
         for (int t = 0; t < NF; ++t) {
-          const int ra = wr + 32 * t + l32, rb = wc + 32 * t + l32, ch = 2 * ks + hf;
+          const int ra = wr + 32 * t + l32, rb = wc + 32 * t + l32;
           fa[p][t] = *(const f16x8*)(st + p * SLICE + ra * 64 + ((ch ^ ((ra >> 2) & 3)) * 16));
           fb[p][t] = *(const f16x8*)(st + (PL + p) * SLICE + rb * 64 + ((ch ^ ((rb >> 2) & 3)) * 16));
         }
@@ -578,17 +586,18 @@ __global__ __launch_bounds__(256, PL == 1 && EPI == ORTH_GRAM ? 3 : 2) void orth
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
           if constexpr (PL == 2) {
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[1][i], fb[0][j], acc[i][j], 0, 0, 0);
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[1][j], acc[i][j], 0, 0, 0);
+            f32x16& x = NF == 1 ? cross[0][0] : acc[i][j];
+            x = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[1][i], fb[0][j], x, 0, 0, 0);
+            x = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[1][j], x, 0, 0, 0);
           }
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[0][j], acc[i][j], 0, 0, 0);
         }
     }
   }
-
+  if constexpr (NF == 1 && PL == 2) acc[0][0] += cross[0][0];
   __builtin_amdgcn_s_waitcnt(WaitVmLgkm<0>::imm);   // no load may reach LDS after the workgroup's end
   if constexpr (PART) {   // [tile, part][wave][16 registers of four][lane]
-    float* to = a.parts + ((int64_t)blockIdx.x * 4 + wave) * (NF * NF * 1024) + lane * 4;
+    float* to = a.parts + ((z * gridDim.x + blockIdx.x) * 4 + wave) * (NF * NF * 1024) + lane * 4;
 #pragma unroll
     for (int i = 0; i < NF; ++i)
 #pragma unroll
@@ -605,17 +614,18 @@ __global__ __launch_bounds__(256, PL == 1 && EPI == ORTH_GRAM ? 3 : 2) void orth
 
 // The tiles that were split along K: one wave a quarter, its parts added in
 // their order.
-template <int EPI, typename IO>
+template <int EPI, int TILE, typename IO>
 __global__ __launch_bounds__(64) void orth_join(OrthGemmArgs a) {
-  constexpr int NF = 2;
+  constexpr int NF = TILE / 64, WT = TILE / 2;
   constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
-  __shared__ __align__(16) char lds[64 * 64 * 2];
+  __shared__ __align__(16) char lds[WT * WT * 2];
   const int wave = blockIdx.x & 3, tile = blockIdx.x >> 2;
+  const int64_t z = blockIdx.z;
   int ti, tj;
-  place<SYM>(a.full + tile, a.N / 128, ti, tj);
+  place<SYM>(a.full + tile, a.N / TILE, ti, tj);
   f32x16 acc[NF][NF] = {};
   for (int p = 0; p < a.split; ++p) {
-    const float* from = a.parts + (((int64_t)tile * a.split + p) * 4 + wave) * (NF * NF * 1024) + threadIdx.x * 4;
+    const float* from = a.parts + (((z * (gridDim.x >> 2) + tile) * a.split + p) * 4 + wave) * (NF * NF * 1024) + threadIdx.x * 4;
 #pragma unroll
     for (int i = 0; i < NF; ++i)
 #pragma unroll
@@ -627,7 +637,7 @@ __global__ __launch_bounds__(64) void orth_join(OrthGemmArgs a) {
           for (int r = 0; r < 4; ++r) acc[i][j][4 * q + r] += v[r];
         }
   }
-  finish<EPI, NF, IO>(a, acc, ti * 128 + (wave >> 1) * 64, tj * 128 + (wave & 1) * 64, ti != tj, 0, lds);
+  finish<EPI, NF, IO>(a, acc, ti * TILE + (wave >> 1) * WT, tj * TILE + (wave & 1) * WT, ti != tj, z, lds);
 }
 
 template <typename IO>
@@ -645,23 +655,35 @@ void gemm_tiles(const OrthGemmArgs& a, hipStream_t s) {
     const unsigned mt = (unsigned)(a.M / tile), nt = (unsigned)(a.N / tile);
     return dim3(sym ? mt * (mt + 1) / 2 : mt * nt, 1, (unsigned)a.io.batch);
   };
+  OrthGemmArgs b = a;
   dim3 g = grid(128);
   if ((int64_t)g.x * g.z < 256) {
-    launch_kernel(orth_gemm<EPI, PL, 64, 4, false, IO>, grid(64), dim3(256), 0, s, a);
+    // Tiles of 64.  Few of them with a long K are bound by a compute unit's
+    // loads in flight: they are split along K, so that more units load.
+    g = grid(64);
+    const int64_t tiles = (int64_t)g.x * g.z;
+    b.full = 0;
+    b.split = a.parts ? (int)std::min<int64_t>({4, ORTH_FEW_PARTS / tiles, a.K / 32 / 8}) : 1;
+    if (b.split > 1) {
+      const dim3 parts(g.x * (unsigned)b.split, 1, g.z), quarters(g.x * 4, 1, g.z);
+      launch_kernel(orth_gemm<EPI, PL, 64, 2, true, IO>, parts, dim3(256), 0, s, b);
+      launch_kernel(orth_join<EPI, 64, IO>, quarters, dim3(64), 0, s, b);
+    } else {
+      launch_kernel(orth_gemm<EPI, PL, 64, 2, false, IO>, g, dim3(256), 0, s, b);
+    }
     return;
   }
   // Whole rounds of one workgroup a compute unit take whole tiles; the tiles
   // left over, which would take another round for a few of them (528 tiles of a
   // symmetric 4096: 16), are split along K into up to 8 parts each.
-  OrthGemmArgs b = a;
-  b.full = (int)(g.x / 256 * 256);
-  const int rest = (int)g.x - b.full;
-  b.split = a.parts && rest ? std::min(ORTH_PARTS / rest, 8) : 1;
+  const int rest = (int)(g.x % 256);
+  b.full = (int)g.x - rest;
+  b.split = a.parts && g.z == 1 && rest ? std::min(ORTH_PARTS / rest, 8) : 1;
   if (b.split > 1) g.x = (unsigned)b.full;
   launch_kernel(orth_gemm<EPI, PL, 128, 2, false, IO>, g, dim3(256), 0, s, b);
   if (b.split > 1) {
     launch_kernel(orth_gemm<EPI, PL, 128, 2, true, IO>, dim3((unsigned)(rest * b.split)), dim3(256), 0, s, b);
-    launch_kernel(orth_join<EPI, IO>, dim3((unsigned)rest * 4), dim3(64), 0, s, b);
+    launch_kernel(orth_join<EPI, 128, IO>, dim3((unsigned)rest * 4), dim3(64), 0, s, b);
   }
 }
 template <int EPI, typename IO>

@@ -82,6 +82,12 @@ struct MixArgs {
   int32_t nsegs;
   int64_t seglen;
 };
+// Walks of one shape (da, dc), sequences and segments that a launch takes side
+// by side: the backward's three, or its two passes over the segments.
+struct MixMany {
+  MixArgs w[3];
+  int32_t n, seqs;
+};
 struct MixScanArgs {
   int32_t seqs, heads, nsegs, elems;
   int64_t tokens, seglen;
@@ -111,10 +117,10 @@ struct MixStepArgs {
 };
 constexpr int MIX_MAX_DIM = 128;
 constexpr int64_t MIX_MAX_STRIDE = 1 << 23;   // elements from a token to the next: 64 rows within 2^31 bytes
-void launch_mix_walk(const MixArgs& a, int dtype, hipStream_t s);    // outputs (and final states)
-void launch_mix_states(const MixArgs& a, int dtype, hipStream_t s);  // each segment's own state into seg
-void launch_mix_scan(const MixScanArgs& a, hipStream_t s);           // seg: own states -> states at the starts
-void launch_mix_sum(const MixSumArgs& a, int dtype, hipStream_t s);
+void launch_mix_walk(const MixArgs* a, int n, int dtype, hipStream_t s);    // outputs (and final states)
+void launch_mix_states(const MixArgs* a, int n, int dtype, hipStream_t s);  // each segment's own state into seg
+void launch_mix_scan(const MixScanArgs* a, int n, hipStream_t s);           // seg: own states -> states at the starts
+void launch_mix_sum(const MixSumArgs& a, const MixSumArgs& b, int dtype, hipStream_t s);
 void launch_mix_step(const MixStepArgs& a, int dtype, hipStream_t s);
 
 // ---- orthogonalised update ---------------------------------------------------
@@ -144,7 +150,8 @@ struct OrthMat {
   int64_t plane;        // elements from the hi to the lo plane
   int64_t batch;        // elements from one matrix to the next
 };
-constexpr int ORTH_PARTS = 512;       // partial tiles of a product's last round
+constexpr int ORTH_PARTS = 512;       // partial tiles (128) of a product's last round
+constexpr int ORTH_FEW_PARTS = 256;   // partial tiles (64) of a product with few tiles
 enum OrthEpi { ORTH_GRAM, ORTH_POLY, ORTH_APPLY, ORTH_OUT };
 struct OrthGemmArgs {
   int32_t M, N, K;      // padded; C [M, N] = A [M, K] B [N, K]^T
@@ -154,7 +161,7 @@ struct OrthGemmArgs {
   float sacc, sold;     // result = sacc acc + sold old
   float diag;           // POLY: + diag I
   int32_t cplanes;      // planes of the result that are written
-  float* parts;         // room for ORTH_PARTS tiles' partial sums, nullable (one matrix only)
+  float* parts;         // room for ORTH_PARTS or ORTH_FEW_PARTS tiles' partial sums, nullable
   int32_t full, split;  // set at the launch: tiles taken whole, parts of each tile behind them
   OrthIo io;            // OUT
 };

@@ -161,23 +161,26 @@ MixArgs mix_base(const pc_linear_attention* d, const Split& sp) {
   return a;
 }
 
-// The states at the segments' starts (nothing to do for one segment).
-void mix_starts(const pc_linear_attention* d, const MixArgs& a, const float* init, hipStream_t s) {
-  if (a.nsegs <= 1) return;
-  launch_mix_states(a, d->dtype, s);
+// The states at the segments' starts (nothing to do for one segment) of n walks
+// of the shape (dim_k, dim_v), from the states in a[k].init.
+void mix_starts(const pc_linear_attention* d, const MixArgs* a, int n, hipStream_t s) {
+  if (a[0].nsegs <= 1) return;
+  launch_mix_states(a, n, d->dtype, s);
   check_launch();
-  MixScanArgs c{};
-  c.seqs = a.seqs;
-  c.heads = a.heads;
-  c.nsegs = a.nsegs;
-  c.elems = d->dim_k * d->dim_v;
-  c.tokens = a.tokens;
-  c.seglen = a.seglen;
-  c.cu = a.cu;
-  c.log_decay = a.log_decay;
-  c.init = init;
-  c.seg = a.seg;
-  launch_mix_scan(c, s);
+  MixScanArgs c[2]{};
+  for (int k = 0; k < n; ++k) {
+    c[k].seqs = a[k].seqs;
+    c[k].heads = a[k].heads;
+    c[k].nsegs = a[k].nsegs;
+    c[k].elems = d->dim_k * d->dim_v;
+    c[k].tokens = a[k].tokens;
+    c[k].seglen = a[k].seglen;
+    c[k].cu = a[k].cu;
+    c[k].log_decay = a[k].log_decay;
+    c[k].init = a[k].init;
+    c[k].seg = a[k].seg;
+  }
+  launch_mix_scan(c, n, s);
   check_launch();
 }
 
@@ -214,9 +217,13 @@ OrthPlan orth_plan(int64_t batch, int32_t rows, int32_t cols, void* ws) {
   p.b = mat(p.mp, p.mp);
   p.part = p.total;
   p.total += (size_t)batch * ORTH_NORM_BLOCKS * sizeof(double);
-  p.split = batch == 1 && (int64_t)(p.mp / ORTH_TILE) * (p.np / ORTH_TILE) >= 256;
+  // partial sums of split tiles: of a last round of tiles of 128 (one matrix), or of few tiles of 64
+  const int64_t t128 = (int64_t)(p.mp / 128) * (p.np / 128) * batch, s64 = (int64_t)(p.mp / 64) * (p.mp / 64 + 1) / 2 * batch;
+  const size_t parts = batch == 1 && t128 >= 256 ? (size_t)ORTH_PARTS * 128 * 128 * sizeof(float)
+                       : 2 * s64 <= ORTH_FEW_PARTS ? (size_t)ORTH_FEW_PARTS * 64 * 64 * sizeof(float) : 0;
+  p.split = parts > 0;
   p.parts = (size_t)round_up((int64_t)p.total, 256);
-  if (p.split) p.total = p.parts + (size_t)ORTH_PARTS * ORTH_TILE * ORTH_TILE * sizeof(float);
+  if (p.split) p.total = p.parts + parts;
   return p;
 }
 
@@ -385,8 +392,8 @@ int pc_linear_attention_forward(int device, const pc_linear_attention* d, void* 
     a.init = d->state_in;
     a.fin = d->state_out;
     a.seg = (float*)((char*)ws + w.seg_f);
-    mix_starts(d, a, d->state_in, s);
-    launch_mix_walk(a, d->dtype, s);
+    mix_starts(d, &a, 1, s);
+    launch_mix_walk(&a, 1, d->dtype, s);
     check_launch();
   });
 }
@@ -410,61 +417,58 @@ int pc_linear_attention_backward(int device, const pc_linear_attention* d, void*
     const int group = d->heads / d->kv_heads, dk = d->dim_k, dv = d->dim_v;
     char* base = (char*)ws;
     const MixTensor q = tensor(d->q, 1), k = tensor(d->k, group), v = tensor(d->v, group), go = tensor(d->d_o, 1);
-    // the states of the forward pass at the segments' starts, for dq
+    // the walk that makes the forward's states (used for them alone), and dq,
+    // contracted with the state's columns
     MixArgs f = mix_base(d, mix_segments(d));
     f.off = 1;
     f.wscale = 1.0f;
-    f.seg = (float*)(base + w.seg_f);
-    MixArgs fs = f;
-    fs.da = dk;
-    fs.dc = dv;
-    fs.st_r = dv;
-    fs.st_c = 1;
-    fs.b = k;
-    fs.c = v;
-    mix_starts(d, fs, d->state_in, s);
-    // dq: contracted with the state's columns
-    f.da = dv;
-    f.dc = dk;
-    f.st_r = 1;
-    f.st_c = dv;
-    f.a = go;
-    f.b = v;
-    f.c = k;
-    f.oscale = d->scale;
     f.init = d->state_in;
-    f.out = d->d_q.data;
-    f.o_ts = d->d_q.token_stride;
-    f.o_hs = d->d_q.head_stride;
-    launch_mix_walk(f, d->dtype, s);
-    check_launch();
-    // the adjoint states from the sequences' ends.  The carried state is the
-    // one already decayed onto the token before (off 0), so it starts as the
-    // given gradient and ends as the gradient of state_in; scale belongs to a
-    // token's part in it.
-    MixArgs r = mix_base(d, mix_segments(d));
-    r.rev = 1;
-    r.off = 0;
-    r.wscale = d->scale;
-    r.oscale = 1.0f;
-    r.init = d->dstate_out;
-    r.seg = (float*)(base + w.seg_r);
-    MixArgs rk = r;
-    r.da = dk;
-    r.dc = dv;
-    r.st_r = dv;
-    r.st_c = 1;
-    r.a = k;
-    r.b = q;
-    r.c = go;
-    mix_starts(d, r, d->dstate_out, s);
-    rk.da = dv;
-    rk.dc = dk;
-    rk.st_r = 1;
-    rk.st_c = dv;
-    rk.a = v;
-    rk.b = go;
-    rk.c = q;
+    f.seg = (float*)(base + w.seg_f);
+    MixArgs q_walk = f;
+    f.da = dk;
+    f.dc = dv;
+    f.st_r = dv;
+    f.st_c = 1;
+    f.b = k;
+    f.c = v;
+    q_walk.da = dv;
+    q_walk.dc = dk;
+    q_walk.st_r = 1;
+    q_walk.st_c = dv;
+    q_walk.a = go;
+    q_walk.b = v;
+    q_walk.c = k;
+    q_walk.oscale = d->scale;
+    q_walk.out = d->d_q.data;
+    q_walk.o_ts = d->d_q.token_stride;
+    q_walk.o_hs = d->d_q.head_stride;
+    // dv and dk from the adjoint states, from the sequences' ends.  The carried
+    // state is the one already decayed onto the token before (off 0), so it
+    // starts as the given gradient and ends as the gradient of state_in; scale
+    // belongs to a token's part in it.
+    MixArgs v_walk = mix_base(d, mix_segments(d));
+    v_walk.rev = 1;
+    v_walk.off = 0;
+    v_walk.wscale = d->scale;
+    v_walk.oscale = 1.0f;
+    v_walk.init = d->dstate_out;
+    v_walk.seg = (float*)(base + w.seg_r);
+    MixArgs k_walk = v_walk;
+    v_walk.da = dk;
+    v_walk.dc = dv;
+    v_walk.st_r = dv;
+    v_walk.st_c = 1;
+    v_walk.a = k;
+    v_walk.b = q;
+    v_walk.c = go;
+    v_walk.fin = d->dstate_in;
+    k_walk.da = dv;
+    k_walk.dc = dk;
+    k_walk.st_r = 1;
+    k_walk.st_c = dv;
+    k_walk.a = v;
+    k_walk.b = go;
+    k_walk.c = q;
     auto target = [&](MixArgs& a, const pc_heads& to, size_t part, int dim) {
       if (group == 1) {
         a.out = to.data;
@@ -477,14 +481,19 @@ int pc_linear_attention_backward(int device, const pc_linear_attention* d, void*
         a.out_f32 = 1;
       }
     };
-    target(rk, d->d_k, w.dk, dk);
-    target(r, d->d_v, w.dv, dv);
-    launch_mix_walk(rk, d->dtype, s);
+    target(k_walk, d->d_k, w.dk, dk);
+    target(v_walk, d->d_v, w.dv, dv);
+    const MixArgs starts[2] = {f, v_walk};
+    mix_starts(d, starts, 2, s);
+    // dv's walk apart where it overwrites the states that dk's walk starts from
+    const MixArgs walks[3] = {q_walk, k_walk, v_walk};
+    const bool apart = d->dstate_in && d->dstate_in == d->dstate_out;
+    launch_mix_walk(walks, apart ? 2 : 3, d->dtype, s);
     check_launch();
-    // last, since dstate_in may be dstate_out
-    r.fin = d->dstate_in;
-    launch_mix_walk(r, d->dtype, s);
-    check_launch();
+    if (apart) {
+      launch_mix_walk(walks + 2, 1, d->dtype, s);
+      check_launch();
+    }
     if (group > 1 && d->num_tokens > 0) {
       auto sum = [&](const pc_heads& to, size_t part, int dim) {
         MixSumArgs m{};
@@ -498,11 +507,10 @@ int pc_linear_attention_backward(int device, const pc_linear_attention* d, void*
         m.out = to.data;
         m.o_ts = to.token_stride;
         m.o_hs = to.head_stride;
-        launch_mix_sum(m, d->dtype, s);
-        check_launch();
+        return m;
       };
-      sum(d->d_k, w.dk, dk);
-      sum(d->d_v, w.dv, dv);
+      launch_mix_sum(sum(d->d_k, w.dk, dk), sum(d->d_v, w.dv, dv), d->dtype, s);
+      check_launch();
     }
   });
 }
