@@ -559,10 +559,15 @@ __global__ __launch_bounds__(256) void mix_scan(MixScanArgs m0, MixScanArgs m1) 
   float* p = m.seg + ((int64_t)seq * m.nsegs * m.heads + head) * m.elems + e;
   const int64_t step = (int64_t)m.heads * m.elems;
   float run = m.init ? m.init[((int64_t)seq * m.heads + head) * m.elems + e] : 0.0f;
-  for (int s = 0; s < live; ++s) {
-    const float own = s + 1 < live ? p[s * step] : 0.0f;
-    p[s * step] = run;
-    run = run * ls + own;
+  for (int s0 = 0; s0 < live; s0 += 8) {   // eight loads in flight; the last segment's own state is not needed (nor made)
+    float own[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) own[k] = s0 + k + 1 < live ? p[(s0 + k) * step] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (s0 + k < live) p[(s0 + k) * step] = run;
+      run = run * ls + own[k];
+    }
   }
 }
 

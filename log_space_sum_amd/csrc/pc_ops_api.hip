@@ -104,22 +104,34 @@ void check_out(const pc_linear_attention* d, const pc_heads& t, int heads, int d
 }
 
 // Segments of the longest sequence.  One walk of a (sequence, head) is a chain
-// of chunks, so where sequences and heads are too few to fill the card the
-// sequences are cut; a cut costs a second reading of b and c and a state for
-// each segment and head, so a segment has at least four chunks.  Ragged batches
-// are counted as full sequences of the same number of tokens.
+// of chunks (about 3 us each when little else runs), so where sequences and
+// heads are too few to fill the card the sequences are cut.  A cut costs a
+// second reading of b and c, two more launches, and a state for each segment
+// and head that is written and read twice:
+//  - up to five chunks are not cut (one sequence of 300 x 4 heads x 64: 18 us
+//    whole, 20 in three; 16 of 200 x 8 heads: 18 and 24),
+//  - a segment has two chunks or more, and tokens enough that their own bytes
+//    are as many as the state's (two sequences of 4000 x 8 heads x 128: 53 us in
+//    segments of 256 tokens, 58 in segments of 128),
+//  - the scan goes through the segments one after the other, so their number is
+//    at most of the order of the root of the chunks' number.
+// Ragged batches are counted as full sequences of the same number of tokens.
 struct Split {
   int nsegs;
   int64_t len;
 };
 Split mix_segments(const pc_linear_attention* d) {
   const int64_t longest = std::max<int64_t>(1, std::min(d->max_seqlen, d->num_tokens));
+  const int64_t chunk = d->dtype == PC_DTYPE_BF16 ? 64 : 32, chunks = (longest + chunk - 1) / chunk;
+  if (chunks <= 5) return {1, chunks * chunk};
   const int64_t full = std::min<int64_t>(d->num_seqs, (d->num_tokens + longest - 1) / longest);
   const int64_t walks = std::max<int64_t>(1, full * d->heads);
   const int64_t room = std::max(d->dim_k, d->dim_v) > 64 ? 512 : 1024;   // walks that the card holds at a time
-  const int64_t least = d->dtype == PC_DTYPE_BF16 ? 256 : 128;
-  const int64_t n = std::max<int64_t>(1, std::min((room + walks - 1) / walks, (longest + least - 1) / least));
-  const int64_t len = ((longest + n - 1) / n + 63) / 64 * 64;
+  const double mean = 2.0 * d->dim_k * d->dim_v / (d->dim_k + d->dim_v);
+  const int64_t least = std::max(2 * chunk, (int64_t)(3.2 * mean / (d->dtype == PC_DTYPE_F32 ? 4 : 2)));
+  const int64_t n = std::max<int64_t>(1, std::min({(room + walks - 1) / walks, (longest + least - 1) / least,
+                                                   (int64_t)std::sqrt(32.0 * (double)chunks)}));
+  const int64_t len = ((longest + n - 1) / n + chunk - 1) / chunk * chunk;
   return {(int)((longest + len - 1) / len), len};
 }
 
