@@ -9,14 +9,19 @@
 // and the matrix itself is read twice and written once.  Squaring the matrix
 // costs half of the digits, so A, M and Q are held in 64 bits (one workgroup
 // a matrix, on the float64 matrix instruction); the result is then at least as
-// exact as float32 steps on X.
+// exact as float32 steps on X.  Bound by latency: 64 matrices of 1024 x 16
+// float32 take 12 us, of which the steps, a chain of 17 products in one wave,
+// are about four.
 //
 // Larger m: three products a step on the float16 matrix instruction.  An
 // operand is split into two float16 planes of a value scaled by a power of two
 // (hi + lo: 22 bits; the spectra are bounded, so the scales are known before
 // the call), and hi hi + hi lo + lo hi are summed in float32: the accuracy of
 // float32 steps at three times the cost of a 16-bit product.  The symmetric
-// products (A, A^2) compute the tiles on and above the diagonal only.
+// products (A, A^2) compute the tiles on and above the diagonal only.  Bound by
+// the matrix instructions: at 4096 x 4096 B X runs at 1.09 PFLOP/s of float16
+// products (380 us for three of 137 GFLOP; a library product reaches 1.08), A^2
+// at 1.0, A in one plane at 0.7 (its LDS reads).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -299,7 +304,8 @@ __global__ __launch_bounds__(NT) void orth_small(OrthIo io, OrthPoly poly) {
 // larger m: norm, planes, products
 // ---------------------------------------------------------------------------
 
-// Partial sums of the squares, in 64 bits; grid (ORTH_NORM_BLOCKS, batch).
+// Partial sums of the squares, in 64 bits (bound by G's bytes and the launch:
+// 4096 x 4096 bfloat16 14 us); grid (ORTH_NORM_BLOCKS, batch).
 template <typename IO>
 __global__ __launch_bounds__(256) void orth_norm(OrthIo io, double* part) {
   __shared__ double red[4];
@@ -339,12 +345,13 @@ __device__ __forceinline__ void planes_of(float v, uint16_t& hi, uint16_t& lo) {
 __device__ __forceinline__ float f16_value(uint16_t u) { return (float)__builtin_bit_cast(f16, u); }
 
 // The planes of X = scale G / (|G| + eps) and of its transpose, pads 0; one
-// 32 x 32 tile a block, grid (np / 32, mp / 32, batch).
+// 32 x 32 tile a block, grid (np / 32, mp / 32, batch).  Bound by the planes'
+// bytes: 40 us for 4096 x 4096 bfloat16 (33 MB read, 134 MB written).
 template <typename IO>
 __global__ __launch_bounds__(256) void orth_split(OrthIo io, const double* part, float scale, int mp, int np, OrthMat x,
                                                   OrthMat xt) {
   __shared__ float tile[32][33];
-  __shared__ float s_mul;
+  __shared__ double s_mul;   // (in 64 bits: 1 / |G| of a tiny matrix is past float32)
   const int p0 = blockIdx.x * 32, i0 = blockIdx.y * 32;
   const int64_t b = blockIdx.z;
   if (threadIdx.x < 64) {
@@ -353,7 +360,7 @@ __global__ __launch_bounds__(256) void orth_split(OrthIo io, const double* part,
     for (int k = 0; k < ORTH_NORM_BLOCKS / 64; ++k) s += part[b * ORTH_NORM_BLOCKS + 64 * k + threadIdx.x];
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
-    if (threadIdx.x == 0) s_mul = (float)((double)scale / (sqrt(s) + (double)io.eps));
+    if (threadIdx.x == 0) s_mul = (double)scale / (sqrt(s) + (double)io.eps);
   }
   const IO* g = (const IO*)io.g + b * io.g_batch;
   const int c = threadIdx.x & 31;
@@ -365,16 +372,16 @@ __global__ __launch_bounds__(256) void orth_split(OrthIo io, const double* part,
     tile[i - i0][p - p0] = v;
   }
   __syncthreads();
-  const float mul = s_mul;
+  const double mul = s_mul;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int r = (threadIdx.x >> 5) + 8 * k;
     uint16_t hi, lo;
-    planes_of(tile[r][c] * mul, hi, lo);
+    planes_of((float)(tile[r][c] * mul), hi, lo);
     const int64_t e = b * x.batch + panel(i0 + r, p0 + c, mp);
     x.p[e] = hi;
     x.p[e + x.plane] = lo;
-    planes_of(tile[c][r] * mul, hi, lo);
+    planes_of((float)(tile[c][r] * mul), hi, lo);
     const int64_t t = b * xt.batch + panel(p0 + r, i0 + c, np);
     xt.p[t] = hi;
     xt.p[t + xt.plane] = lo;
@@ -612,7 +619,8 @@ __global__ __launch_bounds__(256, PL == 1 && EPI == ORTH_GRAM ? 3 : 2) void orth
   }
 }
 
-// The tiles that were split along K: one wave a quarter, its parts added in
+// The tiles that were split along K (10 us for 16 tiles in 8 parts, bound by
+// latency): one wave a quarter, its parts added in
 // their order.
 template <int EPI, int TILE, typename IO>
 __global__ __launch_bounds__(64) void orth_join(OrthGemmArgs a) {
@@ -675,10 +683,11 @@ void gemm_tiles(const OrthGemmArgs& a, hipStream_t s) {
   }
   // Whole rounds of one workgroup a compute unit take whole tiles; the tiles
   // left over, which would take another round for a few of them (528 tiles of a
-  // symmetric 4096: 16), are split along K into up to 8 parts each.
+  // symmetric 4096: 16), are split along K into up to 8 parts each, of 8 slices
+  // or more.
   const int rest = (int)(g.x % 256);
   b.full = (int)g.x - rest;
-  b.split = a.parts && g.z == 1 && rest ? std::min(ORTH_PARTS / rest, 8) : 1;
+  b.split = a.parts && g.z == 1 && rest ? std::max(1, std::min({ORTH_PARTS / rest, 8, a.K / 32 / 8})) : 1;
   if (b.split > 1) g.x = (unsigned)b.full;
   launch_kernel(orth_gemm<EPI, PL, 128, 2, false, IO>, g, dim3(256), 0, s, b);
   if (b.split > 1) {

@@ -432,9 +432,169 @@ def test_orthogonalize_edges(rows, cols):
         L.pc_orthogonalize(g, out, steps=4, coefficients=(20.0, 1.0, 1.0), ws=L.orthogonalize_workspace(g))
 
 
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(2100, 2100), (25600, 300), (1100, 4200)])
+def test_orthogonalize_many_tiles(rows, cols, typ):
+    """Sizes with whole rounds of tiles and some left over, with a long and a short K; the steps in float64 on the GPU."""
+    import log_space_sum_amd as L
+    torch, types = T()
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(rows)
+    g = (torch.randn((rows, cols), generator=gen, device=DEV) * 0.1).to(types[typ])
+    out = torch.empty_like(g)
+    L.pc_orthogonalize(g, out, ws=L.orthogonalize_workspace(g))
+    m, n = sorted((rows, cols))
+    x = g.double().t() if rows > cols else g.double()
+    x = x / (x.square().sum().sqrt() + 1e-7)
+    short = lambda v: (v * 2.0 ** 13).half().double() / 2.0 ** 13  # noqa: E731
+    for step, (a, b, c) in enumerate([QUINTIC] * 5):
+        r = [short] * 3 if typ == "bf16" and step < 2 else [short if typ == "bf16" else (lambda v: v)] + [lambda v: v] * 2
+        A = r[0](x) @ r[0](x).t().contiguous()
+        x = a * x + r[2](b * A + c * (r[1](A) @ r[1](A))) @ r[2](x)
+    ref = x.t() if rows > cols else x
+    tol = _orth_tol([QUINTIC] * 5, m, n, typ)
+    d = out.double() - ref
+    assert float(d.norm()) <= tol + U[typ] * float(ref.norm())
+    assert float(d.abs().max()) <= tol / 10 + U[typ] * float(ref.abs().max())
+    first = out.clone()
+    L.pc_orthogonalize(g, out, ws=L.orthogonalize_workspace(g))
+    assert torch.equal(first, out)
+
+
+def test_orthogonalize_tiny_values():
+    """Matrices whose norm's inverse is past float32, without eps."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    rng = np.random.default_rng(11)
+    for rows, cols in ((20, 40), (70, 140)):
+        g = put(rng.normal(size=(rows, cols)) * 1e-37)
+        out = torch.empty_like(g)
+        L.pc_orthogonalize(g, out, eps=0.0, ws=L.orthogonalize_workspace(g))
+        ref = R.orthogonalize(get(g), [QUINTIC] * 5, 0.0)
+        assert np.linalg.norm(get(out) - ref) <= _orth_tol([QUINTIC] * 5, rows, cols, "f32")
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
+
+def test_offsets_past_32_bits():
+    """Rows, tokens, slots and matrices that lie more than 2^31 elements into their buffers."""
+    import log_space_sum_amd as L
+    torch, types = T()
+    rng = np.random.default_rng(12)
+    far = 2 ** 31 + 64
+    buf = torch.empty(far + 2 ** 22, dtype=types["bf16"], device=DEV)
+    # layer norm: two rows 2^31 apart
+    x = torch.as_strided(buf, (2, 100), (far, 1))
+    x.copy_(put(rng.normal(size=(2, 100)), "bf16"))
+    y = torch.empty((2, 100), device=DEV, dtype=types["bf16"])
+    L.pc_layer_norm_forward(x, None, None, y)
+    ry, _, _ = R.layer_norm(get(x))
+    near(y, ry, U["bf16"] * np.abs(ry) + 100 * E32 * 8, "norm")
+    # orthogonalise: two matrices 2^31 apart, thin and wide
+    for rows, cols in ((8, 50), (70, 90)):
+        g = torch.as_strided(buf, (2, rows, cols), (far, cols, 1))
+        g.copy_(put(rng.normal(size=(2, rows, cols)), "bf16"))
+        out = torch.empty((2, rows, cols), device=DEV, dtype=types["bf16"])
+        L.pc_orthogonalize(g, out, ws=L.orthogonalize_workspace(g))
+        for b in range(2):
+            ref = R.orthogonalize(get(g)[b], [QUINTIC] * 5, 1e-7, _operands("bf16", min(rows, cols), 5))
+            assert np.linalg.norm(get(out)[b] - ref) <= _orth_tol([QUINTIC] * 5, *sorted((rows, cols)), "bf16") + U["bf16"] * np.linalg.norm(ref)
+    # linear attention: the last tokens of a long buffer
+    H, d = 4, 64
+    n = buf.numel() // (H * d)
+    t = buf[:n * H * d].view(n, H, d)
+    t[-90:] = put(rng.normal(size=(90, H, d)), "bf16")
+    cu = torch.tensor([n - 90, n - 20, n], dtype=torch.int32, device=DEV)
+    g = put(np.array([-0.1, 0.0, -1.0, -0.01]))
+    s = torch.empty((2, H, d, d), device=DEV)
+    o = torch.empty_like(t)
+    L.pc_linear_attention_forward(t, t, t, g, o, cu, 70, state_out=s, ws=L.linear_attention_workspace(t, t, t, cu, 70))
+    z = get(t[-90:])
+    ro, rs = R.linear_attention(z, z, z, get(g), [0, 70, 90], d ** -0.5)
+    mo, ms = R.linear_attention(*[np.abs(z)] * 3, get(g), [0, 70, 90], d ** -0.5)
+    near(o[-90:], ro, _bound("bf16", 200, mo, ro), "o")
+    near(s, rs, 200 * E32 * ms, "state")
+    del o, t, buf, x, g
+    torch.cuda.empty_cache()
+    # a pool of states with more than 2^31 elements
+    slots, H, d = 131075, 4, 64
+    pool = torch.empty((slots, H, d, d), device=DEV)
+    last = torch.tensor([slots - 1, slots, slots - 2], dtype=torch.int32, device=DEV)
+    pool[-2:] = 0
+    q = put(rng.normal(size=(3, H, d)))
+    o, g = torch.zeros_like(q), put(np.zeros(4))
+    L.pc_linear_attention_step(q, q, q, g, pool, o, last, scale=1.0)
+    z = get(q)
+    want = np.einsum("bhk,bhk->bh", z, z)[..., None] * z
+    want[1] = 0
+    near(o, want, 80 * E32 * np.einsum("bhk,bhk->bh", z, z)[..., None] * np.abs(z), "step")
+
+
+def test_linear_attention_many_short_sequences():
+    """More sequences than one grid takes three times over; one token each."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    rng = np.random.default_rng(13)
+    n, H, d = 30000, 1, 4
+    q, k, v, do = (put(rng.normal(size=(n, H, d))) for _ in range(4))
+    cu = torch.arange(n + 1, dtype=torch.int32, device=DEV)
+    s0, ds = put(rng.normal(size=(n, H, d, d))), put(rng.normal(size=(n, H, d, d)))
+    g, lam = put(np.array([-0.5])), np.exp(-0.5)
+    o, s1, d0 = torch.empty_like(q), torch.empty_like(s0), torch.empty_like(s0)
+    dq, dk, dv = (torch.empty_like(q) for _ in range(3))
+    L.pc_linear_attention_forward(q, k, v, g, o, cu, 1, s0, s1, 1.0, L.linear_attention_workspace(q, k, v, cu, 1))
+    L.pc_linear_attention_backward(do, q, k, v, g, dq, dk, dv, cu, 1, s0, ds, d0, 1.0,
+                                   L.linear_attention_workspace(q, k, v, cu, 1, backward=True))
+    Q, K, V, G, S, D = (get(x) for x in (q, k, v, do, s0, ds))
+    S = lam * S + K[..., :, None] * V[..., None, :]
+    D = D + Q[..., :, None] * G[..., None, :]
+    tol = 64 * E32 * 200   # sums of four products of normal values, at most about 6^3
+    for got, want in ((s1, S), (o, np.einsum("thk,thkv->thv", Q, S)), (dq, np.einsum("thkv,thv->thk", S, G)),
+                      (dk, np.einsum("thkv,thv->thk", D, V)), (dv, np.einsum("thkv,thk->thv", D, K)), (d0, lam * D)):
+        near(got, want, tol, "one token")
+
+
+def test_calls_on_two_streams_at_once():
+    """Two calls of each operator at the same time, on their own streams and workspaces, give the results of one alone."""
+    import log_space_sum_amd as L
+    torch, types = T()
+    rng = np.random.default_rng(14)
+    data = []
+    for _ in range(2):
+        q, k, v, do, cu, dcu = _att(rng, [900, 500], 4, 2, 64, 64, "bf16")
+        m = put(rng.normal(size=(1400, 256)), "bf16")
+        data.append(dict(q=q, k=k, v=v, do=do, cu=dcu, m=m, g=put(DECAYS[:4]), o=torch.empty_like(q), dq=torch.empty_like(q),
+                         dk=torch.empty_like(k), dv=torch.empty_like(v), up=torch.empty_like(m), dx=torch.empty_like(m),
+                         w=torch.empty(256, device=DEV), mean=torch.zeros(1400, device=DEV), rstd=torch.ones(1400, device=DEV),
+                         w1=L.linear_attention_workspace(q, k, v, dcu), w2=L.linear_attention_workspace(q, k, v, dcu, backward=True),
+                         w3=L.orthogonalize_workspace(m), w4=L.layer_norm_workspace(1400, 256, DEV)))
+    names = ("o", "dq", "dk", "dv", "up", "dx", "w")
+
+    def calls(s):
+        L.pc_linear_attention_forward(s["q"], s["k"], s["v"], s["g"], s["o"], s["cu"], ws=s["w1"])
+        L.pc_linear_attention_backward(s["do"], s["q"], s["k"], s["v"], s["g"], s["dq"], s["dk"], s["dv"], s["cu"], ws=s["w2"])
+        L.pc_orthogonalize(s["m"], s["up"], ws=s["w3"])
+        L.pc_layer_norm_backward(s["m"], s["m"], None, s["mean"], s["rstd"], s["dx"], s["w"], None, s["w4"])
+
+    for s in data:
+        calls(s)
+    torch.cuda.synchronize()
+    want = [{n: s[n].clone() for n in names} for s in data]
+    streams = [torch.cuda.Stream() for _ in data]
+    for _ in range(5):
+        for s in data:
+            for n in names:
+                s[n].fill_(3)
+        torch.cuda.synchronize()
+        for s, st in zip(data, streams):
+            with torch.cuda.stream(st):
+                calls(s)
+        torch.cuda.synchronize()
+        for s, w in zip(data, want):
+            assert all(torch.equal(s[n], w[n]) for n in names)
+
 
 def test_captured_calls_replay():
     """All calls in one captured graph on a stream of its own; every replay equals the eager results on new inputs,
