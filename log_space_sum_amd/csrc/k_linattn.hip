@@ -552,9 +552,11 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
 // The states at the segments' starts from the segments' own states, in place
 // (bound by the states' bytes: 16 segments x 32 heads x 128 x 128, 13 us or 5 TB/s):
 // start_0 = init, start_{s+1} = l^seglen start_s + own_s.
+// EV elements a thread; four segments' loads in flight.
+template <int EV>
 __global__ __launch_bounds__(256) void mix_scan(MixScanArgs m0, MixScanArgs m1) {
   const MixScanArgs& m = (int)blockIdx.z < m0.seqs ? m0 : m1;
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * EV;
   const int head = blockIdx.y, seq = blockIdx.z % m0.seqs;
   if (e >= m.elems) return;
   int64_t t0 = 0, t1 = m.tokens;
@@ -566,15 +568,20 @@ __global__ __launch_bounds__(256) void mix_scan(MixScanArgs m0, MixScanArgs m1) 
   const float ls = decay_pow(m.log_decay[head], (float)m.seglen);
   float* p = m.seg + ((int64_t)seq * m.nsegs * m.heads + head) * m.elems + e;
   const int64_t step = (int64_t)m.heads * m.elems;
-  float run = m.init ? m.init[((int64_t)seq * m.heads + head) * m.elems + e] : 0.0f;
-  for (int s0 = 0; s0 < live; s0 += 8) {   // eight loads in flight; the last segment's own state is not needed (nor made)
-    float own[8];
+  struct Some {
+    float v[EV];
+  } run = {}, own[4];
+  if (m.init) __builtin_memcpy(&run, m.init + ((int64_t)seq * m.heads + head) * m.elems + e, sizeof(run));
+  // (the last segment's own state is not needed, nor made: its place is loaded and not used)
+  for (int s0 = 0; s0 < live; s0 += 4) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) own[k] = s0 + k + 1 < live ? p[(s0 + k) * step] : 0.0f;
+    for (int k = 0; k < 4; ++k) __builtin_memcpy(&own[k], p + min(s0 + k, live - 1) * step, sizeof(run));
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (s0 + k < live) p[(s0 + k) * step] = run;
-      run = run * ls + own[k];
+    for (int k = 0; k < 4; ++k) {
+      if (s0 + k >= live) break;
+      __builtin_memcpy(p + (s0 + k) * step, &run, sizeof(run));
+#pragma unroll
+      for (int v = 0; v < EV; ++v) run.v[v] = run.v[v] * ls + own[k].v[v];
     }
   }
 }
@@ -726,9 +733,12 @@ void launch_mix_states(const MixArgs* a, int n, int dtype, hipStream_t s) { walk
 
 void launch_mix_scan(const MixScanArgs* a, int n, hipStream_t s) {
   const bool both = n == 2 && 2 * (int64_t)a[0].seqs <= 65535;
-  for (int k = 0; k < n; k += both ? 2 : 1)
-    launch_kernel(mix_scan, dim3((unsigned)((a[k].elems + 255) / 256), (unsigned)a[k].heads, (unsigned)(a[k].seqs * (both ? 2 : 1))),
-                  dim3(256), 0, s, a[k], a[both ? 1 : k]);
+  for (int k = 0; k < n; k += both ? 2 : 1) {
+    const int ev = a[k].elems % 4 == 0 ? 4 : 1;
+    const dim3 grid((unsigned)((a[k].elems / ev + 255) / 256), (unsigned)a[k].heads, (unsigned)(a[k].seqs * (both ? 2 : 1)));
+    if (ev == 4) launch_kernel(mix_scan<4>, grid, dim3(256), 0, s, a[k], a[both ? 1 : k]);
+    else launch_kernel(mix_scan<1>, grid, dim3(256), 0, s, a[k], a[both ? 1 : k]);
+  }
 }
 
 void launch_mix_sum(const MixSumArgs& a, const MixSumArgs& b, int dtype, hipStream_t s) {

@@ -345,13 +345,16 @@ __device__ __forceinline__ void planes_of(float v, uint16_t& hi, uint16_t& lo) {
 __device__ __forceinline__ float f16_value(uint16_t u) { return (float)__builtin_bit_cast(f16, u); }
 
 // The planes of X = scale G / (|G| + eps) and of its transpose, pads 0; one
-// 32 x 32 tile a block, grid (np / 32, mp / 32, batch).  Bound by the planes'
-// bytes: 40 us for 4096 x 4096 bfloat16 (33 MB read, 134 MB written).
+// 32 x 32 tile a block, grid (np / 32, mp / 32, batch).  Such a tile of a panel
+// is one run of 2 KB: half of the threads write X's, 16 bytes of a plane each,
+// half its transpose's.  Bound by the planes' bytes (4096 x 4096 bfloat16: 33 MB
+// read, 134 MB written, 40 us).
 template <typename IO>
 __global__ __launch_bounds__(256) void orth_split(OrthIo io, const double* part, float scale, int mp, int np, OrthMat x,
                                                   OrthMat xt) {
   __shared__ float tile[32][33];
-  __shared__ double s_mul;   // (in 64 bits: 1 / |G| of a tiny matrix is past float32)
+  __shared__ float s_mant;   // scale / (|G| + eps) = s_mant 2^s_exp: of a tiny matrix it is past float32
+  __shared__ int s_exp;
   const int p0 = blockIdx.x * 32, i0 = blockIdx.y * 32;
   const int64_t b = blockIdx.z;
   if (threadIdx.x < 64) {
@@ -360,7 +363,11 @@ __global__ __launch_bounds__(256) void orth_split(OrthIo io, const double* part,
     for (int k = 0; k < ORTH_NORM_BLOCKS / 64; ++k) s += part[b * ORTH_NORM_BLOCKS + 64 * k + threadIdx.x];
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
-    if (threadIdx.x == 0) s_mul = (double)scale / (sqrt(s) + (double)io.eps);
+    if (threadIdx.x == 0) {
+      int e;
+      s_mant = (float)frexp((double)scale / (sqrt(s) + (double)io.eps), &e);
+      s_exp = e;
+    }
   }
   const IO* g = (const IO*)io.g + b * io.g_batch;
   const int c = threadIdx.x & 31;
@@ -372,20 +379,17 @@ __global__ __launch_bounds__(256) void orth_split(OrthIo io, const double* part,
     tile[i - i0][p - p0] = v;
   }
   __syncthreads();
-  const double mul = s_mul;
+  const float mant = s_mant;
+  const int ex = s_exp;
+  const bool turned = threadIdx.x >= 128;
+  const int row = (threadIdx.x & 127) >> 2, k8 = (threadIdx.x & 3) * 8;
+  uint16_t hi[8], lo[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int r = (threadIdx.x >> 5) + 8 * k;
-    uint16_t hi, lo;
-    planes_of((float)(tile[r][c] * mul), hi, lo);
-    const int64_t e = b * x.batch + panel(i0 + r, p0 + c, mp);
-    x.p[e] = hi;
-    x.p[e + x.plane] = lo;
-    planes_of((float)(tile[c][r] * mul), hi, lo);
-    const int64_t t = b * xt.batch + panel(p0 + r, i0 + c, np);
-    xt.p[t] = hi;
-    xt.p[t + xt.plane] = lo;
-  }
+  for (int e = 0; e < 8; ++e) planes_of(ldexpf(turned ? tile[k8 + e][row] : tile[row][k8 + e], ex) * mant, hi[e], lo[e]);
+  const OrthMat& to = turned ? xt : x;
+  uint16_t* at = to.p + b * to.batch + (turned ? panel(p0 + row, i0 + k8, np) : panel(i0 + row, p0 + k8, mp));
+  __builtin_memcpy(__builtin_assume_aligned(at, 16), hi, 16);
+  __builtin_memcpy(__builtin_assume_aligned(at + to.plane, 16), lo, 16);
 }
 
 // Row and column of a tile: on and above the diagonal, column after column, or
