@@ -27,12 +27,15 @@
 // sequences, see mix_segments) that walk side by side: one pass makes each
 // segment's own state, a scan joins them, and the walk starts from there.
 //
-// What bounds it: at dim 128 the matrix instructions (29% of the time busy), the
-// vector instructions that split planes (43%) and LDS (45%) share a walk, at 2.9
+// What bounds it: at dim 128 the matrix instructions (busy 32% of the time), the
+// vector instructions that split planes (47%) and LDS (51%) share a walk, at 2.9
 // TB/s of the tokens' bytes; at dim 64 and below, or with few tokens, the chain
 // of chunks.  16384 tokens x 32 heads x 128 bfloat16 (541 MB): segments' states
-// 87 us, scan 14, walk 190 when profiled, 248 us together unprofiled.  Waves of
-// 32 columns (four of them) measured the same, 12% slower for float32.
+// 87 us, scan 13, walk 190 when profiled, 243 us together unprofiled.  Measured
+// and not taken: waves of 32 columns (the same, 12% slower for float32), the
+// state's update before the inside products' barrier (the same at dim 64, 5%
+// slower at 128), tiles with exchanged chunks instead of padding (half of the
+// bank conflicts, but registers past the limit of two workgroups: the same).
 //
 // Precision: bfloat16 tensors are multiplied in bfloat16 with float32 sums.
 // The decay weights are not exact in bfloat16: l^{n-off-j} c_j is split into
@@ -74,7 +77,8 @@ template <>
 struct Ops<bf16> {
   static constexpr int C = 64;       // tokens of a chunk
   static constexpr int EV = 8;       // elements of a staged unit
-  // row padding of the tiles read by rows, and by columns (16 lanes' 4 rows of 32 bytes lie in different banks then)
+  // row padding of the tiles read by rows, and by columns (16 lanes' 4 rows of 32 bytes lie in different banks then);
+  // b's tile is read by both in a walk (there the first measured 3% faster)
   static constexpr int PAD = 8, CPAD = 16;
   static constexpr int CPLANES = 3;  // planes of the weighted c, and of the state in the output's product
   static constexpr int SPLANES = 2;
@@ -247,7 +251,7 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
   using quad = typename O::quad;
   constexpr int C = O::C, CB = C / 16, EV = O::EV, NT = 64 * NW;
   constexpr int DA = 16 * DKB, DC = 16 * NW;
-  constexpr int LA = DA + O::PAD, LB = DA + O::CPAD, LC = DC + O::CPAD, LP = C + O::PAD;
+  constexpr int LA = DA + O::PAD, LB = DA + (WALK ? O::PAD : O::CPAD), LC = DC + O::CPAD, LP = C + O::PAD;
   constexpr int UA = C * DA / EV / NT, UC = C * DC / EV / NT;   // staged units of a thread
   static_assert(UA * NT * EV == C * DA && UC * NT * EV == C * DC, "whole units");
   constexpr int CP = O::CPLANES, SP = O::SPLANES, PP = O::PPLANES;
