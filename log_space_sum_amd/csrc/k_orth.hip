@@ -407,6 +407,15 @@ __device__ __forceinline__ void place(int tile, int nt, int& ti, int& tj) {
   }
 }
 
+// Between a wave's writes to its own LDS and its lanes' reads of each other's
+// (and back): LDS takes a wave's operations in their order, so only the
+// compiler, for which differently typed accesses are independent, has to keep it.
+__device__ __forceinline__ void wave_fence() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_wave_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
 // What is done with a wave's WT x WT piece of a product, at row row_w and column
 // col_w: scaled, the other terms added, rounded and written.  A lane holds rows
 // 8 (r / 4) + 4 hf + r % 4 of column l32 of every 32 x 32 block.  Panels go
@@ -434,6 +443,7 @@ __device__ __forceinline__ void finish(const OrthGemmArgs& a, f32x16 (&acc)[NF][
       for (int n = 0; n < LINES; ++n) in[n] = *(const uint4*)(line(a.old, a.M, row_w, col_w, n) + p * a.old.plane);
 #pragma unroll
       for (int n = 0; n < LINES; ++n) *(uint4*)(mine + n * 1024 + lane * 16) = in[n];
+      wave_fence();
 #pragma unroll
       for (int i = 0; i < NF; ++i)
 #pragma unroll
@@ -441,7 +451,7 @@ __device__ __forceinline__ void finish(const OrthGemmArgs& a, f32x16 (&acc)[NF][
 #pragma unroll
           for (int r = 0; r < 16; ++r)
             acc[i][j][r] += a.sold * f16_value(*(const uint16_t*)(mine + ((j * WT + 32 * i + 8 * (r >> 2) + 4 * hf + (r & 3)) * 32 + l32) * 2));
-      __builtin_amdgcn_wave_barrier();
+      wave_fence();
     }
   }
   if constexpr (EPI == ORTH_POLY) {   // a I
@@ -479,10 +489,11 @@ __device__ __forceinline__ void finish(const OrthGemmArgs& a, f32x16 (&acc)[NF][
 #pragma unroll
           for (int r = 0; r < 16; ++r)
             *(f16*)(mine + ((j * WT + 32 * i + 8 * (r >> 2) + 4 * hf + (r & 3)) * 32 + l32) * 2) = (f16)acc[i][j][r];
+      wave_fence();
 #pragma unroll
       for (int n = 0; n < LINES; ++n)
         *(uint4*)(line(a.c, a.M, row_w, col_w, n) + p * a.c.plane) = *(const uint4*)(mine + n * 1024 + lane * 16);
-      __builtin_amdgcn_wave_barrier();
+      wave_fence();
       if (mirror) {
 #pragma unroll
         for (int i = 0; i < NF; ++i)
@@ -495,10 +506,11 @@ __device__ __forceinline__ void finish(const OrthGemmArgs& a, f32x16 (&acc)[NF][
               for (int r = 0; r < 4; ++r) h[r] = (f16)acc[i][j][4 * q + r];
               __builtin_memcpy(__builtin_assume_aligned(mine + ((i * WT + 32 * j + l32) * 32 + 8 * q + 4 * hf) * 2, 8), h, 8);
             }
+        wave_fence();
 #pragma unroll
         for (int n = 0; n < LINES; ++n)
           *(uint4*)(line(turned, a.N, col_w, row_w, n) + p * turned.plane) = *(const uint4*)(mine + n * 1024 + lane * 16);
-        __builtin_amdgcn_wave_barrier();
+        wave_fence();
       }
       // what the plane leaves
 #pragma unroll
@@ -512,10 +524,12 @@ __device__ __forceinline__ void finish(const OrthGemmArgs& a, f32x16 (&acc)[NF][
 }
 
 // C = A B^T on TILE x TILE tiles, four waves of half of that, K in slices of 32
-// through an LDS ring of ST stages, KS slices a stage.
-// TILE 128, or 64 where tiles of 128 would leave compute units without one.  PL planes of each operand: 1 one product, 2
-// three.  Slot s of a row's four 16-byte chunks holds chunk s ^ ((row >> 2) & 3),
-// so the 16 rows a wave reads at a time lie in different banks.
+// through an LDS ring of ST stages of KS slices.  TILE 128, or 64 where tiles of
+// 128 would leave compute units without one (3 x 333 x 1000, A: 25 us in tiles
+// of 128, 13 in tiles of 64, 11 split along K).  PL planes of each operand: 1
+// one product, 2 three.  Slot s of a row's four 16-byte chunks holds chunk
+// s ^ ((row >> 2) & 3), so the 16 rows a wave reads at a time lie in different
+// banks.
 template <int EPI, int PL, int TILE, int ST, bool PART, typename IO>
 __global__ __launch_bounds__(256, PL == 1 && EPI == ORTH_GRAM ? 3 : 2) void orth_gemm(OrthGemmArgs a) {
   constexpr int SLICE = TILE * 64;   // bytes of an operand plane's slice
@@ -623,9 +637,8 @@ __global__ __launch_bounds__(256, PL == 1 && EPI == ORTH_GRAM ? 3 : 2) void orth
   }
 }
 
-// The tiles that were split along K (10 us for 16 tiles in 8 parts, bound by
-// latency): one wave a quarter, its parts added in
-// their order.
+// The tiles that were split along K: one wave a quarter, its parts added in
+// their order (16 tiles in 8 parts: 10 us, bound by latency).
 template <int EPI, int TILE, typename IO>
 __global__ __launch_bounds__(64) void orth_join(OrthGemmArgs a) {
   constexpr int NF = TILE / 64, WT = TILE / 2;
