@@ -22,8 +22,12 @@ __device__ __forceinline__ void lds_load16(const void* sbase, uint32_t voff, uin
   const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
   const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b);
   const uint64_t sb = (hi << 32) | lo;
-  // one wait state between the SALU write of M0 and the LDS DMA reading it
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sb), "s"(m0)
+  // Wait states that the compiler does not see to inside the assembly: one
+  // between the SALU write of M0 and the LDS DMA that reads it, and five between
+  // the VALU's write of the base (a v_readfirstlane, which may be the
+  // instruction in front) and the vector load that reads it, which would take
+  // the registers' old value, an earlier load's base.
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sb), "s"(m0)
                : "memory", "m0");
 }
 
@@ -53,7 +57,7 @@ __device__ __forceinline__ void lds_load4(const void* sbase, uint32_t voff, uint
   const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
   const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b);
   const uint64_t sb = (hi << 32) | lo;
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(sb), "s"(m0)
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(sb), "s"(m0)
                : "memory", "m0");
 }
 

@@ -1,6 +1,7 @@
 """The operators in front of a conditional circuit on the CPU: the float64 definitions against differences and
 against each other, and every refusal of the C ABI (refused before any device work)."""
 import ctypes as C
+import re
 
 import numpy as np
 import pytest
@@ -211,3 +212,16 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         L.pc_linear_attention_step(q[0], q, q, None, q, q)
     with pytest.raises(ValueError, match="dimensions"):
         L.pc_orthogonalize(x[0], x[0])
+
+
+@pytest.mark.parametrize("load", ["global_load_lds_dwordx4", "global_load_lds_dword "])
+def test_ring_loads_wait_for_their_base(load):
+    """Inline assembly gets no wait states from the compiler: five between the VALU's write of the base's scalar
+    registers, which may be the instruction in front, and the vector load that reads them."""
+    import pathlib
+    text = (pathlib.Path(L.__file__).parent / "csrc" / "pc_ring.h").read_text()
+    found = [a for a in re.findall(r'asm volatile\("([^"]*)"', text) if load in a]
+    assert len(found) == 1
+    before = found[0].replace("\\t", "").split("\\n")
+    at = next(i for i, op in enumerate(before) if op.startswith(load))
+    assert sum(int(op.split()[1]) + 1 if op.startswith("s_nop") else 1 for op in before[:at]) >= 5
