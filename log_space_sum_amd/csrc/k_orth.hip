@@ -336,8 +336,12 @@ __global__ __launch_bounds__(256) void orth_norm(OrthIo io, double* part) {
   if (threadIdx.x == 0) part[(int64_t)blockIdx.y * ORTH_NORM_BLOCKS + blockIdx.x] = red[0] + red[1] + red[2] + red[3];
 }
 
-// A value's planes.
+// A value's planes.  The value is rounded to float32 first, for both: the
+// compiler may fuse the product behind v with one of its conversions and not with
+// the other, and where v then lies halfway the low plane belongs to another high
+// one (off by 2^-11 in one element of some thousands: 7e-6 of the result).
 __device__ __forceinline__ void planes_of(float v, uint16_t& hi, uint16_t& lo) {
+  asm volatile("" : "+v"(v));
   const f16 h = (f16)v;
   hi = __builtin_bit_cast(uint16_t, h);
   lo = __builtin_bit_cast(uint16_t, (f16)(v - (float)h));

@@ -474,6 +474,37 @@ def test_orthogonalize_tiny_values():
         assert np.linalg.norm(get(out) - ref) <= _orth_tol([QUINTIC] * 5, rows, cols, "f32")
 
 
+@pytest.mark.parametrize("rows,cols", [(128, 256), (333, 1000), (700, 700)])
+def test_orthogonalize_has_no_element_that_stands_out(rows, cols):
+    """The two planes of every value belong together.  Errors of many small roundings are nearly normal: the largest
+    of 10^6 lies at 5 of their deviations, 7.4 of the median size, 24 with rows and columns that differ by a factor
+    of 3.  One value whose planes do not match is off by 2^-11, 2^11 of a rounding to two planes."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    g = put(np.random.default_rng(13).normal(size=(rows, cols)) * 1e-3)
+    out = torch.empty_like(g)
+    L.pc_orthogonalize(g, out, ws=L.orthogonalize_workspace(g))
+    d = np.abs(get(out) - R.orthogonalize(get(g), [QUINTIC] * 5, 1e-7))
+    assert d.max() <= 24 * np.median(d)
+
+
+@pytest.mark.parametrize("batch,rows,cols,typ", [(3, 333, 1000, "f32"), (2, 700, 700, "f16"), (1, 1100, 1300, "bf16")])
+def test_orthogonalize_gives_the_same_bits_every_time(batch, rows, cols, typ):
+    """Sums have a fixed order: every call, whatever its workspace held before, gives the first one's bits."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    g = put(np.random.default_rng(12).normal(size=(batch, rows, cols)), typ)
+    ws = L.orthogonalize_workspace(g)
+    first, out = torch.empty_like(g), torch.empty_like(g)
+    L.pc_orthogonalize(g, first, ws=ws)
+    wrong = torch.zeros((), device=DEV, dtype=torch.int64)
+    for k in range(400):
+        ws.fill_(127 if k % 2 else 60)
+        L.pc_orthogonalize(g, out, ws=ws)
+        wrong += (out != first).sum()
+    assert int(wrong) == 0
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
