@@ -17,11 +17,13 @@
 // operand is split into two float16 planes of a value scaled by a power of two
 // (hi + lo: 22 bits; the spectra are bounded, so the scales are known before
 // the call), and hi hi + hi lo + lo hi are summed in float32: the accuracy of
-// float32 steps at three times the cost of a 16-bit product.  The symmetric
-// products (A, A^2) compute the tiles on and above the diagonal only.  Bound by
-// the matrix instructions: at 4096 x 4096 B X runs at 1.09 PFLOP/s of float16
-// products (380 us for three of 137 GFLOP; a library product reaches 1.08), A^2
-// at 1.0, A in one plane at 0.7 (its LDS reads).
+// float32 steps at three times the cost of a 16-bit product.  So it is for
+// every type: one plane of A's operands alone would put 4e-4 of the result on
+// top of a bfloat16 result's own rounding (1.7e-3).  The symmetric products (A,
+// A^2) compute the tiles on and above the diagonal only.  Bound by the matrix
+// instructions: at 4096 x 4096 B X runs at 1.09 PFLOP/s of float16 products
+// (380 us for three of 137 GFLOP; a library product reaches 1.08), A and A^2 at
+// 1.0.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -440,7 +442,7 @@ __device__ __forceinline__ void finish(const OrthGemmArgs& a, f32x16 (&acc)[NF][
   for (int i = 0; i < NF; ++i)
 #pragma unroll
     for (int j = 0; j < NF; ++j) acc[i][j] *= a.sacc;
-  if (a.old.p) {
+  if constexpr (EPI == ORTH_POLY) {   // b A + a I
     for (int p = 0; p < 2; ++p) {
       uint4 in[LINES];
 #pragma unroll
@@ -457,8 +459,6 @@ __device__ __forceinline__ void finish(const OrthGemmArgs& a, f32x16 (&acc)[NF][
             acc[i][j][r] += a.sold * f16_value(*(const uint16_t*)(mine + ((j * WT + 32 * i + 8 * (r >> 2) + 4 * hf + (r & 3)) * 32 + l32) * 2));
       wave_fence();
     }
-  }
-  if constexpr (EPI == ORTH_POLY) {   // a I
 #pragma unroll
     for (int i = 0; i < NF; ++i)
 #pragma unroll
@@ -485,57 +485,66 @@ __device__ __forceinline__ void finish(const OrthGemmArgs& a, f32x16 (&acc)[NF][
   const OrthMat& turned = SYM ? a.c : a.ct;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    if (p < a.cplanes) {
+    // one float32 value for all of a plane's conversions (see planes_of)
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          float v = acc[i][j][r];
+          asm volatile("" : "+v"(v));
+          acc[i][j][r] = v;
+        }
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          *(f16*)(mine + ((j * WT + 32 * i + 8 * (r >> 2) + 4 * hf + (r & 3)) * 32 + l32) * 2) = (f16)acc[i][j][r];
+    wave_fence();
+#pragma unroll
+    for (int n = 0; n < LINES; ++n)
+      *(uint4*)(line(a.c, a.M, row_w, col_w, n) + p * a.c.plane) = *(const uint4*)(mine + n * 1024 + lane * 16);
+    wave_fence();
+    if (mirror) {
 #pragma unroll
       for (int i = 0; i < NF; ++i)
 #pragma unroll
         for (int j = 0; j < NF; ++j)
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            *(f16*)(mine + ((j * WT + 32 * i + 8 * (r >> 2) + 4 * hf + (r & 3)) * 32 + l32) * 2) = (f16)acc[i][j][r];
+          for (int q = 0; q < 4; ++q) {
+            f16 h[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) h[r] = (f16)acc[i][j][4 * q + r];
+            __builtin_memcpy(__builtin_assume_aligned(mine + ((i * WT + 32 * j + l32) * 32 + 8 * q + 4 * hf) * 2, 8), h, 8);
+          }
       wave_fence();
 #pragma unroll
       for (int n = 0; n < LINES; ++n)
-        *(uint4*)(line(a.c, a.M, row_w, col_w, n) + p * a.c.plane) = *(const uint4*)(mine + n * 1024 + lane * 16);
+        *(uint4*)(line(turned, a.N, col_w, row_w, n) + p * turned.plane) = *(const uint4*)(mine + n * 1024 + lane * 16);
       wave_fence();
-      if (mirror) {
-#pragma unroll
-        for (int i = 0; i < NF; ++i)
-#pragma unroll
-          for (int j = 0; j < NF; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              f16 h[4];
-#pragma unroll
-              for (int r = 0; r < 4; ++r) h[r] = (f16)acc[i][j][4 * q + r];
-              __builtin_memcpy(__builtin_assume_aligned(mine + ((i * WT + 32 * j + l32) * 32 + 8 * q + 4 * hf) * 2, 8), h, 8);
-            }
-        wave_fence();
-#pragma unroll
-        for (int n = 0; n < LINES; ++n)
-          *(uint4*)(line(turned, a.N, col_w, row_w, n) + p * turned.plane) = *(const uint4*)(mine + n * 1024 + lane * 16);
-        wave_fence();
-      }
-      // what the plane leaves
-#pragma unroll
-      for (int i = 0; i < NF; ++i)
-#pragma unroll
-        for (int j = 0; j < NF; ++j)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[i][j][r] -= (float)(f16)acc[i][j][r];
     }
+    // what the plane leaves
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] -= (float)(f16)acc[i][j][r];
   }
 }
 
 // C = A B^T on TILE x TILE tiles, four waves of half of that, K in slices of 32
 // through an LDS ring of ST stages of KS slices.  TILE 128, or 64 where tiles of
 // 128 would leave compute units without one (3 x 333 x 1000, A: 25 us in tiles
-// of 128, 13 in tiles of 64, 11 split along K).  PL planes of each operand: 1
-// one product, 2 three.  Slot s of a row's four 16-byte chunks holds chunk
-// s ^ ((row >> 2) & 3), so the 16 rows a wave reads at a time lie in different
-// banks.
-template <int EPI, int PL, int TILE, int ST, bool PART, typename IO>
-__global__ __launch_bounds__(256, PL == 1 && EPI == ORTH_GRAM ? 3 : 2) void orth_gemm(OrthGemmArgs a) {
+// of 128, 13 in tiles of 64, 11 split along K).  Three products of the operands'
+// planes.  Slot s of a row's four 16-byte chunks holds chunk s ^ ((row >> 2) & 3),
+// so the 16 rows a wave reads at a time lie in different banks.
+template <int EPI, int TILE, int ST, bool PART, typename IO>
+__global__ __launch_bounds__(256, 2) void orth_gemm(OrthGemmArgs a) {
+  constexpr int PL = 2;              // planes of an operand
   constexpr int SLICE = TILE * 64;   // bytes of an operand plane's slice
   constexpr int WT = TILE / 2, NF = WT / 32, LR = TILE / 4;   // a wave's rows, its 32-row blocks, the rows it loads
   constexpr int STAGE = 2 * PL * SLICE;
@@ -614,16 +623,14 @@ __global__ __launch_bounds__(256, PL == 1 && EPI == ORTH_GRAM ? 3 : 2) void orth
       for (int i = 0; i < NF; ++i)
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-          if constexpr (PL == 2) {
-            f32x16& x = NF == 1 ? cross[0][0] : acc[i][j];
-            x = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[1][i], fb[0][j], x, 0, 0, 0);
-            x = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[1][j], x, 0, 0, 0);
-          }
+          f32x16& x = NF == 1 ? cross[0][0] : acc[i][j];
+          x = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[1][i], fb[0][j], x, 0, 0, 0);
+          x = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[1][j], x, 0, 0, 0);
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][i], fb[0][j], acc[i][j], 0, 0, 0);
         }
     }
   }
-  if constexpr (NF == 1 && PL == 2) acc[0][0] += cross[0][0];
+  if constexpr (NF == 1) acc[0][0] += cross[0][0];
   __builtin_amdgcn_s_waitcnt(WaitVmLgkm<0>::imm);   // no load may reach LDS after the workgroup's end
   if constexpr (PART) {   // [tile, part][wave][16 registers of four][lane]
     float* to = a.parts + ((z * gridDim.x + blockIdx.x) * 4 + wave) * (NF * NF * 1024) + lane * 4;
@@ -677,8 +684,8 @@ void small(const OrthIo& io, const OrthPoly& p, hipStream_t s) {
   else launch_kernel(orth_small<IO, 4, 512>, grid, dim3(512), 0, s, io, p);
 }
 
-template <int EPI, int PL, typename IO>
-void gemm_tiles(const OrthGemmArgs& a, hipStream_t s) {
+template <int EPI, typename IO>
+void gemm(const OrthGemmArgs& a, hipStream_t s) {
   const bool sym = EPI == ORTH_GRAM || EPI == ORTH_POLY;
   auto grid = [&](int tile) {
     const unsigned mt = (unsigned)(a.M / tile), nt = (unsigned)(a.N / tile);
@@ -695,10 +702,10 @@ void gemm_tiles(const OrthGemmArgs& a, hipStream_t s) {
     b.split = a.parts ? (int)std::min<int64_t>({4, ORTH_FEW_PARTS / tiles, a.K / 32 / 8}) : 1;
     if (b.split > 1) {
       const dim3 parts(g.x * (unsigned)b.split, 1, g.z), quarters(g.x * 4, 1, g.z);
-      launch_kernel(orth_gemm<EPI, PL, 64, 2, true, IO>, parts, dim3(256), 0, s, b);
+      launch_kernel(orth_gemm<EPI, 64, 2, true, IO>, parts, dim3(256), 0, s, b);
       launch_kernel(orth_join<EPI, 64, IO>, quarters, dim3(64), 0, s, b);
     } else {
-      launch_kernel(orth_gemm<EPI, PL, 64, 2, false, IO>, g, dim3(256), 0, s, b);
+      launch_kernel(orth_gemm<EPI, 64, 2, false, IO>, g, dim3(256), 0, s, b);
     }
     return;
   }
@@ -710,18 +717,12 @@ void gemm_tiles(const OrthGemmArgs& a, hipStream_t s) {
   b.full = (int)g.x - rest;
   b.split = a.parts && g.z == 1 && rest ? std::max(1, std::min({ORTH_PARTS / rest, 8, a.K / 32 / 8})) : 1;
   if (b.split > 1) g.x = (unsigned)b.full;
-  launch_kernel(orth_gemm<EPI, PL, 128, 2, false, IO>, g, dim3(256), 0, s, b);
+  launch_kernel(orth_gemm<EPI, 128, 2, false, IO>, g, dim3(256), 0, s, b);
   if (b.split > 1) {
-    launch_kernel(orth_gemm<EPI, PL, 128, 2, true, IO>, dim3((unsigned)(rest * b.split)), dim3(256), 0, s, b);
+    launch_kernel(orth_gemm<EPI, 128, 2, true, IO>, dim3((unsigned)(rest * b.split)), dim3(256), 0, s, b);
     launch_kernel(orth_join<EPI, 128, IO>, dim3((unsigned)rest * 4), dim3(64), 0, s, b);
   }
 }
-template <int EPI, typename IO>
-void gemm(const OrthGemmArgs& a, int planes, hipStream_t s) {
-  if (planes == 1) gemm_tiles<EPI, 1, IO>(a, s);
-  else gemm_tiles<EPI, 2, IO>(a, s);
-}
-
 }  // namespace
 
 #define PC_ORTH_TYPES(f)                    \
@@ -754,12 +755,12 @@ void launch_orth_split(const OrthIo& io, int dtype, const double* part, float sc
 #undef F
 }
 
-void launch_orth_gemm(const OrthGemmArgs& a, int epi, int planes, int dtype, hipStream_t s) {
-  if (epi == ORTH_GRAM) gemm<ORTH_GRAM, float>(a, planes, s);
-  else if (epi == ORTH_POLY) gemm<ORTH_POLY, float>(a, planes, s);
-  else if (epi == ORTH_APPLY) gemm<ORTH_APPLY, float>(a, planes, s);
+void launch_orth_gemm(const OrthGemmArgs& a, int epi, int dtype, hipStream_t s) {
+  if (epi == ORTH_GRAM) gemm<ORTH_GRAM, float>(a, s);
+  else if (epi == ORTH_POLY) gemm<ORTH_POLY, float>(a, s);
+  else if (epi == ORTH_APPLY) gemm<ORTH_APPLY, float>(a, s);
   else {
-#define F(T) gemm<ORTH_OUT, T>(a, planes, s);
+#define F(T) gemm<ORTH_OUT, T>(a, s);
     PC_ORTH_TYPES(F)
 #undef F
   }

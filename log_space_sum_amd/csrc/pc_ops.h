@@ -156,11 +156,10 @@ enum OrthEpi { ORTH_GRAM, ORTH_POLY, ORTH_APPLY, ORTH_OUT };
 struct OrthGemmArgs {
   int32_t M, N, K;      // padded; C [M, N] = A [M, K] B [N, K]^T
   OrthMat a, b;
-  OrthMat old;          // added to the product, nullable (panels of [M, N])
+  OrthMat old;          // POLY: added to the product (panels of [M, N])
   OrthMat c, ct;        // the result's panels and its transpose's (GRAM / POLY: c alone, both halves)
-  float sacc, sold;     // result = sacc acc + sold old
+  float sacc, sold;     // result = sacc acc (POLY: + sold old)
   float diag;           // POLY: + diag I
-  int32_t cplanes;      // planes of the result that are written
   float* parts;         // room for ORTH_PARTS or ORTH_FEW_PARTS tiles' partial sums, nullable
   int32_t full, split;  // set at the launch: tiles taken whole, parts of each tile behind them
   OrthIo io;            // OUT
@@ -169,6 +168,6 @@ void launch_orth_small(const OrthIo& io, const OrthPoly& p, int dtype, hipStream
 void launch_orth_norm(const OrthIo& io, int dtype, double* part, hipStream_t s);
 void launch_orth_split(const OrthIo& io, int dtype, const double* part, float scale, int mp, int np, const OrthMat& x,
                        const OrthMat& xt, hipStream_t s);
-void launch_orth_gemm(const OrthGemmArgs& a, int epi, int planes, int dtype, hipStream_t s);
+void launch_orth_gemm(const OrthGemmArgs& a, int epi, int dtype, hipStream_t s);
 
 }  // namespace pc

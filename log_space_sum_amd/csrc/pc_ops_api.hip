@@ -635,14 +635,6 @@ int pc_orthogonalize(int device, int dtype, int64_t batch, int32_t rows, int32_t
       const OrthMat &x = p.x[k & 1], &xt = p.xt[k & 1];
       const float sa = orth_scale(bound.x[k] * bound.x[k]), sb = orth_scale(bound.p[k]);
       const float sn = k + 1 < steps ? orth_scale(bound.x[k + 1]) : 1.0f;
-      // Planes of the products' operands.  float32 and float16 results: two
-      // everywhere (22 bits).  bfloat16 results: A's operands in one (11 bits)
-      // in every step, and all of the first two of five or more steps, whose
-      // error the later steps do not raise: together within 8e-4 of the result
-      // (normwise; square, wide, orthogonal, rank-1 and power-law spectra),
-      // against 1.7e-3 of bfloat16's own rounding, for 19/30 of the matrix
-      // instructions.  (One plane in any later step costs 1e-3 or more.)
-      const bool bf = dtype == PC_DTYPE_BF16, early = bf && k < 2 && k + 3 < steps;
       OrthGemmArgs a{};
       a.io = io;
       a.parts = p.split ? (float*)((char*)ws + p.parts) : nullptr;
@@ -652,31 +644,24 @@ int pc_orthogonalize(int device, int dtype, int64_t batch, int32_t rows, int32_t
       a.a = a.b = x;
       a.c = p.a;
       a.sacc = sa / (sx * sx);
-      a.cplanes = 2;
-      launch_orth_gemm(a, ORTH_GRAM, bf ? 1 : 2, dtype, s);
+      launch_orth_gemm(a, ORTH_GRAM, dtype, s);
       check_launch();
-      // B = a I + b A + c A^2, then X <- B X.  One plane: without a I, whose
-      // part of X is added in float32 instead (it is most of the result, and
-      // would be rounded with X)
+      // B = a I + b A + c A^2, then X <- B X
       a.K = p.mp;
       a.a = a.b = a.old = p.a;
       a.c = p.b;
       a.sacc = sb * c[2] / (sa * sa);
       a.sold = sb * c[1] / sa;
-      a.diag = early ? 0.0f : sb * c[0];
-      a.cplanes = early ? 1 : 2;
-      launch_orth_gemm(a, ORTH_POLY, early ? 1 : 2, dtype, s);
+      a.diag = sb * c[0];
+      launch_orth_gemm(a, ORTH_POLY, dtype, s);
       check_launch();
-      a.cplanes = 2;
       a.N = p.np;
       a.a = p.b;
       a.b = xt;
-      a.old = early ? x : OrthMat{};
       a.c = p.x[(k + 1) & 1];
       a.ct = p.xt[(k + 1) & 1];
       a.sacc = sn / (sb * sx);
-      a.sold = sn * c[0] / sx;
-      launch_orth_gemm(a, k + 1 < steps ? ORTH_APPLY : ORTH_OUT, early ? 1 : 2, dtype, s);
+      launch_orth_gemm(a, k + 1 < steps ? ORTH_APPLY : ORTH_OUT, dtype, s);
       check_launch();
       sx = sn;
     }

@@ -505,6 +505,39 @@ def test_orthogonalize_gives_the_same_bits_every_time(batch, rows, cols, typ):
     assert int(wrong) == 0
 
 
+# Accuracy of the planes.  A value in two float16 planes is off by at most 2^-23 of itself, the product of the two
+# small planes that is left out by 2^-24 of the product's terms, and a float32 sum of n terms by about sqrt(n) 2^-25 of
+# its terms' norm: each of a step's three products is off by less than 1e-6 of its norm for n <= 1300, and the steps on
+# random matrices, whose singular values and perturbations grow alike, add them up to 2e-6 of the result (the steps
+# with rounded operands: tests/test_operators.py).  Ten times that is allowed; one plane anywhere costs 4e-4 or more.
+PLANES = 2e-5
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("batch,rows,cols", [(2, 65, 65), (1, 70, 400), (2, 300, 129), (1, 256, 128), (3, 333, 1000), (1, 700, 700),
+                                             (1, 1100, 1300)])
+def test_orthogonalize_is_float32_exact_in_every_type(batch, rows, cols, typ):
+    """The result before its rounding is within PLANES of the definition.  float32: that, normwise and element by
+    element (nearly normal errors: the largest of 10^6 below 24 deviations).  16-bit types: an element whose value lies
+    d from the definition's rounds differently in a share d / step of the cases, then by a step, at most 2 u of the
+    value: the squares of the differences from the rounded definition sum to at most 2 u PLANES of the result's."""
+    import log_space_sum_amd as L
+    torch, types = T()
+    g = put(np.random.default_rng(rows + 3 * cols).normal(size=(batch, rows, cols)) * 1e-3, typ)
+    out = torch.empty_like(g)
+    L.pc_orthogonalize(g, out, ws=L.orthogonalize_workspace(g))
+    for b in range(batch):
+        ref = R.orthogonalize(get(g)[b], [QUINTIC] * 5, 1e-7)
+        size, rms = np.linalg.norm(ref), np.sqrt((ref * ref).mean())
+        d = get(out)[b] - ref
+        assert (np.abs(d) <= U[typ] * np.abs(ref) + 24 * PLANES * rms + TINY[typ]).all()
+        if typ == "f32":
+            assert np.linalg.norm(d) <= (PLANES + E32) * size
+        else:
+            off = get(out)[b] - get(put(ref, typ))
+            assert np.linalg.norm(off) <= np.sqrt(2 * U[typ] * PLANES) * size
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------

@@ -58,6 +58,39 @@ def test_orthogonalize_moves_the_singular_values():
     np.testing.assert_allclose(x, (u * t) @ vt, rtol=1e-10, atol=1e-12)
 
 
+def _rounded_steps(g, planes, steps=5):
+    """Newton-Schulz steps in float32 whose operands are `planes` float16 planes of a scaled value."""
+    scale = np.float32(2.0 ** 13)
+
+    def product(a, b):
+        hi, lo = [], []
+        for x in (a, b):
+            x = x * scale
+            h = x.astype(np.float16).astype(np.float32)
+            hi.append(h)
+            lo.append((x - h).astype(np.float16).astype(np.float32) if planes == 2 else 0 * h)
+        return (hi[0] @ lo[1] + lo[0] @ hi[1] + hi[0] @ hi[1]) / (scale * scale)
+
+    x = (g / np.linalg.norm(g)).astype(np.float32)
+    a, b, c = (np.float32(v) for v in (3.4445, -4.7750, 2.0315))
+    for _ in range(steps):
+        A = product(x, x.T)
+        x = product(a * np.eye(len(A), dtype=np.float32) + b * A + c * product(A, A), x)
+    return x.astype(np.float64)
+
+
+@pytest.mark.parametrize("m,n", [(65, 65), (70, 400), (129, 300), (333, 1000)])
+def test_the_bounds_of_the_update_tell_one_plane_from_two(m, n):
+    """2e-5 of the result normwise and 24 times that of its root mean square for an element (what the GPU tests allow a
+    float32 result): two planes stay ten times below, one plane is far beyond both."""
+    g = np.random.default_rng(m).normal(size=(m, n))
+    ref = R.orthogonalize(g, [(3.4445, -4.7750, 2.0315)] * 5, 0.0)
+    size, rms = np.linalg.norm(ref), np.sqrt((ref * ref).mean())
+    two, one = (_rounded_steps(g, p) - ref for p in (2, 1))
+    assert np.linalg.norm(two) <= 4e-6 * size and np.abs(two).max() <= 24 * 4e-6 * rms
+    assert np.linalg.norm(one) > 20 * 2e-5 * size and np.abs(one).max() > 5 * 24 * 2e-5 * rms
+
+
 # ---- refusals: host-side checks, nothing reaches a device -------------------
 
 P = 4096   # an address that is never read
