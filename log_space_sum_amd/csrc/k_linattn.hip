@@ -38,13 +38,14 @@
 // bank conflicts, but registers past the limit of two workgroups: the same).
 //
 // Precision: bfloat16 tensors are multiplied in bfloat16 with float32 sums.
-// The decay weights are not exact in bfloat16: l^{n-off-j} c_j is split into
-// three bfloat16 planes, so the state keeps float32 accuracy however long the
-// walk; in the output's products the carried state and the inside products
-// (a_i . b_j) l^{i-j} are split into two (2^-17 of a value is left out, far
-// below the output's own rounding; one plane would add 2^-9 of every term).  float32 and float16 tensors run on the
-// float32 matrix instruction throughout (float16's range cannot hold the
-// state or its planes).
+// What is not exact in bfloat16, the decay-weighted l^{n-off-j} c_j, the carried
+// state and the inside products (a_i . b_j) l^{i-j}, is split into three
+// bfloat16 planes (24 bits), so state and output keep float32 accuracy however
+// long the walk.  (Two planes of the state and of the inside products are 6 to 8%
+// faster, 252 against 268 us for 16384 x 32 heads x 128, but leave 2^-17 of every
+// term: after rounding, outputs 9e-5 off the rounded definition's, 2e-5 with three.)
+// float32 and float16 tensors run on the float32 matrix instruction throughout
+// (float16's range cannot hold the state or its planes).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -80,9 +81,8 @@ struct Ops<bf16> {
   // row padding of the tiles read by rows, and by columns (16 lanes' 4 rows of 32 bytes lie in different banks then);
   // b's tile is read by both in a walk (there the first measured 3% faster)
   static constexpr int PAD = 8, CPAD = 16;
-  static constexpr int CPLANES = 3;  // planes of the weighted c, and of the state in the output's product
-  static constexpr int SPLANES = 2;
-  static constexpr int PPLANES = 2;  // of the inside products
+  // planes of the weighted c, of the state in the output's product, and of the inside products
+  static constexpr int CPLANES = 3, SPLANES = 3, PPLANES = 3;
   typedef uint2 quad;
   static __device__ __forceinline__ f32x4 mma(quad a0, quad a1, quad b0, quad b1, f32x4 acc) {
     const uint4 a = {a0.x, a0.y, a1.x, a1.y}, b = {b0.x, b0.y, b1.x, b1.y};
@@ -119,9 +119,7 @@ struct Ops<float> {
   static constexpr int C = 32;
   static constexpr int EV = 4;
   static constexpr int PAD = 4, CPAD = 4;
-  static constexpr int CPLANES = 1;
-  static constexpr int SPLANES = 1;
-  static constexpr int PPLANES = 1;
+  static constexpr int CPLANES = 1, SPLANES = 1, PPLANES = 1;
   typedef f32x4 quad;
   static __device__ __forceinline__ f32x4 mma(quad a0, quad a1, quad b0, quad b1, f32x4 acc) {
 #pragma unroll
@@ -251,7 +249,13 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
   using quad = typename O::quad;
   constexpr int C = O::C, CB = C / 16, EV = O::EV, NT = 64 * NW;
   constexpr int DA = 16 * DKB, DC = 16 * NW;
-  constexpr int LA = DA + O::PAD, LB = DA + (WALK ? O::PAD : O::CPAD), LC = DC + O::CPAD, LP = C + O::PAD;
+  constexpr int LA = DA + O::PAD, LB = DA + (WALK ? O::PAD : O::CPAD), LC = DC + O::CPAD;
+  // A plane of the inside products: of every 32 rows the columns up to their
+  // last, so that three planes leave room for a third workgroup at dim 64 and a
+  // second at 128 (all columns: 57 and 80 KB; the first 70 instead of 61 us for
+  // a ragged forward of 24 x 1500 x 16 heads).
+  constexpr int SPZ = 512 * CB / 2 * (CB / 2 + 1) + 16 * CB * O::PAD;
+  auto sp_row = [](int i) { return 512 * (i >> 5) * ((i >> 5) + 1) + 32 * (i >> 5) * O::PAD + (i & 31) * (32 * ((i >> 5) + 1) + O::PAD); };
   constexpr int UA = C * DA / EV / NT, UC = C * DC / EV / NT;   // staged units of a thread
   static_assert(UA * NT * EV == C * DA && UC * NT * EV == C * DC, "whole units");
   constexpr int CP = O::CPLANES, SP = O::SPLANES, PP = O::PPLANES;
@@ -259,11 +263,11 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
   __shared__ __align__(16) CT sa[WALK ? C * LA : 8];
   __shared__ __align__(16) CT sb[C * LB];
   __shared__ __align__(16) CT sc[C * LC];
-  __shared__ __align__(16) CT sp[WALK ? PP * C * LP : 8];
+  __shared__ __align__(16) CT sp[WALK ? PP * SPZ : 8];
   // weights: of a token's part in the state (for the chunk's size), of the
   // inside products at distance d = i - j (at C - 1 - d; 0 behind C - 1), and
   // of the state in token i's output
-  __shared__ __align__(16) float swt[C], sdec[2 * C], siw[C];
+  __shared__ __align__(16) float swt[C], sdec[C + 16], siw[C];
   __shared__ int sbad[2];
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, l16 = lane & 15;
@@ -309,12 +313,12 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
     }
   }
   if constexpr (WALK) {
-    for (int e = tid; e < 2 * C; e += NT) sdec[e] = e < C ? m.pscale * decay_pow(gam, (float)(C - 1 - e)) : 0.0f;
+    for (int e = tid; e < C + 16; e += NT) sdec[e] = e < C ? m.pscale * decay_pow(gam, (float)(C - 1 - e)) : 0.0f;
     for (int e = tid; e < C; e += NT) siw[e] = m.oscale * decay_pow(gam, (float)(e + m.off));
     // the products' tiles right of the diagonal that a 32-wide step reads: always 0
     for (int e = tid; e < PP * C * 16; e += NT) {
-      const int i = e >> 4, ib = (i % C) >> 4;
-      if ((ib & 1) == 0) sp[i * LP + O::at(16 * (ib + 1) + (e & 15))] = CT{};
+      const int i = (e >> 4) % C, ib = i >> 4;
+      if ((ib & 1) == 0) sp[e / (C * 16) * SPZ + sp_row(i) + O::at(16 * (ib + 1) + (e & 15))] = CT{};
     }
   }
 
@@ -438,7 +442,7 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
           quad pl[PP];
           split<CT, PP>(w, pl);
 #pragma unroll
-          for (int p = 0; p < PP; ++p) *(quad*)(sp + (p * C + 16 * ib + l16) * LP + O::at(16 * jb + 4 * g)) = pl[p];
+          for (int p = 0; p < PP; ++p) *(quad*)(sp + p * SPZ + sp_row(16 * ib + l16) + O::at(16 * jb + 4 * g)) = pl[p];
         }
       }
       // the state's part of the output
@@ -482,7 +486,7 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
 #pragma unroll
             for (int ib = b; ib < CB; ++ib) {
               quad p0, p1;
-              O::row2(sp + (p * C + 16 * ib + l16) * LP, b / 2, g, p0, p1);
+              O::row2(sp + p * SPZ + sp_row(16 * ib + l16), b / 2, g, p0, p1);
               o[ib] = O::mma(c0, c1, p0, p1, o[ib]);
             }
         }

@@ -216,6 +216,31 @@ def test_linear_attention(lens, H, K, dk, dv, typ):
     assert torch.equal(dz, d0)
 
 
+@pytest.mark.parametrize("typ", ["bf16", "f16"])
+@pytest.mark.parametrize("lens,H,K,dk,dv", [([700, 300], 4, 4, 64, 64), ([400, 513], 2, 1, 128, 128), ([450], 3, 3, 96, 40)])
+def test_linear_attention_rounds_a_float32_exact_result(lens, H, K, dk, dv, typ):
+    """Outputs and gradients before their rounding are off by the roundings of float32 sums of a chunk's and the state's
+    terms, sqrt(terms) 2^-25 of the result (roundings of partial sums that average out).  An element whose value lies d
+    from the definition's rounds differently in a share d / step of the cases, then by a step, at most 2 u of the value:
+    the squares of the differences from the rounded definition sum to 2 u sqrt(terms) 2^-25 of the result's."""
+    import log_space_sum_amd as L
+    torch, types = T()
+    rng = np.random.default_rng(dk + dv)
+    q, k, v, do, cu, dcu = _att(rng, lens, H, K, dk, dv, typ)
+    g = put(np.array([-0.02, 0.0, -0.5, -3e-3])[:H])
+    s0, ds = (put(rng.normal(size=(len(lens), H, dk, dv))) for _ in range(2))
+    o, dq, dk_, dv_ = torch.empty_like(do), *(torch.empty_like(t) for t in (q, k, v))
+    L.pc_linear_attention_forward(q, k, v, g, o, dcu, max(lens), s0, ws=L.linear_attention_workspace(q, k, v, dcu, max(lens)))
+    L.pc_linear_attention_backward(do, q, k, v, g, dq, dk_, dv_, dcu, max(lens), s0, ds,
+                                   ws=L.linear_attention_workspace(q, k, v, dcu, max(lens), backward=True))
+    A = [get(t) for t in (q, k, v, g)]
+    ref = (R.linear_attention(*A, cu, dk ** -0.5, get(s0))[0],
+           *R.linear_attention_grad(get(do), *A, cu, dk ** -0.5, get(s0), get(ds))[:3])
+    for got, want, name in zip((o, dq, dk_, dv_), ref, ("o", "dq", "dk", "dv")):
+        off = np.linalg.norm(get(got) - get(put(want, typ)))
+        assert off <= np.sqrt(2 * U[typ] * np.sqrt(max(dk, dv) + 64) / 2 * E32) * np.linalg.norm(want), name
+
+
 @pytest.mark.parametrize("typ", ["f32", "bf16"])
 def test_linear_attention_strides(typ):
     """q, k, v as parts of one packed tensor, outputs head by head, one sequence without cu_seqlens."""
