@@ -8,10 +8,21 @@
 //   M = a I + b A + c A^2,   Q <- Q M,   A <- A M^2,
 // and the matrix itself is read twice and written once.  Squaring the matrix
 // costs half of the digits, so A, M and Q are held in 64 bits (one workgroup
-// a matrix, on the float64 matrix instruction); the result is then at least as
-// exact as float32 steps on X.  Bound by latency: 64 matrices of 1024 x 16
-// float32 take 12 us, of which the steps, a chain of 17 products in one wave,
-// are about four.
+// a matrix, on the float64 matrix instruction).  Bound by latency: 64 matrices of
+// 1024 x 16 float32 take 13.7 us, of which the steps, a chain of 17 products in one
+// wave, are about four.  The last product Q X_0 is taken in 64 bits as well, since
+// its terms cancel where G has no singular value: Q is the product of the a's there
+// (in float32: 1.1 us less, but 5e-5 of the result for a rank 1 matrix after five
+// steps, 4e-4 after six, and no result where Q / |G| leaves float32's range).
+// This holds for few steps.  Where G has a small or no singular value, A's
+// rounding leaves an eigenvalue of about -1e-16 there, which every step multiplies
+// by up to a^2 (16 steps of the usual a = 3.4: past 1, and then without bound).
+// Past a growth of Q of ORTH_GROWTH the steps therefore run on a factor X' with X' X'^T = A_0 + d I
+// (Cholesky), X' <- M X', and A = X' X'^T is formed afresh in every step: it has
+// no negative eigenvalue beyond its rounding, which is not carried on.  d, above
+// the rounding of A_0, keeps the factorisation definite and |X'| >= |X| in every
+// direction, so Q X_0 stays within the steps' bounds, and Q below top / sqrt(d),
+// which 64 bits hold (rank 1 and 4 matrices after 32 steps: 1e-8 of the result).
 //
 // Larger m: three products a step on the float16 matrix instruction.  An
 // operand is split into two float16 planes of a value scaled by a power of two
@@ -135,7 +146,56 @@ __device__ __forceinline__ f32x4 load_i(const IO* x, const OrthIo& io, int i, in
   return v;
 }
 
-template <typename IO, int MB, int NT>
+// C = M B of [16 MB]^2 matrices in LDS, M symmetric; C may be B.
+template <int MB, int LD, int W>
+__device__ __forceinline__ void small_multiply(const double* M, const double* B, double* C) {
+  constexpr int T = MB * MB, MINE = (T + W - 1) / W;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  f64x4 acc[MINE];
+#pragma unroll
+  for (int k = 0; k < MINE; ++k) {
+    const int t = wave + W * k, ib = t / MB, jb = t % MB;
+    acc[k] = f64x4{0.0, 0.0, 0.0, 0.0};
+    if (t >= T) continue;
+#pragma unroll
+    for (int q = 0; q < 4 * MB; ++q)
+      acc[k] = __builtin_amdgcn_mfma_f64_16x16x4f64(M[(16 * ib + l16) * LD + 4 * q + g], B[(4 * q + g) * LD + 16 * jb + l16],
+                                                    acc[k], 0, 0, 0);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < MINE; ++k) {
+    const int t = wave + W * k, ib = t / MB, jb = t % MB;
+    if (t >= T) continue;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) C[(16 * ib + g + 4 * r) * LD + 16 * jb + l16] = acc[k][r];
+  }
+  __syncthreads();
+}
+
+// L with L L^T = S of a [D, D] matrix in LDS, column by column; S is used up.
+// A pivot below `least` (S is definite up to rounding) is taken as that.
+template <int D, int LD, int NT>
+__device__ __forceinline__ void small_cholesky(double* S, double* L, double least) {
+  for (int k = 0; k < D; ++k) {
+    double pivot = S[k * LD + k];
+    pivot = pivot < least ? least : pivot;   // (NaN stays)
+    const double r = 1.0 / sqrt(pivot);
+    if ((int)threadIdx.x < D) {
+      const int i = threadIdx.x;
+      L[i * LD + k] = i < k ? 0.0 : (i == k ? pivot : S[i * LD + k]) * r;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < D * D; e += NT) {
+      const int i = e / D, j = e % D;
+      if (i > k && j > k) S[i * LD + j] -= L[i * LD + k] * L[j * LD + k];
+    }
+    __syncthreads();
+  }
+}
+
+// LONG: many steps, on a factor of A (see the top).
+template <typename IO, int MB, int NT, bool LONG>
 __global__ __launch_bounds__(NT) void orth_small(OrthIo io, OrthPoly poly) {
   constexpr int D = 16 * MB, LD = D + 2, W = NT / 64, T = MB * (MB + 1) / 2;
   // the waves' parts of the Gram matrix, then the matrices of the steps
@@ -190,8 +250,7 @@ __global__ __launch_bounds__(NT) void orth_small(OrthIo io, OrthPoly poly) {
   }
   __syncthreads();
 
-  float q[MB][MB][4];   // [block of i][block of k][e]: Q[16 ib + l16][16 kb + 4 g + e] / |G|
-  if constexpr (MB == 1) {
+  if constexpr (MB == 1 && !LONG) {
     // one wave takes all steps in its registers
 #pragma unroll
     for (int k = 0; k < (256 + NT - 1) / NT; ++k)
@@ -218,12 +277,9 @@ __global__ __launch_bounds__(NT) void orth_small(OrthIo io, OrthPoly poly) {
         if (s + 1 < poly.steps) A = product16(product16(A, M), M);
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) pool[256 + l16 * LD + g + 4 * r] = Q[r] * inv;
+      for (int r = 0; r < 4; ++r) sQ[l16 * LD + g + 4 * r] = Q[r] * inv;
     }
-    // columns g + 4 r of row l16 -> columns 4 g + e
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 4; ++e) q[0][0][e] = (float)pool[256 + l16 * LD + 4 * g + e];
   } else {
     for (int e = tid; e < D * LD; e += NT) sA[e] = 0.0;
     __syncthreads();
@@ -246,60 +302,73 @@ __global__ __launch_bounds__(NT) void orth_small(OrthIo io, OrthPoly poly) {
     }
     __syncthreads();
     const double inv = s_inv;
-    for (int e = tid; e < D * D; e += NT) sA[e / D * LD + e % D] *= inv * inv;
+    for (int e = tid; e < D * D; e += NT)
+      sA[e / D * LD + e % D] = sA[e / D * LD + e % D] * (inv * inv) + (LONG && e / D == e % D ? poly.shift : 0.0);
     __syncthreads();
+    double* sX = sT;   // LONG: the factor
+    if constexpr (LONG) small_cholesky<D, LD, NT>(sA, sX, 0.25 * poly.shift);
     for (int s = 0; s < poly.steps; ++s) {
       const double a = poly.c[s][0], b = poly.c[s][1], c = poly.c[s][2];
+      if constexpr (LONG)
+        small_product<MB, LD, W>(sX, sX, [&](int i, int j, double v) { sA[i * LD + j] = sA[j * LD + i] = v; });
       small_product<MB, LD, W>(sA, sA, [&](int i, int j, double v) {
         const double u = (i == j ? a : 0.0) + b * sA[i * LD + j] + c * v;
         sM[i * LD + j] = sM[j * LD + i] = u;
         if (s == 0) sQ[i * LD + j] = sQ[j * LD + i] = u;
       });
+      if constexpr (LONG) {
+        if (s > 0) small_multiply<MB, LD, W>(sM, sQ, sQ);
+        if (s + 1 < poly.steps) small_multiply<MB, LD, W>(sM, sX, sX);
+        continue;
+      }
       if (s > 0) small_product<MB, LD, W>(sQ, sM, [&](int i, int j, double v) { sQ[i * LD + j] = sQ[j * LD + i] = v; });
       if (s + 1 < poly.steps) {
         small_product<MB, LD, W>(sA, sM, [&](int i, int j, double v) { sT[i * LD + j] = sT[j * LD + i] = v; });
         small_product<MB, LD, W>(sT, sM, [&](int i, int j, double v) { sA[i * LD + j] = sA[j * LD + i] = v; });
       }
     }
-#pragma unroll
-    for (int ib = 0; ib < MB; ++ib)
-#pragma unroll
-      for (int kb = 0; kb < MB; ++kb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) q[ib][kb][e] = (float)(sQ[(16 * ib + l16) * LD + 16 * kb + 4 * g + e] * inv);
+    for (int e = tid; e < D * D; e += NT) sQ[e / D * LD + e % D] *= inv;
+    __syncthreads();
   }
 
-  // out = (Q / |G|) G
+  // out = (Q / |G|) G, in 64 bits: where G has no singular value Q is the product
+  // of the a's, and its terms cancel
+  double q[MB][MB][4];   // [block of i][block of k][e]: Q[16 ib + l16][16 kb + 4 g + e] / |G|
+#pragma unroll
+  for (int ib = 0; ib < MB; ++ib)
+#pragma unroll
+    for (int kb = 0; kb < MB; ++kb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[ib][kb][e] = sQ[(16 * ib + l16) * LD + 16 * kb + 4 * g + e];
   IO* y = (IO*)io.out + (int64_t)blockIdx.x * io.o_batch;
+  // 16 columns p a wave; the operands are exchanged where the tensor's rows run
+  // along i, so that 16 lanes always write consecutive elements
+  auto columns = [&](auto tall) {
+    constexpr bool TALL = decltype(tall)::value;
 #pragma unroll 2
-  for (int p0 = wave * 16; p0 < n; p0 += W * 16) {
-    const int p = p0 + l16;
-    f32x4 v[MB];
+    for (int p0 = wave * 16; p0 < n; p0 += W * 16) {
+      f32x4 v[MB];
 #pragma unroll
-    for (int kb = 0; kb < MB; ++kb) v[kb] = load_i<IO>(x, io, 16 * kb + 4 * g, p);
+      for (int kb = 0; kb < MB; ++kb) v[kb] = load_i<IO>(x, io, 16 * kb + 4 * g, p0 + l16);
 #pragma unroll
-    for (int ib = 0; ib < MB; ++ib) {
-      f32x4 o = {};
+      for (int ib = 0; ib < MB; ++ib) {
+        f64x4 o = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-      for (int kb = 0; kb < MB; ++kb)
+        for (int kb = 0; kb < MB; ++kb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o = __builtin_amdgcn_mfma_f32_16x16x4f32(q[ib][kb][e], v[kb][e], o, 0, 0, 0);
-      // a lane holds rows i = 4 g + r of column p
-      const int i = 16 * ib + 4 * g;
-      if (p < n) {
-        if (io.tall && i + 4 <= m) {
-          IO u[4];
+          for (int e = 0; e < 4; ++e)
+            o = TALL ? __builtin_amdgcn_mfma_f64_16x16x4f64((double)v[kb][e], q[ib][kb][e], o, 0, 0, 0)
+                     : __builtin_amdgcn_mfma_f64_16x16x4f64(q[ib][kb][e], (double)v[kb][e], o, 0, 0, 0);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) u[r] = from_f32<IO>(o[r]);
-          __builtin_memcpy(y + (int64_t)p * io.o_row + i, u, sizeof(u));
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (i + r < m) y[at_x<IO>(io, io.o_row, i + r, p)] = from_f32<IO>(o[r]);
+        for (int r = 0; r < 4; ++r) {
+          const int i = 16 * ib + (TALL ? l16 : g + 4 * r), p = p0 + (TALL ? g + 4 * r : l16);
+          if (i < m && p < n) y[TALL ? (int64_t)p * io.o_row + i : (int64_t)i * io.o_row + p] = from_f32<IO>((float)o[r]);
         }
       }
     }
-  }
+  };
+  if (io.tall) columns(std::true_type{});
+  else columns(std::false_type{});
 }
 
 // ---------------------------------------------------------------------------
@@ -679,9 +748,17 @@ __global__ __launch_bounds__(64) void orth_join(OrthGemmArgs a) {
 template <typename IO>
 void small(const OrthIo& io, const OrthPoly& p, hipStream_t s) {
   const dim3 grid((unsigned)io.batch);
-  if (io.m <= 16) launch_kernel(orth_small<IO, 1, 1024>, grid, dim3(1024), 0, s, io, p);
-  else if (io.m <= 32) launch_kernel(orth_small<IO, 2, 512>, grid, dim3(512), 0, s, io, p);
-  else launch_kernel(orth_small<IO, 4, 512>, grid, dim3(512), 0, s, io, p);
+#define PC_ORTH_SMALL(MB, NT)                                                            \
+  if (p.shift > 0.0) launch_kernel(orth_small<IO, MB, NT, true>, grid, dim3(NT), 0, s, io, p); \
+  else launch_kernel(orth_small<IO, MB, NT, false>, grid, dim3(NT), 0, s, io, p);
+  if (io.m <= 16) {
+    PC_ORTH_SMALL(1, 1024)
+  } else if (io.m <= 32) {
+    PC_ORTH_SMALL(2, 512)
+  } else {
+    PC_ORTH_SMALL(4, 512)
+  }
+#undef PC_ORTH_SMALL
 }
 
 template <int EPI, typename IO>

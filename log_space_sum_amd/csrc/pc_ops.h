@@ -135,11 +135,13 @@ struct OrthIo {
   int64_t o_batch, o_row;
   float eps;
 };
-constexpr int ORTH_SMALL = 64;       // all steps on the Gram matrix, in 64 bits, up to this m
+constexpr int ORTH_SMALL = 64;       // all steps on m x m matrices, in 64 bits, up to this m
 constexpr int ORTH_MAX_STEPS = 32;
+constexpr double ORTH_GROWTH = 2048.0;   // of Q, up to which its steps run on A itself
 struct OrthPoly {
   int32_t steps;
   float c[ORTH_MAX_STEPS][3];
+  double shift;                      // past that growth: added to A's diagonal; else 0
 };
 constexpr int ORTH_TILE = 128;       // rows and columns of the operands are padded to it
 constexpr int ORTH_NORM_BLOCKS = 512; // partial sums of a matrix's norm

@@ -563,6 +563,95 @@ def test_orthogonalize_is_float32_exact_in_every_type(batch, rows, cols, typ):
             assert np.linalg.norm(off) <= np.sqrt(2 * U[typ] * PLANES) * size
 
 
+CUBIC = (1.5, -0.5, 0.0)
+TUNED = [(8.287, -23.596, 17.300), (4.107, -2.948, 0.545), (3.949, -2.909, 0.552), (3.318, -2.488, 0.510), (2.301, -1.669, 0.419)]
+
+
+def _exact_rank(rng, m, n, rank):
+    """A matrix of small whole numbers of exactly this rank (or less), in every type."""
+    return rng.integers(-4, 5, size=(m, rank)).astype(float) @ rng.integers(-4, 5, size=(rank, n))
+
+
+def _by_singular_values(g, co):
+    """The steps on the singular values with the coefficients that the library takes, float32; the values that should
+    be 0 kept there; the largest growth of a relative error of one; the smallest one at the start."""
+    u, s, v = np.linalg.svd(g, full_matrices=False)
+    t = s / np.linalg.norm(g)
+    t[t < 1e-12] = 0
+    live, grow, least = t > 0, np.ones(len(t)), t[t > 0].min()
+    for a, b, c in np.float32(co).astype(np.float64):
+        grow = grow * np.maximum(1, np.abs(a + 3 * b * t ** 2 + 5 * c * t ** 4))
+        t = a * t + b * t ** 3 + c * t ** 5
+    return (u * t) @ v, grow[live].max(), least
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("m,n", [(16, 1024), (4, 37), (33, 500), (64, 300), (20, 20)])
+def test_orthogonalize_many_steps_of_thin_matrices(m, n, typ):
+    """Matrices without full rank, whose missing singular values must stay out of the result however many the steps.
+    What the m x m form may add: Q's rounding in 64 bits, m 2^-53 of the largest Q, 2 / sqrt(d) (a few times), and the
+    shift d, relative to the smallest singular value's square, times the growth of a relative error over the steps.
+    Up to a growth of Q of 2048 the steps run on A itself, whose rounding grows as Q's square."""
+    import log_space_sum_amd as L
+    torch, types = T()
+    rng = np.random.default_rng(m * n)
+    for rank in (1, 4):
+        g = np.stack([_exact_rank(rng, m, n, rank) for _ in range(2)])
+        x = put(g, typ)
+        assert (get(x) == g).all()
+        for co in ([QUINTIC] * 6, [QUINTIC] * 8, [QUINTIC] * 10, [QUINTIC] * 16, [QUINTIC] * 20, [QUINTIC] * 32, [CUBIC] * 32):
+            out = torch.empty_like(x)
+            L.pc_orthogonalize(x, out, steps=len(co), coefficients=co, eps=0.0, ws=L.orthogonalize_workspace(x))
+            growth = np.prod([a for a, _, _ in co])
+            for b in range(2):
+                ref, grow, least = _by_singular_values(g[b], co)
+                d = 4 * (n / 8 + 16 + m) * 2.0 ** -53
+                tol = 8 * m * 2.0 ** -53 / np.sqrt(d) + d / least ** 2 * grow + (8 * m * 2.0 ** -53 * growth ** 2 if growth <= 2048 else 0)
+                e = np.linalg.norm(get(out)[b] - ref)
+                assert e <= (tol + U[typ]) * np.linalg.norm(ref), (rank, len(co), co[0], e / np.linalg.norm(ref), tol)
+
+
+@pytest.mark.parametrize("m,n", [(4, 37), (33, 500), (64, 130)])
+def test_orthogonalize_at_the_ends_of_float32(m, n):
+    """Rank 1 and 4 matrices scaled by a power of two, which changes nothing: subnormal elements whose norm's inverse, times
+    the growth of Q, is far past float32, and elements near its largest."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    rng = np.random.default_rng(m + n)
+    for rank in (1, 4):
+        g = _exact_rank(rng, m, n, rank)
+        outs = []
+        for e in (0, -140, 118):
+            x = put(np.ldexp(g, e))
+            assert (get(x) == np.ldexp(g, e)).all()
+            outs.append(torch.empty_like(x))
+            L.pc_orthogonalize(x, outs[-1], eps=0.0, ws=L.orthogonalize_workspace(x))
+        ref, _, _ = _by_singular_values(g, [QUINTIC] * 5)
+        for out in outs:
+            assert np.linalg.norm(get(out) - ref) <= (E32 + 8 * m * 2.0 ** -53 * 485.0 ** 2) * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("rows,cols", [(16, 1024), (500, 48), (90, 130)])
+def test_orthogonalize_many_steps_stay_bounded(rows, cols):
+    """Rank 1 up to float32's rounding of its elements, whose small singular values the steps raise to the others' size;
+    a matrix of zeros and one with a NaN beside it.  The quintic's values stay below 1.2 (float32 steps for more than
+    64 rows: their roundings join, each below 1e-6 of the value)."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    rng = np.random.default_rng(15)
+    g = torch.stack([put(rng.normal(size=(rows, 1)) @ rng.normal(size=(1, cols))) for _ in range(4)])
+    g[1] = 0
+    g[2, 3, 4] = float("nan")
+    for steps in (7, 12, 16, 20, 32):
+        out = torch.empty_like(g)
+        L.pc_orthogonalize(g, out, steps=steps, ws=L.orthogonalize_workspace(g))
+        assert not out[1].any() and not torch.isfinite(out[2]).any()
+        for b in (0, 3):
+            s = np.linalg.svd(get(out)[b], compute_uv=False)
+            assert np.isfinite(s).all() and s.max() <= 1.21, (steps, s.max())
+            assert s.max() >= 0.6
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
