@@ -250,8 +250,11 @@ void check_orth(int dtype, int64_t batch, int32_t rows, int32_t cols) {
 
 // Bounds of the singular values at every step and of the step's polynomials
 // b t + c t^2 and a + b t + c t^2 (t the squared singular value), where they start in [0, 1]: the
-// largest magnitudes at the interval's ends and the extrema inside it, with a
-// margin for rounding.
+// largest magnitudes at the interval's ends and the extrema inside it.  What
+// goes into the next step's interval is widened by 2^-20, as far as a step's
+// rounding (two float16 planes, 2^-22) can carry a value: triples tuned for their
+// own interval rise steeply behind its end, so a wider margin would compound
+// into a growth that is none.  The 2% are room in the scales alone.
 struct OrthBounds {
   double x[ORTH_MAX_STEPS + 1], p[ORTH_MAX_STEPS];
 };
@@ -260,7 +263,7 @@ OrthBounds orth_bounds(int steps, const float* coef) {
   double top = 1.0;
   for (int s = 0; s < steps; ++s) {
     const double a = coef[3 * s], b = coef[3 * s + 1], c = coef[3 * s + 2], tmax = top * top;
-    o.x[s] = top;
+    o.x[s] = 1.02 * top;
     double next = 0.0, poly = 0.0;
     auto at = [&](double t) {
       if (!(t >= 0.0 && t <= tmax)) return;
@@ -280,10 +283,10 @@ OrthBounds orth_bounds(int steps, const float* coef) {
       at(-a / (3.0 * b));
     }
     o.p[s] = 1.02 * poly;
-    top = 1.02 * next;
+    top = (1.0 + std::ldexp(1.0, -20)) * next;
     if (!(top <= 1024.0)) fail(PC_ERR_INVALID_ARG, "coefficients of step " + std::to_string(s) + " let the matrix grow past 1024");
   }
-  o.x[steps] = top;
+  o.x[steps] = 1.02 * top;
   return o;
 }
 // The shift of A's diagonal that the steps on m x m matrices need, 0 where

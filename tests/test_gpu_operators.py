@@ -611,6 +611,29 @@ def test_orthogonalize_many_steps_of_thin_matrices(m, n, typ):
                 assert e <= (tol + U[typ]) * np.linalg.norm(ref), (rank, len(co), co[0], e / np.linalg.norm(ref), tol)
 
 
+@pytest.mark.parametrize("rows,cols", [(20, 300), (64, 64), (130, 90), (300, 300)])
+def test_orthogonalize_with_a_triple_for_each_step(rows, cols):
+    """Triples tuned step by step, which rise steeply behind their interval.  A step's roundings, 3 2^-22 of X, grow by at
+    most the largest |p'| between 0 and the largest singular value in each later step."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    rng = np.random.default_rng(rows)
+    for g in (rng.normal(size=(rows, cols)), rng.integers(-4, 5, size=(rows, 1)) @ rng.integers(-4, 5, size=(1, cols))):
+        x = put(g)
+        out = torch.empty_like(x)
+        co = [(a / 1.01, b / 1.01 ** 3, c / 1.01 ** 5) for a, b, c in TUNED[:-1]] + TUNED[-1:] + [(1.875, -1.25, 0.375)] * 2
+        L.pc_orthogonalize(x, out, steps=len(co), coefficients=co, ws=L.orthogonalize_workspace(x))
+        co = np.float32(co).astype(np.float64)
+        ref = R.orthogonalize(get(x), co, 1e-7)
+        t = np.linalg.svd(get(x), compute_uv=False)
+        t, tol = t / np.linalg.norm(t), 0.0
+        for a, b, c in co:
+            z = np.linspace(0, t.max(), 2001)
+            tol = (tol + 3 * 2.0 ** -22 * np.linalg.norm(t)) * np.abs(a + 3 * b * z ** 2 + 5 * c * z ** 4).max()
+            t = a * t + b * t ** 3 + c * t ** 5
+        assert np.linalg.norm(get(out) - ref) <= tol + E32 * np.linalg.norm(ref)
+
+
 @pytest.mark.parametrize("m,n", [(4, 37), (33, 500), (64, 130)])
 def test_orthogonalize_at_the_ends_of_float32(m, n):
     """Rank 1 and 4 matrices scaled by a power of two, which changes nothing: subnormal elements whose norm's inverse, times

@@ -231,6 +231,43 @@ def test_orthogonalize_refuses(code, change):
                                                              "ob", "orow", "steps", "co", "eps", "ws", "nws")], None))
 
 
+TUNED = [(8.287, -23.596, 17.300), (4.107, -2.948, 0.545), (3.949, -2.909, 0.552), (3.318, -2.488, 0.510), (2.301, -1.669, 0.419)]
+
+
+SAFE = [(a / 1.01, b / 1.01 ** 3, c / 1.01 ** 5) for a, b, c in TUNED[:-1]] + TUNED[-1:]
+POLAR = (1.875, -1.25, 0.375)
+
+
+def _largest(triples):
+    """The largest singular value that steps from [0, 1] reach: the image of an interval from 0 is one (up to the sign)."""
+    x, top = 1.0, 0.0
+    for a, b, c in triples:
+        z = np.linspace(0, x, 200001)
+        x = np.abs(a * z + b * z ** 3 + c * z ** 5).max()
+        top = max(top, x)
+        if top > 1e6:
+            break
+    return top
+
+
+@pytest.mark.parametrize("triples,accepted", [
+    (TUNED, True),                                                              # each tuned for the interval before it
+    (SAFE, True), (SAFE + [POLAR] * 20, True),
+    (TUNED + [POLAR] * 20, False),                                              # 2.97 after TUNED, which POLAR raises
+    ([(1.5, -0.5, 0.0)] * 32, True), ([(3.4445, -4.7750, 2.0315)] * 32, True),
+    ([(3.9, 0.0, 0.0)] * 5, True), ([(4.1, 0.0, 0.0)] * 5, False), ([(1.6, 0.2, 0.0)] * 12, False),
+    (TUNED[:1] * 5, False)])
+def test_orthogonalize_takes_the_schedules_that_stay_bounded(triples, accepted):
+    """A schedule is refused where singular values from [0, 1] can pass 1024, and only there; one that is taken is
+    refused here for its missing workspace, before any device work."""
+    assert (_largest(triples) <= 1024) == accepted
+    flat = (C.c_float * (3 * len(triples)))(*[v for t in triples for v in t])
+    a = {**ORTH, "steps": len(triples), "co": flat, "ws": None, "nws": 0}
+    rc = L.lib().pc_orthogonalize(*[a[k] for k in ("device", "dtype", "batch", "rows", "cols", "g", "gb", "gr", "out", "ob",
+                                                   "orow", "steps", "co", "eps", "ws", "nws")], None)
+    assert rc == (L.PC_ERR_WORKSPACE if accepted else L.PC_ERR_INVALID_ARG), L.pc_last_error()
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     torch = pytest.importorskip("torch")
     x = torch.zeros(3, 4)
