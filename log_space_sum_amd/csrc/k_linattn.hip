@@ -595,24 +595,26 @@ __global__ __launch_bounds__(256) void mix_scan(MixScanArgs m0, MixScanArgs m1) 
 }
 
 // Gradients of shared key / value heads (bound by the partial sums' bytes): the sum over the heads that share one,
-// in their order.  Only tokens of the sequences are written.
+// in their order.  Only tokens of the sequences are written.  (A launch takes fewer than 2^32 threads: past
+// MIX_SUM_BLOCKS blocks each takes several pieces.)
+constexpr int64_t MIX_SUM_BLOCKS = 1 << 22;
 template <typename IO>
 __global__ __launch_bounds__(256) void mix_sum(MixSumArgs m0, MixSumArgs m1) {
   const MixSumArgs& m = blockIdx.y ? m1 : m0;
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = m.kv_heads * m.dim;
-  const int64_t t = e / per;
-  const int h = (int)(e % per) / m.dim, d = (int)(e % per) % m.dim;
   int64_t t0 = 0, t1 = m.tokens;
   if (m.cu) {
     t0 = min(max((int64_t)m.cu[0], (int64_t)0), m.tokens);
     t1 = min(max((int64_t)m.cu[m.seqs], t0), m.tokens);
   }
-  if (t < t0 || t >= t1) return;
-  const float* p = m.part + (t * m.kv_heads + h) * (int64_t)m.group * m.dim + d;
-  float s = 0.0f;
-  for (int k = 0; k < m.group; ++k) s += p[(int64_t)k * m.dim];
-  ((IO*)m.out)[t * m.o_ts + (int64_t)h * m.o_hs + d] = from_f32<IO>(s);
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < (t1 - t0) * per; e += (int64_t)gridDim.x * 256) {
+    const int64_t t = t0 + e / per;
+    const int h = (int)(e % per) / m.dim, d = (int)(e % per) % m.dim;
+    const float* p = m.part + (t * m.kv_heads + h) * (int64_t)m.group * m.dim + d;
+    float s = 0.0f;
+    for (int k = 0; k < m.group; ++k) s += p[(int64_t)k * m.dim];
+    ((IO*)m.out)[t * m.o_ts + (int64_t)h * m.o_hs + d] = from_f32<IO>(s);
+  }
 }
 
 // ---- single tokens ----------------------------------------------------------
@@ -622,9 +624,12 @@ __global__ __launch_bounds__(256) void mix_sum(MixSumArgs m0, MixSumArgs m1) {
 // thread, the rows dealt out over the workgroup's row groups, whose partial
 // outputs are added in a fixed order.  Rows that name the same slot are
 // successive tokens of that state: the first of them does them all, in order.
+constexpr int MIX_STEP_ROWS = 32768;   // rows of a launch's second dimension; more go along the third
 template <typename IO, int CV>
 __global__ __launch_bounds__(256) void mix_step(MixStepArgs m) {
-  const int head = blockIdx.x % m.heads, first = blockIdx.x / m.heads, tid = threadIdx.x;
+  const int64_t at = (int64_t)blockIdx.z * MIX_STEP_ROWS + blockIdx.y;
+  if (at >= m.batch) return;
+  const int head = blockIdx.x, first = (int)at, tid = threadIdx.x;
   const int kv = head / m.group;
   const int slot = m.slot ? m.slot[first] : first;
   if (slot < 0 || slot >= m.slots) return;
@@ -751,14 +756,15 @@ void launch_mix_scan(const MixScanArgs* a, int n, hipStream_t s) {
 
 void launch_mix_sum(const MixSumArgs& a, const MixSumArgs& b, int dtype, hipStream_t s) {
   const int64_t n = a.tokens * a.kv_heads * std::max(a.dim, b.dim);
-  const dim3 grid((unsigned)((n + 255) / 256), 2);
+  const dim3 grid((unsigned)std::min<int64_t>((n + 255) / 256, MIX_SUM_BLOCKS), 2);
   if (dtype == PC_DTYPE_F32) launch_kernel(mix_sum<float>, grid, dim3(256), 0, s, a, b);
   else if (dtype == PC_DTYPE_F16) launch_kernel(mix_sum<f16>, grid, dim3(256), 0, s, a, b);
   else launch_kernel(mix_sum<bf16>, grid, dim3(256), 0, s, a, b);
 }
 
 void launch_mix_step(const MixStepArgs& a, int dtype, hipStream_t s) {
-  const dim3 grid((unsigned)a.heads * (unsigned)a.batch);
+  const dim3 grid((unsigned)a.heads, (unsigned)std::min(a.batch, MIX_STEP_ROWS),
+                  (unsigned)((a.batch + (int64_t)MIX_STEP_ROWS - 1) / MIX_STEP_ROWS));
   // rows of four columns can be loaded as vectors when none is cut
   const bool four = a.dv % 4 == 0;
 #define PC_MIX_STEP(T)                                                          \

@@ -733,6 +733,52 @@ def test_offsets_past_32_bits():
     near(o, want, 80 * E32 * np.einsum("bhk,bhk->bh", z, z)[..., None] * np.abs(z), "step")
 
 
+def test_linear_attention_step_of_more_rows_than_a_launch_has_blocks():
+    """2^24 rows and some: as many blocks of 256 threads along one dimension are 2^32, which no launch takes."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    n = 2 ** 24 + 5
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(3)
+    q, k, v = (torch.randn((n, 1, 1), generator=gen, device=DEV) for _ in range(3))
+    state, o = torch.randn((n, 1, 1, 1), generator=gen, device=DEV), torch.empty((n, 1, 1), device=DEV)
+    before = state.double()
+    L.pc_linear_attention_step(q, k, v, put(np.array([-0.5])), state, o, scale=1.0)
+    left = np.exp(-0.5) * before[..., 0]
+    want = left + k.double() * v.double()
+    size = left.abs() + (k * v).abs()
+    # the decay's, two products' and the sum's roundings, and one more of the output's product
+    assert ((state[..., 0].double() - want).abs() <= 4 * E32 * size + TINY["f32"]).all()
+    assert ((o.double() - q.double() * want).abs() <= 5 * E32 * size * q.abs() + TINY["f32"]).all()
+
+
+def test_linear_attention_gradients_of_more_elements_than_a_launch_has_threads():
+    """Shared heads, 2^20 + 256 tokens x 32 key heads x 128: 2^32 sums of two heads and some.  Inputs are one token
+    repeated (stride 0); the sequences are the first and the last tokens, the ones between stay as they were."""
+    import log_space_sum_amd as L
+    torch, types = T()
+    n, K, dk, few = 2 ** 20 + 256, 32, 128, 40
+    rng = np.random.default_rng(21)
+    one = [put(rng.normal(size=(1, h, d)), "bf16") for h, d in ((2 * K, dk), (K, dk), (K, 1), (2 * K, 1))]
+    q, k, v, do = (t.expand(n, -1, -1) for t in one)
+    dq, dk_, dv_ = (torch.empty((n, h, d), device=DEV, dtype=types["bf16"]) for h, d in ((2 * K, dk), (K, dk), (K, 1)))
+    dk_[few:few + 10] = 5
+    dk_[n - few - 10:n - few] = 5
+    g = put(np.full(2 * K, -0.1))
+    for start, end in ((0, few), (n - few, n)):
+        cu = torch.tensor([start, end], dtype=torch.int32, device=DEV)
+        L.pc_linear_attention_backward(do, q, k, v, g, dq, dk_, dv_, cu, few, scale=1.0,
+                                       ws=L.linear_attention_workspace(q, k, v, cu, few, backward=True))
+        A = [np.repeat(get(t), few, 0) for t in one]
+        want = R.linear_attention_grad(A[3], *A[:3], get(g), [0, few], 1.0)
+        size = R.linear_attention_grad(np.abs(A[3]), *[np.abs(a) for a in A[:3]], get(g), [0, few], 1.0)
+        for got, ref, mag, name in zip((dq, dk_, dv_), want, size, ("dq", "dk", "dv")):
+            near(got[start:end], ref, _bound("bf16", dk + few + 40, mag, ref), name)
+    assert (dk_[few:few + 10] == 5).all() and (dk_[n - few - 10:n - few] == 5).all()
+    del dq, dk_, dv_
+    torch.cuda.empty_cache()
+
+
 def test_linear_attention_many_short_sequences():
     """More sequences than one grid takes three times over; one token each."""
     import log_space_sum_amd as L
