@@ -296,8 +296,8 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
   f32x4 st[DKB];
   {
     const float* from = nullptr;
-    if (WALK) from = m.nsegs > 1 ? m.seg + (((int64_t)seq * m.nsegs + sgm) * m.heads + head) * elems
-                                 : (m.init ? m.init + ((int64_t)seq * m.heads + head) * elems : nullptr);
+    if (WALK) from = live > 1 ? m.seg + ((seg_slot(m.packed, m.nsegs, m.seglen, seq, t0) + sgm) * m.heads + head) * elems
+                              : (m.init ? m.init + ((int64_t)seq * m.heads + head) * elems : nullptr);
 #pragma unroll
     for (int kb = 0; kb < DKB; ++kb) {
       const int row = 16 * kb + 4 * g;
@@ -545,7 +545,7 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
   }
 
   float* to = nullptr;
-  if (!WALK) to = m.seg + (((int64_t)seq * m.nsegs + sgm) * m.heads + head) * elems;
+  if (!WALK) to = m.seg + ((seg_slot(m.packed, m.nsegs, m.seglen, seq, t0) + sgm) * m.heads + head) * elems;
   else if (m.fin && sgm == live - 1) to = m.fin + ((int64_t)seq * m.heads + head) * elems;
   if (!to) return;
 #pragma unroll
@@ -560,7 +560,8 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
 // The states at the segments' starts from the segments' own states, in place
 // (bound by the states' bytes: 16 segments x 32 heads x 128 x 128, 13 us or 5 TB/s):
 // start_0 = init, start_{s+1} = l^seglen start_s + own_s.
-// EV elements a thread; four segments' loads in flight.
+// EV elements a thread; four segments' loads in flight.  A sequence of one
+// segment walks from its given state.
 template <int EV>
 __global__ __launch_bounds__(256) void mix_scan(MixScanArgs m0, MixScanArgs m1) {
   const MixScanArgs& m = (int)blockIdx.z < m0.seqs ? m0 : m1;
@@ -573,8 +574,9 @@ __global__ __launch_bounds__(256) void mix_scan(MixScanArgs m0, MixScanArgs m1) 
     t1 = min(max((int64_t)m.cu[seq + 1], t0), m.tokens);
   }
   const int live = (int)min(max((t1 - t0 + m.seglen - 1) / m.seglen, (int64_t)1), (int64_t)m.nsegs);
+  if (live == 1) return;
   const float ls = decay_pow(m.log_decay[head], (float)m.seglen);
-  float* p = m.seg + ((int64_t)seq * m.nsegs * m.heads + head) * m.elems + e;
+  float* p = m.seg + (seg_slot(m.packed, m.nsegs, m.seglen, seq, t0) * m.heads + head) * m.elems + e;
   const int64_t step = (int64_t)m.heads * m.elems;
   struct Some {
     float v[EV];

@@ -78,8 +78,8 @@ struct MixArgs {
   const float* init;    // [seqs, heads, da x dc], nullable: 0
   float* fin;           // the states after the last token, nullable
   int32_t st_r, st_c;   // strides of a state's row (da) and column (dc)
-  float* seg;           // [seqs, nsegs, heads, da x dc] states at the segments' starts, when nsegs > 1
-  int32_t nsegs;
+  float* seg;           // [slots, heads, da x dc] states at the segments' starts, when nsegs > 1 (see seg_slot)
+  int32_t nsegs, packed;
   int64_t seglen;
 };
 // Walks of one shape (da, dc), sequences and segments that a launch takes side
@@ -89,13 +89,20 @@ struct MixMany {
   int32_t n, seqs;
 };
 struct MixScanArgs {
-  int32_t seqs, heads, nsegs, elems;
+  int32_t seqs, heads, nsegs, packed, elems;
   int64_t tokens, seglen;
   const int32_t* cu;
   const float* log_decay;
   const float* init;
   float* seg;
 };
+// Where the states of a sequence's segments lie, of its first: in a row for
+// every sequence, or packed by the sequences' first tokens t0.  Only sequences of
+// more than one segment have any; such a one of n tokens has ceil(n / seglen)
+// <= floor(2 n / seglen) of them, so the next one's begin behind its last.
+__host__ __device__ inline int64_t seg_slot(int packed, int nsegs, int64_t seglen, int64_t seq, int64_t t0) {
+  return packed ? 2 * t0 / seglen : seq * nsegs;
+}
 struct MixSumArgs {     // out[t, h] = sum of the group's heads of part[t, h * group ..], of the sequences' tokens
   int64_t tokens;
   int32_t seqs, kv_heads, group, dim;

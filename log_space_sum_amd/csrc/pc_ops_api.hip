@@ -135,13 +135,26 @@ Split mix_segments(const pc_linear_attention* d) {
   return {(int)((longest + len - 1) / len), len};
 }
 
+// The states' slots (see seg_slot): packed where that takes fewer, as with many
+// sequences of which few can have a second segment (4096 of 512 tokens whose
+// longest is not given, 16 heads x 128: 65 slots instead of 131072 = 137 GB).
+struct Slots {
+  int64_t n;
+  bool packed;
+};
+Slots mix_slots(const pc_linear_attention* d, const Split& sp) {
+  if (sp.nsegs <= 1) return {0, false};
+  const int64_t rows = (int64_t)d->num_seqs * sp.nsegs, packed = 2 * d->num_tokens / sp.len + 1;
+  return {std::min(rows, packed), packed < rows};
+}
+
 struct MixWs {
   size_t seg_f = 0, seg_r = 0, dk = 0, dv = 0, total = 0;
 };
 MixWs mix_ws(const pc_linear_attention* d, bool backward) {
   MixWs w;
   const Split sp = mix_segments(d);
-  const size_t states = sp.nsegs > 1 ? (size_t)d->num_seqs * sp.nsegs * d->heads * d->dim_k * d->dim_v * sizeof(float) : 0;
+  const size_t states = (size_t)mix_slots(d, sp).n * d->heads * d->dim_k * d->dim_v * sizeof(float);
   auto take = [&](size_t bytes) {
     const size_t at = w.total;
     w.total += (bytes + 255) / 256 * 256;
@@ -169,6 +182,7 @@ MixArgs mix_base(const pc_linear_attention* d, const Split& sp) {
   a.log_decay = d->log_decay;
   a.pscale = d->scale;
   a.nsegs = sp.nsegs;
+  a.packed = mix_slots(d, sp).packed;
   a.seglen = sp.len;
   return a;
 }
@@ -184,6 +198,7 @@ void mix_starts(const pc_linear_attention* d, const MixArgs* a, int n, hipStream
     c[k].seqs = a[k].seqs;
     c[k].heads = a[k].heads;
     c[k].nsegs = a[k].nsegs;
+    c[k].packed = a[k].packed;
     c[k].elems = d->dim_k * d->dim_v;
     c[k].tokens = a[k].tokens;
     c[k].seglen = a[k].seglen;

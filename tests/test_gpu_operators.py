@@ -779,6 +779,40 @@ def test_linear_attention_gradients_of_more_elements_than_a_launch_has_threads()
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+def test_linear_attention_of_many_sequences_without_a_bound_of_the_lengths(typ):
+    """Short, empty and a few long sequences with max_seqlen left out: few of them have segments, whose states are packed.
+    States in place, and a workspace that holds NaN before."""
+    import log_space_sum_amd as L
+    torch, types = T()
+    rng = np.random.default_rng(17)
+    lens = [int(x) for x in rng.integers(0, 30, size=150)]
+    lens[0], lens[40], lens[41], lens[42], lens[90], lens[-1] = 700, 129, 0, 300, 257, 400
+    H, K, dk, dv = 4, 2, 16, 24
+    q, k, v, do, cu, dcu = _att(rng, lens, H, K, dk, dv, typ, tail=3)
+    g = put(DECAYS[[0, 1, 5, 6]])
+    s0, ds = (put(rng.normal(size=(len(lens), H, dk, dv))) for _ in range(2))
+    o, s1, d0 = torch.empty_like(do), s0.clone(), ds.clone()
+    dq, dk_, dv_ = (torch.empty_like(t) for t in (q, k, v))
+    ws = L.linear_attention_workspace(q, k, v, dcu)
+    assert 0 < ws.numel() < len(lens) * H * dk * dv * 4 * 2
+    L.pc_linear_attention_forward(q, k, v, g, o, dcu, None, s1, s1, 0.3, ws.fill_(255))
+    L.pc_linear_attention_backward(do, q, k, v, g, dq, dk_, dv_, dcu, None, s0, d0, d0, 0.3,
+                                   L.linear_attention_workspace(q, k, v, dcu, backward=True).fill_(255))
+    A = [get(t) for t in (q, k, v, g, s0, do, ds)]
+    B = [np.abs(a) for a in A]
+    ro, rs = R.linear_attention(*A[:4], cu, 0.3, A[4])
+    mo, ms = R.linear_attention(*B[:3], A[3], cu, 0.3, B[4])
+    live, terms = cu[-1], dk + max(lens) + 40
+    near(o[:live], ro[:live], _bound(typ, terms, mo, ro)[:live], "o")
+    near(s1, rs, TINY["f32"] + E32 * np.abs(rs) + terms * E32 * ms, "state")
+    want = R.linear_attention_grad(A[5], *A[:4], cu, 0.3, A[4], A[6])
+    size = R.linear_attention_grad(B[5], *B[:3], A[3], cu, 0.3, B[4], B[6])
+    for got, ref, mag, name in zip((dq, dk_, dv_), want, size, ("dq", "dk", "dv")):
+        near(got[:live], ref[:live], _bound(typ, terms + H, mag, ref)[:live], name)
+    near(d0, want[3], TINY["f32"] + E32 * np.abs(want[3]) + terms * E32 * size[3], "dstate")
+
+
 def test_linear_attention_many_short_sequences():
     """More sequences than one grid takes three times over; one token each."""
     import log_space_sum_amd as L

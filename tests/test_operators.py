@@ -210,6 +210,42 @@ def test_linear_attention_workspace():
     _refuses(L.PC_ERR_INVALID_ARG, f(C.byref(d), 0, None))
 
 
+@pytest.mark.parametrize("seqs,tokens,heads,dim", [(4096, 512, 16, 128), (1000, 100, 8, 128), (65535, 30, 4, 64), (300, 700, 32, 32)])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_linear_attention_workspace_without_a_bound_of_the_lengths(seqs, tokens, heads, dim, dtype):
+    """Many sequences whose longest is not given (max_seqlen: all tokens): the segments' states take no more than the
+    tokens themselves, for each direction."""
+    n, f = C.c_size_t(), L.lib().pc_linear_attention_workspace_bytes
+    d = _attention(dtype=dtype, heads=heads, kv_heads=heads, dim_k=dim, dim_v=dim, num_seqs=seqs, num_tokens=seqs * tokens,
+                   max_seqlen=seqs * tokens)
+    own = 4 * seqs * tokens * heads * dim * (2 if dtype else 4)     # q, k, v, o
+    assert f(C.byref(d), 0, C.byref(n)) == L.PC_OK and n.value <= own
+    assert f(C.byref(d), 1, C.byref(n)) == L.PC_OK and n.value <= 2 * own
+
+
+def _segments(lens, total, seglen, nsegs):
+    """The packed places of every sequence's segments, as the kernels take them."""
+    places, t0 = [], 0
+    for n in lens:
+        live = min(max(-(-n // seglen), 1), nsegs)
+        if live > 1:
+            places += [2 * t0 // seglen + s for s in range(live)]
+        t0 += n
+    assert t0 <= total
+    return places
+
+
+def test_segments_places_are_distinct():
+    rng = np.random.default_rng(5)
+    for trial in range(400):
+        seglen = int(rng.choice([64, 128, 192, 1000]))
+        lens = [int(x) for x in rng.choice([0, 1, seglen - 1, seglen, seglen + 1, 2 * seglen, 2 * seglen + 1, 5 * seglen + 3, 7], size=30)]
+        total = sum(lens) + int(rng.integers(0, 9))
+        for nsegs in (2, 3, 40):
+            p = _segments(lens, total, seglen, nsegs)
+            assert len(set(p)) == len(p) and all(0 <= x < 2 * total // seglen + 1 for x in p)
+
+
 ORTH = dict(device=0, dtype=0, batch=2, rows=96, cols=80, g=P, gb=7680, gr=80, out=P, ob=7680, orow=80, steps=5, co=FLOATS,
             eps=1e-7, ws=P, nws=1 << 40)
 DIVERGES = (C.c_float * 96)(*([8.0, 0.0, 0.0] * 32))
