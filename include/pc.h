@@ -436,7 +436,7 @@ typedef struct pc_heads {
  *  state_in, state_out: device float32 [num_seqs, heads, dim_k, dim_v], the
  *    states before and after the sequences, nullable (0 / not wanted); they
  *    may be the same buffer.  An empty sequence hands its state through.
- *  Token strides are at most 2^23.
+ *  Token strides of whole sequences are at most 2^23 (single tokens: any).
  * A value that is not finite reaches the outputs of its own and later tokens
  * of its sequence only. */
 typedef struct pc_linear_attention {

@@ -87,16 +87,16 @@ void check_call(const pc_linear_attention* d) {
   need(std::isfinite(d->scale) && d->scale != 0.0f, "scale must be finite and not 0");
 }
 
-void check_heads(const pc_linear_attention* d, const pc_heads& t, const char* what) {
+void check_heads(const pc_linear_attention* d, const pc_heads& t, const char* what, bool chunks = true) {
   need(t.data || d->num_tokens == 0, std::string("null ") + what);
   need(t.token_stride >= 0 && t.head_stride >= 0, std::string("negative stride of ") + what);
   // a chunk's rows are addressed with 32-bit byte offsets
-  if (t.token_stride > MIX_MAX_STRIDE)
+  if (chunks && d->num_tokens > 1 && t.token_stride > MIX_MAX_STRIDE)
     fail(PC_ERR_UNSUPPORTED, std::string("token stride of ") + what + " above " + std::to_string(MIX_MAX_STRIDE));
 }
 // an output's elements must be distinct
-void check_out(const pc_linear_attention* d, const pc_heads& t, int heads, int dim, const char* what) {
-  check_heads(d, t, what);
+void check_out(const pc_linear_attention* d, const pc_heads& t, int heads, int dim, const char* what, bool chunks = true) {
+  check_heads(d, t, what, chunks);
   const int64_t ts = t.token_stride, hs = t.head_stride;
   const bool tokens_outside = (heads == 1 || hs >= dim) && (d->num_tokens <= 1 || ts >= (heads - 1) * hs + dim);
   const bool heads_outside = (d->num_tokens <= 1 || ts >= dim) && (heads == 1 || hs >= (d->num_tokens - 1) * ts + dim);
@@ -568,10 +568,10 @@ int pc_linear_attention_step(int device, const pc_linear_attention* d, void* str
     check_mix(d);
     need(d->log_decay, "null log_decay");
     need(std::isfinite(d->scale) && d->scale != 0.0f, "scale must be finite and not 0");
-    check_heads(d, d->q, "q");
-    check_heads(d, d->k, "k");
-    check_heads(d, d->v, "v");
-    check_out(d, d->o, d->heads, d->dim_v, "o");
+    check_heads(d, d->q, "q", false);
+    check_heads(d, d->k, "k", false);
+    check_heads(d, d->v, "v", false);
+    check_out(d, d->o, d->heads, d->dim_v, "o", false);
     need(d->num_slots >= 0 && d->num_slots <= INT_MAX, "num_slots must be in [0, 2^31)");
     need(d->slots || d->num_slots >= d->num_tokens, "fewer slots than rows");
     need((int64_t)d->heads * d->num_tokens <= INT_MAX, "more than 2^31 rows times heads");

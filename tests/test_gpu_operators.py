@@ -357,6 +357,41 @@ def test_linear_attention_step_slots():
         assert (o[i] == 8).all()
 
 
+def test_linear_attention_of_single_tokens_far_apart():
+    """Rows at one position of a padded batch, more than 2^23 elements apart: as single tokens, and one of them as a
+    sequence of one token."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    rng = np.random.default_rng(10)
+    n, H, dk, dv, far = 3, 2, 16, 24, 2 ** 23 + 40
+    buf = torch.zeros(n * far, device=DEV)
+    rows = [torch.as_strided(buf, (n, H, d), (far, d, 1), at) for d, at in ((dk, 0), (dk, 100), (dv, 200), (dv, 300))]
+    q, k, v, o = rows
+    for t in (q, k, v):
+        t.copy_(put(rng.normal(size=t.shape)))
+    g, state = put(DECAYS[:H]), put(rng.normal(size=(n, H, dk, dv)))
+    before = get(state)
+    L.pc_linear_attention_step(q, k, v, g, state, o, scale=0.5)
+    A = [get(t) for t in (q, k, v, g)]
+    cu = list(range(n + 1))
+    ro, rs = R.linear_attention(*A, cu, 0.5, before)
+    mo, ms = R.linear_attention(*[np.abs(a) for a in A[:3]], A[3], cu, 0.5, np.abs(before))
+    near(o, ro, _bound("f32", dk + 8, mo, ro), "o")
+    near(state, rs, TINY["f32"] + 4 * E32 * ms, "state")
+    o.zero_()
+    one = [t[1:2] for t in rows]
+    L.pc_linear_attention_forward(*one[:3], g, one[3], state_in=put(before[1:2]), scale=0.5, ws=L.linear_attention_workspace(*one[:3]))
+    near(one[3], ro[1:2], _bound("f32", dk + 40, mo, ro)[1:2], "one token")
+    dq, dk_, dv_ = (torch.empty(1, *t.shape[1:], device=DEV) for t in one[:3])
+    L.pc_linear_attention_backward(one[3], *one[:3], g, dq, dk_, dv_, state_in=put(before[1:2]), scale=0.5,
+                                   ws=L.linear_attention_workspace(*one[:3], backward=True))
+    B = [get(t) for t in one] + [before[1:2]]
+    want = R.linear_attention_grad(B[3], *B[:3], A[3], [0, 1], 0.5, B[4])
+    size = R.linear_attention_grad(np.abs(B[3]), *[np.abs(a) for a in B[:3]], A[3], [0, 1], 0.5, np.abs(B[4]))
+    for got, ref, mag in zip((dq, dk_, dv_), want, size):
+        near(got, ref, _bound("f32", dv + 40, mag, ref), "gradients of one token")
+
+
 def test_linear_attention_steps_continue_a_prompt():
     import log_space_sum_amd as L
     torch, types = T()

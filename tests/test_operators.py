@@ -195,6 +195,18 @@ def test_linear_attention_step_refuses(code, change):
     _refuses(code, L.lib().pc_linear_attention_step(0, C.byref(_attention(**change)), None))
 
 
+def test_linear_attention_strides_that_are_taken():
+    """Rows of single tokens may lie anywhere (positions of a padded batch); chunks of whole sequences hold offsets of
+    32 bits.  (No slots, or no sequences: nothing reaches a device.)"""
+    far = dict(q=L.pc_heads(P, 1 << 24, 16), k=L.pc_heads(P, 1 << 40, 16), v=L.pc_heads(P, 1 << 30, 24), o=L.pc_heads(P, 1 << 25, 24))
+    step, whole = L.lib().pc_linear_attention_step, L.lib().pc_linear_attention_forward
+    assert step(0, C.byref(_attention(**far, num_slots=0, slots=P)), None) == L.PC_OK, L.pc_last_error()
+    _refuses(L.PC_ERR_UNSUPPORTED, whole(0, C.byref(_attention(**far, num_seqs=0)), P, 1 << 40, None))
+    # a single token's stride is not used
+    assert whole(0, C.byref(_attention(**far, num_seqs=0, num_tokens=1)), P, 1 << 40, None) == L.PC_OK, L.pc_last_error()
+    _refuses(L.PC_ERR_INVALID_ARG, step(0, C.byref(_attention(q=L.pc_heads(P, -1, 16), num_slots=0, slots=P)), None))
+
+
 def test_linear_attention_workspace():
     n = C.c_size_t()
     f = L.lib().pc_linear_attention_workspace_bytes
