@@ -340,6 +340,7 @@ int pc_layer_norm_forward(int device, int dtype, int64_t rows, int32_t cols, con
     need(x && y, "null x or y");
     need(x_stride >= cols || (x_stride >= 0 && rows == 1), "x_stride below cols");
     need(y_stride >= cols || (y_stride >= 0 && rows == 1), "y_stride below cols");
+    need(y != x || y_stride == x_stride || rows == 1, "y is x at another stride");
     DeviceGuard dg(device);
     NormArgs a{};
     a.rows = rows;
@@ -376,6 +377,7 @@ int pc_layer_norm_backward(int device, int dtype, int64_t rows, int32_t cols, co
     check_norm(rows, cols);
     need(rows == 0 || (dy && x && mean && rstd && dx), "null dy, x, mean, rstd or dx");
     for (int64_t st : {dy_stride, x_stride, dx_stride}) need(st >= cols || (st >= 0 && rows <= 1), "a row stride is below cols");
+    need(rows <= 1 || ((dx != dy || dx_stride == dy_stride) && (dx != x || dx_stride == x_stride)), "dx is dy or x at another stride");
     const bool params = dweight || dbias;
     if (rows == 0 && !params) return;
     if (params) check_ws(ws, ws_bytes, norm_ws(rows, cols));
@@ -637,6 +639,8 @@ int pc_orthogonalize(int device, int dtype, int64_t batch, int32_t rows, int32_t
     need(g_batch >= 0, "g_batch is negative");
     need(batch <= 1 || out_batch >= span || (out_batch >= cols && out_row >= (batch - 1) * out_batch + cols),
          "the matrices of out overlap");
+    need(out != g || batch == 0 || ((rows == 1 || out_row == g_row) && (batch == 1 || out_batch == g_batch)),
+         "out is g at other strides");
     OrthPlan p = orth_plan(batch, rows, cols, ws);
     check_ws(ws, ws_bytes, p.total);
     if (batch == 0) return;

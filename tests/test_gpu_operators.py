@@ -116,6 +116,26 @@ def test_layer_norm_backward(rows, cols, typ):
     assert torch.equal(dx, first[0])
 
 
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(37, 512), (3, 5000), (5000, 65), (70, 9)])
+def test_layer_norm_backward_in_place(rows, cols, typ):
+    """dx over dy and over x gives the bits of a dx of its own."""
+    import log_space_sum_amd as L
+    torch, types = T()
+    rng = np.random.default_rng(rows)
+    x, dy = put(rng.normal(size=(rows, cols)), typ), put(rng.normal(size=(rows, cols)), typ)
+    w, mean, rstd = put(rng.normal(size=cols)), put(rng.normal(size=rows) * 0.1), put(np.exp(rng.normal(size=rows) * 0.1))
+    ws, out = L.layer_norm_workspace(rows, cols, DEV), []
+    for place in (None, "dy", "x"):
+        a, b = dy.clone(), x.clone()
+        dx = {None: torch.empty_like(x), "dy": a, "x": b}[place]
+        dw, db = torch.empty(cols, device=DEV), torch.empty(cols, device=DEV)
+        L.pc_layer_norm_backward(a, b, w, mean, rstd, dx, dw, db, ws)
+        out.append((dx, dw, db))
+    for other in out[1:]:
+        assert all(torch.equal(p, q) for p, q in zip(out[0], other))
+
+
 def test_layer_norm_edges():
     import log_space_sum_amd as L
     torch, _ = T()

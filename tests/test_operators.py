@@ -316,6 +316,24 @@ def test_orthogonalize_takes_the_schedules_that_stay_bounded(triples, accepted):
     assert rc == (L.PC_ERR_WORKSPACE if accepted else L.PC_ERR_INVALID_ARG), L.pc_last_error()
 
 
+def test_calls_in_place_keep_the_strides():
+    """An output that is the input at other strides would be overwritten while it is read."""
+    a = {**NORM, "ys": 9}
+    fwd = lambda a: L.lib().pc_layer_norm_forward(*[a[k] for k in ("device", "dtype", "rows", "cols", "x", "xs", "w", "b", "eps", "y",  # noqa: E731
+                                                                   "ys", "mean", "rstd")], None)
+    _refuses(L.PC_ERR_INVALID_ARG, fwd(a))
+    for change in (dict(dxs=9, dys=9), dict(dxs=9, xs=9), dict(dxs=9, x=2 * P)):
+        a = {**NBWD, **change}
+        _refuses(L.PC_ERR_INVALID_ARG, L.lib().pc_layer_norm_backward(*[a[k] for k in ("device", "dtype", "rows", "cols", "dy", "dys",
+                                                                                       "x", "xs", "w", "mean", "rstd", "dx", "dxs", "dw",
+                                                                                       "db", "ws", "nws")], None))
+    for change in (dict(orow=81, ob=8000), dict(ob=7681), dict(batch=1, orow=81), dict(rows=1, batch=2, ob=90, gb=80)):
+        a = {**ORTH, **change}
+        _refuses(L.PC_ERR_INVALID_ARG, L.lib().pc_orthogonalize(*[a[k] for k in ("device", "dtype", "batch", "rows", "cols", "g", "gb",
+                                                                                 "gr", "out", "ob", "orow", "steps", "co", "eps", "ws",
+                                                                                 "nws")], None))
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     torch = pytest.importorskip("torch")
     x = torch.zeros(3, 4)
