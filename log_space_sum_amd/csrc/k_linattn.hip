@@ -27,14 +27,14 @@
 // sequences, see mix_segments) that walk side by side: one pass makes each
 // segment's own state, a scan joins them, and the walk starts from there.
 //
-// What bounds it: at dim 128 the matrix instructions (busy 32% of the time), the
-// vector instructions that split planes (47%) and LDS (51%) share a walk, at 2.9
+// What bounds it: at dim 128 the matrix instructions (busy 36% of the time), the
+// vector instructions that split planes (52%) and LDS (51%) share a walk, at 2.6
 // TB/s of the tokens' bytes; at dim 64 and below, or with few tokens, the chain
 // of chunks.  16384 tokens x 32 heads x 128 bfloat16 (541 MB): segments' states
-// 87 us, scan 13, walk 190 when profiled, 243 us together unprofiled.  Measured
+// 87 us, scan 13, walk 210 when profiled, 262 us together unprofiled.  Measured
 // and not taken: waves of 32 columns (the same, 12% slower for float32), the
 // state's update before the inside products' barrier (the same at dim 64, 5%
-// slower at 128), tiles with exchanged chunks instead of padding (half of the
+// slower at 128; these with two planes), tiles with exchanged chunks instead of padding (half of the
 // bank conflicts, but registers past the limit of two workgroups: the same).
 //
 // Precision: bfloat16 tensors are multiplied in bfloat16 with float32 sums.
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(64 * NW, F != FULL ? 2 : NW == 8 ? 4 : 3) void mix_
   constexpr int LA = DA + O::PAD, LB = DA + (WALK ? O::PAD : O::CPAD), LC = DC + O::CPAD;
   // A plane of the inside products: of every 32 rows the columns up to their
   // last, so that three planes leave room for a third workgroup at dim 64 and a
-  // second at 128 (all columns: 57 and 80 KB; the first 70 instead of 61 us for
+  // second at 128 (all columns: 57 and 80 KB; the first 70 instead of 63 us for
   // a ragged forward of 24 x 1500 x 16 heads).
   constexpr int SPZ = 512 * CB / 2 * (CB / 2 + 1) + 16 * CB * O::PAD;
   auto sp_row = [](int i) { return 512 * (i >> 5) * ((i >> 5) + 1) + 32 * (i >> 5) * O::PAD + (i & 31) * (32 * ((i >> 5) + 1) + O::PAD); };

@@ -17,12 +17,13 @@
 // This holds for few steps.  Where G has a small or no singular value, A's
 // rounding leaves an eigenvalue of about -1e-16 there, which every step multiplies
 // by up to a^2 (16 steps of the usual a = 3.4: past 1, and then without bound).
-// Past a growth of Q of ORTH_GROWTH the steps therefore run on a factor X' with X' X'^T = A_0 + d I
-// (Cholesky), X' <- M X', and A = X' X'^T is formed afresh in every step: it has
-// no negative eigenvalue beyond its rounding, which is not carried on.  d, above
-// the rounding of A_0, keeps the factorisation definite and |X'| >= |X| in every
-// direction, so Q X_0 stays within the steps' bounds, and Q below top / sqrt(d),
-// which 64 bits hold (rank 1 and 4 matrices after 32 steps: 1e-8 of the result).
+// Past a growth of Q of ORTH_GROWTH the steps therefore run on a factor X' with
+// X' X'^T = A_0 + d I (Cholesky), X' <- M X', and A = X' X'^T is formed afresh in
+// every step: it has no negative eigenvalue beyond its rounding, which is not
+// carried on.  d, above the rounding of A_0, keeps the factorisation definite and
+// |X'| >= |X| in every direction, so Q X_0 stays within the steps' bounds, and Q
+// below top / sqrt(d), which 64 bits hold (rank 1 and 4 matrices after 32 steps:
+// 1e-8 of the result).
 //
 // Larger m: three products a step on the float16 matrix instruction.  An
 // operand is split into two float16 planes of a value scaled by a power of two
@@ -32,9 +33,9 @@
 // every type: one plane of A's operands alone would put 4e-4 of the result on
 // top of a bfloat16 result's own rounding (1.7e-3).  The symmetric products (A,
 // A^2) compute the tiles on and above the diagonal only.  Bound by the matrix
-// instructions: at 4096 x 4096 B X runs at 1.09 PFLOP/s of float16 products
-// (380 us for three of 137 GFLOP; a library product reaches 1.08), A and A^2 at
-// 1.0.
+// instructions: at 4096 x 4096 B X runs at 1.06 PFLOP/s of float16 products
+// (390 us for three of 137 GFLOP; a library product reaches 1.08), A and A^2 at
+// 0.95 (with the tiles left over).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -126,7 +126,10 @@ Split mix_segments(const pc_linear_attention* d) {
   if (chunks <= 5) return {1, chunks * chunk};
   const int64_t full = std::min<int64_t>(d->num_seqs, (d->num_tokens + longest - 1) / longest);
   const int64_t walks = std::max<int64_t>(1, full * d->heads);
-  const int64_t room = std::max(d->dim_k, d->dim_v) > 64 ? 512 : 1024;   // walks that the card holds at a time
+  // walks aimed at: two workgroups a compute unit at dim 128, four of the smallest
+  // at 64 and below (of bfloat16 at dim 64 three fit, of dims between 64 and 128
+  // one or two: there some walks take a second round)
+  const int64_t room = std::max(d->dim_k, d->dim_v) > 64 ? 512 : 1024;
   const double mean = 2.0 * d->dim_k * d->dim_v / (d->dim_k + d->dim_v);
   const int64_t least = std::max(2 * chunk, (int64_t)(3.2 * mean / (d->dtype == PC_DTYPE_F32 ? 4 : 2)));
   const int64_t n = std::max<int64_t>(1, std::min({(room + walks - 1) / walks, (longest + least - 1) / least,
