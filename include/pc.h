@@ -492,7 +492,7 @@ int pc_linear_attention_step(int device, const pc_linear_attention* d, void* str
  * bounded: coefficients with which one could pass 1024 are refused.
  * G and out: dtype, rows and matrices at their strides (g_batch etc., elements;
  * out may be G with the same strides).  Products run at float32 level for every
- * dtype; the result is rounded once.  A matrix of zeros gives zeros (eps > 0); one with a value that is
+ * dtype; the result alone is rounded to it.  A matrix of zeros gives zeros (eps > 0); one with a value that is
  * not finite gives values that are not.
  * Errors: PC_ERR_INVALID_ARG (sizes, strides, eps, steps, coefficients),
  * PC_ERR_UNSUPPORTED (a dimension above 32768, batch above 65535, unknown
