@@ -482,6 +482,122 @@ int pc_linear_attention_backward(int device, const pc_linear_attention* d, void*
  * name the same slot are successive tokens of that state, in the rows' order. */
 int pc_linear_attention_step(int device, const pc_linear_attention* d, void* stream);
 
+/* Norm of query and key heads with the rotation by position, in one pass.  Of
+ * every head x [dim] (1 .. 256) of every token
+ *   g = x / sqrt(mean(x^2) + eps) weight     (norm 1; norm 0: g = x)
+ * and the pairs (a, b) of its first rotary_dim elements are turned by
+ * positions[token] freq[pair]:
+ *   y_a = magnitude (g_a cos - g_b sin),  y_b = magnitude (g_b cos + g_a sin)
+ * (the other elements are g).  Pair i is elements (i, i + rotary_dim / 2), or with
+ * interleaved 1 (2 i, 2 i + 1).  Queries and keys go through the same call; heads or
+ * kv_heads may be 0.  Angles are taken in 64 bits for any position.
+ *  positions: device int32 [num_tokens] (any value); freq: device float64
+ *    [rotary_dim / 2], radians a position (pc_rotary_frequencies); weights: device
+ *    float32 [dim], nullable (1).
+ * Outputs may be their inputs (same strides). */
+typedef struct pc_rotary {
+  int32_t dtype;
+  int32_t heads, kv_heads, dim;
+  int64_t num_tokens;
+  int32_t rotary_dim, interleaved, norm;
+  float eps, magnitude;
+  const int32_t* positions;
+  const double* freq;
+  const float *q_weight, *k_weight;
+  pc_heads q, k;              /* forward: inputs; backward: the forward's inputs (norm 1 only) */
+  pc_heads q_out, k_out;      /* forward: outputs */
+  pc_heads d_q_out, d_k_out;  /* backward: gradients of the outputs */
+  pc_heads d_q, d_k;          /* backward: gradients of the inputs (overwritten) */
+  float *d_q_weight, *d_k_weight;  /* backward, norm 1: [dim], overwritten, nullable: not wanted */
+} pc_rotary;
+
+/* freq[i] = base^(-2 i / rotary_dim) (host arrays), and for contexts longer than
+ * those it is meant for:
+ *  PC_ROTARY_LINEAR: divided by factor (positions are squeezed);
+ *  PC_ROTARY_BASE: base factor^(rotary_dim / (rotary_dim - 2)) in place of base (the
+ *    slowest pair is divided by factor, the fastest kept);
+ *  PC_ROTARY_PARTS: a pair of `high` turns or more over `original` positions is
+ *    kept, one of `low` or fewer is divided by factor, between them linear in the turns.
+ * Errors: PC_ERR_INVALID_ARG. */
+#define PC_ROTARY_PLAIN  0
+#define PC_ROTARY_LINEAR 1
+#define PC_ROTARY_BASE   2
+#define PC_ROTARY_PARTS  3
+int pc_rotary_frequencies(int32_t rotary_dim, double base, int scaling, double factor, double original, double low, double high,
+                          double* freq);
+
+/* Errors of all three: PC_ERR_INVALID_ARG, PC_ERR_UNSUPPORTED (dim above 256,
+ * unknown dtype), PC_ERR_WORKSPACE, PC_ERR_HIP.  The backward's workspace is needed
+ * for the weights' gradients only; results are the same bits at every run. */
+int pc_rotary_forward(int device, const pc_rotary* d, void* stream);
+int pc_rotary_workspace_bytes(const pc_rotary* d, size_t* bytes);
+int pc_rotary_backward(int device, const pc_rotary* d, void* ws, size_t ws_bytes, void* stream);
+
+/* One tensor of a cache in pages, [num_pages, page_size, kv_heads, dim]: its first
+ * element and three strides. */
+typedef struct pc_pages {
+  void* data;
+  int64_t page_stride, token_stride, head_stride;
+} pc_pages;
+
+/* Causal softmax attention: along every sequence
+ *   o_i = sum_{j <= i} p_ij v_j,   p_ij = exp(scale q_i . k_j - lse_i),
+ *   lse_i = log sum_{j <= i} exp(scale q_i . k_j)
+ * Fields not used by a call are ignored.
+ *  heads, kv_heads: heads of q and o, and of k and v; kv_heads divides heads,
+ *    and head h reads key / value head h / (heads / kv_heads).
+ *  dim_k, dim_v: 1 .. 128.  num_tokens: at most 2^30.
+ *  num_seqs, cu_seqlens: as pc_linear_attention's (num_seqs at most 2^24).
+ *  scale: finite, not 0.
+ *  lse: device float32 [num_tokens, heads]; forward: nullable, backward: what the forward left.
+ * Outputs are what float32 arithmetic gives, rounded once to their type.  What a row
+ * may not attend does not reach it, also if it is not finite. */
+typedef struct pc_attention {
+  int32_t dtype;
+  int32_t heads, kv_heads, dim_k, dim_v;
+  int32_t num_seqs;
+  int64_t num_tokens;
+  const int32_t* cu_seqlens;
+  float scale;
+  pc_heads q, k, v, o;
+  float* lse;
+  /* backward: the gradient of o, and those of q, k, v (overwritten) */
+  pc_heads d_o, d_q, d_k, d_v;
+  /* new tokens over a cache in pages */
+  pc_pages k_cache, v_cache;
+  int32_t num_pages, page_size, max_pages;
+  const int32_t* page_table;   /* device int32 [num_seqs, max_pages], rows at page_table_stride */
+  int64_t page_table_stride;
+  const int32_t* cached;       /* device int32 [num_seqs]: tokens that the cache holds of each sequence */
+  int64_t max_seqlen;          /* bounds of the new tokens of a sequence and of all its tokens, for the choice */
+  int64_t max_length;          /* of the split (results do not depend on them beyond rounding) */
+} pc_attention;
+
+/* Workspace of the forward (backward 0) or backward (1) pass. */
+int pc_attention_workspace_bytes(const pc_attention* d, int backward, size_t* bytes);
+
+/* Whole sequences: o (and lse) from q, k, v.
+ * Errors: PC_ERR_INVALID_ARG, PC_ERR_UNSUPPORTED (dims above 128, unknown
+ * dtype), PC_ERR_WORKSPACE, PC_ERR_HIP. */
+int pc_attention_forward(int device, const pc_attention* d, void* ws, size_t ws_bytes, void* stream);
+
+/* The gradients d_q, d_k, d_v from d_o, q, k, v and the forward's o and lse (P is
+ * exp(scale q . k - lse) and the rows' sums are d_o . o, of the o and lse given); those
+ * of a shared key / value head are summed in float32 over the heads that share it.
+ * Results are the same bits at every run. */
+int pc_attention_backward(int device, const pc_attention* d, void* ws, size_t ws_bytes, void* stream);
+
+/* New tokens over a cache: sequence i has cached[i] tokens in the cache (clamped to
+ * [0, max_pages page_size]) and the new tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1 of q, k, v behind
+ * them (any number, 0 included; without cu_seqlens: one sequence, or num_seqs =
+ * num_tokens and one token each).  Position p lies in row p % page_size of page
+ * page_table[i][p / page_size].  Each new token attends all tokens up to itself, and the new keys
+ * and values are stored at their positions.  A page outside [0, num_pages) is none: its
+ * cached positions are not attended, and new tokens are attended but not stored there,
+ * nor beyond max_pages page_size.  Pages that hold new tokens must be no other sequence's in the same call. */
+int pc_attention_cached_workspace_bytes(const pc_attention* d, size_t* bytes);
+int pc_attention_cached(int device, const pc_attention* d, void* ws, size_t ws_bytes, void* stream);
+
 /* Orthogonalised update: each of `batch` matrices [rows, cols] is replaced by
  * an approximation of its nearest orthogonal one (U V^T of its singular value
  * decomposition), by Newton-Schulz steps.  With X = G / (|G| + eps), |G| the

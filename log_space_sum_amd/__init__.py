@@ -80,6 +80,31 @@ class pc_linear_attention(C.Structure):
                 ("state", C.c_void_p), ("num_slots", C.c_int64), ("slots", C.c_void_p)]
 
 
+class pc_pages(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("page_stride", C.c_int64), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class pc_attention(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("heads", C.c_int32), ("kv_heads", C.c_int32), ("dim_k", C.c_int32),
+                ("dim_v", C.c_int32), ("num_seqs", C.c_int32), ("num_tokens", C.c_int64), ("cu_seqlens", C.c_void_p),
+                ("scale", C.c_float), ("q", pc_heads), ("k", pc_heads), ("v", pc_heads), ("o", pc_heads),
+                ("lse", C.c_void_p), ("d_o", pc_heads), ("d_q", pc_heads), ("d_k", pc_heads), ("d_v", pc_heads),
+                ("k_cache", pc_pages), ("v_cache", pc_pages), ("num_pages", C.c_int32), ("page_size", C.c_int32),
+                ("max_pages", C.c_int32), ("page_table", C.c_void_p), ("page_table_stride", C.c_int64),
+                ("cached", C.c_void_p), ("max_seqlen", C.c_int64), ("max_length", C.c_int64)]
+
+
+class pc_rotary(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("heads", C.c_int32), ("kv_heads", C.c_int32), ("dim", C.c_int32),
+                ("num_tokens", C.c_int64), ("rotary_dim", C.c_int32), ("interleaved", C.c_int32), ("norm", C.c_int32),
+                ("eps", C.c_float), ("magnitude", C.c_float), ("positions", C.c_void_p), ("freq", C.c_void_p),
+                ("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("q", pc_heads), ("k", pc_heads),
+                ("q_out", pc_heads), ("k_out", pc_heads), ("d_q_out", pc_heads), ("d_k_out", pc_heads),
+                ("d_q", pc_heads), ("d_k", pc_heads), ("d_q_weight", C.c_void_p), ("d_k_weight", C.c_void_p)]
+
+
+ROTARY_SCALINGS = {None: 0, "linear": 1, "base": 2, "parts": 3}
+
 EXPORTS = {
     "pc_compile_layout": (C.c_int, [C.POINTER(pc_circuit_desc), C.c_int, C.POINTER(C.c_void_p)]),
     "pc_destroy": (C.c_int, [C.c_void_p]),
@@ -115,6 +140,16 @@ EXPORTS = {
     "pc_orthogonalize": (C.c_int, [C.c_int, C.c_int, C.c_int64, C.c_int32, C.c_int32, C.c_void_p, C.c_int64, C.c_int64,
                                    C.c_void_p, C.c_int64, C.c_int64, C.c_int32, C.POINTER(C.c_float), C.c_float,
                                    C.c_void_p, C.c_size_t, C.c_void_p]),
+    "pc_rotary_frequencies": (C.c_int, [C.c_int32, C.c_double, C.c_int, C.c_double, C.c_double, C.c_double, C.c_double,
+                                        C.POINTER(C.c_double)]),
+    "pc_rotary_forward": (C.c_int, [C.c_int, C.POINTER(pc_rotary), C.c_void_p]),
+    "pc_rotary_workspace_bytes": (C.c_int, [C.POINTER(pc_rotary), C.POINTER(C.c_size_t)]),
+    "pc_rotary_backward": (C.c_int, [C.c_int, C.POINTER(pc_rotary), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "pc_attention_workspace_bytes": (C.c_int, [C.POINTER(pc_attention), C.c_int, C.POINTER(C.c_size_t)]),
+    "pc_attention_forward": (C.c_int, [C.c_int, C.POINTER(pc_attention), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "pc_attention_backward": (C.c_int, [C.c_int, C.POINTER(pc_attention), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "pc_attention_cached_workspace_bytes": (C.c_int, [C.POINTER(pc_attention), C.POINTER(C.c_size_t)]),
+    "pc_attention_cached": (C.c_int, [C.c_int, C.POINTER(pc_attention), C.c_void_p, C.c_size_t, C.c_void_p]),
     "pc_last_error": (C.c_char_p, []),
     "pc_layout_info": (C.c_int, [C.c_void_p, C.POINTER(pc_layout_summary)]),
     "pc_layer_class": (C.c_int, [C.c_void_p, C.c_int, C.POINTER(C.c_int)]),
@@ -676,6 +711,187 @@ def pc_linear_attention_step(q, k, v, log_decay, state, o, slots=None, scale=Non
     d.state = _dense(state, dev, torch.float32, (d.num_slots, H, dk, dv), "state")
     d.slots = _dense(slots, dev, torch.int32, (T,), "slots")
     _check(lib().pc_linear_attention_step(dev, d, _stream_of(dev, stream)))
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, original=0.0, low=1.0, high=32.0,
+                       device="cuda"):
+    """The pairs' frequencies for pc_rotary_forward: float64 [rotary_dim / 2], base ** (-2 i / rotary_dim) radians a
+    position.  scaling, for contexts `factor` times longer than meant: "linear" (all divided by factor), "base" (a larger
+    base: the slowest pair is divided by factor), "parts" (pairs of at most `low` turns over `original` positions are
+    divided by factor, of at least `high` kept, between them in proportion)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {list(ROTARY_SCALINGS)}, got {scaling!r}")
+    n = int(rotary_dim)
+    host = (C.c_double * max(1, n // 2))()
+    _check(lib().pc_rotary_frequencies(n, base, ROTARY_SCALINGS[scaling], factor, original, low, high, host))
+    torch = _torch()
+    return torch.tensor(list(host)[:n // 2], dtype=torch.float64, device=device)
+
+
+def _three(t, what):
+    if t.dim() != 3:
+        raise ValueError(f"{what} must have three dimensions (tokens, heads, dim)")
+    return t
+
+
+def _rotary(q, k, positions, freq, interleaved, magnitude, norm, eps, q_weight, k_weight):
+    """The descriptor for heads like q [tokens, heads, dim] and k [tokens, kv_heads, dim] (None: no keys)."""
+    torch = _torch()
+    dev = _device(_three(q, "q"), "q")
+    T, H, dim = q.shape
+    d = pc_rotary(_dtype(q, "q"), H, 0 if k is None else _three(k, "k").shape[1], dim, T, 2 * freq.numel(),
+                  1 if interleaved else 0, 1 if norm else 0, eps, magnitude)
+    d.positions = _dense(positions, dev, torch.int32, (T,), "positions")
+    d.freq = _dense(freq, dev, torch.float64, (freq.numel(),), "freq")
+    if norm:
+        d.q_weight = _dense(q_weight, dev, torch.float32, (dim,), "q_weight")
+        d.k_weight = _dense(k_weight, dev, torch.float32, (dim,), "k_weight")
+    elif q_weight is not None or k_weight is not None:
+        raise ValueError("weights belong to the norm: norm is False")
+    return d, dev, q.dtype, (T, H, dim), (T, d.kv_heads, dim)
+
+
+def pc_rotary_forward(q, k, q_out, k_out, positions, freq, interleaved=False, magnitude=1.0, norm=False, q_weight=None,
+                      k_weight=None, eps=1e-6, stream=None):
+    """q_out, k_out = the heads of q [tokens, heads, dim] and k [tokens, kv_heads, dim] (None: none), normalised by their
+    root mean square and weighted (norm; weights: float32 [dim] or None), and turned by positions (int32 [tokens]) times
+    freq (rotary_frequencies; its pairs take the first elements, the others are not turned).  Pair i is elements
+    (i, i + pairs), interleaved: (2 i, 2 i + 1).  Outputs may be their inputs."""
+    d, dev, dt, sq, sk = _rotary(q, k, positions, freq, interleaved, magnitude, norm, eps, q_weight, k_weight)
+    _heads(d.q, q, dev, dt, sq, "q")
+    _heads(d.q_out, q_out, dev, dt, sq, "q_out")
+    if k is not None:
+        _heads(d.k, k, dev, dt, sk, "k")
+        _heads(d.k_out, k_out, dev, dt, sk, "k_out")
+    _check(lib().pc_rotary_forward(dev, d, _stream_of(dev, stream)))
+
+
+def rotary_workspace(q, k=None):
+    """A workspace tensor for pc_rotary_backward with gradients of weights, on heads like q and k."""
+    T, H, dim = _three(q, "q").shape
+    d = pc_rotary(_dtype(q, "q"), H, 0 if k is None else _three(k, "k").shape[1], dim, T)
+    return _torch().empty(_bytes(lib().pc_rotary_workspace_bytes, d), dtype=_torch().uint8, device=q.device)
+
+
+def pc_rotary_backward(dq_out, dk_out, dq, dk, positions, freq, interleaved=False, magnitude=1.0, norm=False, q=None, k=None,
+                       q_weight=None, k_weight=None, dq_weight=None, dk_weight=None, eps=1e-6, ws=None, stream=None):
+    """dq, dk from dq_out, dk_out (the gradients of the forward call's outputs), and with norm, from its q and k,
+    dq_weight and dk_weight (float32 [dim], overwritten, or None: not wanted).  dq may be dq_out or q, dk likewise.
+    ws: rotary_workspace(q, k), needed for the weights' gradients."""
+    d, dev, dt, sq, sk = _rotary(dq_out, dk_out, positions, freq, interleaved, magnitude, norm, eps, q_weight, k_weight)
+    f32, dim = _torch().float32, sq[2]
+    _heads(d.d_q_out, dq_out, dev, dt, sq, "dq_out")
+    _heads(d.d_q, dq, dev, dt, sq, "dq")
+    if norm:
+        _heads(d.q, q, dev, dt, sq, "q")
+        d.d_q_weight = _dense(dq_weight, dev, f32, (dim,), "dq_weight")
+        d.d_k_weight = _dense(dk_weight, dev, f32, (dim,), "dk_weight")
+    elif dq_weight is not None or dk_weight is not None:
+        raise ValueError("weights belong to the norm: norm is False")
+    if dk_out is not None:
+        _heads(d.d_k_out, dk_out, dev, dt, sk, "dk_out")
+        _heads(d.d_k, dk, dev, dt, sk, "dk")
+        if norm:
+            _heads(d.k, k, dev, dt, sk, "k")
+    pws, nws = _ws_ptr(ws, dev)
+    _check(lib().pc_rotary_backward(dev, d, pws, nws, _stream_of(dev, stream)))
+
+
+def _softmax_attention(q, k, v, scale, cu_seqlens):
+    """The descriptor of q [tokens, heads, dim_k], k [tokens, kv_heads, dim_k], v [tokens, kv_heads, dim_v]."""
+    dev, dt = _device(_three(q, "q"), "q"), q.dtype
+    T, H, dk = q.shape
+    K, dv = _three(k, "k").shape[1], _three(v, "v").shape[2]
+    d = pc_attention(_dtype(q, "q"), H, K, dk, dv, 1, T)
+    d.scale = dk ** -0.5 if scale is None else scale
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must have one dimension and at least one entry")
+        d.num_seqs = cu_seqlens.numel() - 1
+        d.cu_seqlens = _dense(cu_seqlens, dev, _torch().int32, cu_seqlens.shape, "cu_seqlens")
+    _heads(d.q, q, dev, dt, (T, H, dk), "q")
+    _heads(d.k, k, dev, dt, (T, K, dk), "k")
+    _heads(d.v, v, dev, dt, (T, K, dv), "v")
+    return d, dev, dt, (T, H, K, dk, dv)
+
+
+def attention_workspace(q, k, v, cu_seqlens=None, max_seqlen=None, backward=False):
+    """A workspace tensor for pc_attention_forward, or with backward for pc_attention_backward, on tensors of these
+    shapes."""
+    d, _, _, _ = _softmax_attention(q, k, v, None, cu_seqlens)
+    n = _bytes(lib().pc_attention_workspace_bytes, d, 1 if backward else 0)
+    return _torch().empty(n, dtype=_torch().uint8, device=q.device)
+
+
+def pc_attention_forward(q, k, v, o, lse=None, cu_seqlens=None, max_seqlen=None, scale=None, ws=None, stream=None):
+    """Causal softmax attention: o [tokens, heads, dim_v] and lse (float32 [tokens, heads], kept for the backward pass, or
+    None) from q, k, v along every sequence.  cu_seqlens: int32 [sequences + 1] on the GPU (None: one sequence);
+    max_seqlen: a bound of the longest (None: the number of tokens); scale: None for dim_k ** -0.5;
+    ws: attention_workspace(...)."""
+    d, dev, dt, (T, H, K, dk, dv) = _softmax_attention(q, k, v, scale, cu_seqlens)
+    _heads(d.o, o, dev, dt, (T, H, dv), "o")
+    d.lse = _dense(lse, dev, _torch().float32, (T, H), "lse")
+    pws, nws = _ws_ptr(ws, dev)
+    _check(lib().pc_attention_forward(dev, d, pws, nws, _stream_of(dev, stream)))
+
+
+def pc_attention_backward(do, q, k, v, o, lse, dq, dk, dv, cu_seqlens=None, max_seqlen=None, scale=None, ws=None, stream=None):
+    """dq, dk, dv from do and the forward call's q, k, v, o and lse; ws: attention_workspace(..., backward=True)."""
+    d, dev, dt, (T, H, K, nk, nv) = _softmax_attention(q, k, v, scale, cu_seqlens)
+    _heads(d.o, o, dev, dt, (T, H, nv), "o")
+    _heads(d.d_o, do, dev, dt, (T, H, nv), "do")
+    d.lse = _dense(lse, dev, _torch().float32, (T, H), "lse")
+    _heads(d.d_q, dq, dev, dt, (T, H, nk), "dq")
+    _heads(d.d_k, dk, dev, dt, (T, K, nk), "dk")
+    _heads(d.d_v, dv, dev, dt, (T, K, nv), "dv")
+    pws, nws = _ws_ptr(ws, dev)
+    _check(lib().pc_attention_backward(dev, d, pws, nws, _stream_of(dev, stream)))
+
+
+def _cached_sizes(d, dev, k_cache, page_table, cu_seqlens, max_seqlen, max_length):
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must have four dimensions (pages, page_size, kv_heads, dim_k)")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must have two dimensions (sequences, pages of each)")
+    n = d.num_seqs = page_table.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+    d.num_pages, d.page_size, d.max_pages = k_cache.shape[0], k_cache.shape[1], page_table.shape[1]
+    d.page_table = _operand(page_table, dev, _torch().int32, (n, d.max_pages), "page_table")
+    d.page_table_stride = page_table.stride(0)
+    d.max_seqlen = max_seqlen if max_seqlen is not None else 1 if cu_seqlens is None and n > 1 else d.num_tokens
+    d.max_length = max_length if max_length is not None else d.max_pages * d.page_size
+    return n
+
+
+def attention_cached_workspace(q, k_cache, v_cache, page_table, cu_seqlens=None, max_seqlen=None, max_length=None):
+    """A workspace tensor for pc_attention_cached on new tokens like q and these arguments."""
+    T, H, dk = _three(q, "q").shape
+    d = pc_attention(_dtype(q, "q"), H, k_cache.shape[2], dk, v_cache.shape[3], 1, T)
+    _cached_sizes(d, _device(q, "q"), k_cache, page_table, cu_seqlens, max_seqlen, max_length)
+    return _torch().empty(_bytes(lib().pc_attention_cached_workspace_bytes, d), dtype=_torch().uint8, device=q.device)
+
+
+def _pages(to, t, dev, dtype, shape, what):
+    to.data = _operand(t, dev, dtype, shape, what)
+    to.page_stride, to.token_stride, to.head_stride, _ = t.stride()
+
+
+def pc_attention_cached(q, k, v, k_cache, v_cache, page_table, lengths, o, cu_seqlens=None, max_seqlen=None, max_length=None,
+                        scale=None, ws=None, stream=None):
+    """Causal softmax attention of new tokens over a cache in pages, which they join.  Sequence i has lengths[i] tokens
+    (int32 [sequences]) in k_cache [pages, page_size, kv_heads, dim_k] and v_cache, position p in row p % page_size of page
+    page_table[i, p // page_size] (int32 [sequences, pages of each]), and the new tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1
+    of q, k, v behind them (cu_seqlens None: all of them with one sequence, else one token each).  Writes
+    o [tokens, heads, dim_v] and the new tokens' rows of the caches.  max_seqlen, max_length: bounds of a
+    sequence's new tokens and of all its tokens (None: those of the shapes); ws: attention_cached_workspace(...) with the same."""
+    i32 = _torch().int32
+    d, dev, dt, (T, H, K, dk, dv) = _softmax_attention(q, k, v, scale, cu_seqlens)
+    n = _cached_sizes(d, dev, k_cache, page_table, cu_seqlens, max_seqlen, max_length)
+    _heads(d.o, o, dev, dt, (T, H, dv), "o")
+    _pages(d.k_cache, k_cache, dev, dt, (d.num_pages, d.page_size, K, dk), "k_cache")
+    _pages(d.v_cache, v_cache, dev, dt, (d.num_pages, d.page_size, K, dv), "v_cache")
+    d.cached = _dense(lengths, dev, i32, (n,), "lengths")
+    pws, nws = _ws_ptr(ws, dev)
+    _check(lib().pc_attention_cached(dev, d, pws, nws, _stream_of(dev, stream)))
 
 
 def _matrices(t, what):

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpc.so")
 SOURCES = ["pc_compile.cpp", "pc_api.hip", "k_gemm.hip", "k_elem.hip", "k_lowrank.hip", "k_vbatch.hip", "k_f8gemm.hip",
-           "pc_ops_api.hip", "k_norm.hip", "k_linattn.hip", "k_orth.hip"]
+           "pc_ops_api.hip", "k_norm.hip", "k_linattn.hip", "k_orth.hip",
+           "k_rotary.hip", "k_attn_fwd.hip", "k_attn_bwd.hip", "k_attn_cached.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",

@@ -1,0 +1,248 @@
+// k_attn.h -- what the softmax attention's kernels share: how a type is
+// multiplied, tiles in LDS and their fragments, where rows lie.
+//
+// Every product runs on the 32 x 32 x 16 matrix instruction.  Its operands: a
+// lane holds 8 consecutive elements of the contracted dimension, from 8 h, of row
+// (column) l of 32, with l = lane % 32, h = lane / 32; its result: a lane holds
+// column l and of the rows 8 (r / 4) + 4 h + r % 4, r = 0 .. 15.  So a result's
+// registers are the next product's operand where the contraction takes the
+// elements in that order on both sides: the other operand is read from LDS by the
+// transposing read, four rows of one column at a time, from rows 4 h and 8 + 4 h of
+// every 16.  Scores and weights never pass through LDS.
+//
+// Precision.  16-bit tensors are multiplied as they are.  What a kernel computes
+// and multiplies again (the weights P, the gradients dS of the scores) is split into
+// planes, each the rounding of what the planes before it leave: three of bfloat16 (24 bits), or
+// two of float16 (22 bits).  One plane, the usual choice, would add an error as
+// large as the output's own rounding; with these, outputs are what float32 arithmetic
+// gives, rounded once.  float32 tensors are split into three bfloat16 planes
+// too, and products of planes p, q with p + q <= 2 are summed (24 bits).
+#pragma once
+#include <type_traits>
+
+#include "pc_ops.h"
+
+namespace pc {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+typedef uint4 frag;     // 8 elements of 16 bits
+
+constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.693147180559945309f;
+
+// ---- types -------------------------------------------------------------------
+// IN: planes of a tensor's values, W: planes of computed ones.  BIAS: weights are
+// held as 2^BIAS times themselves (float16: its small numbers have few bits).
+struct Bf16Planes {
+  static __device__ __forceinline__ f32x16 mma(frag a, frag b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
+  }
+  static __device__ __forceinline__ float low(uint32_t u) { return __uint_as_float(u << 16); }
+  static __device__ __forceinline__ float high(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+};
+template <typename T>
+struct Num;
+template <>
+struct Num<bf16> : Bf16Planes {
+  static constexpr int IN = 1, W = 3, BIAS = 0;
+};
+template <>
+struct Num<float> : Bf16Planes {
+  static constexpr int IN = 3, W = 3, BIAS = 0;
+};
+template <>
+struct Num<f16> {
+  static constexpr int IN = 1, W = 2, BIAS = 14;
+  static __device__ __forceinline__ f32x16 mma(frag a, frag b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, f16x2));
+  }
+  static __device__ __forceinline__ float low(uint32_t u) { return (float)__builtin_bit_cast(f16x2, u)[0]; }
+  static __device__ __forceinline__ float high(uint32_t u) { return (float)__builtin_bit_cast(f16x2, u)[1]; }
+};
+
+// The planes of 8 values.
+template <typename N, int P>
+__device__ __forceinline__ void planes_of(const float (&v)[8], frag (&out)[P]) {
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = v[e];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w[e] = N::pack(x[2 * e], x[2 * e + 1]);
+      if (p + 1 < P) {
+        x[2 * e] -= N::low(w[e]);
+        x[2 * e + 1] -= N::high(w[e]);
+      }
+    }
+    out[p] = frag{w[0], w[1], w[2], w[3]};
+  }
+}
+
+// c + a b over all planes that count, the small ones first.
+template <typename N, int PA, int PB>
+__device__ __forceinline__ f32x16 mma_planes(const frag (&a)[PA], const frag (&b)[PB], f32x16 c) {
+  constexpr int TOP = (PA > PB ? PA : PB) - 1;
+#pragma unroll
+  for (int s = TOP; s >= 0; --s)
+#pragma unroll
+    for (int p = 0; p < PA; ++p)
+      if (s - p >= 0 && s - p < PB) c = N::mma(a[p], b[s - p], c);
+  return c;
+}
+
+// ---- rows in memory -------------------------------------------------------------
+// 8 elements of a row as they lie there.
+template <typename T>
+struct Unit {
+  T v[8];
+};
+// Elements d .. d + 7 of a row of `dim`; those behind it are 0.  FULL: there are none.
+template <bool FULL, typename T>
+__device__ __forceinline__ Unit<T> load_unit(const T* row, int d, int dim) {
+  Unit<T> u;
+  if (FULL || (dim & 7) == 0) {
+    if (FULL || d < dim) __builtin_memcpy(&u, row + d, sizeof(u));
+    else u = Unit<T>{};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u.v[e] = d + e < dim ? row[d + e] : T{};
+  }
+  return u;
+}
+template <typename T>
+__device__ __forceinline__ void frags_of(const Unit<T>& u, frag (&out)[Num<T>::IN]) {
+  if constexpr (Num<T>::IN == 1) {
+    __builtin_memcpy(&out[0], &u, sizeof(frag));
+  } else {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = u.v[e];
+    planes_of<Num<T>>(x, out);
+  }
+}
+
+// ---- tiles in LDS ------------------------------------------------------------------
+// A tile of rows of D elements, in planes, read by rows and by columns.  The row pitch: 16
+// bytes more than a multiple of 256 (of 128 for D = 64), so that 16 rows' 16-byte reads lie in
+// different banks.
+template <typename T, int ROWS, int D>
+struct Tile {
+  static constexpr int PITCH = D + 8;
+  static constexpr int PLANE = ROWS * PITCH;
+  alignas(16) uint16_t at[Num<T>::IN * PLANE];
+
+  __device__ __forceinline__ void put(int row, int d, const Unit<T>& u) {
+    frag f[Num<T>::IN];
+    frags_of(u, f);
+#pragma unroll
+    for (int p = 0; p < Num<T>::IN; ++p) *(frag*)(at + p * PLANE + row * PITCH + d) = f[p];
+  }
+  // Rows row0 + l, elements 16 step + 8 h ..: the operand whose rows are the tile's.
+  __device__ __forceinline__ void rows(int row0, int step, int lane, frag (&out)[Num<T>::IN]) const {
+#pragma unroll
+    for (int p = 0; p < Num<T>::IN; ++p)
+      out[p] = *(const frag*)(at + p * PLANE + (row0 + (lane & 31)) * PITCH + 16 * step + 8 * (lane >> 5));
+  }
+  // Columns d0 + l of rows row0 + 4 h .. + 3 and row0 + 8 + 4 h .. + 3: the operand that is contracted with a result's registers.
+  __device__ __forceinline__ void cols(int row0, int d0, int lane, frag (&out)[Num<T>::IN]) const {
+    const int l16 = lane & 15;
+    const uint16_t* p0 = at + (row0 + 4 * (lane >> 5) + (l16 >> 2)) * PITCH + d0 + 16 * ((lane >> 4) & 1) + 4 * (l16 & 3);
+#pragma unroll
+    for (int p = 0; p < Num<T>::IN; ++p) {
+      const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p0 + p * PLANE)));
+      const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p0 + p * PLANE + 8 * PITCH)));
+      out[p] = frag{a.x, a.y, b.x, b.y};
+    }
+  }
+};
+
+// ---- lanes ------------------------------------------------------------------------
+// The same lane's value of the other half of the wave, in one of two results.
+__device__ __forceinline__ void both_halves(float x, float& lo, float& hi) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  lo = __uint_as_float(r[0]);
+  hi = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float max_halves(float x) {
+  float a, b;
+  both_halves(x, a, b);
+  return fmaxf(a, b);
+}
+__device__ __forceinline__ float add_halves(float x) {
+  float a, b;
+  both_halves(x, a, b);
+  return a + b;
+}
+// Row 8 (r / 4) + 4 h + r % 4 of a result's register r.
+__device__ __forceinline__ int row_of(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Four values side by side in memory, where they exist (`have` of them).
+template <typename T>
+__device__ __forceinline__ void store4(T* to, const float (&x)[4], int have) {
+  if (have >= 4) {
+    T t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = from_f32<T>(x[e]);
+    __builtin_memcpy(to, t, sizeof(t));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < have) to[e] = from_f32<T>(x[e]);
+  }
+}
+
+// ---- sequences -----------------------------------------------------------------------
+// A sequence's rows are its tokens times the heads that share a key / value head,
+// row = token * group + head.  Rows are taken in tiles of B; sequence i has the
+// slots from floor(cu[i] group / B) + i, one more than it can need at most, so a
+// launch of floor(tokens group / B) + seqs slots holds every tile whatever the
+// lengths are, and a slot's sequence is found by search (64 at a time).  Without cu:
+// one sequence, or of `seqs` sequences one token each.
+struct SeqTile {
+  int seq;             // -1: none
+  int64_t t0, len, tile;
+};
+__device__ __forceinline__ int64_t seq_start(const int32_t* cu, int i, int64_t tokens) {
+  return min(max((int64_t)cu[i], (int64_t)0), tokens);
+}
+__device__ __forceinline__ SeqTile find_tile(const int32_t* cu, int seqs, int64_t tokens, int group, int B, int64_t slot) {
+  if (!cu) {       // one sequence, or one token of each
+    if (seqs <= 1) return {0, 0, tokens, slot};
+    const int64_t per = (group + B - 1) / B, i = slot / per;
+    return i < seqs ? SeqTile{(int)i, i, 1, slot - i * per} : SeqTile{-1, 0, 0, 0};
+  }
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = seqs;
+  while (true) {
+    const int step = (n + 63) >> 6, i = lo + lane * step;
+    const bool ok = lane * step < n && seq_start(cu, i, tokens) * group / B + i <= slot;
+    const int c = __popcll(__ballot(ok));
+    if (c == 0) return {-1, 0, 0, 0};
+    lo += (c - 1) * step;
+    n = min(step, n - (c - 1) * step);
+    if (step == 1) break;
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  const int64_t t0 = seq_start(cu, lo, tokens), t1 = max(seq_start(cu, lo + 1, tokens), t0);
+  return {lo, t0, t1 - t0, slot - (t0 * group / B + lo)};
+}
+
+}  // namespace pc

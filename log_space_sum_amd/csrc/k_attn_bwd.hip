@@ -1,0 +1,493 @@
+// k_attn_bwd.hip -- the gradients of causal softmax attention, from its outputs o and lse.
+//
+//   P_ij = exp(scale q_i . k_j - lse_i),  delta_i = do_i . o_i,  dS_ij = P_ij (do_i . v_j - delta_i)
+//   dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i,   dv_j = sum_i P_ij do_i
+//
+// Two kernels: the first keeps 32 rows of q, do and dq a wave and goes along the
+// keys, as the forward does; the second keeps 32 keys of k, v, dk and dv a wave and
+// goes along the rows of every head that shares them.  Scores are computed in both
+// (13 products' worth of work instead of 11), so that no sum is shared: no atomics,
+// the same bits at every run, and the sums over sharing heads stay in registers.  The first
+// leaves delta for the second.
+#include <algorithm>
+
+#include "k_attn.h"
+
+namespace pc {
+namespace {
+
+// float16 planes of dS: a lane's column (a row of dq, a key of dk) is held as a
+// power of two times itself that keeps its largest element so far below 2^15, moved
+// as the maximum of a softmax is.  bfloat16's range needs none.
+template <typename T>
+struct Scale {
+  static constexpr bool ON = std::is_same_v<T, f16>;
+  float by = ON ? 0x1p126f : 1.0f;
+  template <int DB>
+  __device__ __forceinline__ void move(f32x16& ds, f32x16 (&acc)[DB]) {
+    if constexpr (ON) {
+      float top = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(ds[r]));
+      top = max_halves(top);
+      if (__any(top * by > 32768.0f)) {
+        float to = by;
+        if (top * by > 32768.0f)      // 2^(14 - exponent)
+          to = __uint_as_float(min(max(127 + 14 + 127 - (int)(__float_as_uint(top) >> 23), 1), 253) << 23);
+        const float f = to / by;
+        by = to;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[d][r] *= f;
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) ds[r] *= by;
+    }
+  }
+};
+
+template <int DB>
+__device__ __forceinline__ bool any_not_finite(const f32x16 (&x)[DB]) {
+  float bad = 0.0f;
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) bad = fmaf(x[d][r], 0.0f, bad);
+  return !(bad == 0.0f);
+}
+
+template <typename T>
+__device__ __forceinline__ float dot(const T* a, const T* b, int n) {
+  float s = 0.0f;
+  for (int d = 0; d < n; ++d) s = fmaf(to_f32(a[d]), to_f32(b[d]), s);
+  return s;
+}
+
+// ---- dq -------------------------------------------------------------------------
+template <typename T, int D>
+struct DqShape {
+  static constexpr int IN = Num<T>::IN, BK = IN == 3 ? 32 : 64, BUFS = IN == 3 ? 1 : 2;
+  struct Lds {
+    Tile<T, BK, D> k[BUFS], v[BUFS];
+  };
+};
+
+// A row after the other in float32, for a tile whose results are not finite (see careful_rows of the forward).
+template <typename T>
+__device__ __attribute__((noinline)) void careful_dq(AttnArgs a, int64_t t0, int64_t first, int count, int kvh) {
+  const int lane = threadIdx.x & 63;
+  const T *k0 = (const T*)a.k.p + t0 * a.k.ts + kvh * a.k.hs, *v0 = (const T*)a.v.p + t0 * a.v.ts + kvh * a.v.hs;
+  for (int r = threadIdx.x >> 6; r < count; r += 4) {
+    const int64_t i = (first + r) / a.group, t = t0 + i, h = (int64_t)kvh * a.group + (first + r) % a.group;
+    const T *q = (const T*)a.q.p + t * a.q.ts + h * a.q.hs, *go = (const T*)a.d_o.p + t * a.d_o.ts + h * a.d_o.hs;
+    const T* o = (const T*)a.out.p + t * a.out.ts + h * a.out.hs;
+    const float lse = a.lse[t * a.kv_heads * a.group + h], delta = dot(go, o, a.dv);
+    float acc[2] = {0.0f, 0.0f};
+    for (int64_t j0 = 0; j0 <= i; j0 += 64) {
+      const int64_t j = min(j0 + lane, i);
+      const float p = exp2_fast((dot(q, k0 + j * a.k.ts, a.dk) * a.scale - lse) * LOG2E);
+      const float ds = p * (dot(go, v0 + j * a.v.ts, a.dv) - delta);
+      for (int x = 0; x < min((int64_t)64, i - j0 + 1); ++x) {
+        const float w = __shfl(ds, x);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (lane + 64 * e < a.dk) acc[e] = fmaf(w, to_f32(k0[(j0 + x) * a.k.ts + lane + 64 * e]), acc[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (lane + 64 * e < a.dk) ((T*)a.dq)[t * a.dq_ts + h * a.dq_hs + lane + 64 * e] = from_f32<T>(acc[e] * a.scale);
+  }
+}
+
+template <typename T, int D, bool FULL>
+__global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs a, int64_t slots) {
+  using N = Num<T>;
+  using S = DqShape<T, D>;
+  constexpr int IN = N::IN, W = N::W, BK = S::BK, KB = BK / 32, BUFS = S::BUFS, DS = D / 16, DB = D / 32;
+  constexpr int PER_ROW = D / 8, U = BK * PER_ROW / 256;
+  __shared__ typename S::Lds lds;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
+  const int heads = a.kv_heads * a.group, dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
+  const float c = a.scale * LOG2E;
+  for (int64_t b = blockIdx.x; b < slots * a.kv_heads; b += gridDim.x) {
+    const int kvh = (int)(b % a.kv_heads);
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - b / a.kv_heads);
+    const int64_t first = at.tile * ATTN_ROWS, rows_all = at.len * a.group;
+    if (at.seq < 0 || first >= rows_all) continue;
+    const int64_t tf = first / a.group;
+    const int rem = (int)(first - tf * a.group), count = (int)min((int64_t)ATTN_ROWS, rows_all - first);
+    auto token_of = [&](int i) { return (int)((uint32_t)(rem + i) / (uint32_t)a.group); };
+    const int wave_first = 32 * wave, mine = min(wave_first + (lane & 31), count - 1);
+    const bool wave_on = wave_first < count;
+    const int tl = token_of(mine), hl = rem + mine - tl * a.group;      // this lane's token and head in the tile
+    const int last = (int)tf + tl, first_last = (int)tf + token_of(min(wave_first, count - 1)),
+              last_last = (int)tf + token_of(min(wave_first + 31, count - 1)), end = (int)tf + token_of(count - 1) + 1;
+    const int64_t t = at.t0 + tf + tl, head = (int64_t)kvh * a.group + hl;
+    const float lse2 = a.lse[t * heads + head] * LOG2E;
+    frag q[DS][IN], go[DS][IN];
+    float delta = 0.0f;
+    {
+      const T *pq = (const T*)a.q.p + t * a.q.ts + head * a.q.hs, *pg = (const T*)a.d_o.p + t * a.d_o.ts + head * a.d_o.hs;
+      const T* po = (const T*)a.out.p + t * a.out.ts + head * a.out.hs;
+#pragma unroll
+      for (int s = 0; s < DS; ++s) {
+        frags_of(load_unit<FULL>(pq, 16 * s + 8 * h, dk), q[s]);
+        const Unit<T> g = load_unit<FULL>(pg, 16 * s + 8 * h, dv), o = load_unit<FULL>(po, 16 * s + 8 * h, dv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) delta = fmaf(to_f32(g.v[e]), to_f32(o.v[e]), delta);
+        frags_of(g, go[s]);
+      }
+      delta = add_halves(delta);
+      if (h == 0 && wave_first + lane < count) a.delta[t * heads + head] = delta;
+    }
+    f32x16 acc[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d) acc[d] = f32x16{};
+    Scale<T> scale;
+
+    const T *k0 = (const T*)a.k.p + at.t0 * a.k.ts + kvh * a.k.hs, *v0 = (const T*)a.v.p + at.t0 * a.v.ts + kvh * a.v.hs;
+    Unit<T> rk[U], rv[U];
+    auto fetch = [&](int key) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int id = u * 256 + tid, j = min(key + id / PER_ROW, end - 1), d = id % PER_ROW * 8;
+        rk[u] = load_unit<FULL>(k0 + j * a.k.ts, d, dk);
+        rv[u] = load_unit<FULL>(v0 + j * a.v.ts, d, dv);
+      }
+    };
+    auto stage = [&](int x) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int id = u * 256 + tid;
+        lds.k[x].put(id / PER_ROW, id % PER_ROW * 8, rk[u]);
+        lds.v[x].put(id / PER_ROW, id % PER_ROW * 8, rv[u]);
+      }
+    };
+    auto compute = [&](int x, int key) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+        for (int st = 0; st < DS; ++st) {
+          frag f[IN];
+          if (FULL || 16 * st < dk) {
+            lds.k[x].rows(32 * kb, st, lane, f);
+            s = mma_planes<N>(f, q[st], s);
+          }
+          if (FULL || 16 * st < dv) {
+            lds.v[x].rows(32 * kb, st, lane, f);
+            dp = mma_planes<N>(f, go[st], dp);
+          }
+        }
+        if (key + 32 * kb + 31 > first_last) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const bool off = key + 32 * kb + row_of(r, h) > last;
+            s[r] = off ? 0.0f : exp2_fast(fmaf(s[r], c, -lse2));
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, -lse2));
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
+        scale.move(s, acc);
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          float p[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = s[8 * st + e];
+          frag w[W];
+          planes_of<N>(p, w);
+#pragma unroll
+          for (int d = 0; d < DB; ++d) {
+            if (!FULL && 32 * d >= dk) continue;
+            frag f[IN];
+            lds.k[x].cols(32 * kb + 16 * st, 32 * d, lane, f);
+            acc[d] = mma_planes<N>(f, w, acc[d]);
+          }
+        }
+      }
+    };
+    __syncthreads();
+    fetch(0);
+    if constexpr (BUFS == 2) {
+      stage(0);
+      __syncthreads();
+      int x = 0;
+      for (int key = 0; key < end; key += BK, x ^= 1) {
+        const bool more = key + BK < end;
+        if (more) fetch(key + BK);
+        if (wave_on && key <= last_last) compute(x, key);
+        if (more) stage(x ^ 1);
+        __syncthreads();
+      }
+    } else {
+      for (int key = 0; key < end; key += BK) {
+        stage(0);
+        __syncthreads();
+        if (key + BK < end) fetch(key + BK);
+        if (wave_on && key <= last_last) compute(0, key);
+        __syncthreads();
+      }
+    }
+    const bool store = wave_first + (lane & 31) < count;
+    if (__syncthreads_or(store && any_not_finite(acc))) {
+      careful_dq<T>(a, at.t0, first, count, kvh);
+      continue;
+    }
+    if (!store) continue;
+    const float f = a.scale / scale.by;
+    T* to = (T*)a.dq + t * a.dq_ts + head * a.dq_hs;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int e = 32 * d + 8 * r + 4 * h;
+        const float x[4] = {acc[d][4 * r] * f, acc[d][4 * r + 1] * f, acc[d][4 * r + 2] * f, acc[d][4 * r + 3] * f};
+        store4<T>(to + e, x, dk - e);
+      }
+  }
+}
+
+// ---- dk, dv ---------------------------------------------------------------------
+template <typename T, int D>
+struct DkvShape {
+  static constexpr int IN = Num<T>::IN, BR = 32, BUFS = IN == 3 ? 1 : 2;
+  struct Lds {
+    Tile<T, BR, D> q[BUFS], go[BUFS];
+    alignas(16) float lse2[BUFS][BR];
+    alignas(16) float delta[BUFS][BR];
+  };
+};
+
+template <typename T>
+__device__ __attribute__((noinline)) void careful_dkv(AttnArgs a, int64_t t0, int64_t len, int64_t first, int count, int kvh) {
+  const int lane = threadIdx.x & 63, heads = a.kv_heads * a.group;
+  for (int r = threadIdx.x >> 6; r < count; r += 4) {
+    const int64_t j = first + r;
+    const T *k = (const T*)a.k.p + (t0 + j) * a.k.ts + kvh * a.k.hs, *v = (const T*)a.v.p + (t0 + j) * a.v.ts + kvh * a.v.hs;
+    float dk[2] = {0.0f, 0.0f}, dv[2] = {0.0f, 0.0f};
+    for (int64_t h = (int64_t)kvh * a.group; h < (int64_t)(kvh + 1) * a.group; ++h)
+      for (int64_t i0 = j; i0 < len; i0 += 64) {
+        const int64_t t = t0 + min(i0 + lane, len - 1);
+        const float p = exp2_fast((dot((const T*)a.q.p + t * a.q.ts + h * a.q.hs, k, a.dk) * a.scale - a.lse[t * heads + h]) * LOG2E);
+        const float ds = p * (dot((const T*)a.d_o.p + t * a.d_o.ts + h * a.d_o.hs, v, a.dv) - a.delta[t * heads + h]);
+        for (int x = 0; x < min((int64_t)64, len - i0); ++x) {
+          const float wp = __shfl(p, x), ws = __shfl(ds, x);
+          const T *q = (const T*)a.q.p + (t0 + i0 + x) * a.q.ts + h * a.q.hs, *go = (const T*)a.d_o.p + (t0 + i0 + x) * a.d_o.ts + h * a.d_o.hs;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int d = lane + 64 * e;
+            if (d < a.dk) dk[e] = fmaf(ws, to_f32(q[d]), dk[e]);
+            if (d < a.dv) dv[e] = fmaf(wp, to_f32(go[d]), dv[e]);
+          }
+        }
+      }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int d = lane + 64 * e;
+      if (d < a.dk) ((T*)a.dk_)[(t0 + j) * a.dk_ts + kvh * a.dk_hs + d] = from_f32<T>(dk[e] * a.scale);
+      if (d < a.dv) ((T*)a.dv_)[(t0 + j) * a.dv_ts + kvh * a.dv_hs + d] = from_f32<T>(dv[e]);
+    }
+  }
+}
+
+template <typename T, int D, bool FULL>
+__global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
+  using N = Num<T>;
+  using S = DkvShape<T, D>;
+  constexpr int IN = N::IN, W = N::W, BR = S::BR, BUFS = S::BUFS, DS = D / 16, DB = D / 32;
+  constexpr int PER_ROW = D / 8, U = BR * PER_ROW / 256;
+  __shared__ typename S::Lds lds;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
+  const int heads = a.kv_heads * a.group, dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
+  const float c = a.scale * LOG2E;
+  for (int64_t b = blockIdx.x; b < slots * a.kv_heads; b += gridDim.x) {
+    const int kvh = (int)(b % a.kv_heads);
+    // a sequence's first keys, which have the most rows, first
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, 1, ATTN_ROWS, b / a.kv_heads);
+    const int64_t first64 = at.tile * ATTN_ROWS;
+    if (at.seq < 0 || first64 >= at.len) continue;
+    const int len = (int)at.len, first = (int)first64, count = min(ATTN_ROWS, len - first);
+    const int key = first + min(32 * wave + (lane & 31), count - 1), wave_key = first + 32 * wave;
+    const bool wave_on = 32 * wave < count;
+    frag k[DS][IN], v[DS][IN];
+    {
+      const T *pk = (const T*)a.k.p + (at.t0 + key) * a.k.ts + kvh * a.k.hs, *pv = (const T*)a.v.p + (at.t0 + key) * a.v.ts + kvh * a.v.hs;
+#pragma unroll
+      for (int s = 0; s < DS; ++s) {
+        frags_of(load_unit<FULL>(pk, 16 * s + 8 * h, dk), k[s]);
+        frags_of(load_unit<FULL>(pv, 16 * s + 8 * h, dv), v[s]);
+      }
+    }
+    f32x16 dka[DB], dva[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d) dka[d] = dva[d] = f32x16{};
+    Scale<T> scale;
+
+    Unit<T> rq[U], rg[U];
+    float rl = 0.0f, rd = 0.0f;
+    auto fetch = [&](int head, int row) {
+      const T *q0 = (const T*)a.q.p + at.t0 * a.q.ts + head * a.q.hs, *g0 = (const T*)a.d_o.p + at.t0 * a.d_o.ts + head * a.d_o.hs;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int id = u * 256 + tid, i = min(row + id / PER_ROW, len - 1), d = id % PER_ROW * 8;
+        rq[u] = load_unit<FULL>(q0 + i * a.q.ts, d, dk);
+        rg[u] = load_unit<FULL>(g0 + i * a.d_o.ts, d, dv);
+      }
+      if (tid < BR) {
+        const int64_t i = (at.t0 + min(row + tid, len - 1)) * heads + head;
+        rl = a.lse[i] * LOG2E;
+        rd = a.delta[i];
+      }
+    };
+    auto stage = [&](int x) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int id = u * 256 + tid;
+        lds.q[x].put(id / PER_ROW, id % PER_ROW * 8, rq[u]);
+        lds.go[x].put(id / PER_ROW, id % PER_ROW * 8, rg[u]);
+      }
+      if (tid < BR) {
+        lds.lse2[x][tid] = rl;
+        lds.delta[x][tid] = rd;
+      }
+    };
+    auto compute = [&](int x, int row) {
+      f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+      for (int st = 0; st < DS; ++st) {
+        frag f[IN];
+        if (FULL || 16 * st < dk) {
+          lds.q[x].rows(0, st, lane, f);
+          s = mma_planes<N>(f, k[st], s);
+        }
+        if (FULL || 16 * st < dv) {
+          lds.go[x].rows(0, st, lane, f);
+          dp = mma_planes<N>(f, v[st], dp);
+        }
+      }
+      const bool edge = row < wave_key + 31 || row + 32 > len;
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const f32x4 l4 = *(const f32x4*)&lds.lse2[x][8 * r4 + 4 * h], d4 = *(const f32x4*)&lds.delta[x][8 * r4 + 4 * h];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 4 * r4 + e;
+          s[r] = exp2_fast(fmaf(s[r], c, -l4[e]));
+          if (edge) {
+            const int i = row + row_of(r, h);
+            if (i < key || i >= len) s[r] = 0.0f;
+          }
+          dp[r] = s[r] * (dp[r] - d4[e]);
+        }
+      }
+      scale.move(dp, dka);
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        float p[8];
+        frag w[W];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = N::BIAS ? s[8 * st + e] * (float)(1 << N::BIAS) : s[8 * st + e];
+        planes_of<N>(p, w);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+          if (!FULL && 32 * d >= dv) continue;
+          frag f[IN];
+          lds.go[x].cols(16 * st, 32 * d, lane, f);
+          dva[d] = mma_planes<N>(f, w, dva[d]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = dp[8 * st + e];
+        planes_of<N>(p, w);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+          if (!FULL && 32 * d >= dk) continue;
+          frag f[IN];
+          lds.q[x].cols(16 * st, 32 * d, lane, f);
+          dka[d] = mma_planes<N>(f, w, dka[d]);
+        }
+      }
+    };
+    const int row0 = first / BR * BR;      // the first rows that attend these keys
+    const int h0 = kvh * a.group, h1 = h0 + a.group;
+    __syncthreads();
+    int head = h0, row = row0, x = 0;
+    fetch(head, row);
+    if constexpr (BUFS == 2) {
+      stage(0);
+      __syncthreads();
+    }
+    while (head < h1) {
+      int nh = head, nr = row + BR;
+      if (nr >= len) {
+        nr = row0;
+        ++nh;
+      }
+      if constexpr (BUFS == 1) {
+        stage(0);
+        __syncthreads();
+      }
+      if (nh < h1) fetch(nh, nr);
+      if (wave_on && row + 31 >= wave_key) compute(x, row);
+      if constexpr (BUFS == 2) {
+        if (nh < h1) stage(x ^ 1);
+        x ^= 1;
+      }
+      __syncthreads();
+      head = nh;
+      row = nr;
+    }
+    const bool store = 32 * wave + (lane & 31) < count;
+    if (__syncthreads_or(store && (any_not_finite(dka) || any_not_finite(dva)))) {
+      careful_dkv<T>(a, at.t0, len, first, count, kvh);
+      continue;
+    }
+    if (!store) continue;
+    const float fk = a.scale / scale.by, fv = 1.0f / (float)(1 << N::BIAS);
+    T *tk = (T*)a.dk_ + (at.t0 + key) * a.dk_ts + kvh * a.dk_hs, *tv = (T*)a.dv_ + (at.t0 + key) * a.dv_ts + kvh * a.dv_hs;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int e = 32 * d + 8 * r + 4 * h;
+        const float y[4] = {dka[d][4 * r] * fk, dka[d][4 * r + 1] * fk, dka[d][4 * r + 2] * fk, dka[d][4 * r + 3] * fk};
+        store4<T>(tk + e, y, dk - e);
+        const float z[4] = {dva[d][4 * r] * fv, dva[d][4 * r + 1] * fv, dva[d][4 * r + 2] * fv, dva[d][4 * r + 3] * fv};
+        store4<T>(tv + e, z, dv - e);
+      }
+  }
+}
+
+template <typename T, int D, bool FULL>
+void launch(const AttnArgs& a, hipStream_t s) {
+  const int64_t rows = a.tokens * a.group / ATTN_ROWS + a.seqs, keys = a.tokens / ATTN_ROWS + a.seqs;
+  auto grid = [&](int64_t slots) { return dim3((uint32_t)std::min<int64_t>(slots * a.kv_heads, 1 << 23)); };
+  launch_kernel(attn_dq<T, D, FULL>, grid(rows), dim3(256), 0, s, a, rows);
+  launch_kernel(attn_dkv<T, D, FULL>, grid(keys), dim3(256), 0, s, a, keys);
+}
+template <typename T>
+void bwd(const AttnArgs& a, hipStream_t s) {
+  const int big = a.dk > a.dv ? a.dk : a.dv;
+  const bool same = a.dk == a.dv;
+  if (big <= 64) {
+    if (same && big == 64) launch<T, 64, true>(a, s);
+    else launch<T, 64, false>(a, s);
+  } else {
+    if (same && big == 128) launch<T, 128, true>(a, s);
+    else launch<T, 128, false>(a, s);
+  }
+}
+
+}  // namespace
+
+void launch_attn_bwd(const AttnArgs& a, int dtype, hipStream_t s) {
+  if (dtype == PC_DTYPE_BF16) bwd<bf16>(a, s);
+  else if (dtype == PC_DTYPE_F16) bwd<f16>(a, s);
+  else bwd<float>(a, s);
+}
+
+}  // namespace pc

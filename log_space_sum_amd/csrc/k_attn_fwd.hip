@@ -1,0 +1,72 @@
+// k_attn_fwd.hip -- causal softmax attention over whole packed sequences.
+//
+//   o_i = sum_{j <= i} p_ij v_j / sum_{j <= i} p_ij,   p_ij = exp(scale q_i . k_j - m_i),   lse_i = m_i + log sum p_ij
+//
+// one pass over the keys with a running maximum and sum; see k_attn_core.h for the loop.
+#include <algorithm>
+
+#include "k_attn_core.h"
+
+namespace pc {
+namespace {
+
+template <typename T, int D, bool FULL>
+__global__ __launch_bounds__(256, 2) void attn_fwd(AttnArgs a, int64_t slots) {
+  __shared__ typename FwdShape<T, D>::Lds lds;
+  const int heads = a.kv_heads * a.group;
+  for (int64_t b = blockIdx.x; b < slots * a.kv_heads; b += gridDim.x) {
+    // the last tiles, which have the most keys, first; a head's tiles in one XCD's turn where they divide
+    const int kvh = (int)(b % a.kv_heads);
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - b / a.kv_heads);
+    const int64_t first = at.tile * ATTN_ROWS, rows_all = at.len * a.group;
+    if (at.seq < 0 || first >= rows_all) continue;
+    const int64_t tf = first / a.group, t = at.t0 + tf;
+    Rows<T> rows;
+    rows.q = (const T*)a.q.p + t * a.q.ts + (int64_t)kvh * a.group * a.q.hs;
+    rows.q_ts = a.q.ts;
+    rows.q_hs = a.q.hs;
+    rows.group = a.group;
+    rows.rem = (int)(first - tf * a.group);
+    rows.count = (int)min((int64_t)ATTN_ROWS, rows_all - first);
+    rows.first = (int)tf;
+    Keys<T, false> keys{};
+    keys.k = (const T*)a.k.p + at.t0 * a.k.ts + kvh * a.k.hs;
+    keys.v = (const T*)a.v.p + at.t0 * a.v.ts + kvh * a.v.hs;
+    keys.k_ts = a.k.ts;
+    keys.v_ts = a.v.ts;
+    keys.total = (int)at.len;
+    RowOut out{};
+    out.o = (T*)a.o + t * a.o_ts + (int64_t)kvh * a.group * a.o_hs;
+    out.o_ts = a.o_ts;
+    out.o_hs = a.o_hs;
+    out.heads = heads;
+    out.lse = a.lse ? a.lse + t * heads + kvh * a.group : nullptr;
+    attend_tile<T, D, FULL, false>(lds, keys, rows, out, a.dk, a.dv, fabsf(a.scale) * LOG2E, a.scale < 0.0f, 0,
+                                   rows.last(rows.count - 1) + 1);
+  }
+}
+
+template <typename T>
+void fwd(const AttnArgs& a, hipStream_t s) {
+  const int64_t slots = a.tokens * a.group / ATTN_ROWS + a.seqs;
+  const dim3 grid((uint32_t)std::min<int64_t>(slots * a.kv_heads, 1 << 23));
+  const int big = a.dk > a.dv ? a.dk : a.dv;
+  const bool same = a.dk == a.dv;
+  if (big <= 64) {
+    if (same && big == 64) launch_kernel(attn_fwd<T, 64, true>, grid, dim3(256), 0, s, a, slots);
+    else launch_kernel(attn_fwd<T, 64, false>, grid, dim3(256), 0, s, a, slots);
+  } else {
+    if (same && big == 128) launch_kernel(attn_fwd<T, 128, true>, grid, dim3(256), 0, s, a, slots);
+    else launch_kernel(attn_fwd<T, 128, false>, grid, dim3(256), 0, s, a, slots);
+  }
+}
+
+}  // namespace
+
+void launch_attn_fwd(const AttnArgs& a, int dtype, hipStream_t s) {
+  if (dtype == PC_DTYPE_BF16) fwd<bf16>(a, s);
+  else if (dtype == PC_DTYPE_F16) fwd<f16>(a, s);
+  else fwd<float>(a, s);
+}
+
+}  // namespace pc

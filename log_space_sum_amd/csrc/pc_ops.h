@@ -130,6 +130,73 @@ void launch_mix_scan(const MixScanArgs* a, int n, hipStream_t s);           // s
 void launch_mix_sum(const MixSumArgs& a, const MixSumArgs& b, int dtype, hipStream_t s);
 void launch_mix_step(const MixStepArgs& a, int dtype, hipStream_t s);
 
+// ---- softmax attention -------------------------------------------------------
+struct AttnTensor {
+  const void* p;
+  int64_t ts, hs;       // token and head strides (elements)
+};
+struct AttnCache {      // one of the cache's two tensors: [pages, page_size, kv_heads, dim]
+  void* p;
+  int64_t page_stride, token_stride, head_stride;
+};
+struct AttnPages {
+  AttnCache k, v;
+  const int32_t* table;  // [seqs, max_pages], rows at table_stride
+  int64_t table_stride;
+  const int32_t* past;   // [seqs] tokens in the cache
+  int32_t num_pages, page_size, max_pages;
+  uint32_t magic, shift; // j / page_size = j magic >> shift for 0 <= j < 2^31
+};
+struct AttnArgs {
+  int32_t seqs, kv_heads, group, dk, dv;
+  int64_t tokens;
+  const int32_t* cu;    // [seqs + 1], null: one sequence of all tokens
+  float scale;
+  AttnTensor q, k, v;
+  void* o;
+  int64_t o_ts, o_hs;
+  float* lse;           // [tokens, heads]; forward: nullable output
+  AttnPages pages;      // cached: past and new tokens
+  int32_t nsplit, part_len;   // cached: parts of part_len keys; nsplit > 1: results through part and stat
+  float* part;          // [nsplit, tokens, heads, dv]
+  float2* stat;         // [nsplit, tokens, heads]
+  // backward
+  AttnTensor out, d_o;
+  void *dq, *dk_, *dv_;
+  int64_t dq_ts, dq_hs, dk_ts, dk_hs, dv_ts, dv_hs;
+  float* delta;         // [tokens, heads] sums over a row of d_o o
+};
+constexpr int ATTN_MAX_DIM = 128;
+constexpr int ATTN_ROWS = 128;         // rows of a workgroup, and keys of one in the backward pass
+constexpr int ATTN_FEW_ROWS = 32;      // rows of a workgroup whose waves share them (cached)
+constexpr int ATTN_MAX_SPLIT = 64;     // parts of the keys
+constexpr int ROTARY_MAX_DIM = 256;
+void launch_attn_fwd(const AttnArgs& a, int dtype, hipStream_t s);
+void launch_attn_bwd(const AttnArgs& a, int dtype, hipStream_t s);
+void launch_attn_cached(const AttnArgs& a, int dtype, bool few, hipStream_t s);
+void launch_attn_join(const AttnArgs& a, int dtype, hipStream_t s);
+
+// ---- heads' norm and rotation --------------------------------------------------
+struct RotaryArgs {
+  int64_t tokens;
+  int32_t heads, kv_heads, dim, part;
+  int32_t pairs, norm;
+  float eps, magnitude;
+  const int32_t* positions;
+  const double* freq;   // [part / 2]
+  AttnTensor q, k;      // forward: inputs; backward: the forward's inputs (with norm)
+  AttnTensor dq, dk;    // backward: gradients of the outputs
+  void *qo, *ko;        // outputs
+  int64_t qo_ts, qo_hs, ko_ts, ko_hs;
+  const float *qw, *kw; // [dim], nullable: 1
+  float *dqw, *dkw;     // [dim]
+  float* part_sums;     // backward: [parts][2][dim]
+  int32_t parts;
+};
+int rotary_parts(int64_t tokens, int heads, int kv_heads);
+void launch_rotary_fwd(const RotaryArgs& a, int dtype, hipStream_t s);
+void launch_rotary_bwd(const RotaryArgs& a, int dtype, hipStream_t s);
+
 // ---- orthogonalised update ---------------------------------------------------
 // m <= n: the smaller and the larger dimension of the matrices; tall: the rows
 // are the larger one.  X [m, n] is the matrix or its transpose.

@@ -87,7 +87,8 @@ void check_call(const pc_linear_attention* d) {
   need(std::isfinite(d->scale) && d->scale != 0.0f, "scale must be finite and not 0");
 }
 
-void check_heads(const pc_linear_attention* d, const pc_heads& t, const char* what, bool chunks = true) {
+template <typename D>
+void check_heads(const D* d, const pc_heads& t, const char* what, bool chunks = true) {
   need(t.data || d->num_tokens == 0, std::string("null ") + what);
   need(t.token_stride >= 0 && t.head_stride >= 0, std::string("negative stride of ") + what);
   // a chunk's rows are addressed with 32-bit byte offsets
@@ -95,7 +96,8 @@ void check_heads(const pc_linear_attention* d, const pc_heads& t, const char* wh
     fail(PC_ERR_UNSUPPORTED, std::string("token stride of ") + what + " above " + std::to_string(MIX_MAX_STRIDE));
 }
 // an output's elements must be distinct
-void check_out(const pc_linear_attention* d, const pc_heads& t, int heads, int dim, const char* what, bool chunks = true) {
+template <typename D>
+void check_out(const D* d, const pc_heads& t, int heads, int dim, const char* what, bool chunks = true) {
   check_heads(d, t, what, chunks);
   const int64_t ts = t.token_stride, hs = t.head_stride;
   const bool tokens_outside = (heads == 1 || hs >= dim) && (d->num_tokens <= 1 || ts >= (heads - 1) * hs + dim);
@@ -212,6 +214,135 @@ void mix_starts(const pc_linear_attention* d, const MixArgs* a, int n, hipStream
   }
   launch_mix_scan(c, n, s);
   check_launch();
+}
+
+// ---- softmax attention -----------------------------------------------------------
+
+void check_attn_sizes(const pc_attention* d) {
+  need(d, "null descriptor");
+  check_dtype(d->dtype);
+  need(d->heads >= 1 && d->kv_heads >= 1 && d->heads % d->kv_heads == 0, "kv_heads must divide heads");
+  need(d->heads <= 65535, "more than 65535 heads");
+  need(d->dim_k >= 1 && d->dim_v >= 1, "dim_k and dim_v must be at least 1");
+  if (d->dim_k > ATTN_MAX_DIM || d->dim_v > ATTN_MAX_DIM)
+    fail(PC_ERR_UNSUPPORTED, "dim_k " + std::to_string(d->dim_k) + ", dim_v " + std::to_string(d->dim_v) + " (at most " +
+                                 std::to_string(ATTN_MAX_DIM) + ")");
+  need(d->num_tokens >= 0 && d->num_tokens <= 1 << 30, "num_tokens must be in [0, 2^30]");
+  need(d->num_seqs >= 0 && d->num_seqs <= 1 << 24, "num_seqs must be in [0, 2^24]");
+}
+
+void check_attn(const pc_attention* d, bool cached = false) {
+  check_attn_sizes(d);
+  if (cached) need(d->cu_seqlens || d->num_seqs == 1 || d->num_seqs == d->num_tokens, "without cu_seqlens num_seqs is 1 or num_tokens");
+  else need(d->cu_seqlens || d->num_seqs == 1, "without cu_seqlens num_seqs is 1");
+  need(std::isfinite(d->scale) && d->scale != 0.0f, "scale must be finite and not 0");
+  check_heads(d, d->q, "q", false);
+  check_heads(d, d->k, "k", false);
+  check_heads(d, d->v, "v", false);
+}
+
+AttnTensor attn_tensor(const pc_heads& t) { return {t.data, t.token_stride, t.head_stride}; }
+
+AttnArgs attn_base(const pc_attention* d) {
+  AttnArgs a{};
+  a.seqs = d->num_seqs;
+  a.kv_heads = d->kv_heads;
+  a.group = d->heads / d->kv_heads;
+  a.dk = d->dim_k;
+  a.dv = d->dim_v;
+  a.tokens = d->num_tokens;
+  a.cu = d->cu_seqlens;
+  a.scale = d->scale;
+  a.q = attn_tensor(d->q);
+  a.k = attn_tensor(d->k);
+  a.v = attn_tensor(d->v);
+  a.o = d->o.data;
+  a.o_ts = d->o.token_stride;
+  a.o_hs = d->o.head_stride;
+  a.lse = d->lse;
+  a.nsplit = 1;
+  return a;
+}
+
+void check_pages(const pc_attention* d) {
+  check_attn_sizes(d);
+  need(d->page_size >= 1, "page_size must be at least 1");
+  need(d->num_pages >= 0 && d->max_pages >= 0, "num_pages and max_pages must be at least 0");
+  need((int64_t)d->max_pages * d->page_size + d->num_tokens <= INT_MAX - (1 << 16), "2^31 positions or more");
+  need(d->max_seqlen >= 0 && d->max_length >= 0, "max_seqlen and max_length must be at least 0");
+}
+
+// How new tokens meet a cache.  Rows are the new tokens of a sequence times the
+// heads that share a key / value head.
+struct CachedPlan {
+  bool few;              // up to 64 rows: tiles of 32 that all waves share
+  int nsplit, part_len;
+  size_t part, stat, total;
+};
+CachedPlan cached_plan(const pc_attention* d) {
+  CachedPlan p{};
+  const int64_t group = d->heads / d->kv_heads, tokens = std::max<int64_t>(1, d->num_tokens);
+  const int64_t rows = std::max<int64_t>(1, std::min(d->max_seqlen, tokens)) * group;
+  p.few = rows <= 64;
+  const int64_t tile = p.few ? ATTN_FEW_ROWS : ATTN_ROWS;
+  const int64_t full = std::min<int64_t>(std::max(1, d->num_seqs), (tokens * group + rows - 1) / rows);
+  const int64_t works = std::max<int64_t>(1, full * ((rows + tile - 1) / tile) * d->kv_heads);
+  const int64_t longest = std::max<int64_t>(1, std::min<int64_t>(d->max_length, (int64_t)d->max_pages * d->page_size + tokens));
+  const int64_t aim = p.few ? 1024 : 512;
+  int64_t len = std::max<int64_t>(256, (longest * works + aim - 1) / aim);
+  len = round_up(std::max(len, (longest + ATTN_MAX_SPLIT - 1) / ATTN_MAX_SPLIT), 128);
+  p.nsplit = (int)((longest + len - 1) / len);
+  p.part_len = (int)std::min<int64_t>(len, INT_MAX);
+  if (p.nsplit > 1) {
+    const size_t all = (size_t)p.nsplit * d->num_tokens * d->heads;
+    p.stat = (size_t)round_up((int64_t)(all * d->dim_v * sizeof(float)), 256);
+    p.total = p.stat + all * sizeof(float2);
+  }
+  return p;
+}
+
+// ---- heads' norm and rotation ------------------------------------------------------
+
+void check_rotary(const pc_rotary* d) {
+  need(d, "null descriptor");
+  check_dtype(d->dtype);
+  need(d->num_tokens >= 0 && d->num_tokens <= INT_MAX, "num_tokens must be in [0, 2^31)");
+  need(d->heads >= 0 && d->kv_heads >= 0 && d->heads <= 65535 && d->kv_heads <= 65535, "heads must be in [0, 65535]");
+  need(d->dim >= 1, "dim must be at least 1");
+  if (d->dim > ROTARY_MAX_DIM)
+    fail(PC_ERR_UNSUPPORTED, "dim " + std::to_string(d->dim) + " (at most " + std::to_string(ROTARY_MAX_DIM) + ")");
+  need(d->rotary_dim >= 0 && d->rotary_dim % 2 == 0 && d->rotary_dim <= d->dim, "rotary_dim must be even and at most dim");
+}
+
+RotaryArgs rotary_base(const pc_rotary* d) {
+  check_rotary(d);
+  need(d->interleaved == 0 || d->interleaved == 1, "interleaved must be 0 or 1");
+  need(d->norm == 0 || d->norm == 1, "norm must be 0 or 1");
+  need(std::isfinite(d->magnitude), "magnitude must be finite");
+  need(!d->norm || (std::isfinite(d->eps) && d->eps >= 0.0f), "eps must be finite and at least 0");
+  need(d->num_tokens == 0 || d->positions, "null positions");
+  need(d->rotary_dim == 0 || d->freq, "null freq");
+  RotaryArgs a{};
+  a.tokens = d->num_tokens;
+  a.heads = d->heads;
+  a.kv_heads = d->kv_heads;
+  a.dim = d->dim;
+  a.part = d->rotary_dim;
+  a.pairs = d->interleaved;
+  a.norm = d->norm;
+  a.eps = d->eps;
+  a.magnitude = d->magnitude;
+  a.positions = d->positions;
+  a.freq = d->freq;
+  a.qw = d->q_weight;
+  a.kw = d->k_weight;
+  return a;
+}
+
+// An output that is an input has its strides.
+void check_place(const pc_rotary* d, const pc_heads& out, const pc_heads& in, int heads, const char* what) {
+  need(out.data != in.data || ((d->num_tokens <= 1 || out.token_stride == in.token_stride) && (heads <= 1 || out.head_stride == in.head_stride)),
+       std::string(what) + " is its input at other strides");
 }
 
 // ---- orthogonalised update -----------------------------------------------------
@@ -607,6 +738,220 @@ int pc_linear_attention_step(int device, const pc_linear_attention* d, void* str
     a.o_ts = d->o.token_stride;
     a.o_hs = d->o.head_stride;
     launch_mix_step(a, d->dtype, (hipStream_t)stream);
+    check_launch();
+  });
+}
+
+int pc_attention_workspace_bytes(const pc_attention* d, int backward, size_t* bytes) {
+  return guarded([&] {
+    need(bytes, "null bytes");
+    check_attn_sizes(d);
+    *bytes = backward ? (size_t)d->num_tokens * d->heads * sizeof(float) : 0;
+  });
+}
+
+int pc_attention_forward(int device, const pc_attention* d, void* ws, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    check_device(device);
+    check_attn(d);
+    check_out(d, d->o, d->heads, d->dim_v, "o", false);
+    (void)ws;
+    (void)ws_bytes;
+    if (d->num_seqs == 0 || d->num_tokens == 0) return;
+    DeviceGuard dg(device);
+    launch_attn_fwd(attn_base(d), d->dtype, (hipStream_t)stream);
+    check_launch();
+  });
+}
+
+int pc_attention_backward(int device, const pc_attention* d, void* ws, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    check_device(device);
+    check_attn(d);
+    check_heads(d, d->o, "o", false);
+    check_heads(d, d->d_o, "d_o", false);
+    need(d->lse || d->num_tokens == 0, "null lse");
+    check_out(d, d->d_q, d->heads, d->dim_k, "d_q", false);
+    check_out(d, d->d_k, d->kv_heads, d->dim_k, "d_k", false);
+    check_out(d, d->d_v, d->kv_heads, d->dim_v, "d_v", false);
+    check_ws(ws, ws_bytes, (size_t)d->num_tokens * d->heads * sizeof(float));
+    if (d->num_seqs == 0 || d->num_tokens == 0) return;
+    DeviceGuard dg(device);
+    AttnArgs a = attn_base(d);
+    a.out = attn_tensor(d->o);
+    a.d_o = attn_tensor(d->d_o);
+    a.dq = d->d_q.data;
+    a.dq_ts = d->d_q.token_stride;
+    a.dq_hs = d->d_q.head_stride;
+    a.dk_ = d->d_k.data;
+    a.dk_ts = d->d_k.token_stride;
+    a.dk_hs = d->d_k.head_stride;
+    a.dv_ = d->d_v.data;
+    a.dv_ts = d->d_v.token_stride;
+    a.dv_hs = d->d_v.head_stride;
+    a.delta = (float*)ws;
+    launch_attn_bwd(a, d->dtype, (hipStream_t)stream);
+    check_launch();
+  });
+}
+
+int pc_attention_cached_workspace_bytes(const pc_attention* d, size_t* bytes) {
+  return guarded([&] {
+    need(bytes, "null bytes");
+    check_pages(d);
+    *bytes = cached_plan(d).total;
+  });
+}
+
+int pc_attention_cached(int device, const pc_attention* d, void* ws, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    check_device(device);
+    check_pages(d);
+    check_attn(d, true);
+    check_out(d, d->o, d->heads, d->dim_v, "o", false);
+    auto cache = [&](const pc_pages& c, int dim, const char* what) {
+      need(c.data || d->num_pages == 0, std::string("null ") + what);
+      need(c.page_stride >= 0 && c.token_stride >= 0 && c.head_stride >= 0, std::string("negative stride of ") + what);
+      // two of the three dimensions inside the third, in any order: elements are distinct
+      struct Dim {
+        int64_t n, stride;
+      } x[3] = {{d->num_pages, c.page_stride}, {d->page_size, c.token_stride}, {d->kv_heads, c.head_stride}};
+      std::sort(x, x + 3, [](const Dim& p, const Dim& q) { return p.stride < q.stride; });
+      int64_t span = dim;
+      for (const Dim& y : x) {
+        if (y.n <= 1) continue;
+        need(y.stride >= span, std::string("elements of ") + what + " overlap");
+        span += (y.n - 1) * y.stride;
+      }
+      return AttnCache{c.data, c.page_stride, c.token_stride, c.head_stride};
+    };
+    const CachedPlan p = cached_plan(d);
+    AttnArgs a = attn_base(d);
+    a.lse = nullptr;
+    a.pages.k = cache(d->k_cache, d->dim_k, "k_cache");
+    a.pages.v = cache(d->v_cache, d->dim_v, "v_cache");
+    need(d->cached || d->num_seqs == 0, "null cached");
+    need(d->page_table || d->max_pages == 0 || d->num_seqs == 0, "null page_table");
+    need(d->page_table_stride >= d->max_pages || d->num_seqs <= 1, "page_table_stride below max_pages");
+    check_ws(ws, ws_bytes, p.total);
+    if (d->num_seqs == 0 || d->num_tokens == 0) return;
+    a.pages.table = d->page_table;
+    a.pages.table_stride = d->page_table_stride;
+    a.pages.past = d->cached;
+    a.pages.num_pages = d->num_pages;
+    a.pages.page_size = d->page_size;
+    a.pages.max_pages = d->max_pages;
+    // j / page_size for j < 2^31: s = ceil(log2 page_size), ceil(2^(31 + s) / page_size) fits 32 bits
+    int s = 0;
+    while ((int64_t)1 << s < d->page_size) ++s;
+    a.pages.shift = 31 + s;
+    a.pages.magic = (uint32_t)((((uint64_t)1 << (31 + s)) + d->page_size - 1) / d->page_size);
+    a.nsplit = p.nsplit;
+    a.part_len = p.part_len;
+    a.part = (float*)ws;
+    a.stat = (float2*)((char*)ws + p.stat);
+    DeviceGuard dg(device);
+    launch_attn_cached(a, d->dtype, p.few, (hipStream_t)stream);
+    check_launch();
+    if (p.nsplit > 1) {
+      launch_attn_join(a, d->dtype, (hipStream_t)stream);
+      check_launch();
+    }
+  });
+}
+
+int pc_rotary_frequencies(int32_t rotary_dim, double base, int scaling, double factor, double original, double low, double high,
+                          double* freq) {
+  return guarded([&] {
+    need(rotary_dim >= 0 && rotary_dim % 2 == 0, "rotary_dim must be even and at least 0");
+    need(freq || rotary_dim == 0, "null freq");
+    need(std::isfinite(base) && base > 0.0, "base must be finite and above 0");
+    need(scaling >= PC_ROTARY_PLAIN && scaling <= PC_ROTARY_PARTS, "unknown scaling");
+    need(scaling == PC_ROTARY_PLAIN || (std::isfinite(factor) && factor > 0.0), "factor must be finite and above 0");
+    if (scaling == PC_ROTARY_PARTS)
+      need(std::isfinite(original) && original > 0.0 && std::isfinite(low) && std::isfinite(high) && low < high,
+           "original must be above 0 and low below high");
+    if (scaling == PC_ROTARY_BASE) {
+      need(rotary_dim != 2, "scaling of the base needs two pairs");
+      base *= std::pow(factor, (double)rotary_dim / std::max(1, rotary_dim - 2));
+    }
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+      double f = std::pow(base, -2.0 * i / rotary_dim);
+      if (scaling == PC_ROTARY_LINEAR) f /= factor;
+      if (scaling == PC_ROTARY_PARTS) {
+        const double turns = original * f / 6.283185307179586477, keep = std::min(1.0, std::max(0.0, (turns - low) / (high - low)));
+        f *= keep + (1.0 - keep) / factor;
+      }
+      freq[i] = f;
+    }
+  });
+}
+
+int pc_rotary_workspace_bytes(const pc_rotary* d, size_t* bytes) {
+  return guarded([&] {
+    need(bytes, "null bytes");
+    check_rotary(d);
+    *bytes = (size_t)rotary_parts(d->num_tokens, d->heads, d->kv_heads) * 2 * d->dim * sizeof(float);
+  });
+}
+
+int pc_rotary_forward(int device, const pc_rotary* d, void* stream) {
+  return guarded([&] {
+    check_device(device);
+    RotaryArgs a = rotary_base(d);
+    if (d->heads) check_heads(d, d->q, "q", false), check_out(d, d->q_out, d->heads, d->dim, "q_out", false);
+    if (d->kv_heads) check_heads(d, d->k, "k", false), check_out(d, d->k_out, d->kv_heads, d->dim, "k_out", false);
+    check_place(d, d->q_out, d->q, d->heads, "q_out");
+    check_place(d, d->k_out, d->k, d->kv_heads, "k_out");
+    if (d->num_tokens == 0 || d->heads + d->kv_heads == 0) return;
+    a.q = attn_tensor(d->q);
+    a.k = attn_tensor(d->k);
+    a.qo = d->q_out.data;
+    a.qo_ts = d->q_out.token_stride;
+    a.qo_hs = d->q_out.head_stride;
+    a.ko = d->k_out.data;
+    a.ko_ts = d->k_out.token_stride;
+    a.ko_hs = d->k_out.head_stride;
+    DeviceGuard dg(device);
+    launch_rotary_fwd(a, d->dtype, (hipStream_t)stream);
+    check_launch();
+  });
+}
+
+int pc_rotary_backward(int device, const pc_rotary* d, void* ws, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    check_device(device);
+    RotaryArgs a = rotary_base(d);
+    auto side = [&](const pc_heads& dy, const pc_heads& dx, const pc_heads& x, int heads, const char* n0, const char* n1, const char* n2) {
+      if (!heads) return;
+      check_heads(d, dy, n0, false);
+      check_out(d, dx, heads, d->dim, n1, false);
+      check_place(d, dx, dy, heads, n1);
+      if (!d->norm) return;
+      check_heads(d, x, n2, false);
+      check_place(d, dx, x, heads, n1);
+    };
+    side(d->d_q_out, d->d_q, d->q, d->heads, "d_q_out", "d_q", "q");
+    side(d->d_k_out, d->d_k, d->k, d->kv_heads, "d_k_out", "d_k", "k");
+    const bool weights = d->norm && (d->d_q_weight || d->d_k_weight);
+    a.parts = rotary_parts(d->num_tokens, d->heads, d->kv_heads);
+    if (weights) check_ws(ws, ws_bytes, (size_t)a.parts * 2 * d->dim * sizeof(float));
+    if ((d->num_tokens == 0 || d->heads + d->kv_heads == 0) && !weights) return;
+    a.q = attn_tensor(d->q);
+    a.k = attn_tensor(d->k);
+    a.dq = attn_tensor(d->d_q_out);
+    a.dk = attn_tensor(d->d_k_out);
+    a.qo = d->d_q.data;
+    a.qo_ts = d->d_q.token_stride;
+    a.qo_hs = d->d_q.head_stride;
+    a.ko = d->d_k.data;
+    a.ko_ts = d->d_k.token_stride;
+    a.ko_hs = d->d_k.head_stride;
+    a.dqw = d->d_q_weight;
+    a.dkw = d->d_k_weight;
+    a.part_sums = weights ? (float*)ws : nullptr;
+    DeviceGuard dg(device);
+    launch_rotary_bwd(a, d->dtype, (hipStream_t)stream);
     check_launch();
   });
 }
