@@ -244,13 +244,12 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
           if (key + 32 * kb + row_of(r, h) > last) s[kb][r] = -INFINITY;
     }
     if (PAGED && lds.absent[b] == key) {
+      const uint64_t gone = __ballot(lane < BK && !keys.there(key + lane));
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int j = key + 32 * kb + row_of(r, h);
-          if (j > last || !keys.there(j)) s[kb][r] = -INFINITY;
-        }
+        for (int r = 0; r < 16; ++r)
+          if (gone >> (32 * kb + row_of(r, h)) & 1) s[kb][r] = -INFINITY;
     }
     float top = s[0][0];
 #pragma unroll
