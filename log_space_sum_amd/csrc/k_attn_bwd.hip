@@ -181,15 +181,11 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
             dp = mma_planes<N>(f, go[st], dp);
           }
         }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, -lse2));
         if (key + 32 * kb + 31 > first_last) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const bool off = key + 32 * kb + row_of(r, h) > last;
-            s[r] = off ? 0.0f : exp2_fast(fmaf(s[r], c, -lse2));
-          }
-        } else {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, -lse2));
+          for (int r = 0; r < 16; ++r) s[r] = masked(s[r], key + 32 * kb + row_of(r, h) > last, 0.0f);
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
@@ -376,15 +372,19 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
         const f32x4 l4 = *(const f32x4*)&lds.lse2[x][8 * r4 + 4 * h], d4 = *(const f32x4*)&lds.delta[x][8 * r4 + 4 * h];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = 4 * r4 + e;
-          s[r] = exp2_fast(fmaf(s[r], c, -l4[e]));
-          if (edge) {
-            const int i = row + row_of(r, h);
-            if (i < key || i >= len) s[r] = 0.0f;
-          }
-          dp[r] = s[r] * (dp[r] - d4[e]);
+          s[4 * r4 + e] = exp2_fast(fmaf(s[4 * r4 + e], c, -l4[e]));
+          dp[4 * r4 + e] -= d4[e];
         }
       }
+      if (edge) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int i = row + row_of(r, h);
+          s[r] = masked(s[r], i < key || i >= len, 0.0f);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) dp[r] *= s[r];
       scale.move(dp, dka);
 #pragma unroll
       for (int st = 0; st < 2; ++st) {

@@ -212,7 +212,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(
       if (key + 31 > first_last || gone) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (key + row_of(r, h) > last || (gone >> row_of(r, h) & 1)) s[r] = -INFINITY;
+          s[r] = masked(s[r], key + row_of(r, h) > last || (gone >> row_of(r, h) & 1));
       }
       float top = s[0];
 #pragma unroll

@@ -241,7 +241,7 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (key + 32 * kb + row_of(r, h) > last) s[kb][r] = -INFINITY;
+          s[kb][r] = masked(s[kb][r], key + 32 * kb + row_of(r, h) > last);
     }
     if (PAGED && lds.absent[b] == key) {
       const uint64_t gone = __ballot(lane < BK && !keys.there(key + lane));
@@ -249,7 +249,7 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (gone >> (32 * kb + row_of(r, h)) & 1) s[kb][r] = -INFINITY;
+          s[kb][r] = masked(s[kb][r], gone >> (32 * kb + row_of(r, h)) & 1);
     }
     float top = s[0][0];
 #pragma unroll
