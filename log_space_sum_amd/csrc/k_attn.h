@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "pc_ops.h"
+#include "pc_ring.h"
 
 namespace pc {
 
@@ -197,6 +198,32 @@ struct Tile {
   }
 };
 
+// Direct loads of a tile (16-bit types, rows of D elements, 16-byte aligned): unit u of 256 threads is the LDS chunk
+// u * 256 + thread; which chunk of which row that holds is the row's turn.
+template <int D>
+struct DirectUnit {
+  int row, byte;     // of the tile; of the row
+  __device__ __forceinline__ DirectUnit(int u) {
+    const int id = u * 256 + threadIdx.x;
+    row = id / (D / 8);
+    byte = ((id % (D / 8)) ^ Tile<bf16, 64, D>::turn(row)) * 16;
+  }
+};
+__device__ __forceinline__ uint32_t lds_byte(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+// As lds_load16, from an address of each lane's own.
+__device__ __forceinline__ void lds_load16_at(const void* p, uint32_t to) {
+  const uint32_t m0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)to);
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(m0) : "memory", "m0");
+}
+// Waits for this wave's direct loads; a barrier behind it makes them everybody's.
+__device__ __forceinline__ void direct_wait() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(WaitVmLgkm<0>::imm);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
 // ---- lanes ------------------------------------------------------------------------
 // The same lane's value of the other half of the wave, in one of two results.
 __device__ __forceinline__ void both_halves(float x, float& lo, float& hi) {
@@ -238,6 +265,28 @@ __device__ __forceinline__ void store4(T* to, const float (&x)[4], int have) {
     for (int e = 0; e < 4; ++e)
       if (e < have) to[e] = from_f32<T>(x[e]);
   }
+}
+
+// Whether a tensor's rows can be loaded to LDS directly: 16-byte aligned, a tile's offsets in 32 bits.
+inline bool direct_rows(const void* p, int64_t ts, int64_t hs) {
+  return ((uintptr_t)p | (uintptr_t)(ts * 2) | (uintptr_t)(hs * 2)) % 16 == 0 && ts < (1 << 23);
+}
+// The tile's width D of a call, and whether it is both dims' and (16-bit types) keys and values can be loaded directly.
+struct Fit {
+  int D;
+  bool full;
+};
+template <typename T>
+Fit fit_of(const AttnArgs& a, bool cache) {
+  const int big = a.dk > a.dv ? a.dk : a.dv, D = big <= 64 ? 64 : 128;
+  bool full = a.dk == D && a.dv == D;
+  if (sizeof(T) == 2) {
+    full = full && direct_rows(a.k.p, a.k.ts, a.k.hs) && direct_rows(a.v.p, a.v.ts, a.v.hs);
+    if (cache)
+      for (const AttnCache* c : {&a.pages.k, &a.pages.v})
+        full = full && direct_rows(c->p, c->token_stride, c->head_stride) && c->page_stride % 8 == 0;
+  }
+  return {D, full};
 }
 
 // ---- sequences -----------------------------------------------------------------------

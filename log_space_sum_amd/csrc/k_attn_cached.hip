@@ -350,15 +350,9 @@ void launch(const AttnArgs& a, bool few, hipStream_t s) {
 }
 template <typename T>
 void cached(const AttnArgs& a, bool few, hipStream_t s) {
-  const int big = a.dk > a.dv ? a.dk : a.dv;
-  const bool same = a.dk == a.dv;
-  if (big <= 64) {
-    if (same && big == 64) launch<T, 64, true>(a, few, s);
-    else launch<T, 64, false>(a, few, s);
-  } else {
-    if (same && big == 128) launch<T, 128, true>(a, few, s);
-    else launch<T, 128, false>(a, few, s);
-  }
+  const Fit f = fit_of<T>(a, true);
+  if (f.D == 64) f.full ? launch<T, 64, true>(a, few, s) : launch<T, 64, false>(a, few, s);
+  else f.full ? launch<T, 128, true>(a, few, s) : launch<T, 128, false>(a, few, s);
 }
 
 }  // namespace

@@ -163,6 +163,7 @@ struct FwdShape {
   };
 };
 
+// FULL: rows of D elements of a 16-bit type, 16-byte aligned, at strides below 2^23: tiles go straight to LDS.
 template <typename T, int D, bool FULL, bool PAGED>
 __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, const Keys<T, PAGED> keys, const Rows<T> rows,
                                             const RowOut out, int dk_, int dv_, float c, bool negative, int key0, int key1) {
@@ -170,6 +171,7 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
   using S = FwdShape<T, D>;
   constexpr int IN = N::IN, W = N::W, BK = S::BK, KB = BK / 32, BUFS = S::BUFS, DS = D / 16, DB = D / 32;
   constexpr int NT = 256, PER_ROW = D / 8, U = BK * PER_ROW / NT;
+  constexpr bool DIRECT = FULL && IN == 1;
   const int dk = FULL ? D : dk_, dv = FULL ? D : dv_;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
   const int wave_first = 32 * wave, end = rows.count;
@@ -201,7 +203,46 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
   for (int d = 0; d < DB; ++d) o[d] = f32x16{};
   float m = -INFINITY, shift = (float)N::BIAS, l = 0.0f;
 
-  Unit<T> rk[U], rv[U];
+  Unit<T> rk[DIRECT ? 1 : U], rv[DIRECT ? 1 : U];
+  uint32_t ok[U], ov[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const DirectUnit<D> x(u);
+    ok[u] = (uint32_t)(x.row * (int)keys.k_ts * 2 + x.byte);
+    ov[u] = (uint32_t)(x.row * (int)keys.v_ts * 2 + x.byte);
+  }
+  auto load = [&](int b, int key) {
+    const uint32_t kb = lds_byte(lds.k[b].at) + wave * 1024, vb = lds_byte(lds.v[b].at) + wave * 1024;
+    if constexpr (PAGED) {
+      bool gone = false;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const DirectUnit<D> x(u);
+        const T *kr, *vr;
+        gone |= !keys.find(key + x.row, kr, vr);
+        lds_load16_at((const char*)kr + x.byte, kb + u * 4096);
+        lds_load16_at((const char*)vr + x.byte, vb + u * 4096);
+      }
+      if (gone) lds.absent[b] = key;
+    } else {
+      const T *kr = keys.k + (int64_t)key * keys.k_ts, *vr = keys.v + (int64_t)key * keys.v_ts;
+      if (key + BK <= keys.total) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          lds_load16(kr, ok[u], kb + u * 4096);
+          lds_load16(vr, ov[u], vb + u * 4096);
+        }
+      } else {       // rows behind the last are that one again
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const DirectUnit<D> x(u);
+          const int row = min(x.row, keys.total - 1 - key);
+          lds_load16(kr, (uint32_t)(row * (int)keys.k_ts * 2 + x.byte), kb + u * 4096);
+          lds_load16(vr, (uint32_t)(row * (int)keys.v_ts * 2 + x.byte), vb + u * 4096);
+        }
+      }
+    }
+  };
   bool absent = false;
   auto fetch = [&](int key) {
     absent = false;
@@ -265,6 +306,55 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[d][r] *= f;
     }
+    if constexpr (IN == 1) {
+      // 16 keys a step; the next step's weights are made and its values read between this one's matrix instructions
+      constexpr int STEPS = 2 * KB;
+      auto weights = [&](int step, frag (&w)[W]) {
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          p[e] = exp2_fast(fmaf(s[step >> 1][8 * (step & 1) + e], c, shift));
+          l += p[e];
+        }
+        planes_of<N>(p, w);
+      };
+      auto values = [&](int step, frag (&a)[DB][IN]) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+          if (FULL || 32 * d < dv) lds.v[b].cols(16 * step, 32 * d, lane, a[d]);
+      };
+      frag w[W], a[DB][IN];
+      values(0, a);
+      weights(0, w);
+#pragma unroll
+      for (int step = 0; step < STEPS; ++step) {
+        frag wn[W], an[DB][IN];
+        if (step + 1 < STEPS) {
+          values(step + 1, an);
+          weights(step + 1, wn);
+        }
+#pragma unroll
+        for (int p = W - 1; p >= 0; --p)
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+            if (FULL || 32 * d < dv) o[d] = N::mma(a[d][0], w[p], o[d]);
+        if (FULL && step + 1 < STEPS) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 2 * DB, 0);
+#pragma unroll
+          for (int i = 0; i < W * DB; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x2 | 0x400, (24 + 16 * W + W * DB - 1) / (W * DB), 0);
+          }
+        }
+        if (step + 1 < STEPS) {
+#pragma unroll
+          for (int p = 0; p < W; ++p) w[p] = wn[p];
+#pragma unroll
+          for (int d = 0; d < DB; ++d) a[d][0] = an[d][0];
+        }
+      }
+      return;
+    }
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
@@ -289,8 +379,20 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
 
   __syncthreads();                 // the last tile's readers are done
   if (PAGED && tid < BUFS) lds.absent[tid] = -1;
-  if (key0 < key1) fetch(key0);
-  if constexpr (BUFS == 2) {
+  if constexpr (DIRECT) {
+    if (PAGED) __syncthreads();
+    if (key0 < key1) load(0, key0);
+    direct_wait();
+    __syncthreads();
+    int b = 0;
+    for (int key = key0; key < key1; key += BK, b ^= 1) {
+      if (key + BK < key1) load(b ^ 1, key + BK);
+      if (wave_on && key <= last_last) compute(b, key);
+      direct_wait();
+      __syncthreads();
+    }
+  } else if constexpr (BUFS == 2) {
+    if (key0 < key1) fetch(key0);
     if (PAGED) __syncthreads();
     if (key0 < key1) stage(0, key0);
     __syncthreads();
@@ -303,6 +405,7 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
       __syncthreads();
     }
   } else {
+    if (key0 < key1) fetch(key0);
     if (PAGED) __syncthreads();
     for (int key = key0; key < key1; key += BK) {
       stage(0, key);

@@ -50,15 +50,10 @@ template <typename T>
 void fwd(const AttnArgs& a, hipStream_t s) {
   const int64_t slots = a.tokens * a.group / ATTN_ROWS + a.seqs;
   const dim3 grid((uint32_t)std::min<int64_t>(slots * a.kv_heads, 1 << 23));
-  const int big = a.dk > a.dv ? a.dk : a.dv;
-  const bool same = a.dk == a.dv;
-  if (big <= 64) {
-    if (same && big == 64) launch_kernel(attn_fwd<T, 64, true>, grid, dim3(256), 0, s, a, slots);
-    else launch_kernel(attn_fwd<T, 64, false>, grid, dim3(256), 0, s, a, slots);
-  } else {
-    if (same && big == 128) launch_kernel(attn_fwd<T, 128, true>, grid, dim3(256), 0, s, a, slots);
-    else launch_kernel(attn_fwd<T, 128, false>, grid, dim3(256), 0, s, a, slots);
-  }
+  const Fit f = fit_of<T>(a, false);
+  auto go = [&](auto kernel) { launch_kernel(kernel, grid, dim3(256), 0, s, a, slots); };
+  if (f.D == 64) f.full ? go(attn_fwd<T, 64, true>) : go(attn_fwd<T, 64, false>);
+  else f.full ? go(attn_fwd<T, 128, true>) : go(attn_fwd<T, 128, false>);
 }
 
 }  // namespace
