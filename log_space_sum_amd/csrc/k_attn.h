@@ -198,17 +198,19 @@ struct Tile {
   }
 };
 
-// Direct loads of a tile (16-bit types, rows of D elements, 16-byte aligned): unit u of 256 threads is the LDS chunk
-// u * 256 + thread; which chunk of which row that holds is the row's turn.
-template <int D>
+// Direct loads of a tile (16-bit types, rows of D elements, 16-byte aligned): unit u of NT threads is the LDS chunk
+// u * NT + thread; which chunk of which row that holds is the row's turn, the same for all of a thread's units, which
+// lie STEP rows apart.
+template <int D, int NT = 256>
 struct DirectUnit {
-  int row, byte;     // of the tile; of the row
-  __device__ __forceinline__ DirectUnit(int u) {
-    const int id = u * 256 + threadIdx.x;
-    row = id / (D / 8);
-    byte = ((id % (D / 8)) ^ Tile<bf16, 64, D>::turn(row)) * 16;
+  static constexpr int STEP = NT / (D / 8);
+  int row, byte;     // of the first unit: row of the tile, byte of the row
+  __device__ __forceinline__ DirectUnit(int tid) {
+    row = tid / (D / 8);
+    byte = ((tid % (D / 8)) ^ Tile<bf16, 64, D>::turn(row)) * 16;
   }
 };
+static_assert(DirectUnit<128>::STEP % 16 == 0 && DirectUnit<64>::STEP % 16 == 0, "turns repeat every 16 rows");
 __device__ __forceinline__ uint32_t lds_byte(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
@@ -252,6 +254,14 @@ __device__ __forceinline__ float masked(float x, bool off, float to = -INFINITY)
 }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The thread's number, from which nothing is computed before this place: the registers of a workgroup's loop over
+// tiles are full, and values made in front of it would be spilled, to be waited for behind loads in flight.
+__device__ __forceinline__ int thread_here() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 // Four values side by side in memory, where they exist (`have` of them).
 template <typename T>
 __device__ __forceinline__ void store4(T* to, const float (&x)[4], int have) {
@@ -271,17 +281,19 @@ __device__ __forceinline__ void store4(T* to, const float (&x)[4], int have) {
 inline bool direct_rows(const void* p, int64_t ts, int64_t hs) {
   return ((uintptr_t)p | (uintptr_t)(ts * 2) | (uintptr_t)(hs * 2)) % 16 == 0 && ts < (1 << 23);
 }
-// The tile's width D of a call, and whether it is both dims' and (16-bit types) keys and values can be loaded directly.
+// The tile's width D of a call, and whether it is both dims' and (16-bit types) keys and values, those of the cache, and
+// rows can be loaded directly.
 struct Fit {
   int D;
   bool full;
 };
 template <typename T>
-Fit fit_of(const AttnArgs& a, bool cache) {
+Fit fit_of(const AttnArgs& a, bool cache, bool rows = false) {
   const int big = a.dk > a.dv ? a.dk : a.dv, D = big <= 64 ? 64 : 128;
   bool full = a.dk == D && a.dv == D;
   if (sizeof(T) == 2) {
     full = full && direct_rows(a.k.p, a.k.ts, a.k.hs) && direct_rows(a.v.p, a.v.ts, a.v.hs);
+    if (rows) full = full && direct_rows(a.q.p, a.q.ts, a.q.hs) && direct_rows(a.d_o.p, a.d_o.ts, a.d_o.hs);
     if (cache)
       for (const AttnCache* c : {&a.pages.k, &a.pages.v})
         full = full && direct_rows(c->p, c->token_stride, c->head_stride) && c->page_stride % 8 == 0;
@@ -324,5 +336,13 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t* cu, int seqs, int64_
   const int64_t t0 = seq_start(cu, lo, tokens), t1 = max(seq_start(cu, lo + 1, tokens), t0);
   return {lo, t0, t1 - t0, slot - (t0 * group / B + lo)};
 }
+
+// Which head and which of `n` others (slots, parts) block b takes: heads innermost.
+struct Turn {
+  int head;
+  int64_t other;
+};
+__host__ __device__ inline int64_t turns(int64_t n, int heads) { return n * heads; }
+__device__ __forceinline__ Turn turn_of(int64_t b, int64_t n, int heads) { return {(int)(b % heads), b / heads}; }
 
 }  // namespace pc

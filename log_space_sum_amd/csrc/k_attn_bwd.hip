@@ -111,9 +111,11 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
   const int heads = a.kv_heads * a.group, dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
   const float c = a.scale * LOG2E;
-  for (int64_t b = blockIdx.x; b < slots * a.kv_heads; b += gridDim.x) {
-    const int kvh = (int)(b % a.kv_heads);
-    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - b / a.kv_heads);
+  for (int64_t b = blockIdx.x; b < turns(slots, a.kv_heads); b += gridDim.x) {
+    const Turn turn = turn_of(b, slots, a.kv_heads);
+    const int kvh = turn.head;
+    if (turn.other >= slots) continue;
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - turn.other);
     const int64_t first = at.tile * ATTN_ROWS, rows_all = at.len * a.group;
     if (at.seq < 0 || first >= rows_all) continue;
     const int64_t tf = first / a.group;
@@ -260,9 +262,9 @@ struct DkvShape {
 };
 
 template <typename T>
-__device__ __attribute__((noinline)) void careful_dkv(AttnArgs a, int64_t t0, int64_t len, int64_t first, int count, int kvh) {
+__device__ __attribute__((noinline)) void careful_dkv(AttnArgs a, int64_t t0, int64_t len, int64_t first, int count, int kvh, int nwaves) {
   const int lane = threadIdx.x & 63, heads = a.kv_heads * a.group;
-  for (int r = threadIdx.x >> 6; r < count; r += 4) {
+  for (int r = threadIdx.x >> 6; r < count; r += nwaves) {
     const int64_t j = first + r;
     const T *k = (const T*)a.k.p + (t0 + j) * a.k.ts + kvh * a.k.hs, *v = (const T*)a.v.p + (t0 + j) * a.v.ts + kvh * a.v.hs;
     float dk[2] = {0.0f, 0.0f}, dv[2] = {0.0f, 0.0f};
@@ -301,10 +303,12 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
   const int heads = a.kv_heads * a.group, dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
   const float c = a.scale * LOG2E;
-  for (int64_t b = blockIdx.x; b < slots * a.kv_heads; b += gridDim.x) {
-    const int kvh = (int)(b % a.kv_heads);
+  for (int64_t b = blockIdx.x; b < turns(slots, a.kv_heads); b += gridDim.x) {
+    const Turn turn = turn_of(b, slots, a.kv_heads);
+    const int kvh = turn.head;
+    if (turn.other >= slots) continue;
     // a sequence's first keys, which have the most rows, first
-    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, 1, ATTN_ROWS, b / a.kv_heads);
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, 1, ATTN_ROWS, turn.other);
     const int64_t first64 = at.tile * ATTN_ROWS;
     if (at.seq < 0 || first64 >= at.len) continue;
     const int len = (int)at.len, first = (int)first64, count = min(ATTN_ROWS, len - first);
@@ -443,7 +447,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
     }
     const bool store = 32 * wave + (lane & 31) < count;
     if (__syncthreads_or(store && (any_not_finite(dka) || any_not_finite(dva)))) {
-      careful_dkv<T>(a, at.t0, len, first, count, kvh);
+      careful_dkv<T>(a, at.t0, len, first, count, kvh, 4);
       continue;
     }
     if (!store) continue;
@@ -462,24 +466,262 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
   }
 }
 
+// The same for 16-bit types with eight waves: a pair of waves shares 32 keys, the first makes their dv (from
+// S and P), the second their dk (from S, dP and dS), so that either fits the registers of two waves a SIMD.  S is
+// made twice (9 products' work for 8).
+constexpr int PAIRS = 2;
+template <typename T, int D>
+struct PairShape {
+  static constexpr int BR = 64, KEYS = 32 * PAIRS, NT = 128 * PAIRS;
+  struct Lds {
+    Tile<T, BR, D> q[2], go[2];
+    alignas(16) float lse2[2][BR];
+    alignas(16) float delta[2][BR];
+    int bad;
+  };
+};
+
+// One wave's part of a tile of 128 keys: DK: dk, else dv, of its 32.
+template <typename T, int D, bool FULL, bool DK>
+__device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, const AttnArgs& a, const SeqTile& at, int kvh) {
+  using N = Num<T>;
+  using S = PairShape<T, D>;
+  constexpr int W = N::W, BR = S::BR, DS = D / 16, DB = D / 32, NT = S::NT;
+  constexpr int PER_ROW = D / 8, U = BR * PER_ROW / NT;
+  const int tid = thread_here(), wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
+  const int heads = a.kv_heads * a.group, dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
+  const float c = a.scale * LOG2E;
+  const DirectUnit<D, NT> unit(tid);
+  const uint32_t oq = (uint32_t)(unit.row * (int)a.q.ts * 2 + unit.byte), og = (uint32_t)(unit.row * (int)a.d_o.ts * 2 + unit.byte);
+  const int len = (int)at.len, first = (int)(at.tile * S::KEYS), count = min(S::KEYS, len - first), block = 32 * (wave % PAIRS);
+  const int key = first + min(block + (lane & 31), count - 1), wave_key = first + block;
+  const bool wave_on = block < count;
+  frag k[DS], v[DK ? DS : 1];
+  {
+    const T *pk = (const T*)a.k.p + (at.t0 + key) * a.k.ts + kvh * a.k.hs, *pv = (const T*)a.v.p + (at.t0 + key) * a.v.ts + kvh * a.v.hs;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      frag f[1];
+      frags_of(load_unit<FULL>(pk, 16 * s + 8 * h, dk), f);
+      k[s] = f[0];
+      if constexpr (DK) {
+        frags_of(load_unit<FULL>(pv, 16 * s + 8 * h, dv), f);
+        v[s] = f[0];
+      }
+    }
+  }
+  f32x16 acc[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) acc[d] = f32x16{};
+  Scale<T> scale;
+
+  Unit<T> rq[FULL ? 1 : U], rg[FULL ? 1 : U];
+  float rs = 0.0f;
+  auto fetch = [&](int x, int head, int row) {
+    const T *q0 = (const T*)a.q.p + (at.t0 + row) * a.q.ts + head * a.q.hs, *g0 = (const T*)a.d_o.p + (at.t0 + row) * a.d_o.ts + head * a.d_o.hs;
+    if constexpr (FULL) {
+      const uint32_t qb = lds_byte(lds.q[x].at) + wave * 1024, gb = lds_byte(lds.go[x].at) + wave * 1024;
+      if (row + BR <= len) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          lds_load16(q0 + u * unit.STEP * a.q.ts, oq, qb + u * NT * 16);
+          lds_load16(g0 + u * unit.STEP * a.d_o.ts, og, gb + u * NT * 16);
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = min(unit.row + u * unit.STEP, len - 1 - row);
+          lds_load16(q0, (uint32_t)(r * (int)a.q.ts * 2 + unit.byte), qb + u * NT * 16);
+          lds_load16(g0, (uint32_t)(r * (int)a.d_o.ts * 2 + unit.byte), gb + u * NT * 16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int id = u * NT + tid, d = id % PER_ROW * 8;
+        const int64_t r = min(id / PER_ROW, len - 1 - row);
+        rq[u] = load_unit<FULL>(q0 + r * a.q.ts, d, dk);
+        rg[u] = load_unit<FULL>(g0 + r * a.d_o.ts, d, dv);
+      }
+    }
+    if (tid < 2 * BR) {
+      const int64_t i = (at.t0 + min(row + (tid & (BR - 1)), len - 1)) * heads + head;
+      rs = tid < BR ? a.lse[i] * LOG2E : a.delta[i];
+    }
+  };
+  auto stage = [&](int x) {
+    if constexpr (!FULL) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int id = u * NT + tid;
+        lds.q[x].put(id / PER_ROW, id % PER_ROW * 8, rq[u]);
+        lds.go[x].put(id / PER_ROW, id % PER_ROW * 8, rg[u]);
+      }
+    }
+    if (tid < BR) lds.lse2[x][tid] = rs;
+    else if (tid < 2 * BR) lds.delta[x][tid - BR] = rs;
+  };
+  // acc += tile^T x for 32 rows of a tile and a result x of them; the second 16 rows' values are read and
+  // planes made between the first's matrix instructions
+  auto add = [&](const Tile<T, BR, D>& tile, int r0, const f32x16& x, int dim) {
+    frag w[2][W], f[2][DB][1];
+    auto ready = [&](int st) {
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+        if (FULL || 32 * d < dim) tile.cols(r0 + 16 * st, 32 * d, lane, f[st][d]);
+      float p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = x[8 * st + e];
+      planes_of<N>(p, w[st]);
+    };
+    ready(0);
+    if (FULL) __builtin_amdgcn_sched_barrier(0);
+    ready(1);
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int p = W - 1; p >= 0; --p)
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+          if (FULL || 32 * d < dim) acc[d] = N::mma(f[st][d][0], w[st][p], acc[d]);
+    if (FULL) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 2 * DB, 0);
+#pragma unroll
+      for (int k = 0; k < W * DB; ++k) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);
+      }
+    }
+  };
+  auto compute = [&](int x, int row, int r0) {
+    // a block's rows of q are all asked for before they are used, those of do meanwhile
+    frag fq[DS][1], fg[DK ? DS : 1][1];
+#pragma unroll
+    for (int st = 0; st < DS; ++st)
+      if (FULL || 16 * st < dk) lds.q[x].rows(r0, st, lane, fq[st]);
+    if (FULL) __builtin_amdgcn_sched_barrier(0);
+    f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+    for (int st = 0; st < DS; ++st) {
+      if constexpr (DK) {
+        if (FULL || 16 * st < dv) lds.go[x].rows(r0, st, lane, fg[st]);
+        if (FULL || 16 * st < dk) s = N::mma(fq[st][0], k[st], s);
+        if (FULL) __builtin_amdgcn_sched_barrier(0);
+      } else if (FULL || 16 * st < dk) {
+        if (st & 1) dp = N::mma(fq[st][0], k[st], dp);
+        else s = N::mma(fq[st][0], k[st], s);
+      }
+    }
+    if constexpr (DK) {
+#pragma unroll
+      for (int st = 0; st < DS; ++st)
+        if (FULL || 16 * st < dv) dp = N::mma(fg[st][0], v[st], dp);
+    } else {
+      s += dp;
+    }
+#pragma unroll
+    for (int r4 = 0; r4 < 4; ++r4) {
+      const f32x4 l4 = *(const f32x4*)&lds.lse2[x][r0 + 8 * r4 + 4 * h];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[4 * r4 + e] = exp2_fast(fmaf(s[4 * r4 + e], c, -l4[e]));
+    }
+    if (row < wave_key + 31 || row + 32 > len) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int i = row + row_of(r, h);
+        s[r] = masked(s[r], i < key || i >= len, 0.0f);
+      }
+    }
+    if constexpr (DK) {
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const f32x4 d4 = *(const f32x4*)&lds.delta[x][r0 + 8 * r4 + 4 * h];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[4 * r4 + e] *= dp[4 * r4 + e] - d4[e];
+      }
+      scale.move(s, acc);
+      add(lds.q[x], r0, s, dk);
+    } else {
+      if (N::BIAS) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] *= (float)(1 << N::BIAS);
+      }
+      add(lds.go[x], r0, s, dv);
+    }
+  };
+  const int h0 = kvh * a.group, h1 = h0 + a.group;      // rows from the tile's first key on attend it
+  __syncthreads();
+  if (tid == 0) lds.bad = 0;
+  int head = h0, row = first, x = 0;
+  fetch(0, head, row);
+  stage(0);
+  direct_wait();
+  __syncthreads();
+  while (head < h1) {
+    int nh = head, nr = row + BR;
+    if (nr >= len) {
+      nr = first;
+      ++nh;
+    }
+    if (nh < h1) fetch(x ^ 1, nh, nr);
+#pragma unroll 1
+    for (int r0 = 0; r0 < BR; r0 += 32)
+      if (wave_on && row + r0 + 31 >= wave_key && row + r0 < len) compute(x, row + r0, r0);
+    if (nh < h1) stage(x ^ 1);
+    direct_wait();
+    __syncthreads();
+    x ^= 1;
+    head = nh;
+    row = nr;
+  }
+  const bool store = block + (lane & 31) < count;
+  if (store && any_not_finite(acc)) lds.bad = 1;
+  __syncthreads();
+  if (lds.bad) {
+    if (!DK) careful_dkv<T>(a, at.t0, len, first, count, kvh, PAIRS);
+    return;
+  }
+  if (!store) return;
+  const float f = DK ? a.scale / scale.by : 1.0f / (float)(1 << N::BIAS);
+  const int dim = DK ? dk : dv;
+  T* to = DK ? (T*)a.dk_ + (at.t0 + key) * a.dk_ts + kvh * a.dk_hs : (T*)a.dv_ + (at.t0 + key) * a.dv_ts + kvh * a.dv_hs;
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int e = 32 * d + 8 * r + 4 * h;
+      const float y[4] = {acc[d][4 * r] * f, acc[d][4 * r + 1] * f, acc[d][4 * r + 2] * f, acc[d][4 * r + 3] * f};
+      store4<T>(to + e, y, dim - e);
+    }
+}
+
+template <typename T, int D, bool FULL>
+__global__ __launch_bounds__(128 * PAIRS, 2) void attn_dkv_pairs(AttnArgs a, int64_t slots) {
+  __shared__ typename PairShape<T, D>::Lds lds;
+  for (int64_t b = blockIdx.x; b < turns(slots, a.kv_heads); b += gridDim.x) {
+    const Turn turn = turn_of(b, slots, a.kv_heads);
+    if (turn.other >= slots) continue;
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, 1, PairShape<T, D>::KEYS, turn.other);
+    if (at.seq < 0 || at.tile * PairShape<T, D>::KEYS >= at.len) continue;
+    // (both parts pass the same barriers)
+    if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >= PAIRS) pair_tile<T, D, FULL, true>(lds, a, at, turn.head);
+    else pair_tile<T, D, FULL, false>(lds, a, at, turn.head);
+  }
+}
+
 template <typename T, int D, bool FULL>
 void launch(const AttnArgs& a, hipStream_t s) {
-  const int64_t rows = a.tokens * a.group / ATTN_ROWS + a.seqs, keys = a.tokens / ATTN_ROWS + a.seqs;
-  auto grid = [&](int64_t slots) { return dim3((uint32_t)std::min<int64_t>(slots * a.kv_heads, 1 << 23)); };
+  const int64_t rows = a.tokens * a.group / ATTN_ROWS + a.seqs, keys = a.tokens / (Num<T>::IN == 1 ? PairShape<T, D>::KEYS : ATTN_ROWS) + a.seqs;
+  auto grid = [&](int64_t slots) { return dim3((uint32_t)std::min<int64_t>(turns(slots, a.kv_heads), 1 << 22)); };
   launch_kernel(attn_dq<T, D, FULL>, grid(rows), dim3(256), 0, s, a, rows);
-  launch_kernel(attn_dkv<T, D, FULL>, grid(keys), dim3(256), 0, s, a, keys);
+  if constexpr (Num<T>::IN == 1) launch_kernel(attn_dkv_pairs<T, D, FULL>, grid(keys), dim3(PairShape<T, D>::NT), 0, s, a, keys);
+  else launch_kernel(attn_dkv<T, D, FULL>, grid(keys), dim3(256), 0, s, a, keys);
 }
 template <typename T>
 void bwd(const AttnArgs& a, hipStream_t s) {
-  const int big = a.dk > a.dv ? a.dk : a.dv;
-  const bool same = a.dk == a.dv;
-  if (big <= 64) {
-    if (same && big == 64) launch<T, 64, true>(a, s);
-    else launch<T, 64, false>(a, s);
-  } else {
-    if (same && big == 128) launch<T, 128, true>(a, s);
-    else launch<T, 128, false>(a, s);
-  }
+  const Fit f = fit_of<T>(a, false, true);
+  if (f.D == 64) f.full ? launch<T, 64, true>(a, s) : launch<T, 64, false>(a, s);
+  else f.full ? launch<T, 128, true>(a, s) : launch<T, 128, false>(a, s);
 }
 
 }  // namespace

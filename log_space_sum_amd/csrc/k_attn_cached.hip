@@ -105,10 +105,12 @@ __device__ __forceinline__ void no_keys(const Work<T>& w) {
 template <typename T, int D, bool FULL>
 __global__ __launch_bounds__(256, 2) void attn_cached_many(AttnArgs a, int64_t slots, int part_len) {
   __shared__ typename FwdShape<T, D>::Lds lds;
-  const int64_t per = (int64_t)a.kv_heads * a.nsplit;
-  for (int64_t b = blockIdx.x; b < slots * per; b += gridDim.x) {
-    const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
-    const Work<T> w = find_work<T>(a, slots - 1 - b / per, kvh, split, ATTN_ROWS, part_len);
+  const int64_t works = slots * a.nsplit;
+  for (int64_t b = blockIdx.x; b < turns(works, a.kv_heads); b += gridDim.x) {
+    const Turn turn = turn_of(b, works, a.kv_heads);
+    if (turn.other >= works) continue;
+    const int kvh = turn.head, split = (int)(turn.other % a.nsplit);
+    const Work<T> w = find_work<T>(a, slots - 1 - turn.other / a.nsplit, kvh, split, ATTN_ROWS, part_len);
     if (w.rows.count == 0) continue;
     if (split == 0) join_cache(a, w, kvh);
     if (w.key0 >= w.key1) no_keys(w);
@@ -145,12 +147,14 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(
   constexpr int IN = N::IN, W = N::W, DS = D / 16, DB = D / 32, PER_ROW = D / 8, U = 32 * PER_ROW / 64;
   __shared__ typename FewShape<T, D>::Lds lds;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
-  const int64_t per = (int64_t)a.kv_heads * a.nsplit;
+  const int64_t works = slots * a.nsplit;
   const int dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
   const float c = fabsf(a.scale) * LOG2E;
-  for (int64_t b = blockIdx.x; b < slots * per; b += gridDim.x) {
-    const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
-    const Work<T> w = find_work<T>(a, b / per, kvh, split, ATTN_FEW_ROWS, part_len);
+  for (int64_t b = blockIdx.x; b < turns(works, a.kv_heads); b += gridDim.x) {
+    const Turn turn = turn_of(b, works, a.kv_heads);
+    if (turn.other >= works) continue;
+    const int kvh = turn.head, split = (int)(turn.other % a.nsplit);
+    const Work<T> w = find_work<T>(a, turn.other / a.nsplit, kvh, split, ATTN_FEW_ROWS, part_len);
     if (w.rows.count == 0) continue;
     if (split == 0) join_cache(a, w, kvh);
     if (w.key0 >= w.key1) {
@@ -344,7 +348,7 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
 template <typename T, int D, bool FULL>
 void launch(const AttnArgs& a, bool few, hipStream_t s) {
   const int64_t slots = a.tokens * a.group / (few ? ATTN_FEW_ROWS : ATTN_ROWS) + a.seqs;
-  const dim3 grid((uint32_t)std::min<int64_t>(slots * a.kv_heads * a.nsplit, 1 << 23));
+  const dim3 grid((uint32_t)std::min<int64_t>(turns(slots * a.nsplit, a.kv_heads), 1 << 23));
   if (few) launch_kernel(attn_cached_few<T, D, FULL>, grid, dim3(256), 0, s, a, slots, a.part_len);
   else launch_kernel(attn_cached_many<T, D, FULL>, grid, dim3(256), 0, s, a, slots, a.part_len);
 }

@@ -173,7 +173,7 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
   constexpr int NT = 256, PER_ROW = D / 8, U = BK * PER_ROW / NT;
   constexpr bool DIRECT = FULL && IN == 1;
   const int dk = FULL ? D : dk_, dv = FULL ? D : dv_;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
+  const int tid = thread_here(), wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
   const int wave_first = 32 * wave, end = rows.count;
   const bool wave_on = wave_first < end;
   const int mine = min(wave_first + (lane & 31), end - 1);     // rows behind the last are that one again, and not stored
@@ -204,24 +204,18 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
   float m = -INFINITY, shift = (float)N::BIAS, l = 0.0f;
 
   Unit<T> rk[DIRECT ? 1 : U], rv[DIRECT ? 1 : U];
-  uint32_t ok[U], ov[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const DirectUnit<D> x(u);
-    ok[u] = (uint32_t)(x.row * (int)keys.k_ts * 2 + x.byte);
-    ov[u] = (uint32_t)(x.row * (int)keys.v_ts * 2 + x.byte);
-  }
+  const DirectUnit<D> unit(tid);
+  const uint32_t ok = (uint32_t)(unit.row * (int)keys.k_ts * 2 + unit.byte), ov = (uint32_t)(unit.row * (int)keys.v_ts * 2 + unit.byte);
   auto load = [&](int b, int key) {
     const uint32_t kb = lds_byte(lds.k[b].at) + wave * 1024, vb = lds_byte(lds.v[b].at) + wave * 1024;
     if constexpr (PAGED) {
       bool gone = false;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const DirectUnit<D> x(u);
         const T *kr, *vr;
-        gone |= !keys.find(key + x.row, kr, vr);
-        lds_load16_at((const char*)kr + x.byte, kb + u * 4096);
-        lds_load16_at((const char*)vr + x.byte, vb + u * 4096);
+        gone |= !keys.find(key + unit.row + u * unit.STEP, kr, vr);
+        lds_load16_at((const char*)kr + unit.byte, kb + u * 4096);
+        lds_load16_at((const char*)vr + unit.byte, vb + u * 4096);
       }
       if (gone) lds.absent[b] = key;
     } else {
@@ -229,16 +223,15 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
       if (key + BK <= keys.total) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          lds_load16(kr, ok[u], kb + u * 4096);
-          lds_load16(vr, ov[u], vb + u * 4096);
+          lds_load16(kr + u * unit.STEP * keys.k_ts, ok, kb + u * 4096);
+          lds_load16(vr + u * unit.STEP * keys.v_ts, ov, vb + u * 4096);
         }
       } else {       // rows behind the last are that one again
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const DirectUnit<D> x(u);
-          const int row = min(x.row, keys.total - 1 - key);
-          lds_load16(kr, (uint32_t)(row * (int)keys.k_ts * 2 + x.byte), kb + u * 4096);
-          lds_load16(vr, (uint32_t)(row * (int)keys.v_ts * 2 + x.byte), vb + u * 4096);
+          const int row = min(unit.row + u * unit.STEP, keys.total - 1 - key);
+          lds_load16(kr, (uint32_t)(row * (int)keys.k_ts * 2 + unit.byte), kb + u * 4096);
+          lds_load16(vr, (uint32_t)(row * (int)keys.v_ts * 2 + unit.byte), vb + u * 4096);
         }
       }
     }
@@ -267,11 +260,12 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
   auto compute = [&](int b, int key) {
     f32x16 s[KB];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      s[kb] = f32x16{};
+    for (int kb = 0; kb < KB; ++kb) s[kb] = f32x16{};
 #pragma unroll
-      for (int st = 0; st < DS; ++st) {
-        if (!FULL && 16 * st >= dk) continue;
+    for (int st = 0; st < DS; ++st) {
+      if (!FULL && 16 * st >= dk) continue;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
         frag a[IN];
         lds.k[b].rows(32 * kb, st, lane, a);
         s[kb] = mma_planes<N>(a, q[st], s[kb]);

@@ -14,10 +14,12 @@ template <typename T, int D, bool FULL>
 __global__ __launch_bounds__(256, 2) void attn_fwd(AttnArgs a, int64_t slots) {
   __shared__ typename FwdShape<T, D>::Lds lds;
   const int heads = a.kv_heads * a.group;
-  for (int64_t b = blockIdx.x; b < slots * a.kv_heads; b += gridDim.x) {
-    // the last tiles, which have the most keys, first; a head's tiles in one XCD's turn where they divide
-    const int kvh = (int)(b % a.kv_heads);
-    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - b / a.kv_heads);
+  for (int64_t b = blockIdx.x; b < turns(slots, a.kv_heads); b += gridDim.x) {
+    const Turn turn = turn_of(b, slots, a.kv_heads);
+    const int kvh = turn.head;
+    if (turn.other >= slots) continue;
+    // the last tiles, which have the most keys, first
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - turn.other);
     const int64_t first = at.tile * ATTN_ROWS, rows_all = at.len * a.group;
     if (at.seq < 0 || first >= rows_all) continue;
     const int64_t tf = first / a.group, t = at.t0 + tf;
@@ -49,7 +51,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd(AttnArgs a, int64_t slots) {
 template <typename T>
 void fwd(const AttnArgs& a, hipStream_t s) {
   const int64_t slots = a.tokens * a.group / ATTN_ROWS + a.seqs;
-  const dim3 grid((uint32_t)std::min<int64_t>(slots * a.kv_heads, 1 << 23));
+  const dim3 grid((uint32_t)std::min<int64_t>(turns(slots, a.kv_heads), 1 << 23));
   const Fit f = fit_of<T>(a, false);
   auto go = [&](auto kernel) { launch_kernel(kernel, grid, dim3(256), 0, s, a, slots); };
   if (f.D == 64) f.full ? go(attn_fwd<T, 64, true>) : go(attn_fwd<T, 64, false>);
