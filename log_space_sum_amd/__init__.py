@@ -797,13 +797,14 @@ def pc_rotary_backward(dq_out, dk_out, dq, dk, positions, freq, interleaved=Fals
     _check(lib().pc_rotary_backward(dev, d, pws, nws, _stream_of(dev, stream)))
 
 
-def _softmax_attention(q, k, v, scale, cu_seqlens):
+def _softmax_attention(q, k, v, scale, cu_seqlens, max_seqlen=None):
     """The descriptor of q [tokens, heads, dim_k], k [tokens, kv_heads, dim_k], v [tokens, kv_heads, dim_v]."""
     dev, dt = _device(_three(q, "q"), "q"), q.dtype
     T, H, dk = q.shape
     K, dv = _three(k, "k").shape[1], _three(v, "v").shape[2]
     d = pc_attention(_dtype(q, "q"), H, K, dk, dv, 1, T)
     d.scale = dk ** -0.5 if scale is None else scale
+    d.max_seqlen = T if max_seqlen is None else max_seqlen
     if cu_seqlens is not None:
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must have one dimension and at least one entry")
@@ -818,7 +819,7 @@ def _softmax_attention(q, k, v, scale, cu_seqlens):
 def attention_workspace(q, k, v, cu_seqlens=None, max_seqlen=None, backward=False):
     """A workspace tensor for pc_attention_forward, or with backward for pc_attention_backward, on tensors of these
     shapes."""
-    d, _, _, _ = _softmax_attention(q, k, v, None, cu_seqlens)
+    d, _, _, _ = _softmax_attention(q, k, v, None, cu_seqlens, max_seqlen)
     n = _bytes(lib().pc_attention_workspace_bytes, d, 1 if backward else 0)
     return _torch().empty(n, dtype=_torch().uint8, device=q.device)
 
@@ -827,8 +828,8 @@ def pc_attention_forward(q, k, v, o, lse=None, cu_seqlens=None, max_seqlen=None,
     """Causal softmax attention: o [tokens, heads, dim_v] and lse (float32 [tokens, heads], kept for the backward pass, or
     None) from q, k, v along every sequence.  cu_seqlens: int32 [sequences + 1] on the GPU (None: one sequence);
     max_seqlen: a bound of the longest (None: the number of tokens); scale: None for dim_k ** -0.5;
-    ws: attention_workspace(...)."""
-    d, dev, dt, (T, H, K, dk, dv) = _softmax_attention(q, k, v, scale, cu_seqlens)
+    ws: attention_workspace(...) (None: keys are not cut into parts, which few long sequences are faster with)."""
+    d, dev, dt, (T, H, K, dk, dv) = _softmax_attention(q, k, v, scale, cu_seqlens, max_seqlen)
     _heads(d.o, o, dev, dt, (T, H, dv), "o")
     d.lse = _dense(lse, dev, _torch().float32, (T, H), "lse")
     pws, nws = _ws_ptr(ws, dev)
@@ -837,7 +838,7 @@ def pc_attention_forward(q, k, v, o, lse=None, cu_seqlens=None, max_seqlen=None,
 
 def pc_attention_backward(do, q, k, v, o, lse, dq, dk, dv, cu_seqlens=None, max_seqlen=None, scale=None, ws=None, stream=None):
     """dq, dk, dv from do and the forward call's q, k, v, o and lse; ws: attention_workspace(..., backward=True)."""
-    d, dev, dt, (T, H, K, nk, nv) = _softmax_attention(q, k, v, scale, cu_seqlens)
+    d, dev, dt, (T, H, K, nk, nv) = _softmax_attention(q, k, v, scale, cu_seqlens, max_seqlen)
     _heads(d.o, o, dev, dt, (T, H, nv), "o")
     _heads(d.d_o, do, dev, dt, (T, H, nv), "do")
     d.lse = _dense(lse, dev, _torch().float32, (T, H), "lse")

@@ -337,12 +337,17 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t* cu, int seqs, int64_
   return {lo, t0, t1 - t0, slot - (t0 * group / B + lo)};
 }
 
-// Which head and which of `n` others (slots, parts) block b takes: heads innermost.
-struct Turn {
-  int head;
-  int64_t other;
-};
-__host__ __device__ inline int64_t turns(int64_t n, int heads) { return n * heads; }
-__device__ __forceinline__ Turn turn_of(int64_t b, int64_t n, int heads) { return {(int)(b % heads), b / heads}; }
+// The sequence of token t (which lies in one): its first token and length.
+__device__ __forceinline__ SeqTile find_token(const int32_t* cu, int seqs, int64_t tokens, int64_t t) {
+  if (!cu) return {0, 0, tokens, 0};
+  int lo = 0, hi = seqs;           // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (seq_start(cu, mid, tokens) <= t) lo = mid;
+    else hi = mid;
+  }
+  const int64_t t0 = seq_start(cu, lo, tokens);
+  return {lo, t0, max(seq_start(cu, lo + 1, tokens) - t0, (int64_t)0), 0};
+}
 
 }  // namespace pc

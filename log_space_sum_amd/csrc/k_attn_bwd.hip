@@ -57,11 +57,90 @@ __device__ __forceinline__ bool any_not_finite(const f32x16 (&x)[DB]) {
   return !(bad == 0.0f);
 }
 
+// Keys (of dq) or rows (of dk and dv) from .. to - 1 of a part, between `first` and `end`.
+struct Part {
+  int from, to;
+};
+__device__ __forceinline__ Part part_of(const AttnArgs& a, int split, int first, int end) {
+  if (a.nsplit == 1) return {first, end};
+  const int64_t lo = (int64_t)split * a.part_len, hi = split + 1 < a.nsplit ? lo + a.part_len : (int64_t)end;
+  return {(int)min(max(lo, (int64_t)first), (int64_t)end), (int)min(hi, (int64_t)end)};
+}
+
 template <typename T>
 __device__ __forceinline__ float dot(const T* a, const T* b, int n) {
   float s = 0.0f;
   for (int d = 0; d < n; ++d) s = fmaf(to_f32(a[d]), to_f32(b[d]), s);
   return s;
+}
+
+// ---- a block of 32 by 32 (16-bit types) ---------------------------------------------
+// s = A x^T and, with BOTH, dp = B y^T for 32 rows of two tiles and a wave's own operands.  The rows of A are
+// all asked for before they are used, those of B meanwhile; a single product goes in two chains.
+template <typename T, int D, bool FULL, bool BOTH, typename TileT>
+__device__ __forceinline__ void block_products(const TileT& ta, const TileT& tb, int r0, int lane, const frag (&x)[D / 16],
+                                               const frag (&y)[BOTH ? D / 16 : 1], int dx, int dy, f32x16& s, f32x16& dp) {
+  using N = Num<T>;
+  constexpr int DS = D / 16;
+  frag fa[DS][1], fb[BOTH ? DS : 1][1];
+#pragma unroll
+  for (int st = 0; st < DS; ++st)
+    if (FULL || 16 * st < dx) ta.rows(r0, st, lane, fa[st]);
+  if (FULL) __builtin_amdgcn_sched_barrier(0);
+  s = dp = f32x16{};
+#pragma unroll
+  for (int st = 0; st < DS; ++st) {
+    if constexpr (BOTH) {
+      if (FULL || 16 * st < dy) tb.rows(r0, st, lane, fb[st]);
+      if (FULL || 16 * st < dx) s = N::mma(fa[st][0], x[st], s);
+      if (FULL) __builtin_amdgcn_sched_barrier(0);
+    } else if (FULL || 16 * st < dx) {
+      if (st & 1) dp = N::mma(fa[st][0], x[st], dp);
+      else s = N::mma(fa[st][0], x[st], s);
+    }
+  }
+  if constexpr (BOTH) {
+#pragma unroll
+    for (int st = 0; st < DS; ++st)
+      if (FULL || 16 * st < dy) dp = N::mma(fb[st][0], y[st], dp);
+  } else {
+    s += dp;
+  }
+}
+// acc += A^T x for 32 rows of a tile and a result x of them; the second 16 rows' values are read and planes made
+// between the first's matrix instructions.
+template <typename T, int D, bool FULL, typename TileT>
+__device__ __forceinline__ void block_add(const TileT& ta, int r0, int lane, const f32x16& x, int dim, f32x16 (&acc)[D / 32]) {
+  using N = Num<T>;
+  constexpr int W = N::W, DB = D / 32;
+  frag w[2][W], f[2][DB][1];
+  auto ready = [&](int st) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+      if (FULL || 32 * d < dim) ta.cols(r0 + 16 * st, 32 * d, lane, f[st][d]);
+    float p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = x[8 * st + e];
+    planes_of<N>(p, w[st]);
+  };
+  ready(0);
+  if (FULL) __builtin_amdgcn_sched_barrier(0);
+  ready(1);
+#pragma unroll
+  for (int st = 0; st < 2; ++st)
+#pragma unroll
+    for (int p = W - 1; p >= 0; --p)
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+        if (FULL || 32 * d < dim) acc[d] = N::mma(f[st][d][0], w[st][p], acc[d]);
+  if (FULL) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 2 * DB, 0);
+#pragma unroll
+    for (int k = 0; k < W * DB; ++k) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);
+    }
+  }
 }
 
 // ---- dq -------------------------------------------------------------------------
@@ -75,7 +154,7 @@ struct DqShape {
 
 // A row after the other in float32, for a tile whose results are not finite (see careful_rows of the forward).
 template <typename T>
-__device__ __attribute__((noinline)) void careful_dq(AttnArgs a, int64_t t0, int64_t first, int count, int kvh) {
+__device__ __attribute__((noinline)) void careful_dq(AttnArgs a, int64_t t0, int64_t first, int count, int kvh, int split, Part part) {
   const int lane = threadIdx.x & 63;
   const T *k0 = (const T*)a.k.p + t0 * a.k.ts + kvh * a.k.hs, *v0 = (const T*)a.v.p + t0 * a.v.ts + kvh * a.v.hs;
   for (int r = threadIdx.x >> 6; r < count; r += 4) {
@@ -84,11 +163,12 @@ __device__ __attribute__((noinline)) void careful_dq(AttnArgs a, int64_t t0, int
     const T* o = (const T*)a.out.p + t * a.out.ts + h * a.out.hs;
     const float lse = a.lse[t * a.kv_heads * a.group + h], delta = dot(go, o, a.dv);
     float acc[2] = {0.0f, 0.0f};
-    for (int64_t j0 = 0; j0 <= i; j0 += 64) {
-      const int64_t j = min(j0 + lane, i);
+    const int64_t last = min(i, (int64_t)part.to - 1);
+    for (int64_t j0 = part.from; j0 <= last; j0 += 64) {
+      const int64_t j = min(j0 + lane, last);
       const float p = exp2_fast((dot(q, k0 + j * a.k.ts, a.dk) * a.scale - lse) * LOG2E);
       const float ds = p * (dot(go, v0 + j * a.v.ts, a.dv) - delta);
-      for (int x = 0; x < min((int64_t)64, i - j0 + 1); ++x) {
+      for (int x = 0; x < min((int64_t)64, last - j0 + 1); ++x) {
         const float w = __shfl(ds, x);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
@@ -97,7 +177,10 @@ __device__ __attribute__((noinline)) void careful_dq(AttnArgs a, int64_t t0, int
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      if (lane + 64 * e < a.dk) ((T*)a.dq)[t * a.dq_ts + h * a.dq_hs + lane + 64 * e] = from_f32<T>(acc[e] * a.scale);
+      if (lane + 64 * e < a.dk) {
+        if (a.nsplit > 1) a.part[(((int64_t)split * a.tokens + t) * a.kv_heads * a.group + h) * a.dk + lane + 64 * e] = acc[e] * a.scale;
+        else ((T*)a.dq)[t * a.dq_ts + h * a.dq_hs + lane + 64 * e] = from_f32<T>(acc[e] * a.scale);
+      }
   }
 }
 
@@ -107,17 +190,17 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
   using S = DqShape<T, D>;
   constexpr int IN = N::IN, W = N::W, BK = S::BK, KB = BK / 32, BUFS = S::BUFS, DS = D / 16, DB = D / 32;
   constexpr int PER_ROW = D / 8, U = BK * PER_ROW / 256;
+  constexpr bool DIRECT = FULL && IN == 1;
   __shared__ typename S::Lds lds;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
   const int heads = a.kv_heads * a.group, dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
   const float c = a.scale * LOG2E;
-  for (int64_t b = blockIdx.x; b < turns(slots, a.kv_heads); b += gridDim.x) {
-    const Turn turn = turn_of(b, slots, a.kv_heads);
-    const int kvh = turn.head;
-    if (turn.other >= slots) continue;
-    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - turn.other);
+  for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
+    const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
+    const int64_t slot = b / a.kv_heads / a.nsplit;
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - slot);
     const int64_t first = at.tile * ATTN_ROWS, rows_all = at.len * a.group;
     if (at.seq < 0 || first >= rows_all) continue;
+    const int tid = thread_here(), wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
     const int64_t tf = first / a.group;
     const int rem = (int)(first - tf * a.group), count = (int)min((int64_t)ATTN_ROWS, rows_all - first);
     auto token_of = [&](int i) { return (int)((uint32_t)(rem + i) / (uint32_t)a.group); };
@@ -127,22 +210,31 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
     const int last = (int)tf + tl, first_last = (int)tf + token_of(min(wave_first, count - 1)),
               last_last = (int)tf + token_of(min(wave_first + 31, count - 1)), end = (int)tf + token_of(count - 1) + 1;
     const int64_t t = at.t0 + tf + tl, head = (int64_t)kvh * a.group + hl;
+    const Part part = part_of(a, split, 0, end);
+    if (part.from >= part.to) continue;
     const float lse2 = a.lse[t * heads + head] * LOG2E;
-    frag q[DS][IN], go[DS][IN];
+    frag q[IN == 1 ? 1 : DS][IN], go[IN == 1 ? 1 : DS][IN], q1[DS], go1[DS];    // (planes; one plane)
     float delta = 0.0f;
     {
       const T *pq = (const T*)a.q.p + t * a.q.ts + head * a.q.hs, *pg = (const T*)a.d_o.p + t * a.d_o.ts + head * a.d_o.hs;
       const T* po = (const T*)a.out.p + t * a.out.ts + head * a.out.hs;
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
-        frags_of(load_unit<FULL>(pq, 16 * s + 8 * h, dk), q[s]);
+        frag f[IN];
+        frags_of(load_unit<FULL>(pq, 16 * s + 8 * h, dk), f);
+        if constexpr (IN == 1) q1[s] = f[0];
+        else
+          for (int i = 0; i < IN; ++i) q[s][i] = f[i];
         const Unit<T> g = load_unit<FULL>(pg, 16 * s + 8 * h, dv), o = load_unit<FULL>(po, 16 * s + 8 * h, dv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) delta = fmaf(to_f32(g.v[e]), to_f32(o.v[e]), delta);
-        frags_of(g, go[s]);
+        frags_of(g, f);
+        if constexpr (IN == 1) go1[s] = f[0];
+        else
+          for (int i = 0; i < IN; ++i) go[s][i] = f[i];
       }
       delta = add_halves(delta);
-      if (h == 0 && wave_first + lane < count) a.delta[t * heads + head] = delta;
+      if (split == 0 && h == 0 && wave_first + lane < count) a.delta[t * heads + head] = delta;
     }
     f32x16 acc[DB];
 #pragma unroll
@@ -150,7 +242,27 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
     Scale<T> scale;
 
     const T *k0 = (const T*)a.k.p + at.t0 * a.k.ts + kvh * a.k.hs, *v0 = (const T*)a.v.p + at.t0 * a.v.ts + kvh * a.v.hs;
-    Unit<T> rk[U], rv[U];
+    const DirectUnit<D> unit(tid);
+    const uint32_t ok = (uint32_t)(unit.row * (int)a.k.ts * 2 + unit.byte), ov = (uint32_t)(unit.row * (int)a.v.ts * 2 + unit.byte);
+    auto load = [&](int x, int key) {
+      const uint32_t kb = lds_byte(lds.k[x].at) + wave * 1024, vb = lds_byte(lds.v[x].at) + wave * 1024;
+      const T *kr = k0 + key * a.k.ts, *vr = v0 + key * a.v.ts;
+      if (key + BK <= end) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          lds_load16(kr + u * unit.STEP * a.k.ts, ok, kb + u * 4096);
+          lds_load16(vr + u * unit.STEP * a.v.ts, ov, vb + u * 4096);
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int row = min(unit.row + u * unit.STEP, end - 1 - key);
+          lds_load16(kr, (uint32_t)(row * (int)a.k.ts * 2 + unit.byte), kb + u * 4096);
+          lds_load16(vr, (uint32_t)(row * (int)a.v.ts * 2 + unit.byte), vb + u * 4096);
+        }
+      }
+    };
+    Unit<T> rk[DIRECT ? 1 : U], rv[DIRECT ? 1 : U];
     auto fetch = [&](int key) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -171,6 +283,9 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         f32x16 s = f32x16{}, dp = f32x16{};
+        if constexpr (IN == 1) {
+          block_products<T, D, FULL, true>(lds.k[x], lds.v[x], 32 * kb, lane, q1, go1, dk, dv, s, dp);
+        } else {
 #pragma unroll
         for (int st = 0; st < DS; ++st) {
           frag f[IN];
@@ -183,6 +298,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
             dp = mma_planes<N>(f, go[st], dp);
           }
         }
+        }
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, -lse2));
         if (key + 32 * kb + 31 > first_last) {
@@ -192,6 +308,10 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
         scale.move(s, acc);
+        if constexpr (IN == 1) {
+          block_add<T, D, FULL>(lds.k[x], 32 * kb, lane, s, dk, acc);
+          continue;
+        }
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
           float p[8];
@@ -210,34 +330,47 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
       }
     };
     __syncthreads();
-    fetch(0);
-    if constexpr (BUFS == 2) {
+    if constexpr (DIRECT) {
+      load(0, part.from);
+      direct_wait();
+      __syncthreads();
+      int x = 0;
+      for (int key = part.from; key < part.to; key += BK, x ^= 1) {
+        if (key + BK < part.to) load(x ^ 1, key + BK);
+        if (wave_on && key <= last_last) compute(x, key);
+        direct_wait();
+        __syncthreads();
+      }
+    } else if constexpr (BUFS == 2) {
+      fetch(part.from);
       stage(0);
       __syncthreads();
       int x = 0;
-      for (int key = 0; key < end; key += BK, x ^= 1) {
-        const bool more = key + BK < end;
+      for (int key = part.from; key < part.to; key += BK, x ^= 1) {
+        const bool more = key + BK < part.to;
         if (more) fetch(key + BK);
         if (wave_on && key <= last_last) compute(x, key);
         if (more) stage(x ^ 1);
         __syncthreads();
       }
     } else {
-      for (int key = 0; key < end; key += BK) {
+      fetch(part.from);
+      for (int key = part.from; key < part.to; key += BK) {
         stage(0);
         __syncthreads();
-        if (key + BK < end) fetch(key + BK);
+        if (key + BK < part.to) fetch(key + BK);
         if (wave_on && key <= last_last) compute(0, key);
         __syncthreads();
       }
     }
     const bool store = wave_first + (lane & 31) < count;
     if (__syncthreads_or(store && any_not_finite(acc))) {
-      careful_dq<T>(a, at.t0, first, count, kvh);
+      careful_dq<T>(a, at.t0, first, count, kvh, split, part);
       continue;
     }
     if (!store) continue;
     const float f = a.scale / scale.by;
+    float* sum = a.nsplit > 1 ? a.part + (((int64_t)split * a.tokens + t) * heads + head) * dk : nullptr;
     T* to = (T*)a.dq + t * a.dq_ts + head * a.dq_hs;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -245,7 +378,8 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
       for (int r = 0; r < 4; ++r) {
         const int e = 32 * d + 8 * r + 4 * h;
         const float x[4] = {acc[d][4 * r] * f, acc[d][4 * r + 1] * f, acc[d][4 * r + 2] * f, acc[d][4 * r + 3] * f};
-        store4<T>(to + e, x, dk - e);
+        if (sum) store4<float>(sum + e, x, dk - e);
+        else store4<T>(to + e, x, dk - e);
       }
   }
 }
@@ -262,18 +396,18 @@ struct DkvShape {
 };
 
 template <typename T>
-__device__ __attribute__((noinline)) void careful_dkv(AttnArgs a, int64_t t0, int64_t len, int64_t first, int count, int kvh, int nwaves) {
+__device__ __attribute__((noinline)) void careful_dkv(AttnArgs a, int64_t t0, int64_t first, int count, int kvh, int nwaves, int split, Part part) {
   const int lane = threadIdx.x & 63, heads = a.kv_heads * a.group;
   for (int r = threadIdx.x >> 6; r < count; r += nwaves) {
     const int64_t j = first + r;
     const T *k = (const T*)a.k.p + (t0 + j) * a.k.ts + kvh * a.k.hs, *v = (const T*)a.v.p + (t0 + j) * a.v.ts + kvh * a.v.hs;
     float dk[2] = {0.0f, 0.0f}, dv[2] = {0.0f, 0.0f};
     for (int64_t h = (int64_t)kvh * a.group; h < (int64_t)(kvh + 1) * a.group; ++h)
-      for (int64_t i0 = j; i0 < len; i0 += 64) {
-        const int64_t t = t0 + min(i0 + lane, len - 1);
+      for (int64_t i0 = max(j, (int64_t)part.from); i0 < part.to; i0 += 64) {
+        const int64_t t = t0 + min(i0 + lane, (int64_t)part.to - 1);
         const float p = exp2_fast((dot((const T*)a.q.p + t * a.q.ts + h * a.q.hs, k, a.dk) * a.scale - a.lse[t * heads + h]) * LOG2E);
         const float ds = p * (dot((const T*)a.d_o.p + t * a.d_o.ts + h * a.d_o.hs, v, a.dv) - a.delta[t * heads + h]);
-        for (int x = 0; x < min((int64_t)64, len - i0); ++x) {
+        for (int x = 0; x < min((int64_t)64, part.to - i0); ++x) {
           const float wp = __shfl(p, x), ws = __shfl(ds, x);
           const T *q = (const T*)a.q.p + (t0 + i0 + x) * a.q.ts + h * a.q.hs, *go = (const T*)a.d_o.p + (t0 + i0 + x) * a.d_o.ts + h * a.d_o.hs;
 #pragma unroll
@@ -287,6 +421,12 @@ __device__ __attribute__((noinline)) void careful_dkv(AttnArgs a, int64_t t0, in
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int d = lane + 64 * e;
+      if (a.nsplit > 1) {
+        const int64_t at = ((int64_t)split * a.tokens + t0 + j) * a.kv_heads + kvh;
+        if (d < a.dk) a.part_k[at * a.dk + d] = dk[e] * a.scale;
+        if (d < a.dv) a.part_v[at * a.dv + d] = dv[e];
+        continue;
+      }
       if (d < a.dk) ((T*)a.dk_)[(t0 + j) * a.dk_ts + kvh * a.dk_hs + d] = from_f32<T>(dk[e] * a.scale);
       if (d < a.dv) ((T*)a.dv_)[(t0 + j) * a.dv_ts + kvh * a.dv_hs + d] = from_f32<T>(dv[e]);
     }
@@ -303,15 +443,16 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
   const int heads = a.kv_heads * a.group, dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
   const float c = a.scale * LOG2E;
-  for (int64_t b = blockIdx.x; b < turns(slots, a.kv_heads); b += gridDim.x) {
-    const Turn turn = turn_of(b, slots, a.kv_heads);
-    const int kvh = turn.head;
-    if (turn.other >= slots) continue;
+  for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
+    const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
+    const int64_t slot = b / a.kv_heads / a.nsplit;
     // a sequence's first keys, which have the most rows, first
-    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, 1, ATTN_ROWS, turn.other);
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, 1, ATTN_ROWS, slot);
     const int64_t first64 = at.tile * ATTN_ROWS;
     if (at.seq < 0 || first64 >= at.len) continue;
     const int len = (int)at.len, first = (int)first64, count = min(ATTN_ROWS, len - first);
+    const Part part = part_of(a, split, first, len);
+    if (part.from >= part.to) continue;
     const int key = first + min(32 * wave + (lane & 31), count - 1), wave_key = first + 32 * wave;
     const bool wave_on = 32 * wave < count;
     frag k[DS][IN], v[DS][IN];
@@ -416,7 +557,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
         }
       }
     };
-    const int row0 = first / BR * BR;      // the first rows that attend these keys
+    const int row0 = part.from;      // (a multiple of BR)
     const int h0 = kvh * a.group, h1 = h0 + a.group;
     __syncthreads();
     int head = h0, row = row0, x = 0;
@@ -427,7 +568,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
     }
     while (head < h1) {
       int nh = head, nr = row + BR;
-      if (nr >= len) {
+      if (nr >= part.to) {
         nr = row0;
         ++nh;
       }
@@ -447,10 +588,11 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
     }
     const bool store = 32 * wave + (lane & 31) < count;
     if (__syncthreads_or(store && (any_not_finite(dka) || any_not_finite(dva)))) {
-      careful_dkv<T>(a, at.t0, len, first, count, kvh, 4);
+      careful_dkv<T>(a, at.t0, first, count, kvh, 4, split, part);
       continue;
     }
     if (!store) continue;
+    const int64_t sum = ((int64_t)split * a.tokens + at.t0 + key) * a.kv_heads + kvh;
     const float fk = a.scale / scale.by, fv = 1.0f / (float)(1 << N::BIAS);
     T *tk = (T*)a.dk_ + (at.t0 + key) * a.dk_ts + kvh * a.dk_hs, *tv = (T*)a.dv_ + (at.t0 + key) * a.dv_ts + kvh * a.dv_hs;
 #pragma unroll
@@ -459,9 +601,11 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
       for (int r = 0; r < 4; ++r) {
         const int e = 32 * d + 8 * r + 4 * h;
         const float y[4] = {dka[d][4 * r] * fk, dka[d][4 * r + 1] * fk, dka[d][4 * r + 2] * fk, dka[d][4 * r + 3] * fk};
-        store4<T>(tk + e, y, dk - e);
+        if (a.nsplit > 1) store4<float>(a.part_k + sum * dk + e, y, dk - e);
+        else store4<T>(tk + e, y, dk - e);
         const float z[4] = {dva[d][4 * r] * fv, dva[d][4 * r + 1] * fv, dva[d][4 * r + 2] * fv, dva[d][4 * r + 3] * fv};
-        store4<T>(tv + e, z, dv - e);
+        if (a.nsplit > 1) store4<float>(a.part_v + sum * dv + e, z, dv - e);
+        else store4<T>(tv + e, z, dv - e);
       }
   }
 }
@@ -483,7 +627,7 @@ struct PairShape {
 
 // One wave's part of a tile of 128 keys: DK: dk, else dv, of its 32.
 template <typename T, int D, bool FULL, bool DK>
-__device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, const AttnArgs& a, const SeqTile& at, int kvh) {
+__device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, const AttnArgs& a, const SeqTile& at, int kvh, int split) {
   using N = Num<T>;
   using S = PairShape<T, D>;
   constexpr int W = N::W, BR = S::BR, DS = D / 16, DB = D / 32, NT = S::NT;
@@ -494,6 +638,8 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
   const DirectUnit<D, NT> unit(tid);
   const uint32_t oq = (uint32_t)(unit.row * (int)a.q.ts * 2 + unit.byte), og = (uint32_t)(unit.row * (int)a.d_o.ts * 2 + unit.byte);
   const int len = (int)at.len, first = (int)(at.tile * S::KEYS), count = min(S::KEYS, len - first), block = 32 * (wave % PAIRS);
+  const Part part = part_of(a, split, first, len);
+  if (part.from >= part.to) return;     // (every wave)
   const int key = first + min(block + (lane & 31), count - 1), wave_key = first + block;
   const bool wave_on = block < count;
   frag k[DS], v[DK ? DS : 1];
@@ -561,64 +707,9 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
     if (tid < BR) lds.lse2[x][tid] = rs;
     else if (tid < 2 * BR) lds.delta[x][tid - BR] = rs;
   };
-  // acc += tile^T x for 32 rows of a tile and a result x of them; the second 16 rows' values are read and
-  // planes made between the first's matrix instructions
-  auto add = [&](const Tile<T, BR, D>& tile, int r0, const f32x16& x, int dim) {
-    frag w[2][W], f[2][DB][1];
-    auto ready = [&](int st) {
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-        if (FULL || 32 * d < dim) tile.cols(r0 + 16 * st, 32 * d, lane, f[st][d]);
-      float p[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = x[8 * st + e];
-      planes_of<N>(p, w[st]);
-    };
-    ready(0);
-    if (FULL) __builtin_amdgcn_sched_barrier(0);
-    ready(1);
-#pragma unroll
-    for (int st = 0; st < 2; ++st)
-#pragma unroll
-      for (int p = W - 1; p >= 0; --p)
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-          if (FULL || 32 * d < dim) acc[d] = N::mma(f[st][d][0], w[st][p], acc[d]);
-    if (FULL) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 2 * DB, 0);
-#pragma unroll
-      for (int k = 0; k < W * DB; ++k) {
-        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);
-      }
-    }
-  };
   auto compute = [&](int x, int row, int r0) {
-    // a block's rows of q are all asked for before they are used, those of do meanwhile
-    frag fq[DS][1], fg[DK ? DS : 1][1];
-#pragma unroll
-    for (int st = 0; st < DS; ++st)
-      if (FULL || 16 * st < dk) lds.q[x].rows(r0, st, lane, fq[st]);
-    if (FULL) __builtin_amdgcn_sched_barrier(0);
-    f32x16 s = f32x16{}, dp = f32x16{};
-#pragma unroll
-    for (int st = 0; st < DS; ++st) {
-      if constexpr (DK) {
-        if (FULL || 16 * st < dv) lds.go[x].rows(r0, st, lane, fg[st]);
-        if (FULL || 16 * st < dk) s = N::mma(fq[st][0], k[st], s);
-        if (FULL) __builtin_amdgcn_sched_barrier(0);
-      } else if (FULL || 16 * st < dk) {
-        if (st & 1) dp = N::mma(fq[st][0], k[st], dp);
-        else s = N::mma(fq[st][0], k[st], s);
-      }
-    }
-    if constexpr (DK) {
-#pragma unroll
-      for (int st = 0; st < DS; ++st)
-        if (FULL || 16 * st < dv) dp = N::mma(fg[st][0], v[st], dp);
-    } else {
-      s += dp;
-    }
+    f32x16 s, dp;
+    block_products<T, D, FULL, DK>(lds.q[x], lds.go[x], r0, lane, k, v, dk, dv, s, dp);
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
       const f32x4 l4 = *(const f32x4*)&lds.lse2[x][r0 + 8 * r4 + 4 * h];
@@ -640,33 +731,33 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
         for (int e = 0; e < 4; ++e) s[4 * r4 + e] *= dp[4 * r4 + e] - d4[e];
       }
       scale.move(s, acc);
-      add(lds.q[x], r0, s, dk);
+      block_add<T, D, FULL>(lds.q[x], r0, lane, s, dk, acc);
     } else {
       if (N::BIAS) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[r] *= (float)(1 << N::BIAS);
       }
-      add(lds.go[x], r0, s, dv);
+      block_add<T, D, FULL>(lds.go[x], r0, lane, s, dv, acc);
     }
   };
   const int h0 = kvh * a.group, h1 = h0 + a.group;      // rows from the tile's first key on attend it
   __syncthreads();
   if (tid == 0) lds.bad = 0;
-  int head = h0, row = first, x = 0;
+  int head = h0, row = part.from, x = 0;
   fetch(0, head, row);
   stage(0);
   direct_wait();
   __syncthreads();
   while (head < h1) {
     int nh = head, nr = row + BR;
-    if (nr >= len) {
-      nr = first;
+    if (nr >= part.to) {
+      nr = part.from;
       ++nh;
     }
     if (nh < h1) fetch(x ^ 1, nh, nr);
 #pragma unroll 1
     for (int r0 = 0; r0 < BR; r0 += 32)
-      if (wave_on && row + r0 + 31 >= wave_key && row + r0 < len) compute(x, row + r0, r0);
+      if (wave_on && row + r0 + 31 >= wave_key && row + r0 < part.to) compute(x, row + r0, r0);
     if (nh < h1) stage(x ^ 1);
     direct_wait();
     __syncthreads();
@@ -678,12 +769,14 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
   if (store && any_not_finite(acc)) lds.bad = 1;
   __syncthreads();
   if (lds.bad) {
-    if (!DK) careful_dkv<T>(a, at.t0, len, first, count, kvh, PAIRS);
+    if (!DK) careful_dkv<T>(a, at.t0, first, count, kvh, PAIRS, split, part);
     return;
   }
   if (!store) return;
   const float f = DK ? a.scale / scale.by : 1.0f / (float)(1 << N::BIAS);
   const int dim = DK ? dk : dv;
+  const int64_t sum = ((int64_t)split * a.tokens + at.t0 + key) * a.kv_heads + kvh;
+  float* parts = a.nsplit == 1 ? nullptr : DK ? a.part_k + sum * dk : a.part_v + sum * dv;
   T* to = DK ? (T*)a.dk_ + (at.t0 + key) * a.dk_ts + kvh * a.dk_hs : (T*)a.dv_ + (at.t0 + key) * a.dv_ts + kvh * a.dv_hs;
 #pragma unroll
   for (int d = 0; d < DB; ++d)
@@ -691,28 +784,28 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
     for (int r = 0; r < 4; ++r) {
       const int e = 32 * d + 8 * r + 4 * h;
       const float y[4] = {acc[d][4 * r] * f, acc[d][4 * r + 1] * f, acc[d][4 * r + 2] * f, acc[d][4 * r + 3] * f};
-      store4<T>(to + e, y, dim - e);
+      if (parts) store4<float>(parts + e, y, dim - e);
+      else store4<T>(to + e, y, dim - e);
     }
 }
 
 template <typename T, int D, bool FULL>
 __global__ __launch_bounds__(128 * PAIRS, 2) void attn_dkv_pairs(AttnArgs a, int64_t slots) {
   __shared__ typename PairShape<T, D>::Lds lds;
-  for (int64_t b = blockIdx.x; b < turns(slots, a.kv_heads); b += gridDim.x) {
-    const Turn turn = turn_of(b, slots, a.kv_heads);
-    if (turn.other >= slots) continue;
-    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, 1, PairShape<T, D>::KEYS, turn.other);
+  for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
+    const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, 1, PairShape<T, D>::KEYS, b / a.kv_heads / a.nsplit);
     if (at.seq < 0 || at.tile * PairShape<T, D>::KEYS >= at.len) continue;
     // (both parts pass the same barriers)
-    if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >= PAIRS) pair_tile<T, D, FULL, true>(lds, a, at, turn.head);
-    else pair_tile<T, D, FULL, false>(lds, a, at, turn.head);
+    if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >= PAIRS) pair_tile<T, D, FULL, true>(lds, a, at, kvh, split);
+    else pair_tile<T, D, FULL, false>(lds, a, at, kvh, split);
   }
 }
 
 template <typename T, int D, bool FULL>
 void launch(const AttnArgs& a, hipStream_t s) {
   const int64_t rows = a.tokens * a.group / ATTN_ROWS + a.seqs, keys = a.tokens / (Num<T>::IN == 1 ? PairShape<T, D>::KEYS : ATTN_ROWS) + a.seqs;
-  auto grid = [&](int64_t slots) { return dim3((uint32_t)std::min<int64_t>(turns(slots, a.kv_heads), 1 << 22)); };
+  auto grid = [&](int64_t slots) { return dim3((uint32_t)std::min<int64_t>(slots * a.nsplit * a.kv_heads, 1 << 22)); };
   launch_kernel(attn_dq<T, D, FULL>, grid(rows), dim3(256), 0, s, a, rows);
   if constexpr (Num<T>::IN == 1) launch_kernel(attn_dkv_pairs<T, D, FULL>, grid(keys), dim3(PairShape<T, D>::NT), 0, s, a, keys);
   else launch_kernel(attn_dkv<T, D, FULL>, grid(keys), dim3(256), 0, s, a, keys);
@@ -724,7 +817,46 @@ void bwd(const AttnArgs& a, hipStream_t s) {
   else f.full ? launch<T, 128, true>(a, s) : launch<T, 128, false>(a, s);
 }
 
+// Sums over the parts: a wave takes a token's heads of dq, dk and dv in turn.  Token i of its sequence has parts of
+// dq up to its own position, and of dk and dv from there on.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_sum(AttnArgs a) {
+  const int lane = threadIdx.x & 63, heads = a.kv_heads * a.group, all = heads + 2 * a.kv_heads;
+  const int64_t t0 = a.cu ? seq_start(a.cu, 0, a.tokens) : 0, t1 = a.cu ? seq_start(a.cu, a.seqs, a.tokens) : a.tokens;
+  for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < a.tokens * all; i += (int64_t)gridDim.x * 4) {
+    const int64_t t = i / all;
+    int h = (int)(i - t * all);
+    if (t < t0 || t >= t1) continue;
+    const SeqTile seq = find_token(a.cu, a.seqs, a.tokens, t);
+    const int64_t at = t - seq.t0;
+    const int mine = (int)min(at / a.part_len, (int64_t)a.nsplit - 1), last = (int)min((seq.len - 1) / a.part_len, (int64_t)a.nsplit - 1);
+    auto sum = [&](const float* part, int n, int dim, int from, int to, void* out, int64_t ts, int64_t hs) {
+      const int64_t step = a.tokens * n * dim;
+      const float* p = part + (t * n + h) * dim;
+      for (int d = lane; d < dim; d += 64) {
+        float x = 0.0f;
+        for (int s = from; s <= to; ++s) x += p[s * step + d];
+        ((T*)out)[t * ts + h * hs + d] = from_f32<T>(x);
+      }
+    };
+    if (h < heads) sum(a.part, heads, a.dk, 0, mine, a.dq, a.dq_ts, a.dq_hs);
+    else if ((h -= heads) < a.kv_heads) sum(a.part_k, a.kv_heads, a.dk, mine, last, a.dk_, a.dk_ts, a.dk_hs);
+    else {
+      h -= a.kv_heads;
+      sum(a.part_v, a.kv_heads, a.dv, mine, last, a.dv_, a.dv_ts, a.dv_hs);
+    }
+  }
+}
+
 }  // namespace
+
+void launch_attn_sum(const AttnArgs& a, int dtype, hipStream_t s) {
+  const int64_t rows = a.tokens * (a.kv_heads * (a.group + 2));
+  const dim3 grid((uint32_t)std::min<int64_t>((rows + 3) / 4, 1 << 22));
+  if (dtype == PC_DTYPE_BF16) launch_kernel(attn_sum<bf16>, grid, dim3(256), 0, s, a);
+  else if (dtype == PC_DTYPE_F16) launch_kernel(attn_sum<f16>, grid, dim3(256), 0, s, a);
+  else launch_kernel(attn_sum<float>, grid, dim3(256), 0, s, a);
+}
 
 void launch_attn_bwd(const AttnArgs& a, int dtype, hipStream_t s) {
   if (dtype == PC_DTYPE_BF16) bwd<bf16>(a, s);

@@ -95,25 +95,16 @@ __device__ __forceinline__ void join_cache(const AttnArgs& a, const Work<T>& w, 
   copy(w.keys.v, a.v.ts, a.pages.v, a.dv);
 }
 
-// A part without keys of these rows.
-template <typename T>
-__device__ __forceinline__ void no_keys(const Work<T>& w) {
-  for (int i = threadIdx.x; i < w.rows.count; i += 256)
-    w.out.stat[(int64_t)w.rows.token(i) * w.out.heads + w.rows.head(i)] = float2{-INFINITY, 0.0f};
-}
-
 template <typename T, int D, bool FULL>
 __global__ __launch_bounds__(256, 2) void attn_cached_many(AttnArgs a, int64_t slots, int part_len) {
   __shared__ typename FwdShape<T, D>::Lds lds;
-  const int64_t works = slots * a.nsplit;
-  for (int64_t b = blockIdx.x; b < turns(works, a.kv_heads); b += gridDim.x) {
-    const Turn turn = turn_of(b, works, a.kv_heads);
-    if (turn.other >= works) continue;
-    const int kvh = turn.head, split = (int)(turn.other % a.nsplit);
-    const Work<T> w = find_work<T>(a, slots - 1 - turn.other / a.nsplit, kvh, split, ATTN_ROWS, part_len);
+  const int64_t per = (int64_t)a.kv_heads * a.nsplit;
+  for (int64_t b = blockIdx.x; b < slots * per; b += gridDim.x) {
+    const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
+    const Work<T> w = find_work<T>(a, slots - 1 - b / per, kvh, split, ATTN_ROWS, part_len);
     if (w.rows.count == 0) continue;
     if (split == 0) join_cache(a, w, kvh);
-    if (w.key0 >= w.key1) no_keys(w);
+    if (w.key0 >= w.key1) no_keys(w.rows, w.out);
     else
       attend_tile<T, D, FULL, true>(lds, w.keys, w.rows, w.out, a.dk, a.dv, fabsf(a.scale) * LOG2E, a.scale < 0.0f, w.key0, w.key1);
   }
@@ -147,18 +138,16 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(
   constexpr int IN = N::IN, W = N::W, DS = D / 16, DB = D / 32, PER_ROW = D / 8, U = 32 * PER_ROW / 64;
   __shared__ typename FewShape<T, D>::Lds lds;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
-  const int64_t works = slots * a.nsplit;
+  const int64_t per = (int64_t)a.kv_heads * a.nsplit;
   const int dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
   const float c = fabsf(a.scale) * LOG2E;
-  for (int64_t b = blockIdx.x; b < turns(works, a.kv_heads); b += gridDim.x) {
-    const Turn turn = turn_of(b, works, a.kv_heads);
-    if (turn.other >= works) continue;
-    const int kvh = turn.head, split = (int)(turn.other % a.nsplit);
-    const Work<T> w = find_work<T>(a, turn.other / a.nsplit, kvh, split, ATTN_FEW_ROWS, part_len);
+  for (int64_t b = blockIdx.x; b < slots * per; b += gridDim.x) {
+    const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
+    const Work<T> w = find_work<T>(a, b / per, kvh, split, ATTN_FEW_ROWS, part_len);
     if (w.rows.count == 0) continue;
     if (split == 0) join_cache(a, w, kvh);
     if (w.key0 >= w.key1) {
-      no_keys(w);
+      no_keys(w.rows, w.out);
       continue;
     }
     const int mine = min(lane & 31, w.rows.count - 1), last = w.rows.last(mine), first_last = w.rows.last(0);
@@ -342,13 +331,14 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       if (lane + 64 * e < a.dv) ((T*)a.o)[t * a.o_ts + h * a.o_hs + lane + 64 * e] = from_f32<T>(acc[e] / l);
+    if (a.lse && lane == 0) a.lse[i] = (top + __log2f(l)) * LN2;
   }
 }
 
 template <typename T, int D, bool FULL>
 void launch(const AttnArgs& a, bool few, hipStream_t s) {
   const int64_t slots = a.tokens * a.group / (few ? ATTN_FEW_ROWS : ATTN_ROWS) + a.seqs;
-  const dim3 grid((uint32_t)std::min<int64_t>(turns(slots * a.nsplit, a.kv_heads), 1 << 23));
+  const dim3 grid((uint32_t)std::min<int64_t>(slots * a.kv_heads * a.nsplit, 1 << 23));
   if (few) launch_kernel(attn_cached_few<T, D, FULL>, grid, dim3(256), 0, s, a, slots, a.part_len);
   else launch_kernel(attn_cached_many<T, D, FULL>, grid, dim3(256), 0, s, a, slots, a.part_len);
 }

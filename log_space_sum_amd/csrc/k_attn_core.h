@@ -88,6 +88,13 @@ __device__ __forceinline__ void put_stat(const RowOut& out, int t, int h, float 
   else if (out.lse) out.lse[at] = (m + __log2f(l)) * LN2;
 }
 
+// A part without keys of these rows.
+template <typename T>
+__device__ __forceinline__ void no_keys(const Rows<T>& rows, const RowOut& out) {
+  for (int i = threadIdx.x; i < rows.count; i += 256)
+    out.stat[(int64_t)rows.token(i) * out.heads + rows.head(i)] = float2{-INFINITY, 0.0f};
+}
+
 // One row after the other in plain float32: the path of a tile whose results are not
 // finite, since there a weight of 0 met an infinity or a NaN that the row may not
 // attend, or planes of infinities gave NaN.  Waves take rows in turn.

@@ -14,12 +14,10 @@ template <typename T, int D, bool FULL>
 __global__ __launch_bounds__(256, 2) void attn_fwd(AttnArgs a, int64_t slots) {
   __shared__ typename FwdShape<T, D>::Lds lds;
   const int heads = a.kv_heads * a.group;
-  for (int64_t b = blockIdx.x; b < turns(slots, a.kv_heads); b += gridDim.x) {
-    const Turn turn = turn_of(b, slots, a.kv_heads);
-    const int kvh = turn.head;
-    if (turn.other >= slots) continue;
+  for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
+    const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
     // the last tiles, which have the most keys, first
-    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - turn.other);
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - b / a.kv_heads / a.nsplit);
     const int64_t first = at.tile * ATTN_ROWS, rows_all = at.len * a.group;
     if (at.seq < 0 || first >= rows_all) continue;
     const int64_t tf = first / a.group, t = at.t0 + tf;
@@ -43,15 +41,25 @@ __global__ __launch_bounds__(256, 2) void attn_fwd(AttnArgs a, int64_t slots) {
     out.o_hs = a.o_hs;
     out.heads = heads;
     out.lse = a.lse ? a.lse + t * heads + kvh * a.group : nullptr;
-    attend_tile<T, D, FULL, false>(lds, keys, rows, out, a.dk, a.dv, fabsf(a.scale) * LOG2E, a.scale < 0.0f, 0,
-                                   rows.last(rows.count - 1) + 1);
+    const int end = rows.last(rows.count - 1) + 1;
+    int key0 = 0, key1 = end;
+    if (a.nsplit > 1) {
+      const int64_t place = ((int64_t)split * a.tokens + t) * heads + kvh * a.group;
+      out.part = a.part + place * a.dv;
+      out.stat = a.stat + place;
+      key0 = (int)min((int64_t)split * a.part_len, (int64_t)end);
+      if (split + 1 < a.nsplit) key1 = (int)min((int64_t)(split + 1) * a.part_len, (int64_t)end);
+    }
+    if (key0 >= key1) no_keys(rows, out);
+    else
+      attend_tile<T, D, FULL, false>(lds, keys, rows, out, a.dk, a.dv, fabsf(a.scale) * LOG2E, a.scale < 0.0f, key0, key1);
   }
 }
 
 template <typename T>
 void fwd(const AttnArgs& a, hipStream_t s) {
   const int64_t slots = a.tokens * a.group / ATTN_ROWS + a.seqs;
-  const dim3 grid((uint32_t)std::min<int64_t>(turns(slots, a.kv_heads), 1 << 23));
+  const dim3 grid((uint32_t)std::min<int64_t>(slots * a.nsplit * a.kv_heads, 1 << 23));
   const Fit f = fit_of<T>(a, false);
   auto go = [&](auto kernel) { launch_kernel(kernel, grid, dim3(256), 0, s, a, slots); };
   if (f.D == 64) f.full ? go(attn_fwd<T, 64, true>) : go(attn_fwd<T, 64, false>);

@@ -157,9 +157,12 @@ struct AttnArgs {
   int64_t o_ts, o_hs;
   float* lse;           // [tokens, heads]; forward: nullable output
   AttnPages pages;      // cached: past and new tokens
-  int32_t nsplit, part_len;   // cached: parts of part_len keys; nsplit > 1: results through part and stat
-  float* part;          // [nsplit, tokens, heads, dv]
+  // nsplit > 1: the keys are cut at multiples of part_len, and parts' results are joined from part and stat (backward: the
+  // keys of dq, and the rows of dk, dv; sums)
+  int32_t nsplit, part_len;
+  float* part;          // [nsplit, tokens, heads, dv]; backward: [nsplit, tokens, heads, dk]
   float2* stat;         // [nsplit, tokens, heads]
+  float *part_k, *part_v;   // backward: [nsplit, tokens, kv_heads, dk], [.., dv]
   // backward
   AttnTensor out, d_o;
   void *dq, *dk_, *dv_;
@@ -170,11 +173,13 @@ constexpr int ATTN_MAX_DIM = 128;
 constexpr int ATTN_ROWS = 128;         // rows of a workgroup, and keys of one in the backward pass
 constexpr int ATTN_FEW_ROWS = 32;      // rows of a workgroup whose waves share them (cached)
 constexpr int ATTN_MAX_SPLIT = 64;     // parts of the keys
+constexpr int ATTN_PART_LEAST = 256, ATTN_PARTS_AIM = 512;   // keys of a part; workgroups below which keys are cut
 constexpr int ROTARY_MAX_DIM = 256;
 void launch_attn_fwd(const AttnArgs& a, int dtype, hipStream_t s);
 void launch_attn_bwd(const AttnArgs& a, int dtype, hipStream_t s);
 void launch_attn_cached(const AttnArgs& a, int dtype, bool few, hipStream_t s);
-void launch_attn_join(const AttnArgs& a, int dtype, hipStream_t s);
+void launch_attn_join(const AttnArgs& a, int dtype, hipStream_t s);   // the parts of fwd's and cached's results
+void launch_attn_sum(const AttnArgs& a, int dtype, hipStream_t s);    // of bwd's
 
 // ---- heads' norm and rotation --------------------------------------------------
 struct RotaryArgs {

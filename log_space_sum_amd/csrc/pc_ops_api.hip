@@ -229,6 +229,7 @@ void check_attn_sizes(const pc_attention* d) {
                                  std::to_string(ATTN_MAX_DIM) + ")");
   need(d->num_tokens >= 0 && d->num_tokens <= 1 << 30, "num_tokens must be in [0, 2^30]");
   need(d->num_seqs >= 0 && d->num_seqs <= 1 << 24, "num_seqs must be in [0, 2^24]");
+  need(d->max_seqlen >= 0 && d->max_length >= 0, "max_seqlen and max_length must be at least 0");
 }
 
 void check_attn(const pc_attention* d, bool cached = false) {
@@ -264,12 +265,49 @@ AttnArgs attn_base(const pc_attention* d) {
   return a;
 }
 
+// Parts of whole sequences' keys (and, for dk and dv, rows), where rows, heads and
+// sequences are too few to fill the card: a tile of 128 rows is a chain of key
+// tiles, 1 to 5 us each.  A part costs its results, written and read once in float32, and a launch that joins them.
+struct AttnSplit {
+  int nsplit, part_len;
+};
+AttnSplit attn_split(const pc_attention* d) {
+  const int64_t group = d->heads / d->kv_heads, tokens = std::max<int64_t>(1, d->num_tokens);
+  const int64_t longest = std::max<int64_t>(1, std::min(d->max_seqlen, tokens));
+  const int64_t full = std::min<int64_t>(std::max(1, d->num_seqs), (tokens + longest - 1) / longest);
+  const int64_t works = full * ((longest * group + ATTN_ROWS - 1) / ATTN_ROWS) * d->kv_heads;
+  int64_t len = std::max<int64_t>(ATTN_PART_LEAST, (longest * works + ATTN_PARTS_AIM - 1) / ATTN_PARTS_AIM);
+  len = round_up(std::max(len, (longest + ATTN_MAX_SPLIT - 1) / ATTN_MAX_SPLIT), 128);
+  return {(int)((longest + len - 1) / len), (int)std::min<int64_t>(len, INT_MAX)};
+}
+struct AttnWs {
+  size_t part = 0, stat = 0, part_k = 0, part_v = 0, delta = 0, total = 0;
+};
+AttnWs attn_ws(const pc_attention* d, bool backward) {
+  AttnWs w;
+  auto take = [&](size_t bytes) {
+    const size_t at = w.total;
+    w.total += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t n = attn_split(d).nsplit, tokens = (size_t)d->num_tokens;
+  if (backward) w.delta = take(tokens * d->heads * sizeof(float));
+  if (n > 1) {
+    w.part = take(n * tokens * d->heads * (backward ? d->dim_k : d->dim_v) * sizeof(float));
+    if (!backward) w.stat = take(n * tokens * d->heads * sizeof(float2));
+    else {
+      w.part_k = take(n * tokens * d->kv_heads * d->dim_k * sizeof(float));
+      w.part_v = take(n * tokens * d->kv_heads * d->dim_v * sizeof(float));
+    }
+  }
+  return w;
+}
+
 void check_pages(const pc_attention* d) {
   check_attn_sizes(d);
   need(d->page_size >= 1, "page_size must be at least 1");
   need(d->num_pages >= 0 && d->max_pages >= 0, "num_pages and max_pages must be at least 0");
   need((int64_t)d->max_pages * d->page_size + d->num_tokens <= INT_MAX - (1 << 16), "2^31 positions or more");
-  need(d->max_seqlen >= 0 && d->max_length >= 0, "max_seqlen and max_length must be at least 0");
 }
 
 // How new tokens meet a cache.  Rows are the new tokens of a sequence times the
@@ -746,7 +784,7 @@ int pc_attention_workspace_bytes(const pc_attention* d, int backward, size_t* by
   return guarded([&] {
     need(bytes, "null bytes");
     check_attn_sizes(d);
-    *bytes = backward ? (size_t)d->num_tokens * d->heads * sizeof(float) : 0;
+    *bytes = attn_ws(d, backward != 0).total;
   });
 }
 
@@ -755,12 +793,24 @@ int pc_attention_forward(int device, const pc_attention* d, void* ws, size_t ws_
     check_device(device);
     check_attn(d);
     check_out(d, d->o, d->heads, d->dim_v, "o", false);
-    (void)ws;
-    (void)ws_bytes;
+    const AttnWs w = attn_ws(d, false);
+    if (ws) check_ws(ws, ws_bytes, w.total);
     if (d->num_seqs == 0 || d->num_tokens == 0) return;
+    AttnArgs a = attn_base(d);
+    if (ws) {       // (without a workspace the keys are not cut)
+      const AttnSplit sp = attn_split(d);
+      a.nsplit = sp.nsplit;
+      a.part_len = sp.part_len;
+      a.part = (float*)((char*)ws + w.part);
+      a.stat = (float2*)((char*)ws + w.stat);
+    }
     DeviceGuard dg(device);
-    launch_attn_fwd(attn_base(d), d->dtype, (hipStream_t)stream);
+    launch_attn_fwd(a, d->dtype, (hipStream_t)stream);
     check_launch();
+    if (a.nsplit > 1) {
+      launch_attn_join(a, d->dtype, (hipStream_t)stream);
+      check_launch();
+    }
   });
 }
 
@@ -774,10 +824,17 @@ int pc_attention_backward(int device, const pc_attention* d, void* ws, size_t ws
     check_out(d, d->d_q, d->heads, d->dim_k, "d_q", false);
     check_out(d, d->d_k, d->kv_heads, d->dim_k, "d_k", false);
     check_out(d, d->d_v, d->kv_heads, d->dim_v, "d_v", false);
-    check_ws(ws, ws_bytes, (size_t)d->num_tokens * d->heads * sizeof(float));
+    const AttnWs w = attn_ws(d, true);
+    check_ws(ws, ws_bytes, w.total);
     if (d->num_seqs == 0 || d->num_tokens == 0) return;
     DeviceGuard dg(device);
     AttnArgs a = attn_base(d);
+    const AttnSplit sp = attn_split(d);
+    a.nsplit = sp.nsplit;
+    a.part_len = sp.part_len;
+    a.part = (float*)((char*)ws + w.part);
+    a.part_k = (float*)((char*)ws + w.part_k);
+    a.part_v = (float*)((char*)ws + w.part_v);
     a.out = attn_tensor(d->o);
     a.d_o = attn_tensor(d->d_o);
     a.dq = d->d_q.data;
@@ -789,9 +846,13 @@ int pc_attention_backward(int device, const pc_attention* d, void* ws, size_t ws
     a.dv_ = d->d_v.data;
     a.dv_ts = d->d_v.token_stride;
     a.dv_hs = d->d_v.head_stride;
-    a.delta = (float*)ws;
+    a.delta = (float*)((char*)ws + w.delta);
     launch_attn_bwd(a, d->dtype, (hipStream_t)stream);
     check_launch();
+    if (a.nsplit > 1) {
+      launch_attn_sum(a, d->dtype, (hipStream_t)stream);
+      check_launch();
+    }
   });
 }
 

@@ -245,7 +245,8 @@ def _check_backward(do, q, k, v, o, lse, grads, cu, scale, typ):
 
 
 SHAPES = [([1], 1, 1, 64, 64), ([130], 2, 1, 64, 64), ([5, 0, 200, 33], 4, 2, 128, 128), ([70, 300], 6, 3, 48, 80), ([129, 1, 1], 3, 1, 7, 33),
-          ([31, 32, 33, 64, 65, 127, 128], 2, 2, 16, 128), ([20] * 70, 5, 1, 24, 40), ([257], 33, 1, 32, 8), ([40], 160, 1, 8, 1), ([600], 1, 1, 1, 128)]
+          ([31, 32, 33, 64, 65, 127, 128], 2, 2, 16, 128), ([20] * 70, 5, 1, 24, 40), ([257], 33, 1, 32, 8), ([40], 160, 1, 8, 1), ([600], 1, 1, 1, 128), ([600, 5, 400], 2, 1, 64, 64),
+          ([520, 256], 3, 1, 128, 96)]
 
 
 @pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
@@ -272,8 +273,18 @@ def test_attention(lens, H, K, dk, dv, typ):
     # the same bits again, and without lse
     first = [t.clone() for t in (o, *grads)]
     L.pc_attention_forward(q, k, v, o, None, ints(cu))
-    L.pc_attention_backward(do, q, k, v, o, lse, *grads, ints(cu), 1, ws=ws)
+    L.pc_attention_backward(do, q, k, v, o, lse, *grads, ints(cu), ws=ws)
     assert all(torch.equal(a, b) for a, b in zip(first, (o, *grads)))
+    # keys in parts where there is a workspace, and not cut where the bound of the lengths says so
+    o.fill_(7.0), lse.fill_(7.0)
+    L.pc_attention_forward(q, k, v, o, lse, ints(cu), ws=L.attention_workspace(q, k, v, ints(cu)))
+    _check_forward(q, k, v, o, lse, cu, dk ** -0.5, typ)
+    for t in grads:
+        t.fill_(7.0)
+    L.pc_attention_backward(do, q, k, v, o, lse, *grads, ints(cu), 1, ws=ws)
+    _check_backward(do, q, k, v, o, lse, grads, cu, dk ** -0.5, typ)
+    for t in (o, lse, *grads):
+        assert (t[:3] == 7).all() and (t[cu[-1]:] == 7).all()
 
 
 @pytest.mark.parametrize("typ", ["bf16", "f16"])
@@ -372,7 +383,7 @@ def test_attention_keeps_what_is_not_finite_in_its_place(typ, what, value):
 
     def run():
         o, lse = torch.empty_like(do), torch.empty((300, H), device=DEV)
-        L.pc_attention_forward(q, k, v, o, lse, ints(cu))
+        L.pc_attention_forward(q, k, v, o, lse, ints(cu), ws=L.attention_workspace(q, k, v, ints(cu)))
         grads = [torch.empty_like(t) for t in (q, k, v)]
         L.pc_attention_backward(do, q, k, v, o, lse, *grads, ints(cu), ws=L.attention_workspace(q, k, v, ints(cu), backward=True))
         return [get(t) for t in (o, lse[..., None], *grads)]
