@@ -204,11 +204,14 @@ struct Tile {
 template <int D, int NT = 256>
 struct DirectUnit {
   static constexpr int STEP = NT / (D / 8);
-  int row, byte;     // of the first unit: row of the tile, byte of the row
+  int row, chunk;    // of the first unit
   __device__ __forceinline__ DirectUnit(int tid) {
     row = tid / (D / 8);
-    byte = ((tid % (D / 8)) ^ Tile<bf16, 64, D>::turn(row)) * 16;
+    chunk = (tid % (D / 8)) ^ Tile<bf16, 64, D>::turn(row);
   }
+  // The unit's byte of a row of `dim` elements.  Chunks behind it hold the first one: they meet zeros in a contraction,
+  // or results that are not stored.
+  __device__ __forceinline__ int byte(int dim) const { return 8 * chunk < dim ? 16 * chunk : 0; }
 };
 static_assert(DirectUnit<128>::STEP % 16 == 0 && DirectUnit<64>::STEP % 16 == 0, "turns repeat every 16 rows");
 __device__ __forceinline__ uint32_t lds_byte(const void* p) {
@@ -281,24 +284,35 @@ __device__ __forceinline__ void store4(T* to, const float (&x)[4], int have) {
 inline bool direct_rows(const void* p, int64_t ts, int64_t hs) {
   return ((uintptr_t)p | (uintptr_t)(ts * 2) | (uintptr_t)(hs * 2)) % 16 == 0 && ts < (1 << 23);
 }
-// The tile's width D of a call, and whether it is both dims' and (16-bit types) keys and values, those of the cache, and
-// rows can be loaded directly.
+// How a call meets the kernels: tiles of width D; FULL: both dims are D (and 16-bit rows can be loaded directly);
+// DIRECT: 16-bit rows can be, dims are multiples of 8; ANY.
+enum FitMode { ANY, DIRECT, FULL };
 struct Fit {
   int D;
-  bool full;
+  FitMode mode;
 };
 template <typename T>
 Fit fit_of(const AttnArgs& a, bool cache, bool rows = false) {
   const int big = a.dk > a.dv ? a.dk : a.dv, D = big <= 64 ? 64 : 128;
-  bool full = a.dk == D && a.dv == D;
-  if (sizeof(T) == 2) {
-    full = full && direct_rows(a.k.p, a.k.ts, a.k.hs) && direct_rows(a.v.p, a.v.ts, a.v.hs);
-    if (rows) full = full && direct_rows(a.q.p, a.q.ts, a.q.hs) && direct_rows(a.d_o.p, a.d_o.ts, a.d_o.hs);
-    if (cache)
-      for (const AttnCache* c : {&a.pages.k, &a.pages.v})
-        full = full && direct_rows(c->p, c->token_stride, c->head_stride) && c->page_stride % 8 == 0;
-  }
-  return {D, full};
+  const bool full = a.dk == D && a.dv == D;
+  if (sizeof(T) != 2) return {D, full ? FULL : ANY};
+  bool direct = a.dk % 8 == 0 && a.dv % 8 == 0 && direct_rows(a.k.p, a.k.ts, a.k.hs) && direct_rows(a.v.p, a.v.ts, a.v.hs);
+  if (rows) direct = direct && direct_rows(a.q.p, a.q.ts, a.q.hs) && direct_rows(a.d_o.p, a.d_o.ts, a.d_o.hs);
+  if (cache)
+    for (const AttnCache* c : {&a.pages.k, &a.pages.v})
+      direct = direct && direct_rows(c->p, c->token_stride, c->head_stride) && c->page_stride % 8 == 0;
+  return {D, direct ? (full ? FULL : DIRECT) : ANY};
+}
+// f(D, mode) as constants.
+template <typename T, typename F>
+void by_fit(const Fit& fit, F&& f) {
+  auto mode = [&](auto d) {
+    if (fit.mode == FULL) f(d, std::integral_constant<FitMode, FULL>{});
+    else if (fit.mode == ANY) f(d, std::integral_constant<FitMode, ANY>{});
+    else if constexpr (sizeof(T) == 2) f(d, std::integral_constant<FitMode, DIRECT>{});
+  };
+  if (fit.D == 64) mode(std::integral_constant<int, 64>{});
+  else mode(std::integral_constant<int, 128>{});
 }
 
 // ---- sequences -----------------------------------------------------------------------

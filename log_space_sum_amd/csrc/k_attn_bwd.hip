@@ -184,13 +184,13 @@ __device__ __attribute__((noinline)) void careful_dq(AttnArgs a, int64_t t0, int
   }
 }
 
-template <typename T, int D, bool FULL>
+template <typename T, int D, FitMode MODE>
 __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs a, int64_t slots) {
   using N = Num<T>;
   using S = DqShape<T, D>;
   constexpr int IN = N::IN, W = N::W, BK = S::BK, KB = BK / 32, BUFS = S::BUFS, DS = D / 16, DB = D / 32;
   constexpr int PER_ROW = D / 8, U = BK * PER_ROW / 256;
-  constexpr bool DIRECT = FULL && IN == 1;
+  constexpr bool FULL = MODE == pc::FULL, DIRECT = IN == 1 && MODE != ANY;
   __shared__ typename S::Lds lds;
   const int heads = a.kv_heads * a.group, dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
   const float c = a.scale * LOG2E;
@@ -243,7 +243,8 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
 
     const T *k0 = (const T*)a.k.p + at.t0 * a.k.ts + kvh * a.k.hs, *v0 = (const T*)a.v.p + at.t0 * a.v.ts + kvh * a.v.hs;
     const DirectUnit<D> unit(tid);
-    const uint32_t ok = (uint32_t)(unit.row * (int)a.k.ts * 2 + unit.byte), ov = (uint32_t)(unit.row * (int)a.v.ts * 2 + unit.byte);
+    const int kbyte = unit.byte(dk), vbyte = unit.byte(dv);
+    const uint32_t ok = (uint32_t)(unit.row * (int)a.k.ts * 2 + kbyte), ov = (uint32_t)(unit.row * (int)a.v.ts * 2 + vbyte);
     auto load = [&](int x, int key) {
       const uint32_t kb = lds_byte(lds.k[x].at) + wave * 1024, vb = lds_byte(lds.v[x].at) + wave * 1024;
       const T *kr = k0 + key * a.k.ts, *vr = v0 + key * a.v.ts;
@@ -257,8 +258,8 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int row = min(unit.row + u * unit.STEP, end - 1 - key);
-          lds_load16(kr, (uint32_t)(row * (int)a.k.ts * 2 + unit.byte), kb + u * 4096);
-          lds_load16(vr, (uint32_t)(row * (int)a.v.ts * 2 + unit.byte), vb + u * 4096);
+          lds_load16(kr, (uint32_t)(row * (int)a.k.ts * 2 + kbyte), kb + u * 4096);
+          lds_load16(vr, (uint32_t)(row * (int)a.v.ts * 2 + vbyte), vb + u * 4096);
         }
       }
     };
@@ -433,9 +434,10 @@ __device__ __attribute__((noinline)) void careful_dkv(AttnArgs a, int64_t t0, in
   }
 }
 
-template <typename T, int D, bool FULL>
+template <typename T, int D, FitMode MODE>
 __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
   using N = Num<T>;
+  constexpr bool FULL = MODE == pc::FULL;
   using S = DkvShape<T, D>;
   constexpr int IN = N::IN, W = N::W, BR = S::BR, BUFS = S::BUFS, DS = D / 16, DB = D / 32;
   constexpr int PER_ROW = D / 8, U = BR * PER_ROW / 256;
@@ -626,9 +628,10 @@ struct PairShape {
 };
 
 // One wave's part of a tile of 128 keys: DK: dk, else dv, of its 32.
-template <typename T, int D, bool FULL, bool DK>
+template <typename T, int D, FitMode MODE, bool DK>
 __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, const AttnArgs& a, const SeqTile& at, int kvh, int split) {
   using N = Num<T>;
+  constexpr bool FULL = MODE == pc::FULL;
   using S = PairShape<T, D>;
   constexpr int W = N::W, BR = S::BR, DS = D / 16, DB = D / 32, NT = S::NT;
   constexpr int PER_ROW = D / 8, U = BR * PER_ROW / NT;
@@ -636,7 +639,8 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
   const int heads = a.kv_heads * a.group, dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
   const float c = a.scale * LOG2E;
   const DirectUnit<D, NT> unit(tid);
-  const uint32_t oq = (uint32_t)(unit.row * (int)a.q.ts * 2 + unit.byte), og = (uint32_t)(unit.row * (int)a.d_o.ts * 2 + unit.byte);
+  const int qbyte = unit.byte(dk), gbyte = unit.byte(dv);
+  const uint32_t oq = (uint32_t)(unit.row * (int)a.q.ts * 2 + qbyte), og = (uint32_t)(unit.row * (int)a.d_o.ts * 2 + gbyte);
   const int len = (int)at.len, first = (int)(at.tile * S::KEYS), count = min(S::KEYS, len - first), block = 32 * (wave % PAIRS);
   const Part part = part_of(a, split, first, len);
   if (part.from >= part.to) return;     // (every wave)
@@ -661,11 +665,11 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
   for (int d = 0; d < DB; ++d) acc[d] = f32x16{};
   Scale<T> scale;
 
-  Unit<T> rq[FULL ? 1 : U], rg[FULL ? 1 : U];
+  Unit<T> rq[MODE != ANY ? 1 : U], rg[MODE != ANY ? 1 : U];
   float rs = 0.0f;
   auto fetch = [&](int x, int head, int row) {
     const T *q0 = (const T*)a.q.p + (at.t0 + row) * a.q.ts + head * a.q.hs, *g0 = (const T*)a.d_o.p + (at.t0 + row) * a.d_o.ts + head * a.d_o.hs;
-    if constexpr (FULL) {
+    if constexpr (MODE != ANY) {
       const uint32_t qb = lds_byte(lds.q[x].at) + wave * 1024, gb = lds_byte(lds.go[x].at) + wave * 1024;
       if (row + BR <= len) {
 #pragma unroll
@@ -677,8 +681,8 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int r = min(unit.row + u * unit.STEP, len - 1 - row);
-          lds_load16(q0, (uint32_t)(r * (int)a.q.ts * 2 + unit.byte), qb + u * NT * 16);
-          lds_load16(g0, (uint32_t)(r * (int)a.d_o.ts * 2 + unit.byte), gb + u * NT * 16);
+          lds_load16(q0, (uint32_t)(r * (int)a.q.ts * 2 + qbyte), qb + u * NT * 16);
+          lds_load16(g0, (uint32_t)(r * (int)a.d_o.ts * 2 + gbyte), gb + u * NT * 16);
         }
       }
     } else {
@@ -696,7 +700,7 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
     }
   };
   auto stage = [&](int x) {
-    if constexpr (!FULL) {
+    if constexpr (MODE == ANY) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int id = u * NT + tid;
@@ -789,7 +793,7 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
     }
 }
 
-template <typename T, int D, bool FULL>
+template <typename T, int D, FitMode MODE>
 __global__ __launch_bounds__(128 * PAIRS, 2) void attn_dkv_pairs(AttnArgs a, int64_t slots) {
   __shared__ typename PairShape<T, D>::Lds lds;
   for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
@@ -797,24 +801,27 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attn_dkv_pairs(AttnArgs a, int
     const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, 1, PairShape<T, D>::KEYS, b / a.kv_heads / a.nsplit);
     if (at.seq < 0 || at.tile * PairShape<T, D>::KEYS >= at.len) continue;
     // (both parts pass the same barriers)
-    if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >= PAIRS) pair_tile<T, D, FULL, true>(lds, a, at, kvh, split);
-    else pair_tile<T, D, FULL, false>(lds, a, at, kvh, split);
+    if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >= PAIRS) pair_tile<T, D, MODE, true>(lds, a, at, kvh, split);
+    else pair_tile<T, D, MODE, false>(lds, a, at, kvh, split);
   }
 }
 
-template <typename T, int D, bool FULL>
-void launch(const AttnArgs& a, hipStream_t s) {
-  const int64_t rows = a.tokens * a.group / ATTN_ROWS + a.seqs, keys = a.tokens / (Num<T>::IN == 1 ? PairShape<T, D>::KEYS : ATTN_ROWS) + a.seqs;
-  auto grid = [&](int64_t slots) { return dim3((uint32_t)std::min<int64_t>(slots * a.nsplit * a.kv_heads, 1 << 22)); };
-  launch_kernel(attn_dq<T, D, FULL>, grid(rows), dim3(256), 0, s, a, rows);
-  if constexpr (Num<T>::IN == 1) launch_kernel(attn_dkv_pairs<T, D, FULL>, grid(keys), dim3(PairShape<T, D>::NT), 0, s, a, keys);
-  else launch_kernel(attn_dkv<T, D, FULL>, grid(keys), dim3(256), 0, s, a, keys);
-}
 template <typename T>
 void bwd(const AttnArgs& a, hipStream_t s) {
-  const Fit f = fit_of<T>(a, false, true);
-  if (f.D == 64) f.full ? launch<T, 64, true>(a, s) : launch<T, 64, false>(a, s);
-  else f.full ? launch<T, 128, true>(a, s) : launch<T, 128, false>(a, s);
+  auto grid = [&](int64_t slots) { return dim3((uint32_t)std::min<int64_t>(slots * a.nsplit * a.kv_heads, 1 << 22)); };
+  by_fit<T>(fit_of<T>(a, false, true), [&](auto d, auto mode) {
+    constexpr int D = decltype(d)::value;
+    constexpr FitMode MODE = decltype(mode)::value;
+    const int64_t rows = a.tokens * a.group / ATTN_ROWS + a.seqs;
+    launch_kernel(attn_dq<T, D, MODE>, grid(rows), dim3(256), 0, s, a, rows);
+    if constexpr (Num<T>::IN == 1) {
+      const int64_t keys = a.tokens / PairShape<T, D>::KEYS + a.seqs;
+      launch_kernel(attn_dkv_pairs<T, D, MODE>, grid(keys), dim3(PairShape<T, D>::NT), 0, s, a, keys);
+    } else {
+      const int64_t keys = a.tokens / ATTN_ROWS + a.seqs;
+      launch_kernel(attn_dkv<T, D, MODE>, grid(keys), dim3(256), 0, s, a, keys);
+    }
+  });
 }
 
 // Sums over the parts: a wave takes a token's heads of dq, dk and dv in turn.  Token i of its sequence has parts of

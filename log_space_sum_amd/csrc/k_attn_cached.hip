@@ -95,7 +95,7 @@ __device__ __forceinline__ void join_cache(const AttnArgs& a, const Work<T>& w, 
   copy(w.keys.v, a.v.ts, a.pages.v, a.dv);
 }
 
-template <typename T, int D, bool FULL>
+template <typename T, int D, FitMode MODE>
 __global__ __launch_bounds__(256, 2) void attn_cached_many(AttnArgs a, int64_t slots, int part_len) {
   __shared__ typename FwdShape<T, D>::Lds lds;
   const int64_t per = (int64_t)a.kv_heads * a.nsplit;
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(256, 2) void attn_cached_many(AttnArgs a, int64_t s
     if (split == 0) join_cache(a, w, kvh);
     if (w.key0 >= w.key1) no_keys(w.rows, w.out);
     else
-      attend_tile<T, D, FULL, true>(lds, w.keys, w.rows, w.out, a.dk, a.dv, fabsf(a.scale) * LOG2E, a.scale < 0.0f, w.key0, w.key1);
+      attend_tile<T, D, MODE, true>(lds, w.keys, w.rows, w.out, a.dk, a.dv, fabsf(a.scale) * LOG2E, a.scale < 0.0f, w.key0, w.key1);
   }
 }
 
@@ -114,7 +114,7 @@ template <typename T, int D>
 struct FewShape {
   struct Lds {
     union {
-      Tile<T, 32, D> v[4];            // each wave's
+      Tile<T, 32, D> own[4];          // each wave's: keys, then values
       alignas(16) float acc[4][32][D + 4];
     };
     float2 stat[4][32];
@@ -125,19 +125,12 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 }
-template <typename P>
-__device__ __forceinline__ P* shfl_ptr(P* p, int lane) {
-  const uint64_t u = (uint64_t)(uintptr_t)p;
-  const uint32_t lo = __shfl((uint32_t)u, lane), hi = __shfl((uint32_t)(u >> 32), lane);
-  return (P*)(uintptr_t)(((uint64_t)hi << 32) | lo);
-}
-
-template <typename T, int D, bool FULL>
+template <typename T, int D, FitMode MODE>
 __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(AttnArgs a, int64_t slots, int part_len) {
   using N = Num<T>;
+  constexpr bool FULL = MODE == pc::FULL;
   constexpr int IN = N::IN, W = N::W, DS = D / 16, DB = D / 32, PER_ROW = D / 8, U = 32 * PER_ROW / 64;
   __shared__ typename FewShape<T, D>::Lds lds;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
   const int64_t per = (int64_t)a.kv_heads * a.nsplit;
   const int dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
   const float c = fabsf(a.scale) * LOG2E;
@@ -150,6 +143,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(
       no_keys(w.rows, w.out);
       continue;
     }
+    const int tid = thread_here(), wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
     const int mine = min(lane & 31, w.rows.count - 1), last = w.rows.last(mine), first_last = w.rows.last(0);
     frag q[DS][IN];
     {
@@ -173,35 +167,55 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(
     for (int d = 0; d < DB; ++d) o[d] = f32x16{};
     float m = -INFINITY, shift = (float)N::BIAS, l = 0.0f;
 
-    Unit<T> rk[DS], rv[U];
+    // Rows are read whole, 16 lanes a row of 128, and go through the wave's part of LDS (a lane with its own key's
+    // row would touch each line four times).  The next tile's rows are in flight over a whole tile, its pages looked up a
+    // tile before that.
+    Unit<T> rk[U], rv[U];
     uint32_t absent = 0;     // keys of the tile in no page
-    auto fetch = [&](int key) {
-      const T *kr, *vr;
-      absent = (uint32_t)__ballot(!w.keys.find(key + (lane & 31), kr, vr));
-#pragma unroll
-      for (int s = 0; s < DS; ++s) rk[s] = load_unit<FULL>(kr, 16 * s + 8 * h, dk);
+    typename Keys<T, true>::Place place{};
+    auto fetch = [&](int key, auto values) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int id = u * 64 + lane;
-        rv[u] = load_unit<FULL>(shfl_ptr(vr, id / PER_ROW), id % PER_ROW * 8, dv);
+        const int id = u * 64 + lane, r = id / PER_ROW, d = id % PER_ROW * 8;
+        const T *kr, *vr;
+        w.keys.rows_of({__shfl(place.page, r), __shfl(place.row, r)}, kr, vr);
+        if constexpr (decltype(values)::value) rv[u] = load_unit<FULL>(vr, d, dv);
+        else rk[u] = load_unit<FULL>(kr, d, dk);
       }
+      if constexpr (decltype(values)::value) {
+        if (key + 128 < w.key1) place = w.keys.locate(key + 128 + (lane & 31));
+      } else {
+        absent = (uint32_t)__ballot(place.page != w.keys.NEW && (uint32_t)place.page >= (uint32_t)w.keys.num_pages);
+      }
+    };
+    auto put = [&](const Unit<T>(&x)[U]) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) lds.own[wave].put((u * 64 + lane) / PER_ROW, (u * 64 + lane) % PER_ROW * 8, x[u]);
+      wave_fence();
     };
     __syncthreads();          // the last work's readers are done
     int key = w.key0 + 32 * wave;
-    if (key < w.key1) fetch(key);
+    if (key < w.key1) {
+      place = w.keys.locate(key + (lane & 31));
+      fetch(key, std::false_type{});
+      fetch(key, std::true_type{});
+    }
     for (; key < w.key1; key += 128) {
+      const bool more = key + 128 < w.key1;
+      const uint32_t gone = absent;
+      put(rk);
+      if (more) fetch(key + 128, std::false_type{});
       f32x16 s = f32x16{};
 #pragma unroll
       for (int st = 0; st < DS; ++st) {
         if (!FULL && 16 * st >= dk) continue;
         frag f[IN];
-        frags_of(rk[st], f);
+        lds.own[wave].rows(0, st, lane, f);
         s = mma_planes<N>(f, q[st], s);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) lds.v[wave].put((u * 64 + lane) / PER_ROW, (u * 64 + lane) % PER_ROW * 8, rv[u]);
-      const uint32_t gone = absent;
-      if (key + 128 < w.key1) fetch(key + 128);
+      wave_fence();
+      put(rv);
+      if (more) fetch(key + 128, std::true_type{});
       if (key + 31 > first_last || gone) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
@@ -219,7 +233,6 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(
 #pragma unroll
           for (int r = 0; r < 16; ++r) o[d][r] *= f;
       }
-      wave_fence();
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
         float p[8];
@@ -234,7 +247,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(
         for (int d = 0; d < DB; ++d) {
           if (!FULL && 32 * d >= dv) continue;
           frag f[IN];
-          lds.v[wave].cols(16 * st, 32 * d, lane, f);
+          lds.own[wave].cols(16 * st, 32 * d, lane, f);
           o[d] = mma_planes<N>(f, x, o[d]);
         }
       }
@@ -335,18 +348,18 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
   }
 }
 
-template <typename T, int D, bool FULL>
-void launch(const AttnArgs& a, bool few, hipStream_t s) {
-  const int64_t slots = a.tokens * a.group / (few ? ATTN_FEW_ROWS : ATTN_ROWS) + a.seqs;
-  const dim3 grid((uint32_t)std::min<int64_t>(slots * a.kv_heads * a.nsplit, 1 << 23));
-  if (few) launch_kernel(attn_cached_few<T, D, FULL>, grid, dim3(256), 0, s, a, slots, a.part_len);
-  else launch_kernel(attn_cached_many<T, D, FULL>, grid, dim3(256), 0, s, a, slots, a.part_len);
-}
 template <typename T>
 void cached(const AttnArgs& a, bool few, hipStream_t s) {
-  const Fit f = fit_of<T>(a, true);
-  if (f.D == 64) f.full ? launch<T, 64, true>(a, few, s) : launch<T, 64, false>(a, few, s);
-  else f.full ? launch<T, 128, true>(a, few, s) : launch<T, 128, false>(a, few, s);
+  const int64_t slots = a.tokens * a.group / (few ? ATTN_FEW_ROWS : ATTN_ROWS) + a.seqs;
+  const dim3 grid((uint32_t)std::min<int64_t>(slots * a.kv_heads * a.nsplit, 1 << 23));
+  Fit fit = fit_of<T>(a, true);
+  if (few && fit.mode == DIRECT) fit.mode = ANY;      // (rows go through registers)
+  by_fit<T>(fit, [&](auto d, auto mode) {
+    constexpr int D = decltype(d)::value;
+    constexpr FitMode MODE = decltype(mode)::value;
+    if (!few) launch_kernel(attn_cached_many<T, D, MODE>, grid, dim3(256), 0, s, a, slots, a.part_len);
+    else if constexpr (MODE != DIRECT) launch_kernel(attn_cached_few<T, D, MODE>, grid, dim3(256), 0, s, a, slots, a.part_len);
+  });
 }
 
 }  // namespace

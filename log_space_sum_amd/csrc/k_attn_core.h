@@ -49,6 +49,26 @@ struct Keys {
     vr = v + (int64_t)j * v_ts;
     return true;
   }
+  // The same in two steps, so that a tile's pages are looked up a tile ahead: where position j lies, and the rows of a place.
+  static constexpr int NEW = -1, NONE = -2;
+  struct Place {
+    int page, row;         // NEW: row of the new tokens
+  };
+  __device__ __forceinline__ Place locate(int j) const {
+    j = min(j, total - 1);
+    if (j >= past) return {NEW, j - past};
+    const int i = (int)(((uint64_t)(uint32_t)j * magic) >> shift), p = table[i];
+    return {p < 0 ? NONE : p, j - i * page_size};
+  }
+  // false: in no page (any rows then)
+  __device__ __forceinline__ bool rows_of(Place at, const T*& kr, const T*& vr) const {
+    const bool fresh = at.page == NEW, ok = fresh || (uint32_t)at.page < (uint32_t)num_pages;
+    const bool cached = ok && !fresh;
+    const int64_t page = cached ? at.page : 0, row = ok ? at.row : 0;
+    kr = (cached ? kc : k) + page * k_page + row * (cached ? k_row : k_ts);
+    vr = (cached ? vc : v) + page * v_page + row * (cached ? v_row : v_ts);
+    return ok;
+  }
   __device__ __forceinline__ bool there(int j) const {
     if constexpr (!PAGED) return true;
     int64_t page;
@@ -170,15 +190,14 @@ struct FwdShape {
   };
 };
 
-// FULL: rows of D elements of a 16-bit type, 16-byte aligned, at strides below 2^23: tiles go straight to LDS.
-template <typename T, int D, bool FULL, bool PAGED>
+template <typename T, int D, FitMode MODE, bool PAGED>
 __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, const Keys<T, PAGED> keys, const Rows<T> rows,
                                             const RowOut out, int dk_, int dv_, float c, bool negative, int key0, int key1) {
   using N = Num<T>;
   using S = FwdShape<T, D>;
   constexpr int IN = N::IN, W = N::W, BK = S::BK, KB = BK / 32, BUFS = S::BUFS, DS = D / 16, DB = D / 32;
   constexpr int NT = 256, PER_ROW = D / 8, U = BK * PER_ROW / NT;
-  constexpr bool DIRECT = FULL && IN == 1;
+  constexpr bool FULL = MODE == pc::FULL, DIRECT = IN == 1 && MODE != ANY;
   const int dk = FULL ? D : dk_, dv = FULL ? D : dv_;
   const int tid = thread_here(), wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
   const int wave_first = 32 * wave, end = rows.count;
@@ -212,19 +231,26 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
 
   Unit<T> rk[DIRECT ? 1 : U], rv[DIRECT ? 1 : U];
   const DirectUnit<D> unit(tid);
-  const uint32_t ok = (uint32_t)(unit.row * (int)keys.k_ts * 2 + unit.byte), ov = (uint32_t)(unit.row * (int)keys.v_ts * 2 + unit.byte);
+  const int kbyte = unit.byte(dk), vbyte = unit.byte(dv);
+  const uint32_t ok = (uint32_t)(unit.row * (int)keys.k_ts * 2 + kbyte), ov = (uint32_t)(unit.row * (int)keys.v_ts * 2 + vbyte);
+  typename Keys<T, PAGED>::Place next{};
+  if (DIRECT && PAGED && key0 < key1) next = keys.locate(key0 + lane);
+  static_assert(!(DIRECT && PAGED) || BK == 64, "a lane a key");
   auto load = [&](int b, int key) {
     const uint32_t kb = lds_byte(lds.k[b].at) + wave * 1024, vb = lds_byte(lds.v[b].at) + wave * 1024;
     if constexpr (PAGED) {
       bool gone = false;
+      const auto place = next;       // of position key + lane
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const T *kr, *vr;
-        gone |= !keys.find(key + unit.row + u * unit.STEP, kr, vr);
-        lds_load16_at((const char*)kr + unit.byte, kb + u * 4096);
-        lds_load16_at((const char*)vr + unit.byte, vb + u * 4096);
+        const int r = unit.row + u * unit.STEP;
+        gone |= !keys.rows_of({__shfl(place.page, r), __shfl(place.row, r)}, kr, vr);
+        lds_load16_at((const char*)kr + kbyte, kb + u * 4096);
+        lds_load16_at((const char*)vr + vbyte, vb + u * 4096);
       }
       if (gone) lds.absent[b] = key;
+      if (key + BK < key1) next = keys.locate(key + BK + lane);
     } else {
       const T *kr = keys.k + (int64_t)key * keys.k_ts, *vr = keys.v + (int64_t)key * keys.v_ts;
       if (key + BK <= keys.total) {
@@ -237,8 +263,8 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int row = min(unit.row + u * unit.STEP, keys.total - 1 - key);
-          lds_load16(kr, (uint32_t)(row * (int)keys.k_ts * 2 + unit.byte), kb + u * 4096);
-          lds_load16(vr, (uint32_t)(row * (int)keys.v_ts * 2 + unit.byte), vb + u * 4096);
+          lds_load16(kr, (uint32_t)(row * (int)keys.k_ts * 2 + kbyte), kb + u * 4096);
+          lds_load16(vr, (uint32_t)(row * (int)keys.v_ts * 2 + vbyte), vb + u * 4096);
         }
       }
     }

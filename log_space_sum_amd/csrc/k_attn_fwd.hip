@@ -10,7 +10,7 @@
 namespace pc {
 namespace {
 
-template <typename T, int D, bool FULL>
+template <typename T, int D, FitMode MODE>
 __global__ __launch_bounds__(256, 2) void attn_fwd(AttnArgs a, int64_t slots) {
   __shared__ typename FwdShape<T, D>::Lds lds;
   const int heads = a.kv_heads * a.group;
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd(AttnArgs a, int64_t slots) {
     }
     if (key0 >= key1) no_keys(rows, out);
     else
-      attend_tile<T, D, FULL, false>(lds, keys, rows, out, a.dk, a.dv, fabsf(a.scale) * LOG2E, a.scale < 0.0f, key0, key1);
+      attend_tile<T, D, MODE, false>(lds, keys, rows, out, a.dk, a.dv, fabsf(a.scale) * LOG2E, a.scale < 0.0f, key0, key1);
   }
 }
 
@@ -60,10 +60,9 @@ template <typename T>
 void fwd(const AttnArgs& a, hipStream_t s) {
   const int64_t slots = a.tokens * a.group / ATTN_ROWS + a.seqs;
   const dim3 grid((uint32_t)std::min<int64_t>(slots * a.nsplit * a.kv_heads, 1 << 23));
-  const Fit f = fit_of<T>(a, false);
-  auto go = [&](auto kernel) { launch_kernel(kernel, grid, dim3(256), 0, s, a, slots); };
-  if (f.D == 64) f.full ? go(attn_fwd<T, 64, true>) : go(attn_fwd<T, 64, false>);
-  else f.full ? go(attn_fwd<T, 128, true>) : go(attn_fwd<T, 128, false>);
+  by_fit<T>(fit_of<T>(a, false), [&](auto d, auto mode) {
+    launch_kernel(attn_fwd<T, decltype(d)::value, decltype(mode)::value>, grid, dim3(256), 0, s, a, slots);
+  });
 }
 
 }  // namespace

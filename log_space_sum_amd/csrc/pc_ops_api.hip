@@ -326,7 +326,7 @@ CachedPlan cached_plan(const pc_attention* d) {
   const int64_t full = std::min<int64_t>(std::max(1, d->num_seqs), (tokens * group + rows - 1) / rows);
   const int64_t works = std::max<int64_t>(1, full * ((rows + tile - 1) / tile) * d->kv_heads);
   const int64_t longest = std::max<int64_t>(1, std::min<int64_t>(d->max_length, (int64_t)d->max_pages * d->page_size + tokens));
-  const int64_t aim = p.few ? 1024 : 512;
+  const int64_t aim = p.few ? 8192 : 512;
   int64_t len = std::max<int64_t>(256, (longest * works + aim - 1) / aim);
   len = round_up(std::max(len, (longest + ATTN_MAX_SPLIT - 1) / ATTN_MAX_SPLIT), 128);
   p.nsplit = (int)((longest + len - 1) / len);
