@@ -130,16 +130,20 @@ template <typename T>
 struct Unit {
   T v[8];
 };
-// Elements d .. d + 7 of a row of `dim`; those behind it are 0.  FULL: there are none.
-template <bool FULL, typename T>
+// Elements d .. d + 7 of a row of `dim`; those behind it are 0.  UNITS: dim is a multiple of 8.
+template <bool UNITS, typename T>
 __device__ __forceinline__ Unit<T> load_unit(const T* row, int d, int dim) {
+  // (loads that are always done, from the row's start where there is nothing: branches around them would be many)
   Unit<T> u;
-  if (FULL || (dim & 7) == 0) {
-    if (FULL || d < dim) __builtin_memcpy(&u, row + d, sizeof(u));
-    else u = Unit<T>{};
+  if constexpr (UNITS) {
+    __builtin_memcpy(&u, row + (d < dim ? d : 0), sizeof(u));
+    if (d >= dim) u = Unit<T>{};
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) u.v[e] = d + e < dim ? row[d + e] : T{};
+    for (int e = 0; e < 8; ++e) {
+      u.v[e] = row[d + e < dim ? d + e : 0];
+      if (d + e >= dim) u.v[e] = T{};
+    }
   }
   return u;
 }
@@ -156,31 +160,32 @@ __device__ __forceinline__ void frags_of(const Unit<T>& u, frag (&out)[Num<T>::I
 }
 
 // ---- tiles in LDS ------------------------------------------------------------------
-// A tile of rows of D (64 or 128) elements, in planes, read by rows and by columns.
-// Rows are not padded; their 16-byte chunks are exchanged, chunk c of row r lying
+// A tile of rows of D (32, 64, 96 or 128) elements, in planes, read by rows and by columns.
+// Rows of P = 64 or 128 elements are not padded; their 16-byte chunks are exchanged, chunk c of row r lying
 // at c ^ turn(r), so that both reads meet every bank once: of 16 consecutive rows one
 // chunk each, and of four rows (from a multiple of four) four chunks each.  (Rows padded by 16 bytes: the
 // column reads meet half of the banks twice, 16384 tokens x 16 heads x 128 bfloat16 1.94 ms.)
 template <typename T, int ROWS, int D>
 struct Tile {
-  static constexpr int PLANE = ROWS * D;
+  static constexpr int P = D <= 64 ? 64 : 128;
+  static constexpr int PLANE = ROWS * P;
   alignas(16) uint16_t at[Num<T>::IN * PLANE];
 
   static __device__ __forceinline__ int turn(int r) {
-    return D == 128 ? (r & 3) << 2 | (r >> 2 & 3) : (r >> 1 & 1) << 2 | (r >> 2 & 3);
+    return P == 128 ? (r & 3) << 2 | (r >> 2 & 3) : (r >> 1 & 1) << 2 | (r >> 2 & 3);
   }
   // d: a multiple of 8
   __device__ __forceinline__ void put(int row, int d, const Unit<T>& u) {
     frag f[Num<T>::IN];
     frags_of(u, f);
 #pragma unroll
-    for (int p = 0; p < Num<T>::IN; ++p) *(frag*)(at + p * PLANE + row * D + (d ^ turn(row) * 8)) = f[p];
+    for (int p = 0; p < Num<T>::IN; ++p) *(frag*)(at + p * PLANE + row * P + (d ^ turn(row) * 8)) = f[p];
   }
   // Rows row0 + l (row0 a multiple of 32), elements 16 step + 8 h ..: the operand whose rows are the tile's.
   __device__ __forceinline__ void rows(int row0, int step, int lane, frag (&out)[Num<T>::IN]) const {
     const int l = lane & 31, x = (turn(l) ^ (lane >> 5)) * 8;
 #pragma unroll
-    for (int p = 0; p < Num<T>::IN; ++p) out[p] = *(const frag*)(at + p * PLANE + row0 * D + l * D + (x ^ 16 * step));
+    for (int p = 0; p < Num<T>::IN; ++p) out[p] = *(const frag*)(at + p * PLANE + row0 * P + l * P + (x ^ 16 * step));
   }
   // Columns d0 + l (d0 a multiple of 32) of rows row0 + 4 h .. + 3 and row0 + 8 + 4 h .. + 3 (row0 a multiple of 16): the
   // operand that is contracted with a result's registers.
@@ -190,9 +195,9 @@ struct Tile {
     const int x = (c ^ turn(r) * 8) + 4 * (l16 & 1), y = (c ^ turn(r + 8) * 8) + 4 * (l16 & 1);
 #pragma unroll
     for (int p = 0; p < Num<T>::IN; ++p) {
-      const uint16_t* p0 = at + p * PLANE + row0 * D + r * D;
+      const uint16_t* p0 = at + p * PLANE + row0 * P + r * P;
       const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p0 + (x ^ d0))));
-      const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p0 + 8 * D + (y ^ d0))));
+      const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p0 + 8 * P + (y ^ d0))));
       out[p] = frag{a.x, a.y, b.x, b.y};
     }
   }
@@ -203,11 +208,11 @@ struct Tile {
 // lie STEP rows apart.
 template <int D, int NT = 256>
 struct DirectUnit {
-  static constexpr int STEP = NT / (D / 8);
+  static constexpr int P = D <= 64 ? 64 : 128, STEP = NT / (P / 8);
   int row, chunk;    // of the first unit
   __device__ __forceinline__ DirectUnit(int tid) {
-    row = tid / (D / 8);
-    chunk = (tid % (D / 8)) ^ Tile<bf16, 64, D>::turn(row);
+    row = tid / (P / 8);
+    chunk = (tid % (P / 8)) ^ Tile<bf16, 64, D>::turn(row);
   }
   // The unit's byte of a row of `dim` elements.  Chunks behind it hold the first one: they meet zeros in a contraction,
   // or results that are not stored.
@@ -284,35 +289,41 @@ __device__ __forceinline__ void store4(T* to, const float (&x)[4], int have) {
 inline bool direct_rows(const void* p, int64_t ts, int64_t hs) {
   return ((uintptr_t)p | (uintptr_t)(ts * 2) | (uintptr_t)(hs * 2)) % 16 == 0 && ts < (1 << 23);
 }
-// How a call meets the kernels: tiles of width D; FULL: both dims are D (and 16-bit rows can be loaded directly);
-// DIRECT: 16-bit rows can be, dims are multiples of 8; ANY.
-enum FitMode { ANY, DIRECT, FULL };
+// How a call meets the kernels: the width D of tiles and results, and whether dims are multiples of 8 (and 16-bit
+// rows can be loaded to LDS directly), or any.
+enum FitMode { ANY, UNITS };
 struct Fit {
   int D;
   FitMode mode;
 };
 template <typename T>
 Fit fit_of(const AttnArgs& a, bool cache, bool rows = false) {
-  const int big = a.dk > a.dv ? a.dk : a.dv, D = big <= 64 ? 64 : 128;
-  const bool full = a.dk == D && a.dv == D;
-  if (sizeof(T) != 2) return {D, full ? FULL : ANY};
-  bool direct = a.dk % 8 == 0 && a.dv % 8 == 0 && direct_rows(a.k.p, a.k.ts, a.k.hs) && direct_rows(a.v.p, a.v.ts, a.v.hs);
-  if (rows) direct = direct && direct_rows(a.q.p, a.q.ts, a.q.hs) && direct_rows(a.d_o.p, a.d_o.ts, a.d_o.hs);
-  if (cache)
-    for (const AttnCache* c : {&a.pages.k, &a.pages.v})
-      direct = direct && direct_rows(c->p, c->token_stride, c->head_stride) && c->page_stride % 8 == 0;
-  return {D, direct ? (full ? FULL : DIRECT) : ANY};
+  const int big = a.dk > a.dv ? a.dk : a.dv;
+  bool units = a.dk % 8 == 0 && a.dv % 8 == 0;
+  if (sizeof(T) == 2) {
+    units = units && direct_rows(a.k.p, a.k.ts, a.k.hs) && direct_rows(a.v.p, a.v.ts, a.v.hs);
+    if (rows) units = units && direct_rows(a.q.p, a.q.ts, a.q.hs) && direct_rows(a.d_o.p, a.d_o.ts, a.d_o.hs);
+    if (cache)
+      for (const AttnCache* c : {&a.pages.k, &a.pages.v})
+        units = units && direct_rows(c->p, c->token_stride, c->head_stride) && c->page_stride % 8 == 0;
+  }
+  const int step = units ? 32 : 64;
+  return {(big + step - 1) / step * step, units ? UNITS : ANY};
 }
 // f(D, mode) as constants.
-template <typename T, typename F>
+template <typename F>
 void by_fit(const Fit& fit, F&& f) {
-  auto mode = [&](auto d) {
-    if (fit.mode == FULL) f(d, std::integral_constant<FitMode, FULL>{});
-    else if (fit.mode == ANY) f(d, std::integral_constant<FitMode, ANY>{});
-    else if constexpr (sizeof(T) == 2) f(d, std::integral_constant<FitMode, DIRECT>{});
-  };
-  if (fit.D == 64) mode(std::integral_constant<int, 64>{});
-  else mode(std::integral_constant<int, 128>{});
+  using Units = std::integral_constant<FitMode, UNITS>;
+  using Any = std::integral_constant<FitMode, ANY>;
+  if (fit.mode == UNITS) {
+    if (fit.D == 32) f(std::integral_constant<int, 32>{}, Units{});
+    else if (fit.D == 64) f(std::integral_constant<int, 64>{}, Units{});
+    else if (fit.D == 96) f(std::integral_constant<int, 96>{}, Units{});
+    else f(std::integral_constant<int, 128>{}, Units{});
+  } else {
+    if (fit.D == 64) f(std::integral_constant<int, 64>{}, Any{});
+    else f(std::integral_constant<int, 128>{}, Any{});
+  }
 }
 
 // ---- sequences -----------------------------------------------------------------------

@@ -77,24 +77,24 @@ __device__ __forceinline__ float dot(const T* a, const T* b, int n) {
 // ---- a block of 32 by 32 (16-bit types) ---------------------------------------------
 // s = A x^T and, with BOTH, dp = B y^T for 32 rows of two tiles and a wave's own operands.  The rows of A are
 // all asked for before they are used, those of B meanwhile; a single product goes in two chains.
-template <typename T, int D, bool FULL, bool BOTH, typename TileT>
+template <typename T, int D, bool UNIT, bool BOTH, typename TileT>
 __device__ __forceinline__ void block_products(const TileT& ta, const TileT& tb, int r0, int lane, const frag (&x)[D / 16],
-                                               const frag (&y)[BOTH ? D / 16 : 1], int dx, int dy, f32x16& s, f32x16& dp) {
+                                               const frag (&y)[BOTH ? D / 16 : 1], f32x16& s, f32x16& dp) {
   using N = Num<T>;
   constexpr int DS = D / 16;
   frag fa[DS][1], fb[BOTH ? DS : 1][1];
 #pragma unroll
   for (int st = 0; st < DS; ++st)
-    if (FULL || 16 * st < dx) ta.rows(r0, st, lane, fa[st]);
-  if (FULL) __builtin_amdgcn_sched_barrier(0);
+    ta.rows(r0, st, lane, fa[st]);
+  if (UNIT) __builtin_amdgcn_sched_barrier(0);
   s = dp = f32x16{};
 #pragma unroll
   for (int st = 0; st < DS; ++st) {
     if constexpr (BOTH) {
-      if (FULL || 16 * st < dy) tb.rows(r0, st, lane, fb[st]);
-      if (FULL || 16 * st < dx) s = N::mma(fa[st][0], x[st], s);
-      if (FULL) __builtin_amdgcn_sched_barrier(0);
-    } else if (FULL || 16 * st < dx) {
+      tb.rows(r0, st, lane, fb[st]);
+      s = N::mma(fa[st][0], x[st], s);
+      if (UNIT) __builtin_amdgcn_sched_barrier(0);
+    } else {
       if (st & 1) dp = N::mma(fa[st][0], x[st], dp);
       else s = N::mma(fa[st][0], x[st], s);
     }
@@ -102,29 +102,29 @@ __device__ __forceinline__ void block_products(const TileT& ta, const TileT& tb,
   if constexpr (BOTH) {
 #pragma unroll
     for (int st = 0; st < DS; ++st)
-      if (FULL || 16 * st < dy) dp = N::mma(fb[st][0], y[st], dp);
+      dp = N::mma(fb[st][0], y[st], dp);
   } else {
     s += dp;
   }
 }
 // acc += A^T x for 32 rows of a tile and a result x of them; the second 16 rows' values are read and planes made
 // between the first's matrix instructions.
-template <typename T, int D, bool FULL, typename TileT>
-__device__ __forceinline__ void block_add(const TileT& ta, int r0, int lane, const f32x16& x, int dim, f32x16 (&acc)[D / 32]) {
+template <typename T, int D, bool UNIT, typename TileT>
+__device__ __forceinline__ void block_add(const TileT& ta, int r0, int lane, const f32x16& x, f32x16 (&acc)[D / 32]) {
   using N = Num<T>;
   constexpr int W = N::W, DB = D / 32;
   frag w[2][W], f[2][DB][1];
   auto ready = [&](int st) {
 #pragma unroll
     for (int d = 0; d < DB; ++d)
-      if (FULL || 32 * d < dim) ta.cols(r0 + 16 * st, 32 * d, lane, f[st][d]);
+      ta.cols(r0 + 16 * st, 32 * d, lane, f[st][d]);
     float p[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) p[e] = x[8 * st + e];
     planes_of<N>(p, w[st]);
   };
   ready(0);
-  if (FULL) __builtin_amdgcn_sched_barrier(0);
+  if (UNIT) __builtin_amdgcn_sched_barrier(0);
   ready(1);
 #pragma unroll
   for (int st = 0; st < 2; ++st)
@@ -132,8 +132,8 @@ __device__ __forceinline__ void block_add(const TileT& ta, int r0, int lane, con
     for (int p = W - 1; p >= 0; --p)
 #pragma unroll
       for (int d = 0; d < DB; ++d)
-        if (FULL || 32 * d < dim) acc[d] = N::mma(f[st][d][0], w[st][p], acc[d]);
-  if (FULL) {
+        acc[d] = N::mma(f[st][d][0], w[st][p], acc[d]);
+  if (UNIT) {
     __builtin_amdgcn_sched_group_barrier(0x100, 2 * DB, 0);
 #pragma unroll
     for (int k = 0; k < W * DB; ++k) {
@@ -185,14 +185,14 @@ __device__ __attribute__((noinline)) void careful_dq(AttnArgs a, int64_t t0, int
 }
 
 template <typename T, int D, FitMode MODE>
-__global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs a, int64_t slots) {
+__global__ __launch_bounds__(256, Num<T>::IN == 3 || MODE == ANY ? 1 : 2) void attn_dq(AttnArgs a, int64_t slots) {
   using N = Num<T>;
   using S = DqShape<T, D>;
   constexpr int IN = N::IN, W = N::W, BK = S::BK, KB = BK / 32, BUFS = S::BUFS, DS = D / 16, DB = D / 32;
-  constexpr int PER_ROW = D / 8, U = BK * PER_ROW / 256;
-  constexpr bool FULL = MODE == pc::FULL, DIRECT = IN == 1 && MODE != ANY;
+  constexpr int PER_ROW = Tile<T, 32, D>::P / 8, U = BK * PER_ROW / 256;
+  constexpr bool UNIT = MODE == UNITS, DIRECT = IN == 1 && UNIT;
   __shared__ typename S::Lds lds;
-  const int heads = a.kv_heads * a.group, dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
+  const int heads = a.kv_heads * a.group, dk = a.dk, dv = a.dv;
   const float c = a.scale * LOG2E;
   for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
     const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
@@ -221,11 +221,11 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
         frag f[IN];
-        frags_of(load_unit<FULL>(pq, 16 * s + 8 * h, dk), f);
+        frags_of(load_unit<UNIT>(pq, 16 * s + 8 * h, dk), f);
         if constexpr (IN == 1) q1[s] = f[0];
         else
           for (int i = 0; i < IN; ++i) q[s][i] = f[i];
-        const Unit<T> g = load_unit<FULL>(pg, 16 * s + 8 * h, dv), o = load_unit<FULL>(po, 16 * s + 8 * h, dv);
+        const Unit<T> g = load_unit<UNIT>(pg, 16 * s + 8 * h, dv), o = load_unit<UNIT>(po, 16 * s + 8 * h, dv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) delta = fmaf(to_f32(g.v[e]), to_f32(o.v[e]), delta);
         frags_of(g, f);
@@ -268,8 +268,8 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int id = u * 256 + tid, j = min(key + id / PER_ROW, end - 1), d = id % PER_ROW * 8;
-        rk[u] = load_unit<FULL>(k0 + j * a.k.ts, d, dk);
-        rv[u] = load_unit<FULL>(v0 + j * a.v.ts, d, dv);
+        rk[u] = load_unit<UNIT>(k0 + j * a.k.ts, d, dk);
+        rv[u] = load_unit<UNIT>(v0 + j * a.v.ts, d, dv);
       }
     };
     auto stage = [&](int x) {
@@ -285,16 +285,16 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
       for (int kb = 0; kb < KB; ++kb) {
         f32x16 s = f32x16{}, dp = f32x16{};
         if constexpr (IN == 1) {
-          block_products<T, D, FULL, true>(lds.k[x], lds.v[x], 32 * kb, lane, q1, go1, dk, dv, s, dp);
+          block_products<T, D, UNIT, true>(lds.k[x], lds.v[x], 32 * kb, lane, q1, go1, s, dp);
         } else {
 #pragma unroll
         for (int st = 0; st < DS; ++st) {
           frag f[IN];
-          if (FULL || 16 * st < dk) {
+          {
             lds.k[x].rows(32 * kb, st, lane, f);
             s = mma_planes<N>(f, q[st], s);
           }
-          if (FULL || 16 * st < dv) {
+          {
             lds.v[x].rows(32 * kb, st, lane, f);
             dp = mma_planes<N>(f, go[st], dp);
           }
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
         for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
         scale.move(s, acc);
         if constexpr (IN == 1) {
-          block_add<T, D, FULL>(lds.k[x], 32 * kb, lane, s, dk, acc);
+          block_add<T, D, UNIT>(lds.k[x], 32 * kb, lane, s, acc);
           continue;
         }
 #pragma unroll
@@ -322,7 +322,6 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_dq(AttnArgs
           planes_of<N>(p, w);
 #pragma unroll
           for (int d = 0; d < DB; ++d) {
-            if (!FULL && 32 * d >= dk) continue;
             frag f[IN];
             lds.k[x].cols(32 * kb + 16 * st, 32 * d, lane, f);
             acc[d] = mma_planes<N>(f, w, acc[d]);
@@ -437,13 +436,13 @@ __device__ __attribute__((noinline)) void careful_dkv(AttnArgs a, int64_t t0, in
 template <typename T, int D, FitMode MODE>
 __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
   using N = Num<T>;
-  constexpr bool FULL = MODE == pc::FULL;
+  constexpr bool UNIT = MODE == UNITS;
   using S = DkvShape<T, D>;
   constexpr int IN = N::IN, W = N::W, BR = S::BR, BUFS = S::BUFS, DS = D / 16, DB = D / 32;
-  constexpr int PER_ROW = D / 8, U = BR * PER_ROW / 256;
+  constexpr int PER_ROW = Tile<T, 32, D>::P / 8, U = BR * PER_ROW / 256;
   __shared__ typename S::Lds lds;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
-  const int heads = a.kv_heads * a.group, dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
+  const int heads = a.kv_heads * a.group, dk = a.dk, dv = a.dv;
   const float c = a.scale * LOG2E;
   for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
     const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
@@ -462,8 +461,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
       const T *pk = (const T*)a.k.p + (at.t0 + key) * a.k.ts + kvh * a.k.hs, *pv = (const T*)a.v.p + (at.t0 + key) * a.v.ts + kvh * a.v.hs;
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
-        frags_of(load_unit<FULL>(pk, 16 * s + 8 * h, dk), k[s]);
-        frags_of(load_unit<FULL>(pv, 16 * s + 8 * h, dv), v[s]);
+        frags_of(load_unit<UNIT>(pk, 16 * s + 8 * h, dk), k[s]);
+        frags_of(load_unit<UNIT>(pv, 16 * s + 8 * h, dv), v[s]);
       }
     }
     f32x16 dka[DB], dva[DB];
@@ -478,8 +477,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int id = u * 256 + tid, i = min(row + id / PER_ROW, len - 1), d = id % PER_ROW * 8;
-        rq[u] = load_unit<FULL>(q0 + i * a.q.ts, d, dk);
-        rg[u] = load_unit<FULL>(g0 + i * a.d_o.ts, d, dv);
+        rq[u] = load_unit<UNIT>(q0 + i * a.q.ts, d, dk);
+        rg[u] = load_unit<UNIT>(g0 + i * a.d_o.ts, d, dv);
       }
       if (tid < BR) {
         const int64_t i = (at.t0 + min(row + tid, len - 1)) * heads + head;
@@ -504,11 +503,11 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
 #pragma unroll
       for (int st = 0; st < DS; ++st) {
         frag f[IN];
-        if (FULL || 16 * st < dk) {
+        {
           lds.q[x].rows(0, st, lane, f);
           s = mma_planes<N>(f, k[st], s);
         }
-        if (FULL || 16 * st < dv) {
+        {
           lds.go[x].rows(0, st, lane, f);
           dp = mma_planes<N>(f, v[st], dp);
         }
@@ -542,7 +541,6 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
         planes_of<N>(p, w);
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
-          if (!FULL && 32 * d >= dv) continue;
           frag f[IN];
           lds.go[x].cols(16 * st, 32 * d, lane, f);
           dva[d] = mma_planes<N>(f, w, dva[d]);
@@ -552,7 +550,6 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
         planes_of<N>(p, w);
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
-          if (!FULL && 32 * d >= dk) continue;
           frag f[IN];
           lds.q[x].cols(16 * st, 32 * d, lane, f);
           dka[d] = mma_planes<N>(f, w, dka[d]);
@@ -631,12 +628,12 @@ struct PairShape {
 template <typename T, int D, FitMode MODE, bool DK>
 __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, const AttnArgs& a, const SeqTile& at, int kvh, int split) {
   using N = Num<T>;
-  constexpr bool FULL = MODE == pc::FULL;
+  constexpr bool UNIT = MODE == UNITS;
   using S = PairShape<T, D>;
   constexpr int W = N::W, BR = S::BR, DS = D / 16, DB = D / 32, NT = S::NT;
-  constexpr int PER_ROW = D / 8, U = BR * PER_ROW / NT;
+  constexpr int PER_ROW = Tile<T, 32, D>::P / 8, U = BR * PER_ROW / NT;
   const int tid = thread_here(), wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
-  const int heads = a.kv_heads * a.group, dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
+  const int heads = a.kv_heads * a.group, dk = a.dk, dv = a.dv;
   const float c = a.scale * LOG2E;
   const DirectUnit<D, NT> unit(tid);
   const int qbyte = unit.byte(dk), gbyte = unit.byte(dv);
@@ -652,10 +649,10 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
 #pragma unroll
     for (int s = 0; s < DS; ++s) {
       frag f[1];
-      frags_of(load_unit<FULL>(pk, 16 * s + 8 * h, dk), f);
+      frags_of(load_unit<UNIT>(pk, 16 * s + 8 * h, dk), f);
       k[s] = f[0];
       if constexpr (DK) {
-        frags_of(load_unit<FULL>(pv, 16 * s + 8 * h, dv), f);
+        frags_of(load_unit<UNIT>(pv, 16 * s + 8 * h, dv), f);
         v[s] = f[0];
       }
     }
@@ -665,11 +662,11 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
   for (int d = 0; d < DB; ++d) acc[d] = f32x16{};
   Scale<T> scale;
 
-  Unit<T> rq[MODE != ANY ? 1 : U], rg[MODE != ANY ? 1 : U];
+  Unit<T> rq[UNIT ? 1 : U], rg[UNIT ? 1 : U];
   float rs = 0.0f;
   auto fetch = [&](int x, int head, int row) {
     const T *q0 = (const T*)a.q.p + (at.t0 + row) * a.q.ts + head * a.q.hs, *g0 = (const T*)a.d_o.p + (at.t0 + row) * a.d_o.ts + head * a.d_o.hs;
-    if constexpr (MODE != ANY) {
+    if constexpr (UNIT) {
       const uint32_t qb = lds_byte(lds.q[x].at) + wave * 1024, gb = lds_byte(lds.go[x].at) + wave * 1024;
       if (row + BR <= len) {
 #pragma unroll
@@ -690,8 +687,8 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
       for (int u = 0; u < U; ++u) {
         const int id = u * NT + tid, d = id % PER_ROW * 8;
         const int64_t r = min(id / PER_ROW, len - 1 - row);
-        rq[u] = load_unit<FULL>(q0 + r * a.q.ts, d, dk);
-        rg[u] = load_unit<FULL>(g0 + r * a.d_o.ts, d, dv);
+        rq[u] = load_unit<UNIT>(q0 + r * a.q.ts, d, dk);
+        rg[u] = load_unit<UNIT>(g0 + r * a.d_o.ts, d, dv);
       }
     }
     if (tid < 2 * BR) {
@@ -700,7 +697,7 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
     }
   };
   auto stage = [&](int x) {
-    if constexpr (MODE == ANY) {
+    if constexpr (!UNIT) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int id = u * NT + tid;
@@ -713,7 +710,7 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
   };
   auto compute = [&](int x, int row, int r0) {
     f32x16 s, dp;
-    block_products<T, D, FULL, DK>(lds.q[x], lds.go[x], r0, lane, k, v, dk, dv, s, dp);
+    block_products<T, D, UNIT, DK>(lds.q[x], lds.go[x], r0, lane, k, v, s, dp);
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
       const f32x4 l4 = *(const f32x4*)&lds.lse2[x][r0 + 8 * r4 + 4 * h];
@@ -735,13 +732,13 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
         for (int e = 0; e < 4; ++e) s[4 * r4 + e] *= dp[4 * r4 + e] - d4[e];
       }
       scale.move(s, acc);
-      block_add<T, D, FULL>(lds.q[x], r0, lane, s, dk, acc);
+      block_add<T, D, UNIT>(lds.q[x], r0, lane, s, acc);
     } else {
       if (N::BIAS) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[r] *= (float)(1 << N::BIAS);
       }
-      block_add<T, D, FULL>(lds.go[x], r0, lane, s, dv, acc);
+      block_add<T, D, UNIT>(lds.go[x], r0, lane, s, acc);
     }
   };
   const int h0 = kvh * a.group, h1 = h0 + a.group;      // rows from the tile's first key on attend it
@@ -794,7 +791,7 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
 }
 
 template <typename T, int D, FitMode MODE>
-__global__ __launch_bounds__(128 * PAIRS, 2) void attn_dkv_pairs(AttnArgs a, int64_t slots) {
+__global__ __launch_bounds__(128 * PAIRS, MODE == ANY ? 1 : 2) void attn_dkv_pairs(AttnArgs a, int64_t slots) {
   __shared__ typename PairShape<T, D>::Lds lds;
   for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
     const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
@@ -809,7 +806,7 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void attn_dkv_pairs(AttnArgs a, int
 template <typename T>
 void bwd(const AttnArgs& a, hipStream_t s) {
   auto grid = [&](int64_t slots) { return dim3((uint32_t)std::min<int64_t>(slots * a.nsplit * a.kv_heads, 1 << 22)); };
-  by_fit<T>(fit_of<T>(a, false, true), [&](auto d, auto mode) {
+  by_fit(fit_of<T>(a, false, true), [&](auto d, auto mode) {
     constexpr int D = decltype(d)::value;
     constexpr FitMode MODE = decltype(mode)::value;
     const int64_t rows = a.tokens * a.group / ATTN_ROWS + a.seqs;

@@ -96,7 +96,7 @@ __device__ __forceinline__ void join_cache(const AttnArgs& a, const Work<T>& w, 
 }
 
 template <typename T, int D, FitMode MODE>
-__global__ __launch_bounds__(256, 2) void attn_cached_many(AttnArgs a, int64_t slots, int part_len) {
+__global__ __launch_bounds__(256, (Num<T>::IN == 3 || MODE == ANY) && D > 64 ? 1 : 2) void attn_cached_many(AttnArgs a, int64_t slots, int part_len) {
   __shared__ typename FwdShape<T, D>::Lds lds;
   const int64_t per = (int64_t)a.kv_heads * a.nsplit;
   for (int64_t b = blockIdx.x; b < slots * per; b += gridDim.x) {
@@ -126,13 +126,13 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 template <typename T, int D, FitMode MODE>
-__global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(AttnArgs a, int64_t slots, int part_len) {
+__global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1 : 2) void attn_cached_few(AttnArgs a, int64_t slots, int part_len) {
   using N = Num<T>;
-  constexpr bool FULL = MODE == pc::FULL;
-  constexpr int IN = N::IN, W = N::W, DS = D / 16, DB = D / 32, PER_ROW = D / 8, U = 32 * PER_ROW / 64;
+  constexpr bool UNIT = MODE == UNITS;
+  constexpr int IN = N::IN, W = N::W, DS = D / 16, DB = D / 32, PER_ROW = Tile<T, 32, D>::P / 8, U = 32 * PER_ROW / 64;
   __shared__ typename FewShape<T, D>::Lds lds;
   const int64_t per = (int64_t)a.kv_heads * a.nsplit;
-  const int dk = FULL ? D : a.dk, dv = FULL ? D : a.dv;
+  const int dk = a.dk, dv = a.dv;
   const float c = fabsf(a.scale) * LOG2E;
   for (int64_t b = blockIdx.x; b < slots * per; b += gridDim.x) {
     const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(
       const T* p = w.rows.row(mine);
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
-        frags_of(load_unit<FULL>(p, 16 * s + 8 * h, dk), q[s]);
+        frags_of(load_unit<UNIT>(p, 16 * s + 8 * h, dk), q[s]);
         if (a.scale < 0.0f) {
 #pragma unroll
           for (int i = 0; i < IN; ++i) {
@@ -179,8 +179,8 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(
         const int id = u * 64 + lane, r = id / PER_ROW, d = id % PER_ROW * 8;
         const T *kr, *vr;
         w.keys.rows_of({__shfl(place.page, r), __shfl(place.row, r)}, kr, vr);
-        if constexpr (decltype(values)::value) rv[u] = load_unit<FULL>(vr, d, dv);
-        else rk[u] = load_unit<FULL>(kr, d, dk);
+        if constexpr (decltype(values)::value) rv[u] = load_unit<UNIT>(vr, d, dv);
+        else rk[u] = load_unit<UNIT>(kr, d, dk);
       }
       if constexpr (decltype(values)::value) {
         if (key + 128 < w.key1) place = w.keys.locate(key + 128 + (lane & 31));
@@ -208,7 +208,6 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(
       f32x16 s = f32x16{};
 #pragma unroll
       for (int st = 0; st < DS; ++st) {
-        if (!FULL && 16 * st >= dk) continue;
         frag f[IN];
         lds.own[wave].rows(0, st, lane, f);
         s = mma_planes<N>(f, q[st], s);
@@ -245,7 +244,6 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 ? 1 : 2) void attn_cached_few(
         planes_of<N>(p, x);
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
-          if (!FULL && 32 * d >= dv) continue;
           frag f[IN];
           lds.own[wave].cols(16 * st, 32 * d, lane, f);
           o[d] = mma_planes<N>(f, x, o[d]);
@@ -352,13 +350,11 @@ template <typename T>
 void cached(const AttnArgs& a, bool few, hipStream_t s) {
   const int64_t slots = a.tokens * a.group / (few ? ATTN_FEW_ROWS : ATTN_ROWS) + a.seqs;
   const dim3 grid((uint32_t)std::min<int64_t>(slots * a.kv_heads * a.nsplit, 1 << 23));
-  Fit fit = fit_of<T>(a, true);
-  if (few && fit.mode == DIRECT) fit.mode = ANY;      // (rows go through registers)
-  by_fit<T>(fit, [&](auto d, auto mode) {
+  by_fit(fit_of<T>(a, true), [&](auto d, auto mode) {
     constexpr int D = decltype(d)::value;
     constexpr FitMode MODE = decltype(mode)::value;
     if (!few) launch_kernel(attn_cached_many<T, D, MODE>, grid, dim3(256), 0, s, a, slots, a.part_len);
-    else if constexpr (MODE != DIRECT) launch_kernel(attn_cached_few<T, D, MODE>, grid, dim3(256), 0, s, a, slots, a.part_len);
+    else launch_kernel(attn_cached_few<T, D, MODE>, grid, dim3(256), 0, s, a, slots, a.part_len);
   });
 }
 

@@ -196,9 +196,9 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
   using N = Num<T>;
   using S = FwdShape<T, D>;
   constexpr int IN = N::IN, W = N::W, BK = S::BK, KB = BK / 32, BUFS = S::BUFS, DS = D / 16, DB = D / 32;
-  constexpr int NT = 256, PER_ROW = D / 8, U = BK * PER_ROW / NT;
-  constexpr bool FULL = MODE == pc::FULL, DIRECT = IN == 1 && MODE != ANY;
-  const int dk = FULL ? D : dk_, dv = FULL ? D : dv_;
+  constexpr int NT = 256, PER_ROW = Tile<T, 32, D>::P / 8, U = BK * PER_ROW / NT;
+  constexpr bool UNIT = MODE == UNITS, DIRECT = IN == 1 && UNIT;
+  const int dk = dk_, dv = dv_;
   const int tid = thread_here(), wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
   const int wave_first = 32 * wave, end = rows.count;
   const bool wave_on = wave_first < end;
@@ -212,7 +212,7 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
     const T* p = rows.row(mine);
 #pragma unroll
     for (int s = 0; s < DS; ++s) {
-      frags_of(load_unit<FULL>(p, 16 * s + 8 * h, dk), q[s]);
+      frags_of(load_unit<UNIT>(p, 16 * s + 8 * h, dk), q[s]);
       if (negative) {
 #pragma unroll
         for (int i = 0; i < IN; ++i) {
@@ -277,8 +277,8 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
       const int id = u * NT + tid, row = id / PER_ROW, d = id % PER_ROW * 8;
       const T *kr, *vr;
       absent |= !keys.find(key + row, kr, vr);
-      rk[u] = load_unit<FULL>(kr, d, dk);
-      rv[u] = load_unit<FULL>(vr, d, dv);
+      rk[u] = load_unit<UNIT>(kr, d, dk);
+      rv[u] = load_unit<UNIT>(vr, d, dv);
     }
   };
   auto stage = [&](int b, int key) {
@@ -296,7 +296,6 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
     for (int kb = 0; kb < KB; ++kb) s[kb] = f32x16{};
 #pragma unroll
     for (int st = 0; st < DS; ++st) {
-      if (!FULL && 16 * st >= dk) continue;
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         frag a[IN];
@@ -348,7 +347,7 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
       auto values = [&](int step, frag (&a)[DB][IN]) {
 #pragma unroll
         for (int d = 0; d < DB; ++d)
-          if (FULL || 32 * d < dv) lds.v[b].cols(16 * step, 32 * d, lane, a[d]);
+          lds.v[b].cols(16 * step, 32 * d, lane, a[d]);
       };
       frag w[W], a[DB][IN];
       values(0, a);
@@ -364,8 +363,8 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
         for (int p = W - 1; p >= 0; --p)
 #pragma unroll
           for (int d = 0; d < DB; ++d)
-            if (FULL || 32 * d < dv) o[d] = N::mma(a[d][0], w[p], o[d]);
-        if (FULL && step + 1 < STEPS) {
+            o[d] = N::mma(a[d][0], w[p], o[d]);
+        if (step + 1 < STEPS) {
           __builtin_amdgcn_sched_group_barrier(0x100, 2 * DB, 0);
 #pragma unroll
           for (int i = 0; i < W * DB; ++i) {
@@ -396,7 +395,6 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
         planes_of<N>(p, w);
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
-          if (!FULL && 32 * d >= dv) continue;
           frag a[IN];
           lds.v[b].cols(32 * kb + 16 * st, 32 * d, lane, a);
           o[d] = mma_planes<N>(a, w, o[d]);

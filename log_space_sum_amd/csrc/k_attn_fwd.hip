@@ -60,7 +60,7 @@ template <typename T>
 void fwd(const AttnArgs& a, hipStream_t s) {
   const int64_t slots = a.tokens * a.group / ATTN_ROWS + a.seqs;
   const dim3 grid((uint32_t)std::min<int64_t>(slots * a.nsplit * a.kv_heads, 1 << 23));
-  by_fit<T>(fit_of<T>(a, false), [&](auto d, auto mode) {
+  by_fit(fit_of<T>(a, false), [&](auto d, auto mode) {
     launch_kernel(attn_fwd<T, decltype(d)::value, decltype(mode)::value>, grid, dim3(256), 0, s, a, slots);
   });
 }
