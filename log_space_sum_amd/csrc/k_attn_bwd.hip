@@ -290,11 +290,11 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || MODE == ANY ? 1 : 2) void a
 #pragma unroll
         for (int st = 0; st < DS; ++st) {
           frag f[IN];
-          {
+          if (32 * (st / 2) < dk) {
             lds.k[x].rows(32 * kb, st, lane, f);
             s = mma_planes<N>(f, q[st], s);
           }
-          {
+          if (32 * (st / 2) < dv) {
             lds.v[x].rows(32 * kb, st, lane, f);
             dp = mma_planes<N>(f, go[st], dp);
           }
@@ -322,6 +322,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || MODE == ANY ? 1 : 2) void a
           planes_of<N>(p, w);
 #pragma unroll
           for (int d = 0; d < DB; ++d) {
+            if (32 * d >= dk) continue;
             frag f[IN];
             lds.k[x].cols(32 * kb + 16 * st, 32 * d, lane, f);
             acc[d] = mma_planes<N>(f, w, acc[d]);
@@ -503,11 +504,11 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
 #pragma unroll
       for (int st = 0; st < DS; ++st) {
         frag f[IN];
-        {
+        if (32 * (st / 2) < dk) {
           lds.q[x].rows(0, st, lane, f);
           s = mma_planes<N>(f, k[st], s);
         }
-        {
+        if (32 * (st / 2) < dv) {
           lds.go[x].rows(0, st, lane, f);
           dp = mma_planes<N>(f, v[st], dp);
         }
@@ -541,6 +542,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
         planes_of<N>(p, w);
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
+          if (32 * d >= dv) continue;
           frag f[IN];
           lds.go[x].cols(16 * st, 32 * d, lane, f);
           dva[d] = mma_planes<N>(f, w, dva[d]);
@@ -550,6 +552,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
         planes_of<N>(p, w);
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
+          if (32 * d >= dk) continue;
           frag f[IN];
           lds.q[x].cols(16 * st, 32 * d, lane, f);
           dka[d] = mma_planes<N>(f, w, dka[d]);

@@ -103,10 +103,10 @@ __global__ __launch_bounds__(256, (Num<T>::IN == 3 || MODE == ANY) && D > 64 ? 1
     const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
     const Work<T> w = find_work<T>(a, slots - 1 - b / per, kvh, split, ATTN_ROWS, part_len);
     if (w.rows.count == 0) continue;
-    if (split == 0) join_cache(a, w, kvh);
     if (w.key0 >= w.key1) no_keys(w.rows, w.out);
     else
       attend_tile<T, D, MODE, true>(lds, w.keys, w.rows, w.out, a.dk, a.dv, fabsf(a.scale) * LOG2E, a.scale < 0.0f, w.key0, w.key1);
+    if (split == 0) join_cache(a, w, kvh);
   }
 }
 
@@ -138,7 +138,6 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1
     const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
     const Work<T> w = find_work<T>(a, b / per, kvh, split, ATTN_FEW_ROWS, part_len);
     if (w.rows.count == 0) continue;
-    if (split == 0) join_cache(a, w, kvh);
     if (w.key0 >= w.key1) {
       no_keys(w.rows, w.out);
       continue;
@@ -208,6 +207,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1
       f32x16 s = f32x16{};
 #pragma unroll
       for (int st = 0; st < DS; ++st) {
+        if (IN == 3 && 32 * (st / 2) >= dk) continue;
         frag f[IN];
         lds.own[wave].rows(0, st, lane, f);
         s = mma_planes<N>(f, q[st], s);
@@ -285,20 +285,21 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1
     const bool store = row < w.rows.count;
     if (__syncthreads_or(store && !(bad == 0.0f))) {
       careful_rows<T, true>(w.keys, w.rows, w.out, dk, dv, a.scale * LOG2E, w.key0, w.key1, 4);
-      continue;
-    }
-    if (!store) continue;
-    const int t = w.rows.token(row), head = w.rows.head(row);
-    if ((tid & 7) == 0) put_stat(w.out, t, head, top, sum);
-    const float inv = w.out.part ? 1.0f : 1.0f / sum;
+    } else if (store) {
+      const int t = w.rows.token(row), head = w.rows.head(row);
+      if ((tid & 7) == 0) put_stat(w.out, t, head, top, sum);
+      const float inv = w.out.part ? 1.0f : 1.0f / sum;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-      const int d = 4 * (tid & 7) + 32 * e;
+      for (int e = 0; e < D / 32; ++e) {
+        const int d = 4 * (tid & 7) + 32 * e;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) x[e][r] *= inv;
-      if (w.out.part) store4<float>(w.out.part + ((int64_t)t * w.out.heads + head) * dv + d, x[e], dv - d);
-      else store4<T>((T*)w.out.o + t * w.out.o_ts + head * w.out.o_hs + d, x[e], dv - d);
+        for (int r = 0; r < 4; ++r) x[e][r] *= inv;
+        if (w.out.part) store4<float>(w.out.part + ((int64_t)t * w.out.heads + head) * dv + d, x[e], dv - d);
+        else store4<T>((T*)w.out.o + t * w.out.o_ts + head * w.out.o_hs + d, x[e], dv - d);
+      }
     }
+    // (behind the results: in front, its loads would be waited for before the first keys')
+    if (split == 0) join_cache(a, w, kvh);
   }
 }
 

@@ -296,6 +296,7 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
     for (int kb = 0; kb < KB; ++kb) s[kb] = f32x16{};
 #pragma unroll
     for (int st = 0; st < DS; ++st) {
+      if (IN == 3 && 32 * (st / 2) >= dk) continue;
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         frag a[IN];
@@ -395,6 +396,7 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
         planes_of<N>(p, w);
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
+          if (32 * d >= dv) continue;
           frag a[IN];
           lds.v[b].cols(32 * kb + 16 * st, 32 * d, lane, a);
           o[d] = mma_planes<N>(a, w, o[d]);
