@@ -130,19 +130,44 @@ template <typename T>
 struct Unit {
   T v[8];
 };
-// Elements d .. d + 7 of a row of `dim`; those behind it are 0.  UNITS: dim is a multiple of 8.
+// A row's address that went between lanes as a number.
+template <typename T>
+__device__ __forceinline__ const T* global_row(uint64_t at) {
+  return (const T*)(const __attribute__((address_space(1))) T*)at;
+}
+// Elements d .. d + 7 of a row of `dim`, with the row's first ones in the place of those behind it.  UNITS: dim is a multiple
+// of 8.  Enough for a tile: what is behind the row meets zeros in a contraction, or makes results that are not stored; if it
+// is not finite, nor are sums that are, and the tile is done again carefully.
 template <bool UNITS, typename T>
 __device__ __forceinline__ Unit<T> load_unit(const T* row, int d, int dim) {
-  // (loads that are always done, from the row's start where there is nothing: branches around them would be many)
   Unit<T> u;
   if constexpr (UNITS) {
     __builtin_memcpy(&u, row + (d < dim ? d : 0), sizeof(u));
-    if (d >= dim) u = Unit<T>{};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u.v[e] = row[d + e < dim ? d + e : 0];
+  }
+  return u;
+}
+// The same with zeros behind the row: a wave's own operands.  By masks whose value the compiler cannot see: it would
+// branch around each load's zeros, and wait for the load there (13 ragged streams x 6 heads x 48, 80 float32 over a cache: 35 us for 28).
+template <bool UNITS, typename T>
+__device__ __forceinline__ Unit<T> load_own(const T* row, int d, int dim) {
+  using Bits = std::conditional_t<sizeof(T) == 2, uint16_t, uint32_t>;
+  Unit<T> u = load_unit<UNITS>(row, d, dim);
+  if constexpr (UNITS) {
+    uint32_t mask = d < dim ? ~0u : 0u, x[sizeof(u) / 4];
+    asm("" : "+v"(mask));
+    __builtin_memcpy(x, &u, sizeof(u));
+#pragma unroll
+    for (uint32_t& w : x) w &= mask;
+    __builtin_memcpy(&u, x, sizeof(u));
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      u.v[e] = row[d + e < dim ? d + e : 0];
-      if (d + e >= dim) u.v[e] = T{};
+      uint32_t mask = d + e < dim ? ~0u : 0u;
+      asm("" : "+v"(mask));
+      u.v[e] = __builtin_bit_cast(T, (Bits)(__builtin_bit_cast(Bits, u.v[e]) & (Bits)mask));
     }
   }
   return u;

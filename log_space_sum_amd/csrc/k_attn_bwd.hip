@@ -221,11 +221,11 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || MODE == ANY ? 1 : 2) void a
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
         frag f[IN];
-        frags_of(load_unit<UNIT>(pq, 16 * s + 8 * h, dk), f);
+        frags_of(load_own<UNIT>(pq, 16 * s + 8 * h, dk), f);
         if constexpr (IN == 1) q1[s] = f[0];
         else
           for (int i = 0; i < IN; ++i) q[s][i] = f[i];
-        const Unit<T> g = load_unit<UNIT>(pg, 16 * s + 8 * h, dv), o = load_unit<UNIT>(po, 16 * s + 8 * h, dv);
+        const Unit<T> g = load_own<UNIT>(pg, 16 * s + 8 * h, dv), o = load_own<UNIT>(po, 16 * s + 8 * h, dv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) delta = fmaf(to_f32(g.v[e]), to_f32(o.v[e]), delta);
         frags_of(g, f);
@@ -462,8 +462,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
       const T *pk = (const T*)a.k.p + (at.t0 + key) * a.k.ts + kvh * a.k.hs, *pv = (const T*)a.v.p + (at.t0 + key) * a.v.ts + kvh * a.v.hs;
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
-        frags_of(load_unit<UNIT>(pk, 16 * s + 8 * h, dk), k[s]);
-        frags_of(load_unit<UNIT>(pv, 16 * s + 8 * h, dv), v[s]);
+        frags_of(load_own<UNIT>(pk, 16 * s + 8 * h, dk), k[s]);
+        frags_of(load_own<UNIT>(pv, 16 * s + 8 * h, dv), v[s]);
       }
     }
     f32x16 dka[DB], dva[DB];
@@ -652,10 +652,10 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
 #pragma unroll
     for (int s = 0; s < DS; ++s) {
       frag f[1];
-      frags_of(load_unit<UNIT>(pk, 16 * s + 8 * h, dk), f);
+      frags_of(load_own<UNIT>(pk, 16 * s + 8 * h, dk), f);
       k[s] = f[0];
       if constexpr (DK) {
-        frags_of(load_unit<UNIT>(pv, 16 * s + 8 * h, dv), f);
+        frags_of(load_own<UNIT>(pv, 16 * s + 8 * h, dv), f);
         v[s] = f[0];
       }
     }

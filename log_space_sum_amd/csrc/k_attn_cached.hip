@@ -149,7 +149,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1
       const T* p = w.rows.row(mine);
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
-        frags_of(load_unit<UNIT>(p, 16 * s + 8 * h, dk), q[s]);
+        frags_of(load_own<UNIT>(p, 16 * s + 8 * h, dk), q[s]);
         if (a.scale < 0.0f) {
 #pragma unroll
           for (int i = 0; i < IN; ++i) {
@@ -168,23 +168,28 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1
 
     // Rows are read whole, 16 lanes a row of 128, and go through the wave's part of LDS (a lane with its own key's
     // row would touch each line four times).  The next tile's rows are in flight over a whole tile, its pages looked up a
-    // tile before that.
+    // tile before that.  A lane knows where one row lies: of the tile's keys, or (lanes from 32 on) of its values.
     Unit<T> rk[U], rv[U];
     uint32_t absent = 0;     // keys of the tile in no page
     typename Keys<T, true>::Place place{};
-    auto fetch = [&](int key, auto values) {
+    uint64_t row_at = 0;
+    auto fetch_keys = [&] {
+      const uint64_t keys_at = (uint64_t)w.keys.key_row(place), values_at = (uint64_t)w.keys.value_row(place);
+      row_at = h ? values_at : keys_at;
+      absent = (uint32_t)__ballot(w.keys.none(place));
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int id = u * 64 + lane, r = id / PER_ROW, d = id % PER_ROW * 8;
-        const T *kr, *vr;
-        w.keys.rows_of({__shfl(place.page, r), __shfl(place.row, r)}, kr, vr);
-        if constexpr (decltype(values)::value) rv[u] = load_unit<UNIT>(vr, d, dv);
-        else rk[u] = load_unit<UNIT>(kr, d, dk);
+        const int id = u * 64 + lane;
+        rk[u] = load_unit<UNIT>(global_row<T>(__shfl(row_at, id / PER_ROW)), id % PER_ROW * 8, dk);
       }
-      if constexpr (decltype(values)::value) {
-        if (key + 128 < w.key1) place = w.keys.locate(key + 128 + (lane & 31));
-      } else {
-        absent = (uint32_t)__ballot(place.page != w.keys.NEW && (uint32_t)place.page >= (uint32_t)w.keys.num_pages);
+    };
+    auto fetch_values = [&](int key) {
+      // (asked for in front of the values, which need not be there when it is used)
+      if (key + 128 < w.key1) place = w.keys.locate(key + 128 + (lane & 31));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int id = u * 64 + lane;
+        rv[u] = load_unit<UNIT>(global_row<T>(__shfl(row_at, 32 + id / PER_ROW)), id % PER_ROW * 8, dv);
       }
     };
     auto put = [&](const Unit<T>(&x)[U]) {
@@ -196,14 +201,14 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1
     int key = w.key0 + 32 * wave;
     if (key < w.key1) {
       place = w.keys.locate(key + (lane & 31));
-      fetch(key, std::false_type{});
-      fetch(key, std::true_type{});
+      fetch_keys();
+      fetch_values(key);
     }
     for (; key < w.key1; key += 128) {
       const bool more = key + 128 < w.key1;
       const uint32_t gone = absent;
       put(rk);
-      if (more) fetch(key + 128, std::false_type{});
+      if (more) fetch_keys();
       f32x16 s = f32x16{};
 #pragma unroll
       for (int st = 0; st < DS; ++st) {
@@ -214,7 +219,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1
       }
       wave_fence();
       put(rv);
-      if (more) fetch(key + 128, std::true_type{});
+      if (more) fetch_values(key + 128);
       if (key + 31 > first_last || gone) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)

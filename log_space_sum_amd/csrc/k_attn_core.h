@@ -49,25 +49,25 @@ struct Keys {
     vr = v + (int64_t)j * v_ts;
     return true;
   }
-  // The same in two steps, so that a tile's pages are looked up a tile ahead: where position j lies, and the rows of a place.
-  static constexpr int NEW = -1, NONE = -2;
+  // The same in two steps, so that a tile's pages are looked up a tile ahead: where position j lies, and the rows of a
+  // place.  Nothing is made of the page in the first, which would wait for it.
   struct Place {
-    int page, row;         // NEW: row of the new tokens
+    int page, row;         // row < 0: the new token -1 - row
   };
   __device__ __forceinline__ Place locate(int j) const {
     j = min(j, total - 1);
-    if (j >= past) return {NEW, j - past};
-    const int i = (int)(((uint64_t)(uint32_t)j * magic) >> shift), p = table[i];
-    return {p < 0 ? NONE : p, j - i * page_size};
+    const int i = (int)(((uint64_t)(uint32_t)j * magic) >> shift);
+    Place at{0, past - 1 - j};
+    if (j < past) at = {table[i], j - i * page_size};
+    return at;
   }
-  // false: in no page (any rows then)
-  __device__ __forceinline__ bool rows_of(Place at, const T*& kr, const T*& vr) const {
-    const bool fresh = at.page == NEW, ok = fresh || (uint32_t)at.page < (uint32_t)num_pages;
-    const bool cached = ok && !fresh;
-    const int64_t page = cached ? at.page : 0, row = ok ? at.row : 0;
-    kr = (cached ? kc : k) + page * k_page + row * (cached ? k_row : k_ts);
-    vr = (cached ? vc : v) + page * v_page + row * (cached ? v_row : v_ts);
-    return ok;
+  __device__ __forceinline__ bool none(Place at) const { return at.row >= 0 && (uint32_t)at.page >= (uint32_t)num_pages; }
+  // The rows of keys and values; of a place in no page any.
+  __device__ __forceinline__ const T* key_row(Place at) const { return row_of(at, kc, k_page, k_row, k, k_ts); }
+  __device__ __forceinline__ const T* value_row(Place at) const { return row_of(at, vc, v_page, v_row, v, v_ts); }
+  __device__ __forceinline__ const T* row_of(Place at, const T* cache, int64_t page, int64_t row, const T* fresh, int64_t ts) const {
+    const bool cached = at.row >= 0 && !none(at);
+    return (cached ? cache : fresh) + (cached ? at.page : 0) * page + (at.row < 0 ? -1 - at.row : cached ? at.row : 0) * (cached ? row : ts);
   }
   __device__ __forceinline__ bool there(int j) const {
     if constexpr (!PAGED) return true;
@@ -212,7 +212,7 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
     const T* p = rows.row(mine);
 #pragma unroll
     for (int s = 0; s < DS; ++s) {
-      frags_of(load_unit<UNIT>(p, 16 * s + 8 * h, dk), q[s]);
+      frags_of(load_own<UNIT>(p, 16 * s + 8 * h, dk), q[s]);
       if (negative) {
 #pragma unroll
         for (int i = 0; i < IN; ++i) {
@@ -239,17 +239,14 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
   auto load = [&](int b, int key) {
     const uint32_t kb = lds_byte(lds.k[b].at) + wave * 1024, vb = lds_byte(lds.v[b].at) + wave * 1024;
     if constexpr (PAGED) {
-      bool gone = false;
-      const auto place = next;       // of position key + lane
+      const auto kr = (uint64_t)keys.key_row(next), vr = (uint64_t)keys.value_row(next);      // of position key + lane
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const T *kr, *vr;
         const int r = unit.row + u * unit.STEP;
-        gone |= !keys.rows_of({__shfl(place.page, r), __shfl(place.row, r)}, kr, vr);
-        lds_load16_at((const char*)kr + kbyte, kb + u * 4096);
-        lds_load16_at((const char*)vr + vbyte, vb + u * 4096);
+        lds_load16_at((const char*)__shfl(kr, r) + kbyte, kb + u * 4096);
+        lds_load16_at((const char*)__shfl(vr, r) + vbyte, vb + u * 4096);
       }
-      if (gone) lds.absent[b] = key;
+      if (keys.none(next)) lds.absent[b] = key;
       if (key + BK < key1) next = keys.locate(key + BK + lane);
     } else {
       const T *kr = keys.k + (int64_t)key * keys.k_ts, *vr = keys.v + (int64_t)key * keys.v_ts;
