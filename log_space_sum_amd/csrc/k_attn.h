@@ -206,6 +206,22 @@ struct Tile {
 #pragma unroll
     for (int p = 0; p < Num<T>::IN; ++p) *(frag*)(at + p * PLANE + row * P + (d ^ turn(row) * 8)) = f[p];
   }
+  // Units first, first + STEP, .. of the tile (STEP threads take the units of whole rows): row and element of the first
+  // and u are apart, which keeps the addresses few.
+  template <int STEP, int U>
+  __device__ __forceinline__ void put_all(int first, const Unit<T> (&x)[U]) {
+    constexpr int PER_ROW = P / 8, ROWS_STEP = STEP / PER_ROW;
+    static_assert(STEP % PER_ROW == 0 && (ROWS_STEP & (ROWS_STEP - 1)) == 0, "turn(a + b) = turn(a) ^ turn(b) where no bit is in both");
+    const int row = first / PER_ROW, at0 = row * P + (first % PER_ROW ^ turn(row)) * 8;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      frag f[Num<T>::IN];
+      frags_of(x[u], f);
+#pragma unroll
+      for (int p = 0; p < Num<T>::IN; ++p)
+        *(frag*)(at + p * PLANE + (at0 ^ turn(u * ROWS_STEP) * 8) + u * ROWS_STEP * P) = f[p];
+    }
+  }
   // Rows row0 + l (row0 a multiple of 32), elements 16 step + 8 h ..: the operand whose rows are the tile's.
   __device__ __forceinline__ void rows(int row0, int step, int lane, frag (&out)[Num<T>::IN]) const {
     const int l = lane & 31, x = (turn(l) ^ (lane >> 5)) * 8;

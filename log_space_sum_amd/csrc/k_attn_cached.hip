@@ -193,33 +193,43 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1
       }
     };
     auto put = [&](const Unit<T>(&x)[U]) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) lds.own[wave].put((u * 64 + lane) / PER_ROW, (u * 64 + lane) % PER_ROW * 8, x[u]);
+      lds.own[wave].template put_all<64>(lane, x);
       wave_fence();
     };
     __syncthreads();          // the last work's readers are done
     int key = w.key0 + 32 * wave;
-    if (key < w.key1) {
-      place = w.keys.locate(key + (lane & 31));
-      fetch_keys();
-      fetch_values(key);
-    }
-    for (; key < w.key1; key += 128) {
-      const bool more = key + 128 < w.key1;
+    // (also a wave without a tile, of the last row: with a branch, the rows of q would be waited for as the last loads)
+    place = w.keys.locate(key + (lane & 31));
+    fetch_keys();
+    fetch_values(key);
+    for (bool more = key < w.key1; more; key += 128) {
       const uint32_t gone = absent;
-      put(rk);
-      if (more) fetch_keys();
-      f32x16 s = f32x16{};
+      f32x16 s;
+      auto scores = [&] {
+        int here = lane;     // (addresses are made again: held over the loop, they would cost a load in flight)
+        asm volatile("" : "+v"(here));
+        s = f32x16{};
 #pragma unroll
-      for (int st = 0; st < DS; ++st) {
-        if (IN == 3 && 32 * (st / 2) >= dk) continue;
-        frag f[IN];
-        lds.own[wave].rows(0, st, lane, f);
-        s = mma_planes<N>(f, q[st], s);
+        for (int st = 0; st < DS; ++st) {
+          if (IN == 3 && 32 * (st / 2) >= dk) continue;
+          frag f[IN];
+          lds.own[wave].rows(0, st, here, f);
+          s = mma_planes<N>(f, q[st], s);
+        }
+        wave_fence();
+      };
+      more = key + 128 < w.key1;
+      put(rk);
+      // (two copies: with a branch at either fetch, the keys would be waited for as if no values came behind them)
+      if (more) {
+        fetch_keys();
+        scores();
+        put(rv);
+        fetch_values(key + 128);
+      } else {
+        scores();
+        put(rv);
       }
-      wave_fence();
-      put(rv);
-      if (more) fetch_values(key + 128);
       if (key + 31 > first_last || gone) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
