@@ -78,8 +78,8 @@ __device__ __forceinline__ float dot(const T* a, const T* b, int n) {
 // s = A x^T and, with BOTH, dp = B y^T for 32 rows of two tiles and a wave's own operands.  The rows of A are
 // all asked for before they are used, those of B meanwhile; a single product goes in two chains.
 template <typename T, int D, bool UNIT, bool BOTH, typename TileT>
-__device__ __forceinline__ void block_products(const TileT& ta, const TileT& tb, int r0, int lane, const frag (&x)[D / 16],
-                                               const frag (&y)[BOTH ? D / 16 : 1], f32x16& s, f32x16& dp) {
+__device__ __forceinline__ void block_products(const TileT& ta, const TileT& tb, int r0, int lane, const frag (&x)[D / 16][1],
+                                               const frag (&y)[BOTH ? D / 16 : 1][1], f32x16& s, f32x16& dp) {
   using N = Num<T>;
   constexpr int DS = D / 16;
   frag fa[DS][1], fb[BOTH ? DS : 1][1];
@@ -92,17 +92,17 @@ __device__ __forceinline__ void block_products(const TileT& ta, const TileT& tb,
   for (int st = 0; st < DS; ++st) {
     if constexpr (BOTH) {
       tb.rows(r0, st, lane, fb[st]);
-      s = N::mma(fa[st][0], x[st], s);
+      s = N::mma(fa[st][0], x[st][0], s);
       if (UNIT) __builtin_amdgcn_sched_barrier(0);
     } else {
-      if (st & 1) dp = N::mma(fa[st][0], x[st], dp);
-      else s = N::mma(fa[st][0], x[st], s);
+      if (st & 1) dp = N::mma(fa[st][0], x[st][0], dp);
+      else s = N::mma(fa[st][0], x[st][0], s);
     }
   }
   if constexpr (BOTH) {
 #pragma unroll
     for (int st = 0; st < DS; ++st)
-      dp = N::mma(fb[st][0], y[st], dp);
+      dp = N::mma(fb[st][0], y[st][0], dp);
   } else {
     s += dp;
   }
@@ -213,25 +213,18 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || MODE == ANY ? 1 : 2) void a
     const Part part = part_of(a, split, 0, end);
     if (part.from >= part.to) continue;
     const float lse2 = a.lse[t * heads + head] * LOG2E;
-    frag q[IN == 1 ? 1 : DS][IN], go[IN == 1 ? 1 : DS][IN], q1[DS], go1[DS];    // (planes; one plane)
+    frag q[DS][IN], go[DS][IN];
     float delta = 0.0f;
     {
       const T *pq = (const T*)a.q.p + t * a.q.ts + head * a.q.hs, *pg = (const T*)a.d_o.p + t * a.d_o.ts + head * a.d_o.hs;
       const T* po = (const T*)a.out.p + t * a.out.ts + head * a.out.hs;
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
-        frag f[IN];
-        frags_of(load_own<UNIT>(pq, 16 * s + 8 * h, dk), f);
-        if constexpr (IN == 1) q1[s] = f[0];
-        else
-          for (int i = 0; i < IN; ++i) q[s][i] = f[i];
+        frags_of(load_own<UNIT>(pq, 16 * s + 8 * h, dk), q[s]);
         const Unit<T> g = load_own<UNIT>(pg, 16 * s + 8 * h, dv), o = load_own<UNIT>(po, 16 * s + 8 * h, dv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) delta = fmaf(to_f32(g.v[e]), to_f32(o.v[e]), delta);
-        frags_of(g, f);
-        if constexpr (IN == 1) go1[s] = f[0];
-        else
-          for (int i = 0; i < IN; ++i) go[s][i] = f[i];
+        frags_of(g, go[s]);
       }
       delta = add_halves(delta);
       if (split == 0 && h == 0 && wave_first + lane < count) a.delta[t * heads + head] = delta;
@@ -285,7 +278,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || MODE == ANY ? 1 : 2) void a
       for (int kb = 0; kb < KB; ++kb) {
         f32x16 s = f32x16{}, dp = f32x16{};
         if constexpr (IN == 1) {
-          block_products<T, D, UNIT, true>(lds.k[x], lds.v[x], 32 * kb, lane, q1, go1, s, dp);
+          block_products<T, D, UNIT, true>(lds.k[x], lds.v[x], 32 * kb, lane, q, go, s, dp);
         } else {
 #pragma unroll
         for (int st = 0; st < DS; ++st) {
@@ -386,16 +379,6 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || MODE == ANY ? 1 : 2) void a
 }
 
 // ---- dk, dv ---------------------------------------------------------------------
-template <typename T, int D>
-struct DkvShape {
-  static constexpr int IN = Num<T>::IN, BR = 32, BUFS = IN == 3 ? 1 : 2;
-  struct Lds {
-    Tile<T, BR, D> q[BUFS], go[BUFS];
-    alignas(16) float lse2[BUFS][BR];
-    alignas(16) float delta[BUFS][BR];
-  };
-};
-
 template <typename T>
 __device__ __attribute__((noinline)) void careful_dkv(AttnArgs a, int64_t t0, int64_t first, int count, int kvh, int nwaves, int split, Part part) {
   const int lane = threadIdx.x & 63, heads = a.kv_heads * a.group;
@@ -434,191 +417,13 @@ __device__ __attribute__((noinline)) void careful_dkv(AttnArgs a, int64_t t0, in
   }
 }
 
-template <typename T, int D, FitMode MODE>
-__global__ __launch_bounds__(256, 1) void attn_dkv(AttnArgs a, int64_t slots) {
-  using N = Num<T>;
-  constexpr bool UNIT = MODE == UNITS;
-  using S = DkvShape<T, D>;
-  constexpr int IN = N::IN, W = N::W, BR = S::BR, BUFS = S::BUFS, DS = D / 16, DB = D / 32;
-  constexpr int PER_ROW = Tile<T, 32, D>::P / 8, U = BR * PER_ROW / 256;
-  __shared__ typename S::Lds lds;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
-  const int heads = a.kv_heads * a.group, dk = a.dk, dv = a.dv;
-  const float c = a.scale * LOG2E;
-  for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
-    const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
-    const int64_t slot = b / a.kv_heads / a.nsplit;
-    // a sequence's first keys, which have the most rows, first
-    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, 1, ATTN_ROWS, slot);
-    const int64_t first64 = at.tile * ATTN_ROWS;
-    if (at.seq < 0 || first64 >= at.len) continue;
-    const int len = (int)at.len, first = (int)first64, count = min(ATTN_ROWS, len - first);
-    const Part part = part_of(a, split, first, len);
-    if (part.from >= part.to) continue;
-    const int key = first + min(32 * wave + (lane & 31), count - 1), wave_key = first + 32 * wave;
-    const bool wave_on = 32 * wave < count;
-    frag k[DS][IN], v[DS][IN];
-    {
-      const T *pk = (const T*)a.k.p + (at.t0 + key) * a.k.ts + kvh * a.k.hs, *pv = (const T*)a.v.p + (at.t0 + key) * a.v.ts + kvh * a.v.hs;
-#pragma unroll
-      for (int s = 0; s < DS; ++s) {
-        frags_of(load_own<UNIT>(pk, 16 * s + 8 * h, dk), k[s]);
-        frags_of(load_own<UNIT>(pv, 16 * s + 8 * h, dv), v[s]);
-      }
-    }
-    f32x16 dka[DB], dva[DB];
-#pragma unroll
-    for (int d = 0; d < DB; ++d) dka[d] = dva[d] = f32x16{};
-    Scale<T> scale;
-
-    Unit<T> rq[U], rg[U];
-    float rl = 0.0f, rd = 0.0f;
-    auto fetch = [&](int head, int row) {
-      const T *q0 = (const T*)a.q.p + at.t0 * a.q.ts + head * a.q.hs, *g0 = (const T*)a.d_o.p + at.t0 * a.d_o.ts + head * a.d_o.hs;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int id = u * 256 + tid, i = min(row + id / PER_ROW, len - 1), d = id % PER_ROW * 8;
-        rq[u] = load_unit<UNIT>(q0 + i * a.q.ts, d, dk);
-        rg[u] = load_unit<UNIT>(g0 + i * a.d_o.ts, d, dv);
-      }
-      if (tid < BR) {
-        const int64_t i = (at.t0 + min(row + tid, len - 1)) * heads + head;
-        rl = a.lse[i] * LOG2E;
-        rd = a.delta[i];
-      }
-    };
-    auto stage = [&](int x) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int id = u * 256 + tid;
-        lds.q[x].put(id / PER_ROW, id % PER_ROW * 8, rq[u]);
-        lds.go[x].put(id / PER_ROW, id % PER_ROW * 8, rg[u]);
-      }
-      if (tid < BR) {
-        lds.lse2[x][tid] = rl;
-        lds.delta[x][tid] = rd;
-      }
-    };
-    auto compute = [&](int x, int row) {
-      f32x16 s = f32x16{}, dp = f32x16{};
-#pragma unroll
-      for (int st = 0; st < DS; ++st) {
-        frag f[IN];
-        if (32 * (st / 2) < dk) {
-          lds.q[x].rows(0, st, lane, f);
-          s = mma_planes<N>(f, k[st], s);
-        }
-        if (32 * (st / 2) < dv) {
-          lds.go[x].rows(0, st, lane, f);
-          dp = mma_planes<N>(f, v[st], dp);
-        }
-      }
-      const bool edge = row < wave_key + 31 || row + 32 > len;
-#pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        const f32x4 l4 = *(const f32x4*)&lds.lse2[x][8 * r4 + 4 * h], d4 = *(const f32x4*)&lds.delta[x][8 * r4 + 4 * h];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[4 * r4 + e] = exp2_fast(fmaf(s[4 * r4 + e], c, -l4[e]));
-          dp[4 * r4 + e] -= d4[e];
-        }
-      }
-      if (edge) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int i = row + row_of(r, h);
-          s[r] = masked(s[r], i < key || i >= len, 0.0f);
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) dp[r] *= s[r];
-      scale.move(dp, dka);
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        float p[8];
-        frag w[W];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = N::BIAS ? s[8 * st + e] * (float)(1 << N::BIAS) : s[8 * st + e];
-        planes_of<N>(p, w);
-#pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          if (32 * d >= dv) continue;
-          frag f[IN];
-          lds.go[x].cols(16 * st, 32 * d, lane, f);
-          dva[d] = mma_planes<N>(f, w, dva[d]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = dp[8 * st + e];
-        planes_of<N>(p, w);
-#pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          if (32 * d >= dk) continue;
-          frag f[IN];
-          lds.q[x].cols(16 * st, 32 * d, lane, f);
-          dka[d] = mma_planes<N>(f, w, dka[d]);
-        }
-      }
-    };
-    const int row0 = part.from;      // (a multiple of BR)
-    const int h0 = kvh * a.group, h1 = h0 + a.group;
-    __syncthreads();
-    int head = h0, row = row0, x = 0;
-    fetch(head, row);
-    if constexpr (BUFS == 2) {
-      stage(0);
-      __syncthreads();
-    }
-    while (head < h1) {
-      int nh = head, nr = row + BR;
-      if (nr >= part.to) {
-        nr = row0;
-        ++nh;
-      }
-      if constexpr (BUFS == 1) {
-        stage(0);
-        __syncthreads();
-      }
-      if (nh < h1) fetch(nh, nr);
-      if (wave_on && row + 31 >= wave_key) compute(x, row);
-      if constexpr (BUFS == 2) {
-        if (nh < h1) stage(x ^ 1);
-        x ^= 1;
-      }
-      __syncthreads();
-      head = nh;
-      row = nr;
-    }
-    const bool store = 32 * wave + (lane & 31) < count;
-    if (__syncthreads_or(store && (any_not_finite(dka) || any_not_finite(dva)))) {
-      careful_dkv<T>(a, at.t0, first, count, kvh, 4, split, part);
-      continue;
-    }
-    if (!store) continue;
-    const int64_t sum = ((int64_t)split * a.tokens + at.t0 + key) * a.kv_heads + kvh;
-    const float fk = a.scale / scale.by, fv = 1.0f / (float)(1 << N::BIAS);
-    T *tk = (T*)a.dk_ + (at.t0 + key) * a.dk_ts + kvh * a.dk_hs, *tv = (T*)a.dv_ + (at.t0 + key) * a.dv_ts + kvh * a.dv_hs;
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int e = 32 * d + 8 * r + 4 * h;
-        const float y[4] = {dka[d][4 * r] * fk, dka[d][4 * r + 1] * fk, dka[d][4 * r + 2] * fk, dka[d][4 * r + 3] * fk};
-        if (a.nsplit > 1) store4<float>(a.part_k + sum * dk + e, y, dk - e);
-        else store4<T>(tk + e, y, dk - e);
-        const float z[4] = {dva[d][4 * r] * fv, dva[d][4 * r + 1] * fv, dva[d][4 * r + 2] * fv, dva[d][4 * r + 3] * fv};
-        if (a.nsplit > 1) store4<float>(a.part_v + sum * dv + e, z, dv - e);
-        else store4<T>(tv + e, z, dv - e);
-      }
-  }
-}
-
-// The same for 16-bit types with eight waves: a pair of waves shares 32 keys, the first makes their dv (from
-// S and P), the second their dk (from S, dP and dS), so that either fits the registers of two waves a SIMD.  S is
-// made twice (9 products' work for 8).
+// A pair of waves shares 32 keys, the first makes their dv (from S and P), the second their dk (from S, dP and
+// dS), so that either fits the registers of two waves a SIMD.  S is made twice (9 products' work for 8).
 constexpr int PAIRS = 2;
 template <typename T, int D>
 struct PairShape {
-  static constexpr int BR = 64, KEYS = 32 * PAIRS, NT = 128 * PAIRS;
+  static constexpr bool F32 = Num<T>::IN == 3;
+  static constexpr int BR = F32 ? 32 : 64, KEYS = 32 * PAIRS, NT = 128 * PAIRS;
   struct Lds {
     Tile<T, BR, D> q[2], go[2];
     alignas(16) float lse2[2][BR];
@@ -627,13 +432,13 @@ struct PairShape {
   };
 };
 
-// One wave's part of a tile of 128 keys: DK: dk, else dv, of its 32.
+// One wave's part of a tile of keys: DK: dk, else dv, of its 32.
 template <typename T, int D, FitMode MODE, bool DK>
 __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, const AttnArgs& a, const SeqTile& at, int kvh, int split) {
   using N = Num<T>;
-  constexpr bool UNIT = MODE == UNITS;
   using S = PairShape<T, D>;
-  constexpr int W = N::W, BR = S::BR, DS = D / 16, DB = D / 32, NT = S::NT;
+  constexpr bool UNIT = MODE == UNITS, DIRECT = UNIT && !S::F32;
+  constexpr int IN = N::IN, W = N::W, BR = S::BR, DS = D / 16, DB = D / 32, NT = S::NT;
   constexpr int PER_ROW = Tile<T, 32, D>::P / 8, U = BR * PER_ROW / NT;
   const int tid = thread_here(), wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, h = lane >> 5;
   const int heads = a.kv_heads * a.group, dk = a.dk, dv = a.dv;
@@ -646,18 +451,13 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
   if (part.from >= part.to) return;     // (every wave)
   const int key = first + min(block + (lane & 31), count - 1), wave_key = first + block;
   const bool wave_on = block < count;
-  frag k[DS], v[DK ? DS : 1];
+  frag k[DS][IN], v[DK ? DS : 1][IN];
   {
     const T *pk = (const T*)a.k.p + (at.t0 + key) * a.k.ts + kvh * a.k.hs, *pv = (const T*)a.v.p + (at.t0 + key) * a.v.ts + kvh * a.v.hs;
 #pragma unroll
     for (int s = 0; s < DS; ++s) {
-      frag f[1];
-      frags_of(load_own<UNIT>(pk, 16 * s + 8 * h, dk), f);
-      k[s] = f[0];
-      if constexpr (DK) {
-        frags_of(load_own<UNIT>(pv, 16 * s + 8 * h, dv), f);
-        v[s] = f[0];
-      }
+      frags_of(load_own<UNIT>(pk, 16 * s + 8 * h, dk), k[s]);
+      if constexpr (DK) frags_of(load_own<UNIT>(pv, 16 * s + 8 * h, dv), v[s]);
     }
   }
   f32x16 acc[DB];
@@ -665,11 +465,11 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
   for (int d = 0; d < DB; ++d) acc[d] = f32x16{};
   Scale<T> scale;
 
-  Unit<T> rq[UNIT ? 1 : U], rg[UNIT ? 1 : U];
+  Unit<T> rq[DIRECT ? 1 : U], rg[DIRECT ? 1 : U];
   float rs = 0.0f;
   auto fetch = [&](int x, int head, int row) {
     const T *q0 = (const T*)a.q.p + (at.t0 + row) * a.q.ts + head * a.q.hs, *g0 = (const T*)a.d_o.p + (at.t0 + row) * a.d_o.ts + head * a.d_o.hs;
-    if constexpr (UNIT) {
+    if constexpr (DIRECT) {
       const uint32_t qb = lds_byte(lds.q[x].at) + wave * 1024, gb = lds_byte(lds.go[x].at) + wave * 1024;
       if (row + BR <= len) {
 #pragma unroll
@@ -700,7 +500,7 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
     }
   };
   auto stage = [&](int x) {
-    if constexpr (!UNIT) {
+    if constexpr (!DIRECT) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int id = u * NT + tid;
@@ -713,7 +513,24 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
   };
   auto compute = [&](int x, int row, int r0) {
     f32x16 s, dp;
-    block_products<T, D, UNIT, DK>(lds.q[x], lds.go[x], r0, lane, k, v, s, dp);
+    if constexpr (IN == 1) {
+      block_products<T, D, UNIT, DK>(lds.q[x], lds.go[x], r0, lane, k, v, s, dp);
+    } else {
+      s = dp = f32x16{};
+#pragma unroll
+      for (int st = 0; st < DS; ++st) {
+        frag f[IN];
+        if (32 * (st / 2) < dk) {
+          lds.q[x].rows(r0, st, lane, f);
+          s = mma_planes<N>(f, k[st], s);
+        }
+        if constexpr (DK)
+          if (32 * (st / 2) < dv) {
+            lds.go[x].rows(r0, st, lane, f);
+            dp = mma_planes<N>(f, v[st], dp);
+          }
+      }
+    }
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
       const f32x4 l4 = *(const f32x4*)&lds.lse2[x][r0 + 8 * r4 + 4 * h];
@@ -735,13 +552,29 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
         for (int e = 0; e < 4; ++e) s[4 * r4 + e] *= dp[4 * r4 + e] - d4[e];
       }
       scale.move(s, acc);
-      block_add<T, D, UNIT>(lds.q[x], r0, lane, s, acc);
-    } else {
-      if (N::BIAS) {
+    } else if (N::BIAS) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] *= (float)(1 << N::BIAS);
+      for (int r = 0; r < 16; ++r) s[r] *= (float)(1 << N::BIAS);
+    }
+    const auto& by = DK ? lds.q[x] : lds.go[x];
+    if constexpr (IN == 1) {
+      block_add<T, D, UNIT>(by, r0, lane, s, acc);
+    } else {
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        float p[8];
+        frag w[W];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = s[8 * st + e];
+        planes_of<N>(p, w);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+          if (32 * d >= (DK ? dk : dv)) continue;
+          frag f[IN];
+          by.cols(r0 + 16 * st, 32 * d, lane, f);
+          acc[d] = mma_planes<N>(f, w, acc[d]);
+        }
       }
-      block_add<T, D, UNIT>(lds.go[x], r0, lane, s, acc);
     }
   };
   const int h0 = kvh * a.group, h1 = h0 + a.group;      // rows from the tile's first key on attend it
@@ -794,7 +627,7 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
 }
 
 template <typename T, int D, FitMode MODE>
-__global__ __launch_bounds__(128 * PAIRS, MODE == ANY ? 1 : 2) void attn_dkv_pairs(AttnArgs a, int64_t slots) {
+__global__ __launch_bounds__(128 * PAIRS, MODE == ANY || (PairShape<T, D>::F32 && D > 64) ? 1 : 2) void attn_dkv(AttnArgs a, int64_t slots) {
   __shared__ typename PairShape<T, D>::Lds lds;
   for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
     const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
@@ -814,13 +647,8 @@ void bwd(const AttnArgs& a, hipStream_t s) {
     constexpr FitMode MODE = decltype(mode)::value;
     const int64_t rows = a.tokens * a.group / ATTN_ROWS + a.seqs;
     launch_kernel(attn_dq<T, D, MODE>, grid(rows), dim3(256), 0, s, a, rows);
-    if constexpr (Num<T>::IN == 1) {
-      const int64_t keys = a.tokens / PairShape<T, D>::KEYS + a.seqs;
-      launch_kernel(attn_dkv_pairs<T, D, MODE>, grid(keys), dim3(PairShape<T, D>::NT), 0, s, a, keys);
-    } else {
-      const int64_t keys = a.tokens / ATTN_ROWS + a.seqs;
-      launch_kernel(attn_dkv<T, D, MODE>, grid(keys), dim3(256), 0, s, a, keys);
-    }
+    const int64_t keys = a.tokens / PairShape<T, D>::KEYS + a.seqs;
+    launch_kernel(attn_dkv<T, D, MODE>, grid(keys), dim3(PairShape<T, D>::NT), 0, s, a, keys);
   });
 }
 
