@@ -569,22 +569,23 @@ typedef struct pc_attention {
   const int32_t* page_table;   /* device int32 [num_seqs, max_pages], rows at page_table_stride */
   int64_t page_table_stride;
   const int32_t* cached;       /* device int32 [num_seqs]: tokens that the cache holds of each sequence */
-  int64_t max_seqlen;          /* bounds of the new tokens of a sequence and of all its tokens, for the choice */
-  int64_t max_length;          /* of the split (results do not depend on them beyond rounding) */
+  /* Bounds of a sequence's (new) tokens, and over a cache of all its tokens, for the choice of the split: results do not
+   * depend on them beyond rounding, and one that is too small only costs speed. */
+  int64_t max_seqlen, max_length;
 } pc_attention;
 
 /* Workspace of the forward (backward 0) or backward (1) pass. */
 int pc_attention_workspace_bytes(const pc_attention* d, int backward, size_t* bytes);
 
-/* Whole sequences: o (and lse) from q, k, v.
- * Errors: PC_ERR_INVALID_ARG, PC_ERR_UNSUPPORTED (dims above 128, unknown
- * dtype), PC_ERR_WORKSPACE, PC_ERR_HIP. */
+/* Whole sequences: o (and lse) from q, k, v.  Without a workspace (ws NULL) the keys of
+ * long sequences are not cut into parts, which is slower where there are few rows.
+ * Errors of these calls: PC_ERR_INVALID_ARG, PC_ERR_UNSUPPORTED (dims above 128, unknown
+ * dtype), PC_ERR_WORKSPACE, PC_ERR_HIP.  Results are the same bits at every run of the same call. */
 int pc_attention_forward(int device, const pc_attention* d, void* ws, size_t ws_bytes, void* stream);
 
 /* The gradients d_q, d_k, d_v from d_o, q, k, v and the forward's o and lse (P is
  * exp(scale q . k - lse) and the rows' sums are d_o . o, of the o and lse given); those
- * of a shared key / value head are summed in float32 over the heads that share it.
- * Results are the same bits at every run. */
+ * of a shared key / value head are summed in float32 over the heads that share it. */
 int pc_attention_backward(int device, const pc_attention* d, void* ws, size_t ws_bytes, void* stream);
 
 /* New tokens over a cache: sequence i has cached[i] tokens in the cache (clamped to

@@ -239,7 +239,17 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
   auto load = [&](int b, int key) {
     const uint32_t kb = lds_byte(lds.k[b].at) + wave * 1024, vb = lds_byte(lds.v[b].at) + wave * 1024;
     if constexpr (PAGED) {
-      const auto kr = (uint64_t)keys.key_row(next), vr = (uint64_t)keys.value_row(next);      // of position key + lane
+      uint64_t kr, vr;       // rows of position key + lane
+      if (key + BK <= keys.past) {
+        // (all in the cache, strides of 32 bits: a quarter of the general form's instructions, of which a tile has
+        // as many as its matrix instructions leave room for; four chunks of 512 behind 8192 587 us without)
+        const uint32_t page = keys.none(next) ? 0u : (uint32_t)next.page, row = (uint32_t)next.row;
+        kr = (uint64_t)keys.kc + (uint64_t)page * (uint32_t)(2 * keys.k_page) + (uint64_t)row * (uint32_t)(2 * keys.k_row);
+        vr = (uint64_t)keys.vc + (uint64_t)page * (uint32_t)(2 * keys.v_page) + (uint64_t)row * (uint32_t)(2 * keys.v_row);
+      } else {
+        kr = (uint64_t)keys.key_row(next);
+        vr = (uint64_t)keys.value_row(next);
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = unit.row + u * unit.STEP;

@@ -558,6 +558,14 @@ def test_attention_cached_in_parts(new, typ):
     c.check(max_length=600)      # too small a bound: the last part is long
 
 
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("total", [128, 129, 256, 257, 511, 512, 513, 640, 769])
+def test_attention_cached_of_lengths_around_a_part(total, typ):
+    """Lengths where calls begin to be cut, and where parts end."""
+    rng = np.random.default_rng(total)
+    Cache(rng, [total - 1, total - 3, total - 2], [1, 3, 1], 4, 2, 64, 40, 16, typ).check()
+
+
 @pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("new", [1, 90])
 def test_attention_cached_pages_that_are_none(new, typ):
@@ -603,6 +611,48 @@ def test_attention_cached_pages_that_are_none(new, typ):
     ws = L.attention_cached_workspace(c.q, e, e, ints(c.table), ints(c.cu))
     L.pc_attention_cached(c.q, c.k, c.v, e, e, ints(c.table), ints([0, 0]), c.o, ints(c.cu), ws=ws)
     _check_forward(c.q, c.k, c.v, c.o, None, c.cu, 0.125, typ)
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dk,dv", [(24, 40), (88, 16), (7, 33)])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_attention_of_narrow_heads_keeps_what_is_not_finite_in_its_place(value, dk, dv, typ):
+    """The same where a head is narrower than the tile that it lies in, whole sequences and their gradients: the first elements of a row
+    stand there in the place of those behind it."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    rng = np.random.default_rng(15)
+    cu, at = [0, 150], 70
+    for what in range(4):
+        q, k, v, do = _qkv(rng, 150, 2, 2, dk, dv, typ)
+
+        def run():
+            o, lse = torch.empty_like(do), torch.empty((150, 2), device=DEV)
+            L.pc_attention_forward(q, k, v, o, lse, ints(cu))
+            grads = [torch.empty_like(t) for t in (q, k, v)]
+            L.pc_attention_backward(do, q, k, v, o, lse, *grads, ints(cu), ws=L.attention_workspace(q, k, v, ints(cu), backward=True))
+            return [get(t) for t in (o, lse[..., None], *grads)]
+        clean = run()
+        (q, k, v, do)[what][at, 1, 2] = value
+        dirty = run()
+        reach = [[(at, at + 1)] * 3 + [(0, at + 1)] * 2, [(at, 150)] * 3 + [(0, 150)] * 2,
+                 [(at, 150), (0, 0), (at, 150), (0, 150), (0, 150)], [(0, 0), (0, 0), (at, at + 1), (0, at + 1), (0, at + 1)]][what]
+        # An element of o that a tile taken again rounds the other way moves delta_i = do_i . o_i, so dq_i by
+        # scale sum_j P_ij k_j of that, at most scale max |k|, and dk_j by scale P_ij q_i, at most scale max |q|.
+        known = lambda x: np.where(np.isfinite(x), np.abs(x), 0.0)  # noqa: E731
+        with np.errstate(invalid="ignore"):
+            moved = (known(get(do)) * known(clean[0] - dirty[0])).sum(-1)
+        moved[reach[0][0]:reach[0][1], 1] = 0.0
+        more = [0.0, 0.0, dk ** -0.5 * known(get(k)).max() * moved[..., None],
+                dk ** -0.5 * known(get(q)).max() * np.broadcast_to(moved.sum(0)[None, :, None], (150, 2, 1)), 0.0]
+        for a, b, (lo, hi), extra, name in zip(clean, dirty, reach, more, ("o", "lse", "dq", "dk", "dv")):
+            free = np.ones(a.shape[:2], bool)
+            free[lo:hi, 1] = False
+            rms = np.sqrt((a * a).mean())
+            assert (np.abs(a - b) <= 2 * U[typ] * np.abs(a) + 1e-5 * rms + extra)[free].all(), name
+        with np.errstate(invalid="ignore"):
+            ro, rl = R.softmax_attention(get(q), get(k), get(v), cu, dk ** -0.5)
+        assert (np.isfinite(dirty[0][at:]) == np.isfinite(ro[at:])).all() and (np.isfinite(dirty[1][at:, :, 0]) == np.isfinite(rl[at:])).all()
 
 
 @pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
