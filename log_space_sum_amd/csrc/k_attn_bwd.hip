@@ -199,8 +199,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || MODE == ANY ? 1 : 2) void a
   const int heads = a.kv_heads * a.group, dk = a.dk, dv = a.dv;
   const float c = a.scale * LOG2E;
   for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
-    const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
-    const int64_t slot = b / a.kv_heads / a.nsplit;
+    const auto [kvh, split, slot] = block_of(b, a.kv_heads, slots);
     const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - slot);
     const int64_t first = at.tile * ATTN_ROWS, rows_all = at.len * a.group;
     if (at.seq < 0 || first >= rows_all) continue;
@@ -634,8 +633,8 @@ template <typename T, int D, FitMode MODE>
 __global__ __launch_bounds__(128 * PAIRS, MODE == ANY || (PairShape<T, D>::F32 && D > 64) ? 1 : 2) void attn_dkv(AttnArgs a, int64_t slots) {
   __shared__ typename PairShape<T, D>::Lds lds;
   for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
-    const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
-    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, 1, PairShape<T, D>::KEYS, b / a.kv_heads / a.nsplit);
+    const auto [kvh, split, slot] = block_of(b, a.kv_heads, slots);
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, 1, PairShape<T, D>::KEYS, slot);
     if (at.seq < 0 || at.tile * PairShape<T, D>::KEYS >= at.len) continue;
     // (both parts pass the same barriers)
     if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >= PAIRS) pair_tile<T, D, MODE, true>(lds, a, at, kvh, split);
@@ -674,7 +673,13 @@ __global__ __launch_bounds__(256) void attn_sum(AttnArgs a) {
       const float* p = part + (t * n + h) * dim;
       for (int d = lane; d < dim; d += 64) {
         float x = 0.0f;
-        for (int s = from; s <= to; ++s) x += p[s * step + d];
+        for (int s = from; s <= to; s += 4) {      // (in the parts' order, four in flight)
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = p[min(s + e, to) * step + d];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x += s + e <= to ? v[e] : 0.0f;
+        }
         ((T*)out)[t * ts + h * hs + d] = from_f32<T>(x);
       }
     };

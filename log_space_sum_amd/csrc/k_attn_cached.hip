@@ -106,7 +106,8 @@ __global__ __launch_bounds__(256, (Num<T>::IN == 3 || MODE == ANY) && D > 64 ? 1
   const int64_t per = (int64_t)a.kv_heads * a.nsplit;
   for (int64_t b = blockIdx.x; b < slots * per; b += gridDim.x) {
     const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
-    const Work<T> w = find_work<T>(a, slots - 1 - b / per, kvh, split, ATTN_ROWS, part_len);
+    const int64_t slot = b / per;
+    const Work<T> w = find_work<T>(a, slots - 1 - slot, kvh, split, ATTN_ROWS, part_len);
     if (w.rows.count == 0) continue;
     if (w.key0 >= w.key1) no_keys(w.rows, w.out);
     else
@@ -140,8 +141,10 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1
   const int dk = a.dk, dv = a.dv;
   const float c = fabsf(a.scale) * LOG2E;
   for (int64_t b = blockIdx.x; b < slots * per; b += gridDim.x) {
+    // parts, which are alike here, lie side by side (as the slowest index: 64 streams of up to 8192 252 us for 235)
     const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
-    const Work<T> w = find_work<T>(a, b / per, kvh, split, ATTN_FEW_ROWS, part_len);
+    const int64_t slot = b / per;
+    const Work<T> w = find_work<T>(a, slot, kvh, split, ATTN_FEW_ROWS, part_len);
     if (w.rows.count == 0) continue;
     if (w.key0 >= w.key1) {
       no_keys(w.rows, w.out);
@@ -342,23 +345,24 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
     const float f = on ? exp2_fast(st.x - top) : 0.0f;
     float l = f * st.y, acc[2] = {0.0f, 0.0f};
     for (int x = 32; x; x >>= 1) l += __shfl_xor(l, x);
-    // eight parts in flight; a part without keys has nothing written
-    for (int s0 = 0; active >> s0; s0 += 8) {
-      float v[8][2];
+    // four parts in flight; a part without keys has nothing written
+    for (int s0 = 0; s0 < a.nsplit; s0 += 4) {
+      float v[4][2];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float* p = a.part + (min(s0 + x, a.nsplit - 1) * n + i) * a.dv;
+      for (int x = 0; x < 4; ++x) {
+        v[x][0] = v[x][1] = 0.0f;
+        if (!(active >> (s0 + x) & 1)) continue;
+        const float* p = a.part + ((s0 + x) * n + i) * a.dv;
 #pragma unroll
         for (int e = 0; e < 2; ++e) v[x][e] = p[min(lane + 64 * e, a.dv - 1)];
       }
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
+      for (int x = 0; x < 4; ++x) {
         const float w = __shfl(f, s0 + x);
-        const bool there = active >> (s0 + x) & 1;
+        if (!(active >> (s0 + x) & 1)) continue;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) acc[e] = there ? fmaf(w, v[x][e], acc[e]) : acc[e];
+        for (int e = 0; e < 2; ++e) acc[e] = fmaf(w, v[x][e], acc[e]);
       }
-      if (s0 == 56) break;     // (a shift by 64 is none)
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e)

@@ -20,9 +20,9 @@ __global__ __launch_bounds__(256, 2) void attn_fwd(AttnArgs a, int64_t slots) {
   __shared__ typename FwdShape<T, D>::Lds lds;
   const int heads = a.kv_heads * a.group;
   for (int64_t b = blockIdx.x; b < slots * a.nsplit * a.kv_heads; b += gridDim.x) {
-    const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
+    const auto [kvh, split, slot] = block_of(b, a.kv_heads, slots);
     // the last tiles, which have the most keys, first
-    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - b / a.kv_heads / a.nsplit);
+    const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, ATTN_ROWS, slots - 1 - slot);
     const int64_t first = at.tile * ATTN_ROWS, rows_all = at.len * a.group;
     if (at.seq < 0 || first >= rows_all) continue;
     const int64_t tf = first / a.group, t = at.t0 + tf;

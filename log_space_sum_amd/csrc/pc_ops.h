@@ -173,7 +173,6 @@ constexpr int ATTN_MAX_DIM = 128;
 constexpr int ATTN_ROWS = 128;         // rows of a workgroup, and keys of one in the backward pass
 constexpr int ATTN_FEW_ROWS = 32;      // rows of a workgroup whose waves share them (cached)
 constexpr int ATTN_MAX_SPLIT = 64;     // parts of the keys
-constexpr int ATTN_PART_LEAST = 256, ATTN_PARTS_AIM = 512;   // keys of a part; workgroups below which keys are cut
 constexpr int ROTARY_MAX_DIM = 256;
 void launch_attn_fwd(const AttnArgs& a, int dtype, hipStream_t s);
 void launch_attn_bwd(const AttnArgs& a, int dtype, hipStream_t s);

@@ -267,16 +267,26 @@ AttnArgs attn_base(const pc_attention* d) {
 
 // Parts of whole sequences' keys (and, for dk and dv, rows), where rows, heads and
 // sequences are too few to fill the card: a tile of 128 rows is a chain of key
-// tiles, 1 to 5 us each.  A part costs its results, written and read once in float32, and a launch that joins them.
+// tiles, 1 to 5 us each.  A part costs its results, written and read once in float32, and a launch that joins them, so
+// tiles (`works`) are cut up to a number, to get `aim` of them, not into less than `least`, and no call of up to
+// `whole` keys.  Measured, heads x dims bfloat16 unless said, cut and not:
+//   forward: 128 works (2048 x 8 (2) x 64) 37, 40 us in two, float32 61, 73; 256 works (4 x 1000 x 8 (2) x 128) 57, 44;
+//     300 keys (8 (2) x 64) 18, 15; 700 19, 25
+//   backward: aims of 512, 1024: 128 works 113, 99, float32 258, 211; 256 works 174, 161; 1000 works (2 x 4000 x 16 (4) x
+//     128) 1223 whole, 1328; least 256, 128: 700 keys 58, 44, float32 7 ragged of up to 900
+//     x 6 (3) x 48, 80 133, 143
 struct AttnSplit {
   int nsplit, part_len;
 };
-AttnSplit attn_split(const pc_attention* d) {
+AttnSplit attn_split(const pc_attention* d, bool backward) {
   const int64_t group = d->heads / d->kv_heads, tokens = std::max<int64_t>(1, d->num_tokens);
   const int64_t longest = std::max<int64_t>(1, std::min(d->max_seqlen, tokens));
   const int64_t full = std::min<int64_t>(std::max(1, d->num_seqs), (tokens + longest - 1) / longest);
   const int64_t works = full * ((longest * group + ATTN_ROWS - 1) / ATTN_ROWS) * d->kv_heads;
-  int64_t len = std::max<int64_t>(ATTN_PART_LEAST, (longest * works + ATTN_PARTS_AIM - 1) / ATTN_PARTS_AIM);
+  const int64_t most = backward ? 768 : 128, aim = backward ? 1024 : 512, least = backward && d->dtype != PC_DTYPE_F32 ? 128 : 256;
+  const int64_t whole = backward ? 0 : d->dtype == PC_DTYPE_F32 ? 256 : 512;
+  if (works > most || longest <= whole) return {1, (int)std::min<int64_t>(longest, INT_MAX)};
+  int64_t len = std::max<int64_t>(least, (longest * works + aim - 1) / aim);
   len = round_up(std::max(len, (longest + ATTN_MAX_SPLIT - 1) / ATTN_MAX_SPLIT), 128);
   return {(int)((longest + len - 1) / len), (int)std::min<int64_t>(len, INT_MAX)};
 }
@@ -290,7 +300,7 @@ AttnWs attn_ws(const pc_attention* d, bool backward) {
     w.total += (bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t n = attn_split(d).nsplit, tokens = (size_t)d->num_tokens;
+  const size_t n = attn_split(d, backward).nsplit, tokens = (size_t)d->num_tokens;
   if (backward) w.delta = take(tokens * d->heads * sizeof(float));
   if (n > 1) {
     w.part = take(n * tokens * d->heads * (backward ? d->dim_k : d->dim_v) * sizeof(float));
@@ -313,7 +323,7 @@ void check_pages(const pc_attention* d) {
 // How new tokens meet a cache.  Rows are the new tokens of a sequence times the
 // heads that share a key / value head.
 struct CachedPlan {
-  bool few;              // up to 64 rows: tiles of 32 that all waves share
+  bool few;              // few rows: tiles of 32 that all waves share
   int nsplit, part_len;
   size_t part, stat, total;
 };
@@ -321,11 +331,16 @@ CachedPlan cached_plan(const pc_attention* d) {
   CachedPlan p{};
   const int64_t group = d->heads / d->kv_heads, tokens = std::max<int64_t>(1, d->num_tokens);
   const int64_t rows = std::max<int64_t>(1, std::min(d->max_seqlen, tokens)) * group;
-  p.few = rows <= 64;
-  const int64_t tile = p.few ? ATTN_FEW_ROWS : ATTN_ROWS;
   const int64_t full = std::min<int64_t>(std::max(1, d->num_seqs), (tokens * group + rows - 1) / rows);
+  // Two tiles of 32 rows read the keys twice, but each key tile is one wave's: faster for few streams and heads (64 rows of
+  // 4 streams x 2 heads x 64 behind 3000 19 us, as one tile of 128 22; 12 streams 25.5, 25; 32 44, 40; 16 x 8 x 128 111, 90; float32 4 streams 21, 33; 16 53, 39).
+  p.few = rows <= ATTN_FEW_ROWS || (rows <= 2 * ATTN_FEW_ROWS && full * d->kv_heads <= 24);
+  const int64_t tile = p.few ? ATTN_FEW_ROWS : ATTN_ROWS;
   const int64_t works = std::max<int64_t>(1, full * ((rows + tile - 1) / tile) * d->kv_heads);
   const int64_t longest = std::max<int64_t>(1, std::min<int64_t>(d->max_length, (int64_t)d->max_pages * d->page_size + tokens));
+  // Few rows: many parts, that streams of different lengths fill the card (64 streams of up to 8192 x 32 (8) heads x 128: 235 us with
+  // 8192 workgroups, 240 with 4096, 248 with 2048).  Many: two workgroups a CU (four chunks of 512 behind 8192 563 us; with 1024
+  // of half the length 591; 16 chunks of 64 behind 4000 187, 210, with 256 258).
   const int64_t aim = p.few ? 8192 : 512;
   // Short ones whole: a launch that joins parts costs 4 us (a token of 8 heads x 64 bfloat16 behind 500: 15 us whole, 18.5 in
   // parts; x 128 17.6, 18.9; behind 1000 18.4, 18.6 and 24, 19; float32 behind 500 19.6, 18.5).
@@ -801,7 +816,7 @@ int pc_attention_forward(int device, const pc_attention* d, void* ws, size_t ws_
     if (d->num_seqs == 0 || d->num_tokens == 0) return;
     AttnArgs a = attn_base(d);
     if (ws) {       // (without a workspace the keys are not cut)
-      const AttnSplit sp = attn_split(d);
+      const AttnSplit sp = attn_split(d, false);
       a.nsplit = sp.nsplit;
       a.part_len = sp.part_len;
       a.part = (float*)((char*)ws + w.part);
@@ -832,7 +847,7 @@ int pc_attention_backward(int device, const pc_attention* d, void* ws, size_t ws
     if (d->num_seqs == 0 || d->num_tokens == 0) return;
     DeviceGuard dg(device);
     AttnArgs a = attn_base(d);
-    const AttnSplit sp = attn_split(d);
+    const AttnSplit sp = attn_split(d, true);
     a.nsplit = sp.nsplit;
     a.part_len = sp.part_len;
     a.part = (float*)((char*)ws + w.part);
