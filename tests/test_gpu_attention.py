@@ -463,6 +463,7 @@ def test_attention_of_many_sequences():
 
 class Cache:
     """A cache in pages with sequences of `past` tokens in shuffled pages, their new tokens, and the definition of a call on them."""
+    gap = 1     # elements in front of each row: 8 leaves the rows of 16-bit types aligned
 
     def __init__(self, rng, past, new, H, K, dk, dv, page, typ, spare=2, order="token"):
         torch, types = T()
@@ -472,7 +473,7 @@ class Cache:
         pages = len(past) * each + spare
         self.table = rng.permutation(pages)[:len(past) * each].reshape(len(past), each)
         shape = {"token": (pages, page, K), "head": (pages, K, page)}[order]
-        self.k_cache, self.v_cache = (put(rng.normal(size=(*shape, d + 1)), typ)[..., 1:] for d in (dk, dv))
+        self.k_cache, self.v_cache = (put(rng.normal(size=(*shape, d + self.gap)), typ)[..., self.gap:] for d in (dk, dv))
         if order == "head":
             self.k_cache, self.v_cache = self.k_cache.transpose(1, 2), self.v_cache.transpose(1, 2)
         self.q, self.k, self.v, self.o = _qkv(rng, self.cu[-1], H, K, dk, dv, typ)
@@ -677,6 +678,51 @@ def test_attention_cached_keeps_what_is_not_finite_in_its_place(new, typ):
     assert (got[new - 1, :2, 3] == math.inf).all()
     want[new - 1, :2, 3] = got[new - 1, :2, 3] = 0
     assert (np.abs(got - want) <= TINY[typ] + U[typ] * np.abs(want) + tol).all()
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("past,new,H,K,dk,dv,page", CACHES)
+def test_attention_cached_of_aligned_rows(past, new, H, K, dk, dv, page, typ, monkeypatch):
+    monkeypatch.setattr(Cache, "gap", 8)
+    Cache(np.random.default_rng(page + dk), past, new, H, K, dk, dv, page, typ).check()
+
+
+@pytest.mark.parametrize("typ", ["bf16", "f16"])
+def test_attention_cached_of_aligned_rows_at_the_edges(typ, monkeypatch):
+    monkeypatch.setattr(Cache, "gap", 8)
+    test_attention_cached_single_tokens_and_orders(typ)
+    for new in (1, 40, 200):
+        test_attention_cached_in_parts(new, typ)
+    for new in (1, 90):
+        test_attention_cached_pages_that_are_none(new, typ)
+    for new in (2, 100):
+        test_attention_cached_keeps_what_is_not_finite_in_its_place(new, typ)
+    for total in (128, 257, 512, 513, 769):
+        test_attention_cached_of_lengths_around_a_part(total, typ)
+
+
+@pytest.mark.parametrize("n", [3, 130])
+def test_attention_cached_chunks_in_far_pages(n):
+    """The same for a chunk: few rows, and many."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    pages, page, K, d = 70000, 64, 4, 128
+    if torch.cuda.mem_get_info()[0] < pages * page * K * d * 2 * 2.5:
+        pytest.skip("memory")
+    kc, vc = (torch.zeros((pages, page, K, d), device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    rng = np.random.default_rng(17)
+    q, k, v, o = _qkv(rng, n, 4, K, d, d, "bf16")
+    pk, pv = put(rng.normal(size=(2, page, K, d)), "bf16"), put(rng.normal(size=(2, page, K, d)), "bf16")
+    kc[pages - 2:], vc[pages - 2:] = pk, pv
+    table = ints([[pages - 2, pages - 1, 1, pages - 3, 2]])
+    cu = ints([0, n])
+    ws = L.attention_cached_workspace(q, kc, vc, table, cu)
+    L.pc_attention_cached(q, k, v, kc, vc, table, ints([2 * page]), o, cu, ws=ws)
+    kk, vv = (np.concatenate([get(p).reshape(2 * page, K, d), get(x)]) for p, x in ((pk, k), (pv, v)))
+    want = R.attend(get(q), kk, vv, d ** -0.5, 2 * page)[0]
+    near(o, want, U["bf16"] * np.abs(want) + _errors(get(q), kk, vv, d ** -0.5, 2 * page)[0], "o")
+    m = min(n, page)
+    assert kc[1, :m].equal(k[:m]) and vc[1, :m].equal(v[:m]) and (n <= page or kc[pages - 3, :page].equal(k[page:2 * page]))
 
 
 def test_attention_cached_far_pages():
