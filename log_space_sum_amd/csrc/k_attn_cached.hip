@@ -9,7 +9,7 @@
 //
 // What bounds it.  Few rows: memory; 64 streams of up to 8192 tokens x 32 (8) heads x 128 bfloat16, a token each, take 235 us
 // (3.7 TB/s; a sum over a tensor reads 4.0).  Many: matrix instructions, as whole sequences; four chunks of 512 behind 8192 x 32 (8)
-// heads x 128 bfloat16 587 us, 0.97 PFLOP/s of its four products' work.  One token behind 1000 x 16 (4) heads x 64: 9.5 us and 3.5
+// heads x 128 bfloat16 562 us, 1.01 PFLOP/s of its four products' work.  One token behind 1000 x 16 (4) heads x 64: 9.5 us and 3.5
 // for joining, the chain of sequence, page, rows, two tiles, exchange.
 //
 // The new keys and values are read from their tensors, not from the cache, so storing

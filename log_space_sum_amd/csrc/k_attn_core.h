@@ -242,7 +242,7 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
       uint64_t kr, vr;       // rows of position key + lane
       if (key + BK <= keys.past) {
         // (all in the cache, strides of 32 bits: a quarter of the general form's instructions, of which a tile has
-        // as many as its matrix instructions leave room for; four chunks of 512 behind 8192 587 us without)
+        // as many as its matrix instructions leave room for; four chunks of 512 behind 8192 562 us, 575 without)
         const uint32_t page = keys.none(next) ? 0u : (uint32_t)next.page, row = (uint32_t)next.row;
         kr = (uint64_t)keys.kc + (uint64_t)page * (uint32_t)(2 * keys.k_page) + (uint64_t)row * (uint32_t)(2 * keys.k_row);
         vr = (uint64_t)keys.vc + (uint64_t)page * (uint32_t)(2 * keys.v_page) + (uint64_t)row * (uint32_t)(2 * keys.v_row);
