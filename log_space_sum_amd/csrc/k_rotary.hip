@@ -14,7 +14,7 @@
 // and its whole part left out, so positions of millions lose nothing.
 //
 // What bounds it: memory.  16384 tokens x 32 (8) heads x 128 bfloat16 take 70 us forward (4.8 TB/s; a copy 5.0); x 16 (16) heads
-// backward 86 us (4.7 TB/s), and 10 for the weights' gradients: each workgroup's sums, then theirs in a fixed order.
+// backward 84 us (4.8 TB/s), 92 with the weights' gradients: each workgroup's sums, then theirs in a fixed order.
 #include <algorithm>
 
 #include "k_attn.h"
@@ -254,18 +254,25 @@ __global__ __launch_bounds__(256) void rotary_bwd(RotaryArgs a, int share) {
   }
 }
 
-// dweight = sum of the blocks' parts in a fixed order: a workgroup for 16 of the 2 dim sums, 16 threads each.
+// dweight = sum of the blocks' parts in a fixed order: a workgroup for four of the 2 dim sums, 64 threads each, eight
+// parts in flight (16 sums with 16 threads each, a part after the other: 10 us for 1024 parts of 256).
 __global__ __launch_bounds__(256) void rotary_weights(RotaryArgs a) {
-  const int i = blockIdx.x * 16 + (threadIdx.x & 15), y = threadIdx.x >> 4;
-  __shared__ float s[16][17];
+  const int i = blockIdx.x * 4 + (threadIdx.x & 3), y = threadIdx.x >> 2;
+  __shared__ float s[4][4];
   float v = 0.0f;
   if (i < 2 * a.dim)
-    for (int p = y; p < a.parts; p += 16) v += a.part_sums[(int64_t)p * 2 * a.dim + i];
-  s[y][threadIdx.x & 15] = v;
+    for (int p = y; p < a.parts; p += 512) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = a.part_sums[(int64_t)min(p + 64 * e, a.parts - 1) * 2 * a.dim + i];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v += p + 64 * e < a.parts ? x[e] : 0.0f;
+    }
+  for (int x = 4; x < 64; x *= 2) v += __shfl_xor(v, x);
+  if ((threadIdx.x & 63) < 4) s[threadIdx.x >> 6][threadIdx.x & 3] = v;
   __syncthreads();
-  if (y != 0 || i >= 2 * a.dim) return;
-  v = 0.0f;
-  for (int p = 0; p < 16; ++p) v += s[p][threadIdx.x & 15];
+  if (threadIdx.x >= 4 || i >= 2 * a.dim) return;
+  v = s[0][threadIdx.x] + s[1][threadIdx.x] + s[2][threadIdx.x] + s[3][threadIdx.x];
   float* to = i < a.dim ? a.dqw : a.dkw;
   if (to) to[i < a.dim ? i : i - a.dim] = v;
 }
@@ -321,7 +328,7 @@ void launch_rotary_bwd(const RotaryArgs& a, int dtype, hipStream_t s) {
   if (!a.norm || !(a.dqw || a.dkw)) return;
   RotaryArgs b = a;
   if (a.tokens == 0) b.parts = 0;
-  launch_kernel(rotary_weights, dim3((2 * a.dim + 15) / 16), dim3(256), 0, s, b);
+  launch_kernel(rotary_weights, dim3((2 * a.dim + 3) / 4), dim3(256), 0, s, b);
 }
 
 }  // namespace pc

@@ -336,7 +336,7 @@ CachedPlan cached_plan(const pc_attention* d) {
   // 4 streams x 2 heads x 64 behind 3000 19 us, as one tile of 128 22; 12 streams 25.5, 25; 32 44, 40; 16 x 8 x 128 111, 90; float32 4 streams 21, 33; 16 53, 39).
   p.few = rows <= ATTN_FEW_ROWS || (rows <= 2 * ATTN_FEW_ROWS && full * d->kv_heads <= 24);
   const int64_t tile = p.few ? ATTN_FEW_ROWS : ATTN_ROWS;
-  const int64_t works = std::max<int64_t>(1, full * ((rows + tile - 1) / tile) * d->kv_heads);
+  const int64_t works = std::min<int64_t>(std::max<int64_t>(1, full * ((rows + tile - 1) / tile) * d->kv_heads), INT_MAX);
   const int64_t longest = std::max<int64_t>(1, std::min<int64_t>(d->max_length, (int64_t)d->max_pages * d->page_size + tokens));
   // Few rows: many parts, that streams of different lengths fill the card (64 streams of up to 8192 x 32 (8) heads x 128: 235 us with
   // 8192 workgroups, 240 with 4096, 248 with 2048).  Many: two workgroups a CU (four chunks of 512 behind 8192 563 us; with 1024

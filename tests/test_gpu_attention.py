@@ -331,6 +331,32 @@ def test_attention_strides(typ):
 
 
 @pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("off", ["q", "o", "qo"])
+def test_attention_of_rows_that_are_aligned_in_part(off, typ):
+    """Aligned keys and values, and queries or outputs an element off."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    rng = np.random.default_rng(19)
+    cu, H, K, d = [0, 130, 200], 4, 2, 64
+    q, k, v, do = _qkv(rng, 200, H, K, d, d, typ)
+
+    def moved(t):
+        wide = torch.zeros((*t.shape[:2], t.shape[2] + 9), device=DEV, dtype=t.dtype)[..., 1:d + 1]
+        wide.copy_(t)
+        return wide
+    o, lse, dq = torch.empty_like(do), torch.empty((200, H), device=DEV), torch.empty_like(q)
+    if "q" in off:
+        q, dq = moved(q), moved(dq)
+    if "o" in off:
+        o, do = moved(o), moved(do)
+    L.pc_attention_forward(q, k, v, o, lse, ints(cu), ws=L.attention_workspace(q, k, v, ints(cu)))
+    _check_forward(q, k, v, o, lse, cu, d ** -0.5, typ)
+    dk, dv = torch.empty_like(k), torch.empty_like(v)
+    L.pc_attention_backward(do, q, k, v, o, lse, dq, dk, dv, ints(cu), ws=L.attention_workspace(q, k, v, ints(cu), backward=True))
+    _check_backward(do, q, k, v, o, lse, (dq, dk, dv), cu, d ** -0.5, typ)
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
 def test_attention_of_large_scores(typ):
     """Scores of hundreds: weights of 1 and 0, sums that move their maximum often."""
     import log_space_sum_amd as L
