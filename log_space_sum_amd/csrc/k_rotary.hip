@@ -14,7 +14,7 @@
 // and its whole part left out, so positions of millions lose nothing.
 //
 // What bounds it: memory.  16384 tokens x 32 (8) heads x 128 bfloat16 take 70 us forward (4.8 TB/s; a copy 5.0); x 16 (16) heads
-// backward 84 us (4.8 TB/s), 92 with the weights' gradients: each workgroup's sums, then theirs in a fixed order.
+// backward 84 us (4.8 TB/s), 88 with the weights' gradients: each workgroup's sums, then theirs in a fixed order.
 #include <algorithm>
 
 #include "k_attn.h"
