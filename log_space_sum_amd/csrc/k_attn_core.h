@@ -236,13 +236,15 @@ __device__ __forceinline__ void attend_tile(typename FwdShape<T, D>::Lds& lds, c
   typename Keys<T, PAGED>::Place next{};
   if (DIRECT && PAGED && key0 < key1) next = keys.locate(key0 + lane);
   static_assert(!(DIRECT && PAGED) || BK == 64, "a lane a key");
+  const int in_cache = keys.num_pages > 0 ? keys.past : 0;     // positions whose rows may be any page's
   auto load = [&](int b, int key) {
     const uint32_t kb = lds_byte(lds.k[b].at) + wave * 1024, vb = lds_byte(lds.v[b].at) + wave * 1024;
     if constexpr (PAGED) {
       uint64_t kr, vr;       // rows of position key + lane
-      if (key + BK <= keys.past) {
+      if (key + BK <= in_cache) {
         // (all in the cache, strides of 32 bits: a quarter of the general form's instructions, of which a tile has
-        // as many as its matrix instructions leave room for; four chunks of 512 behind 8192 562 us, 575 without)
+        // as many as its matrix instructions leave room for; four chunks of 512 behind 8192 562 us, 575 without.  A key
+        // in no page takes page 0, which a cache without pages does not have.)
         const uint32_t page = keys.none(next) ? 0u : (uint32_t)next.page, row = (uint32_t)next.row;
         kr = (uint64_t)keys.kc + (uint64_t)page * (uint32_t)(2 * keys.k_page) + (uint64_t)row * (uint32_t)(2 * keys.k_row);
         vr = (uint64_t)keys.vc + (uint64_t)page * (uint32_t)(2 * keys.v_page) + (uint64_t)row * (uint32_t)(2 * keys.v_row);

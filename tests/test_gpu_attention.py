@@ -641,6 +641,22 @@ def test_attention_cached_pages_that_are_none(new, typ):
 
 
 @pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("past,new", [([64, 40], 90), ([100, 64], 1), ([100, 64], 40), ([5000, 200], 200), ([5000, 200], 2)])
+@pytest.mark.parametrize("gap", [1, 8])
+def test_attention_cached_without_pages(gap, past, new, typ, monkeypatch):
+    """A cache that has no pages at all: whatever the lengths and the table say, new tokens attend new tokens alone."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    monkeypatch.setattr(Cache, "gap", gap)
+    c = Cache(np.random.default_rng(18), past, [new] * 2, 4, 2, 64, 64, 16, typ)
+    c.table[0][:2] = -1, 2 ** 31 - 1
+    e = torch.empty((0, 16, 2, 64), device=DEV, dtype=c.k.dtype)
+    ws = L.attention_cached_workspace(c.q, e, e, ints(c.table), ints(c.cu))
+    L.pc_attention_cached(c.q, c.k, c.v, e, e, ints(c.table), ints(past), c.o, ints(c.cu), ws=ws)
+    _check_forward(c.q, c.k, c.v, c.o, None, c.cu, 0.125, typ)
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("dk,dv", [(24, 40), (88, 16), (7, 33)])
 @pytest.mark.parametrize("value", [math.inf, math.nan])
 def test_attention_of_narrow_heads_keeps_what_is_not_finite_in_its_place(value, dk, dv, typ):
