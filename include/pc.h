@@ -547,7 +547,9 @@ typedef struct pc_pages {
  *  heads, kv_heads: heads of q and o, and of k and v; kv_heads divides heads,
  *    and head h reads key / value head h / (heads / kv_heads).
  *  dim_k, dim_v: 1 .. 128.  num_tokens: at most 2^30.
- *  num_seqs, cu_seqlens: as pc_linear_attention's (num_seqs at most 2^24).
+ *  num_seqs, cu_seqlens: as pc_linear_attention's (num_seqs at most 2^24), in
+ *    ascending order: where they fall, it is not defined which rows are computed
+ *    (no memory outside the tensors is read or written).
  *  scale: finite, not 0.
  *  lse: device float32 [num_tokens, heads]; forward: nullable, backward: what the forward left.
  * Outputs are what float32 arithmetic gives, rounded once to their type.  What a row

@@ -412,7 +412,9 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t* cu, int seqs, int64_
   }
   lo = __builtin_amdgcn_readfirstlane(lo);
   const int64_t t0 = seq_start(cu, lo, tokens), t1 = max(seq_start(cu, lo + 1, tokens), t0);
-  return {lo, t0, t1 - t0, slot - (t0 * group / B + lo)};
+  // (where the offsets fall, the search can end at a sequence that starts behind the slot)
+  const int64_t tile = slot - (t0 * group / B + lo);
+  return {tile < 0 ? -1 : lo, t0, t1 - t0, tile};
 }
 
 // The sequence of token t (which lies in one): its first token and length.

@@ -462,6 +462,49 @@ def test_attention_edges():
     assert (o == 1).all()
 
 
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("cu", [[0, 600, 10, 610], [-4, 30, 20, 50, 2000], [590, 3, 3, 610, 0], [2000, 600, 500, 0], "random"])
+def test_attention_of_offsets_that_fall_stays_inside_its_tensors(cu, typ):
+    """Which rows are computed is not defined then, but nothing around the tensors is touched, whole sequences, their gradients and
+    over a cache; the next call is right."""
+    import log_space_sum_amd as L
+    torch, types = T()
+    rng = np.random.default_rng(24)
+    n, H, K, d, edge = 610, 4, 2, 64, 700
+    if cu == "random":
+        cu = rng.integers(-10, n + 10, 150).tolist()
+
+    def inside(*shape, dtype=types[typ], fill=7.0):
+        whole.append(torch.full((edge + n + edge, *shape), fill, device=DEV, dtype=dtype))
+        return whole[-1][edge:edge + n]
+    whole = []
+    o, dq, dk, dv, lse = inside(H, d), inside(H, d), inside(K, d), inside(K, d), inside(H, dtype=torch.float32)
+    q, k, v, do = _qkv(rng, n, H, K, d, d, typ)
+    bad, good = ints(cu), ints([0, n])
+    seqs = len(cu) - 1
+    table = ints(np.arange(seqs * 70).reshape(seqs, 70) + 5)
+    kc, vc = (torch.full((seqs * 70 + 10, 16, K, d), 7.0, device=DEV, dtype=types[typ]) for _ in range(2))
+    for at in (bad, good):
+        past = ints([30] * (at.numel() - 1))
+        for most in (n, 40):
+            for ws in (None, L.attention_workspace(q, k, v, at, most)):
+                L.pc_attention_forward(q, k, v, o, lse, at, most, ws=ws)
+                if at is good and most == n:
+                    _check_forward(q, k, v, o, lse, [0, n], d ** -0.5, typ)
+            L.pc_attention_backward(do, q, k, v, o, lse, dq, dk, dv, at, most, ws=L.attention_workspace(q, k, v, at, most, backward=True))
+            if at is good and most == n:
+                _check_backward(do, q, k, v, o, lse, (dq, dk, dv), [0, n], d ** -0.5, typ)
+            for m in (n, 3):
+                t = table[:at.numel() - 1]
+                ws = L.attention_cached_workspace(q, kc, vc, t, at, m, most)
+                L.pc_attention_cached(q, k, v, kc, vc, t, past, o, at, m, most, ws=ws)
+        torch.cuda.synchronize()
+        for x in whole:
+            assert (x[:edge] == 7).all() and (x[edge + n:] == 7).all()
+        for x in (kc, vc):
+            assert (x[:5] == 7).all() and (x[seqs * 70 + 5:] == 7).all()
+
+
 def test_attention_of_many_sequences():
     """More sequences than a search step of 64 x 64 tells apart, none, one or two tokens each."""
     import log_space_sum_amd as L
