@@ -552,8 +552,12 @@ typedef struct pc_pages {
  *    (no memory outside the tensors is read or written).
  *  scale: finite, not 0.
  *  lse: device float32 [num_tokens, heads]; forward: nullable, backward: what the forward left.
- * Outputs are what float32 arithmetic gives, rounded once to their type.  What a row
- * may not attend does not reach it, also if it is not finite. */
+ * Outputs are what float32 arithmetic gives, rounded once to their type.  Of
+ * float16 the weights, and the gradients of the scores, keep 22 bits each before
+ * they are multiplied again, and those below 2^-39 of the largest one in their sum
+ * none.  o's sums are divided by the weights' at their end: |v| times the number of
+ * keys has to stay in float32's range.  What a row may not attend does not reach
+ * it, also if it is not finite. */
 typedef struct pc_attention {
   int32_t dtype;
   int32_t heads, kv_heads, dim_k, dim_v;

@@ -13,7 +13,8 @@
 // Precision.  16-bit tensors are multiplied as they are.  What a kernel computes
 // and multiplies again (the weights P, the gradients dS of the scores) is split into
 // planes, each the rounding of what the planes before it leave: three of bfloat16 (24 bits), or
-// two of float16 (22 bits).  One plane, the usual choice, would add an error as
+// two of float16 (22 bits, and none below 2^-39 of a sum's largest: its numbers end at 2^-24, and the
+// largest is held near 2^14).  One plane, the usual choice, would add an error as
 // large as the output's own rounding; with these, outputs are what float32 arithmetic
 // gives, rounded once.  float32 tensors are split into three bfloat16 planes
 // too, and products of planes p, q with p + q <= 2 are summed (24 bits).
@@ -40,8 +41,8 @@ typedef uint4 frag;     // 8 elements of 16 bits
 constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.693147180559945309f;
 
 // ---- types -------------------------------------------------------------------
-// IN: planes of a tensor's values, W: planes of computed ones.  BIAS: weights are
-// held as 2^BIAS times themselves (float16: its small numbers have few bits).
+// IN: planes of a tensor's values, W: planes of computed ones.  BIAS: the forward's
+// weights, at most 1, are held as 2^BIAS times themselves (float16: its small numbers have few bits).
 struct Bf16Planes {
   static __device__ __forceinline__ f32x16 mma(frag a, frag b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);

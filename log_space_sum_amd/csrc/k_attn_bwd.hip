@@ -20,9 +20,11 @@
 namespace pc {
 namespace {
 
-// float16 planes of dS: a lane's column (a row of dq, a key of dk) is held as a
-// power of two times itself that keeps its largest element so far below 2^15, moved
-// as the maximum of a softmax is.  bfloat16's range needs none.
+// float16 planes of dS and, for dv, of P: a lane's column (a row of dq, a key of dk
+// or dv) is held as a power of two times itself that keeps its largest element so
+// far below 2^15, moved as the maximum of a softmax is.  bfloat16's range needs none.
+// (P at a fixed 2^14 would lose all bits of weights below 2^-39: keys that no row
+// looks at, whose dv is an ordinary number again under scaled losses.)
 template <typename T>
 struct Scale {
   static constexpr bool ON = std::is_same_v<T, f16>;
@@ -554,11 +556,8 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[4 * r4 + e] *= dp[4 * r4 + e] - d4[e];
       }
-      scale.move(s, acc);
-    } else if (N::BIAS) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] *= (float)(1 << N::BIAS);
     }
+    scale.move(s, acc);
     const auto& by = DK ? lds.q[x] : lds.go[x];
     if constexpr (IN == 1) {
       block_add<T, D, UNIT>(by, r0, lane, s, acc);
@@ -613,7 +612,7 @@ __device__ __forceinline__ void pair_tile(typename PairShape<T, D>::Lds& lds, co
     return;
   }
   if (!store) return;
-  const float f = DK ? a.scale / scale.by : 1.0f / (float)(1 << N::BIAS);
+  const float f = (DK ? a.scale : 1.0f) / scale.by;
   const int dim = DK ? dk : dv;
   const int64_t sum = ((int64_t)split * a.tokens + at.t0 + key) * a.kv_heads + kvh;
   float* parts = a.nsplit == 1 ? nullptr : DK ? a.part_k + sum * dk : a.part_v + sum * dv;

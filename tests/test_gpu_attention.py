@@ -396,6 +396,27 @@ def test_attention_gradients_of_small_and_large_values(typ, size):
 
 
 @pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,H,dk,dv", [(400, 1, 32, 32), (900, 4, 64, 40), (200, 3, 33, 7)])
+def test_attention_gradients_of_values_with_small_weights(n, H, dk, dv, typ):
+    """A key that no row looks at, of weights of 2^-37 and less, under gradients of a scaled loss (2^13 / H): sums of many rows that a
+    float16 holds again, to the bits of their weights."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    rng = np.random.default_rng(n)
+    q, k, v, do = _qkv(rng, n, H, 1, dk, dv, typ)
+    q[:], k[:] = 0, 0
+    q[..., 0], k[5, 0, 0] = 1, -24
+    v *= 2.0 ** -8
+    do.copy_(put(rng.uniform(0.5, 1, size=(n, H, dv)) * 2.0 ** 13 / H, typ))
+    o, lse = torch.empty_like(do), torch.empty((n, H), device=DEV)
+    L.pc_attention_forward(q, k, v, o, lse, scale=1.0)
+    grads = [torch.empty_like(t) for t in (q, k, v)]
+    L.pc_attention_backward(do, q, k, v, o, lse, *grads, scale=1.0, ws=L.attention_workspace(q, k, v, backward=True))
+    ref = _check_backward(do, q, k, v, o, lse, grads, [0, n], 1.0, typ)
+    assert np.abs(ref[2][5]).min() > 2.0 ** -21
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("what", ["q", "k", "v", "do"])
 @pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
 def test_attention_keeps_what_is_not_finite_in_its_place(typ, what, value):
