@@ -978,10 +978,14 @@ int pc_rotary_forward(int device, const pc_rotary* d, void* stream) {
   return guarded([&] {
     check_device(device);
     RotaryArgs a = rotary_base(d);
-    if (d->heads) check_heads(d, d->q, "q", false), check_out(d, d->q_out, d->heads, d->dim, "q_out", false);
-    if (d->kv_heads) check_heads(d, d->k, "k", false), check_out(d, d->k_out, d->kv_heads, d->dim, "k_out", false);
-    check_place(d, d->q_out, d->q, d->heads, "q_out");
-    check_place(d, d->k_out, d->k, d->kv_heads, "k_out");
+    auto side = [&](const pc_heads& y, const pc_heads& x, int heads, const char* n0, const char* n1) {
+      if (!heads) return;
+      check_heads(d, x, n1, false);
+      check_out(d, y, heads, d->dim, n0, false);
+      check_place(d, y, x, heads, n0);
+    };
+    side(d->q_out, d->q, d->heads, "q_out", "q");
+    side(d->k_out, d->k, d->kv_heads, "k_out", "k");
     if (d->num_tokens == 0 || d->heads + d->kv_heads == 0) return;
     a.q = attn_tensor(d->q);
     a.k = attn_tensor(d->k);

@@ -155,6 +155,15 @@ def test_rotary_workspace():
     assert L.lib().pc_rotary_backward(0, C.byref(none), None, 0, None) == L.PC_OK
 
 
+def test_rotary_of_no_heads_reads_nothing_of_them():
+    """What is said of heads that are not there is no error: null pointers at any strides."""
+    some, other = L.pc_heads(None, 32, 16), L.pc_heads(None, 0, 0)
+    none = _rotary(heads=0, kv_heads=0, norm=0, d_q_weight=None, d_k_weight=None, q=some, k=some, q_out=other, k_out=other, d_q_out=some,
+                   d_k_out=some, d_q=other, d_k=other)
+    assert L.lib().pc_rotary_forward(0, C.byref(none), None) == L.PC_OK, L.pc_last_error()
+    assert L.lib().pc_rotary_backward(0, C.byref(none), None, 0, None) == L.PC_OK, L.pc_last_error()
+
+
 def _attention(**change):
     d = L.pc_attention(dtype=1, heads=4, kv_heads=2, dim_k=16, dim_v=24, num_seqs=2, num_tokens=10, cu_seqlens=P, scale=0.25, lse=P,
                        num_pages=8, page_size=5, max_pages=3, page_table=P, page_table_stride=3, cached=P, max_seqlen=10, max_length=15)
