@@ -580,7 +580,9 @@ typedef struct pc_attention {
   int64_t max_seqlen, max_length;
 } pc_attention;
 
-/* Workspace of the forward (backward 0) or backward (1) pass. */
+/* Workspace of the forward (backward 0) or backward (1) pass on these shapes and this max_seqlen.
+ * Keys are cut into parts only where there are few rows, so a shorter or smaller call can need more
+ * than a longer one: ask for each, or take the largest of all that are to come. */
 int pc_attention_workspace_bytes(const pc_attention* d, int backward, size_t* bytes);
 
 /* Whole sequences: o (and lse) from q, k, v.  Without a workspace (ws NULL) the keys of
@@ -601,7 +603,8 @@ int pc_attention_backward(int device, const pc_attention* d, void* ws, size_t ws
  * page_table[i][p / page_size].  Each new token attends all tokens up to itself, and the new keys
  * and values are stored at their positions.  A page outside [0, num_pages) is none: its
  * cached positions are not attended, and new tokens are attended but not stored there,
- * nor beyond max_pages page_size.  Pages that hold new tokens must be no other sequence's in the same call. */
+ * nor beyond max_pages page_size.  Pages that hold new tokens must be no other sequence's in the same call.
+ * The workspace is that of these shapes, max_seqlen and max_length (a smaller call can need more, as above). */
 int pc_attention_cached_workspace_bytes(const pc_attention* d, size_t* bytes);
 int pc_attention_cached(int device, const pc_attention* d, void* ws, size_t ws_bytes, void* stream);
 

@@ -818,7 +818,8 @@ def _softmax_attention(q, k, v, scale, cu_seqlens, max_seqlen=None):
 
 def attention_workspace(q, k, v, cu_seqlens=None, max_seqlen=None, backward=False):
     """A workspace tensor for pc_attention_forward, or with backward for pc_attention_backward, on tensors of these
-    shapes."""
+    shapes and this max_seqlen.  A smaller call can need a larger one (few rows are cut into parts): make one for each shape,
+    or take the largest."""
     d, _, _, _ = _softmax_attention(q, k, v, None, cu_seqlens, max_seqlen)
     n = _bytes(lib().pc_attention_workspace_bytes, d, 1 if backward else 0)
     return _torch().empty(n, dtype=_torch().uint8, device=q.device)
@@ -864,7 +865,8 @@ def _cached_sizes(d, dev, k_cache, page_table, cu_seqlens, max_seqlen, max_lengt
 
 
 def attention_cached_workspace(q, k_cache, v_cache, page_table, cu_seqlens=None, max_seqlen=None, max_length=None):
-    """A workspace tensor for pc_attention_cached on new tokens like q and these arguments."""
+    """A workspace tensor for pc_attention_cached on new tokens like q and these arguments (as attention_workspace: of these
+    shapes and bounds; a smaller call can need a larger one)."""
     T, H, dk = _three(q, "q").shape
     d = pc_attention(_dtype(q, "q"), H, k_cache.shape[2], dk, v_cache.shape[3], 1, T)
     _cached_sizes(d, _device(q, "q"), k_cache, page_table, cu_seqlens, max_seqlen, max_length)

@@ -245,6 +245,32 @@ def test_attention_workspaces():
     _refuses(L.PC_ERR_INVALID_ARG, f.pc_attention_cached_workspace_bytes(None, C.byref(n)))
 
 
+@pytest.mark.parametrize("call", ["forward", "backward", "cached"])
+def test_attention_workspaces_are_of_one_shape(call):
+    """Sizes do not grow with the shapes: few rows are cut into parts, many are not.  What is asked for a call is what it takes: a
+    byte less is refused, whichever shape it was made for."""
+    f, n = L.lib(), C.c_size_t()
+
+    def bytes_of(d):
+        rc = (f.pc_attention_cached_workspace_bytes(C.byref(d), C.byref(n)) if call == "cached"
+              else f.pc_attention_workspace_bytes(C.byref(d), int(call == "backward"), C.byref(n)))
+        assert rc == L.PC_OK
+        return n.value
+
+    def shape(tokens, seqs):
+        pages = 4096
+        return _attention(num_tokens=tokens, num_seqs=seqs, max_seqlen=tokens // seqs, max_pages=pages, page_table_stride=pages, page_size=16,
+                          max_length=pages * 16, k_cache=L.pc_pages(P, 512, 32, 16), v_cache=L.pc_pages(P, 768, 48, 24))
+    shapes = [(1, 1), (64, 1), (512, 1), (700, 1), (2048, 1), (2048, 2), (4096, 1), (64, 64), (512, 64), (16384, 1), (65536, 8)]
+    sizes = [bytes_of(shape(*x)) for x in shapes]
+    assert any(a > b for a, b in zip(sizes, sizes[1:]))
+    assert sizes == [bytes_of(shape(*x)) for x in shapes]
+    run = getattr(f, "pc_attention_" + call)
+    for x, size in zip(shapes, sizes):
+        if size:
+            _refuses(L.PC_ERR_WORKSPACE, run(0, C.byref(shape(*x)), P, size - 1, None))
+
+
 @pytest.mark.parametrize("size", [1, 2, 3, 5, 7, 16, 24, 100, 1000, 65536, 65537, 2 ** 31 - 1])
 def test_the_division_by_a_page_size(size):
     """What the kernels divide positions by: j magic >> (31 + s) with s = ceil(log2 size)."""
