@@ -129,6 +129,15 @@ def _partner(x, part, inter):
     return y
 
 
+@pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,H,K,d,part", [(9001, 3, 1, 24, 24), (4099, 6, 2, 128, 64)])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+def test_rotary_of_more_tokens_than_waves(n, H, K, d, part, inter, norm, typ):
+    """The backward pass has 4096 waves at most: each takes a second token, its angles anew, its sums carried on."""
+    test_rotary(n, H, K, d, part, inter, norm, typ)
+
+
 def test_rotary_of_far_positions():
     """Positions up to 2^31 - 1 and below 0 with pairs of a radian a position: 64-bit angles."""
     import log_space_sum_amd as L
@@ -393,6 +402,25 @@ def test_attention_gradients_of_small_and_large_values(typ, size):
     if typ == "f16" and max(np.abs(r).max() for r in ref) > 60000:
         pytest.skip("beyond float16")
     _check_backward(do, q, k, v, o, lse, grads, [0, n], d ** -0.5, typ)
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dk,dv", [(32, 32), (64, 40), (33, 7)])
+def test_attention_gradients_of_large_values(dk, dv, typ):
+    """do of thousands with small queries, keys and values: gradients up to the end of float16's range, none beyond it."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    rng = np.random.default_rng(25)
+    n, H = 200, 2
+    q, k, v, do = _qkv(rng, n, H, 1, dk, dv, typ)
+    q, k, v = q * 0.25, k * 0.25, v * 2.0 ** -4
+    do.copy_(put(rng.normal(size=(n, H, dv)) * np.exp(rng.normal(size=(n, 1, 1)) * 0.5) * 1500, typ))
+    o, lse = torch.empty_like(do), torch.empty((n, H), device=DEV)
+    L.pc_attention_forward(q, k, v, o, lse)
+    grads = [torch.empty_like(t) for t in (q, k, v)]
+    L.pc_attention_backward(do, q, k, v, o, lse, *grads, ws=L.attention_workspace(q, k, v, backward=True))
+    ref = _check_backward(do, q, k, v, o, lse, grads, [0, n], dk ** -0.5, typ)
+    assert 3000 < max(np.abs(r).max() for r in ref) < 60000
 
 
 @pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
@@ -805,6 +833,34 @@ def test_attention_cached_of_aligned_rows_at_the_edges(typ, monkeypatch):
         test_attention_cached_keeps_what_is_not_finite_in_its_place(new, typ)
     for total in (128, 257, 512, 513, 769):
         test_attention_cached_of_lengths_around_a_part(total, typ)
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("new,page,index,rest", [(new, *at) for new in (1, 40) for at in (
+    (1, 999, 1), (3, 333, 2), (7, 1000, 7), (100, 60, 99), (1000, 77, 5), (65536, 300, 9), (65537, 300, 9), (1000003, 20, 6))] + [
+    (1, 65521, 32700, 11)])
+def test_attention_cached_finds_pages_of_any_size(new, page, index, rest, typ):
+    """All pages are none but the one that the last `rest` cached positions lie in, from its first row on, and the next: a position
+    that were divided by the page's size to another page, or row, would miss them."""
+    import log_space_sum_amd as L
+    torch, types = T()
+    rng = np.random.default_rng(page % 1000 + new)
+    H, d, past, behind = 4, 16, page * index + rest, -(-new // page) + 1
+    q, k, v, o = _qkv(rng, new, H, 1, d, d, typ)
+    kc, vc = (torch.full((1 + behind, page, 1, d), 7.0, device=DEV, dtype=types[typ]) for _ in range(2))
+    ck, cv = (put(rng.normal(size=(rest, 1, d)), typ) for _ in range(2))
+    kc[0, :rest], vc[0, :rest] = ck, cv
+    table = np.full((1, index + 1 + behind), -1)
+    table[0, index:] = np.arange(1 + behind)
+    cu = ints([0, new])
+    ws = L.attention_cached_workspace(q, kc, vc, ints(table), cu)
+    L.pc_attention_cached(q, k, v, kc, vc, ints(table), ints([past]), o, cu, ws=ws)
+    kk, vv = np.concatenate([get(ck), get(k)]), np.concatenate([get(cv), get(v)])
+    want = R.attend(get(q), kk, vv, d ** -0.5, rest)[0]
+    near(o, want, TINY[typ] + U[typ] * np.abs(want) + _errors(get(q), kk, vv, d ** -0.5, rest)[0], "o")
+    for cache, first, then in ((kc, ck, k), (vc, cv, v)):
+        rows = cache.view(-1, 1, d)
+        assert rows[:rest].equal(first) and rows[rest:rest + new].equal(then) and (rows[rest + new:] == 7).all()
 
 
 @pytest.mark.parametrize("n", [3, 130])
