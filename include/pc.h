@@ -488,7 +488,7 @@ int pc_linear_attention_step(int device, const pc_linear_attention* d, void* str
  * and the pairs (a, b) of its first rotary_dim elements are turned by
  * positions[token] freq[pair]:
  *   y_a = magnitude (g_a cos - g_b sin),  y_b = magnitude (g_b cos + g_a sin)
- * (the other elements are g).  Pair i is elements (i, i + rotary_dim / 2), or with
+ * (the other elements are g; squares are summed in float32).  Pair i is elements (i, i + rotary_dim / 2), or with
  * interleaved 1 (2 i, 2 i + 1).  Queries and keys go through the same call; heads or
  * kv_heads may be 0.  Angles are taken in 64 bits for any position.
  *  positions: device int32 [num_tokens] (any value); freq: device float64
@@ -557,7 +557,7 @@ typedef struct pc_pages {
  * they are multiplied again, and those below 2^-39 of the largest one in their sum
  * none.  o's sums are divided by the weights' at their end: |v| times the number of
  * keys has to stay in float32's range.  What a row may not attend does not reach
- * it, also if it is not finite. */
+ * it, also if it is not finite.  Outputs share no memory with inputs. */
 typedef struct pc_attention {
   int32_t dtype;
   int32_t heads, kv_heads, dim_k, dim_v;

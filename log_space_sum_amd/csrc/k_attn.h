@@ -296,7 +296,9 @@ __device__ __forceinline__ float add_halves(float x) {
 // Row 8 (r / 4) + 4 h + r % 4 of a result's register r.
 __device__ __forceinline__ int row_of(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
 // x, or -inf where `off`, inside a rare branch: the compiler would rather take the masks' instructions of every
-// tile, a quarter of its vector instructions.
+// tile, a quarter of its vector instructions.  Results are always assigned, s[r] = masked(s[r], off), never by
+// `if (off) s[r] = ..`: where `off` had a load behind ||, hipcc 7.2 left such an assignment to a result of 16 registers out
+// (the branch's body was empty, and the register that held -inf was overwritten by the copy of the others).
 __device__ __forceinline__ float masked(float x, bool off, float to = -INFINITY) {
   float y = off ? to : x;
   asm volatile("" : "+v"(y));

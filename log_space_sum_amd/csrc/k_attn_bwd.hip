@@ -11,8 +11,8 @@
 // the rows; a third kernel sums the parts.
 //
 // What bounds it: matrix instructions.  Of bfloat16 the first kernel takes S, dP and three planes of dS, 5 products' work, the
-// second S twice, dP and three planes each of P and dS, 9: 8 x 2048 x 16 heads x 128 in 1.00 ms are 0.96 PFLOP/s of them (a large
-// library product: 1.14); float32, 6 for each, 48 products' work: 3.65 ms, 0.9 PFLOP/s.  Small ones are chains of tiles.
+// second S twice, dP and three planes each of P and dS, 9: 8 x 2048 x 16 heads x 128 in 0.98 ms are 0.98 PFLOP/s of them (a large
+// library product: 1.39); float16, two planes, 11: 0.93 ms; float32, 6 for each, 48: 3.63 ms, 0.9 PFLOP/s.  Small ones are chains of tiles.
 #include <algorithm>
 
 #include "k_attn.h"

@@ -29,9 +29,8 @@ struct Work {
   RowOut out;
   int key0, key1;
 };
-// `len`: keys of a part (parts end at multiples of it), 0: not cut.
 template <typename T>
-__device__ __forceinline__ Work<T> find_work(const AttnArgs& a, int64_t slot, int kvh, int split, int tile, int part_len) {
+__device__ __forceinline__ Work<T> find_work(const AttnArgs& a, int64_t slot, int kvh, int split, int tile) {
   Work<T> w;
   w.rows.count = 0;
   const SeqTile at = find_tile(a.cu, a.seqs, a.tokens, a.group, tile, slot);
@@ -75,8 +74,8 @@ __device__ __forceinline__ Work<T> find_work(const AttnArgs& a, int64_t slot, in
     w.out.stat = a.stat + place;
   }
   const int end = w.rows.last(w.rows.count - 1) + 1;
-  w.key0 = a.nsplit > 1 ? (int)min((int64_t)split * part_len, (int64_t)end) : 0;
-  w.key1 = a.nsplit > 1 && split + 1 < a.nsplit ? (int)min((int64_t)(split + 1) * part_len, (int64_t)end) : end;
+  w.key0 = a.nsplit > 1 ? (int)min((int64_t)split * a.part_len, (int64_t)end) : 0;
+  w.key1 = a.nsplit > 1 && split + 1 < a.nsplit ? (int)min((int64_t)(split + 1) * a.part_len, (int64_t)end) : end;
   return w;
 }
 
@@ -101,13 +100,13 @@ __device__ __forceinline__ void join_cache(const AttnArgs& a, const Work<T>& w, 
 }
 
 template <typename T, int D, FitMode MODE>
-__global__ __launch_bounds__(256, (Num<T>::IN == 3 || MODE == ANY) && D > 64 ? 1 : 2) void attn_cached_many(AttnArgs a, int64_t slots, int part_len) {
+__global__ __launch_bounds__(256, (Num<T>::IN == 3 || MODE == ANY) && D > 64 ? 1 : 2) void attn_cached_many(AttnArgs a, int64_t slots) {
   __shared__ typename FwdShape<T, D>::Lds lds;
   const int64_t per = (int64_t)a.kv_heads * a.nsplit;
   for (int64_t b = blockIdx.x; b < slots * per; b += gridDim.x) {
     const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
     const int64_t slot = b / per;
-    const Work<T> w = find_work<T>(a, slots - 1 - slot, kvh, split, ATTN_ROWS, part_len);
+    const Work<T> w = find_work<T>(a, slots - 1 - slot, kvh, split, ATTN_ROWS);
     if (w.rows.count == 0) continue;
     if (w.key0 >= w.key1) no_keys(w.rows, w.out);
     else
@@ -132,7 +131,7 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 template <typename T, int D, FitMode MODE>
-__global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1 : 2) void attn_cached_few(AttnArgs a, int64_t slots, int part_len) {
+__global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1 : 2) void attn_cached_few(AttnArgs a, int64_t slots) {
   using N = Num<T>;
   constexpr bool UNIT = MODE == UNITS;
   constexpr int IN = N::IN, W = N::W, DS = D / 16, DB = D / 32, PER_ROW = Tile<T, 32, D>::P / 8, U = 32 * PER_ROW / 64;
@@ -144,7 +143,7 @@ __global__ __launch_bounds__(256, Num<T>::IN == 3 || (MODE == ANY && D > 64) ? 1
     // parts, which are alike here, lie side by side (as the slowest index: 64 streams of up to 8192 252 us for 235)
     const int kvh = (int)(b % a.kv_heads), split = (int)(b / a.kv_heads % a.nsplit);
     const int64_t slot = b / per;
-    const Work<T> w = find_work<T>(a, slot, kvh, split, ATTN_FEW_ROWS, part_len);
+    const Work<T> w = find_work<T>(a, slot, kvh, split, ATTN_FEW_ROWS);
     if (w.rows.count == 0) continue;
     if (w.key0 >= w.key1) {
       no_keys(w.rows, w.out);
@@ -378,8 +377,8 @@ void cached(const AttnArgs& a, bool few, hipStream_t s) {
   by_fit(fit_of<T>(a, true), [&](auto d, auto mode) {
     constexpr int D = decltype(d)::value;
     constexpr FitMode MODE = decltype(mode)::value;
-    if (!few) launch_kernel(attn_cached_many<T, D, MODE>, grid, dim3(256), 0, s, a, slots, a.part_len);
-    else launch_kernel(attn_cached_few<T, D, MODE>, grid, dim3(256), 0, s, a, slots, a.part_len);
+    if (!few) launch_kernel(attn_cached_many<T, D, MODE>, grid, dim3(256), 0, s, a, slots);
+    else launch_kernel(attn_cached_few<T, D, MODE>, grid, dim3(256), 0, s, a, slots);
   });
 }
 

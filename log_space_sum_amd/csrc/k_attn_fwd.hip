@@ -7,7 +7,8 @@
 //
 // What bounds it: matrix instructions.  Of 16-bit tensors a tile takes the scores and a product for each plane of the
 // weights (bfloat16 4 products' work in all, float16 3): 16384 tokens x 16 heads x 128 bfloat16 in 1.83 ms are 1.20 PFLOP/s of
-// them, the rate of a large library product (1.14); 24 ragged sequences x 16 heads x 64 float16 70 us.
+// them (a large library product: 1.39); float32, 6 for each, 8 x 2048 x 16 heads x 128 in 0.90 ms, 0.92 PFLOP/s; 24 ragged
+// sequences of up to 1500 x 16 heads x 64 float16 74 us.
 #include <algorithm>
 
 #include "k_attn_core.h"

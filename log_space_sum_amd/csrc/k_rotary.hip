@@ -278,7 +278,7 @@ __global__ __launch_bounds__(256) void rotary_weights(RotaryArgs a) {
 }
 
 // Waves that share a token: as many as there are rows for while tokens are few
-// (2048 waves at most then: eight a compute unit).
+// (doubled below 2048 waves, so fewer than 4096: sixteen a compute unit).
 int share_of(const RotaryArgs& a, int lanes) {
   const int rows = (std::max(a.heads, a.kv_heads) * lanes + 63) / 64;
   int s = 1;
@@ -319,7 +319,7 @@ void launch_any(const RotaryArgs& a, int dtype, bool backward, hipStream_t s) {
 }  // namespace
 
 // Blocks of the backward pass: each leaves one partial sum of the weights' gradients.
-int rotary_parts(int64_t tokens, int heads, int kv_heads) {
+int rotary_parts(int64_t tokens) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(tokens, 1024));
 }
 void launch_rotary_fwd(const RotaryArgs& a, int dtype, hipStream_t s) { launch_any(a, dtype, false, s); }

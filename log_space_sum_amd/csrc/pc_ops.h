@@ -197,7 +197,7 @@ struct RotaryArgs {
   float* part_sums;     // backward: [parts][2][dim]
   int32_t parts;
 };
-int rotary_parts(int64_t tokens, int heads, int kv_heads);
+int rotary_parts(int64_t tokens);
 void launch_rotary_fwd(const RotaryArgs& a, int dtype, hipStream_t s);
 void launch_rotary_bwd(const RotaryArgs& a, int dtype, hipStream_t s);
 

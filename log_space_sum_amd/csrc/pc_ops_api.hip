@@ -270,8 +270,8 @@ AttnArgs attn_base(const pc_attention* d) {
 // tiles, 1 to 5 us each.  A part costs its results, written and read once in float32, and a launch that joins them, so
 // tiles (`works`) are cut up to a number, to get `aim` of them, not into less than `least`, and no call of up to
 // `whole` keys.  Measured, heads x dims bfloat16 unless said, cut and not:
-//   forward: 128 works (2048 x 8 (2) x 64) 37, 40 us in two, float32 61, 73; 256 works (4 x 1000 x 8 (2) x 128) 57, 44;
-//     300 keys (8 (2) x 64) 18, 15; 700 19, 25
+//   forward: 128 works (2048 x 8 (2) x 64, four parts) 37, 50 us, float32 62, 117; 256 works (4 x 1000 x 8 (2) x 128) 57, 44;
+//     300 keys (8 (2) x 64) 18, 15; 700 (three parts) 18, 21, float32 27, 45
 //   backward: aims of 512, 1024: 128 works 113, 99, float32 258, 211; 256 works 174, 161; 1000 works (2 x 4000 x 16 (4) x
 //     128) 1223 whole, 1328; least 256, 128: 700 keys 58, 44, float32 7 ragged of up to 900
 //     x 6 (3) x 48, 80 133, 143
@@ -970,7 +970,7 @@ int pc_rotary_workspace_bytes(const pc_rotary* d, size_t* bytes) {
   return guarded([&] {
     need(bytes, "null bytes");
     check_rotary(d);
-    *bytes = (size_t)rotary_parts(d->num_tokens, d->heads, d->kv_heads) * 2 * d->dim * sizeof(float);
+    *bytes = (size_t)rotary_parts(d->num_tokens) * 2 * d->dim * sizeof(float);
   });
 }
 
@@ -1017,7 +1017,7 @@ int pc_rotary_backward(int device, const pc_rotary* d, void* ws, size_t ws_bytes
     side(d->d_q_out, d->d_q, d->q, d->heads, "d_q_out", "d_q", "q");
     side(d->d_k_out, d->d_k, d->k, d->kv_heads, "d_k_out", "d_k", "k");
     const bool weights = d->norm && (d->d_q_weight || d->d_k_weight);
-    a.parts = rotary_parts(d->num_tokens, d->heads, d->kv_heads);
+    a.parts = rotary_parts(d->num_tokens);
     if (weights) check_ws(ws, ws_bytes, (size_t)a.parts * 2 * d->dim * sizeof(float));
     if ((d->num_tokens == 0 || d->heads + d->kv_heads == 0) && !weights) return;
     a.q = attn_tensor(d->q);
