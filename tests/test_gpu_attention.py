@@ -909,6 +909,64 @@ def test_attention_cached_far_pages():
     assert kc[pages - 2, 0].equal(k[0]) and vc[pages - 2, 0].equal(v[0]) and not kc[0].any() and not kc[pages - 2, 1:].any()
 
 
+@pytest.mark.parametrize("d", [128, 124])
+def test_attention_of_tensors_beyond_32_bits(d):
+    """Rows whose offsets pass 2^32 bytes and 2^31 elements, loaded directly and through registers: norm and rotation in place, whole
+    sequences, gradients and new tokens over a cache; the last sequences against the definition."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    H, K, each, last = 64, 8, 250, 40
+    lens = [each] * 1120 + [last, 1, last]
+    cu = _cu(lens)
+    n = cu[-1]
+    if torch.cuda.mem_get_info()[0] < 7 * n * H * d * 2:
+        pytest.skip("memory")
+    assert n * H * d > 1 << 31
+    g = torch.Generator(device=DEV)
+    g.manual_seed(26)
+    q, do = (torch.randn((n, H, d), generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    k, v = (torch.randn((n, K, d), generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    end = slice(cu[-4], n)
+    near_end = [c - cu[-4] for c in cu[-4:]]
+    pos, freq = torch.arange(n, dtype=torch.int32, device=DEV), L.rotary_frequencies(32, device=DEV)
+    before = get(q[end])
+    L.pc_rotary_forward(q, k, q, k, pos, freq, norm=True)
+    want = R.rotary(before, np.arange(end.start, n), get(freq), norm=True)
+    size = np.abs(R.rotary(before, np.zeros(n - end.start), get(freq), norm=True))
+    near(q[end], want, U["bf16"] * np.abs(want) + (d / 4 + 16) * E * (size + _partner(size, 32, False)), "rotated")
+    o, lse, dq, dk, dv = torch.empty_like(do), torch.empty((n, H), device=DEV), torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    L.pc_attention_forward(q, k, v, o, lse, ints(cu), each, ws=L.attention_workspace(q, k, v, ints(cu), each))
+    L.pc_attention_backward(do, q, k, v, o, lse, dq, dk, dv, ints(cu), each, ws=L.attention_workspace(q, k, v, ints(cu), each, backward=True))
+    _check_forward(q[end], k[end], v[end], o[end], lse[end], near_end, d ** -0.5, "bf16")
+    _check_backward(*(t[end] for t in (do, q, k, v, o, lse)), [t[end] for t in (dq, dk, dv)], near_end, d ** -0.5, "bf16")
+    # new tokens of every sequence with nothing cached: outputs, and their rows in the cache
+    table = ints(np.arange(len(lens)))[:, None]
+    kc, vc = (torch.zeros((len(lens), each, K, d), device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    o.fill_(0)
+    ws = L.attention_cached_workspace(q, kc, vc, table, ints(cu), each, each)
+    L.pc_attention_cached(q, k, v, kc, vc, table, ints([0] * len(lens)), o, ints(cu), each, each, ws=ws)
+    _check_forward(q[end], k[end], v[end], o[end], None, near_end, d ** -0.5, "bf16")
+    assert kc[-1, :last].equal(k[-last:]) and vc[-1, :last].equal(v[-last:]) and not kc[-1, last:].any()
+
+
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+def test_attention_of_the_most_heads(typ):
+    """65535 heads that share one: rows of a token on many tiles."""
+    import log_space_sum_amd as L
+    torch, _ = T()
+    rng = np.random.default_rng(27)
+    n, H, d = 3, 65535, 8
+    q, k, v, do = _qkv(rng, n, H, 1, d, d, typ)
+    o, lse = torch.empty_like(do), torch.empty((n, H), device=DEV)
+    L.pc_attention_forward(q, k, v, o, lse, ws=L.attention_workspace(q, k, v))
+    _check_forward(q, k, v, o, lse, [0, n], d ** -0.5, typ)
+    grads = [torch.empty_like(t) for t in (q, k, v)]
+    L.pc_attention_backward(do, q, k, v, o, lse, *grads, ws=L.attention_workspace(q, k, v, backward=True))
+    _check_backward(do, q, k, v, o, lse, grads, [0, n], d ** -0.5, typ)
+    c = Cache(rng, [20], [n], H, 1, d, d, 16, typ)
+    c.check()
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
